@@ -24,6 +24,14 @@
  *   ddt_build_chain_visibility  a prefill chunk's chain and its causal mask
  *   ddt_prefill_step        chain + causal mask, then the attention, in one call
  *
+ * and the same step for a grouped-query layer, whose cache holds one K row and
+ * one V row per token in pools of their own:
+ *   ddt_gqa_norm_rope_append  per-head norm and rotation of q and k, k and v into the cache
+ *   ddt_gqa_verify_attn     tree-verify attention over grouped-query K/V rows
+ *   ddt_cache_commit        ddt_commit_kv for every layer's pool of any row width
+ *   ddt_cache_copy          rows copied to other rows in every layer's pool
+ *   ddt_cache_compact       live rows moved to the front of every pool
+ *
  * Conventions for every entry point:
  *   - Pointers marked (device) must be device memory of the current CUDA
  *     device; pointers marked (host) are host memory.  The caller owns all
@@ -79,6 +87,8 @@ extern "C" {
 #define DDT_MAX_Q_LEN 128   /* budget + 1 */
 #define DDT_MAX_SPLITS 128
 #define DDT_MAX_VOCAB 262144 /* ddt_accept_sampled */
+#define DDT_GQA_MAX_HEADS 128 /* query heads of the grouped-query calls */
+#define DDT_CACHE_MAX_ROWS (1 << 24) /* ddt_cache_compact: rows of a pool */
 
 typedef enum {
     DDT_OK = 0,
@@ -102,6 +112,7 @@ typedef enum {
 #define DDT_DEVERR_TIMEOUT      0x100u  /* a bounded wait inside a kernel ran out */
 #define DDT_DEVERR_ACCEPTED     0x200u  /* accept_len / accepted_nodes not an accepted path */
 #define DDT_DEVERR_SAMPLE       0x400u  /* sampling accept: links not a tree, or too few coins */
+#define DDT_DEVERR_POSITION     0x800u  /* a token's position outside the rotation table */
 
 const char *ddt_status_string(ddt_status s);
 int32_t ddt_abi_version(void);
@@ -583,6 +594,173 @@ ddt_status ddt_step_graph_destroy(ddt_step_graph *graph);
  * for a limit out of range, DDT_ERR_CUDA if the launch fails, else DDT_OK.
  */
 ddt_status ddt_selftest_wait_timeout(uint32_t poll_limit, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Grouped-query layers.  The pages' stages around the attention (tree, mask,
+ * accept) know nothing of the cache's layout; the calls below are the layer's
+ * part of the step for a model whose cache is not latent: num_heads query
+ * heads share num_kv_heads K/V heads (query head h reads K/V head
+ * h / (num_heads / num_kv_heads)), and a token's cache is one row of K and one
+ * of V, each num_kv_heads * head_dim bf16.  Rows are named by kv_indices /
+ * kv_indptr exactly as in ddt_verify_attn: per request prefix_len_b prefix
+ * slots, then q_len_b slots of the new tokens in node order.
+ *
+ * In these calls a request may have q_len_b = 0 (it is skipped), and total_q
+ * may exceed qo_indptr[batch]: the rows behind the last request are neither
+ * read nor written.  total_kv and total_mask_words are the sizes of kv_indices
+ * and mask; offsets beyond them latch DDT_DEVERR_KV_INDPTR / _MASK_INDPTR and
+ * the request is skipped.  Every argument in device memory may be the output
+ * of the kernel launched just before on the same stream.
+ *
+ * ddt_gqa_norm_rope_append -- what a grouped-query layer does to a projection's
+ * output before its attention, in one pass over it:
+ *   q, k:  y = x * rsqrt(mean(x^2) + eps) * weight over each head's head_dim
+ *          values (weight NULL: y = x), then the pairs of the first rope_dim
+ *          values rotated by the angle table's row of the token's position,
+ *          (a, b) -> (a cos - b sin, b cos + a sin); pair i is (i, i +
+ *          rope_dim/2), or (2i, 2i + 1) when `interleaved`;
+ *   position of token i of request b: prefix_len_b + depth (the tree's depth of
+ *          node i; depth NULL: prefix_len_b + i, a chain), with prefix_len_b =
+ *          kv_len_b - q_len_b (the root sits right behind the prefix);
+ *   q goes to q_out, k and v to rows kv_indices[kv_indptr[b] + prefix_len_b + i]
+ *          of the pools.
+ * Arithmetic is fp32 with one rounding to bf16 at the end; v is copied.
+ *
+ *   q, k, v     (device) bf16 [total_q][heads][head_dim], token t at t * stride
+ *               elements (q_stride, k_stride, v_stride: multiples of 8, at least
+ *               heads * head_dim), so the three may be slices of one projection.
+ *   q_weight, k_weight (device) bf16 [head_dim], each or both NULL: no norm.
+ *   cos_sin     (device) float [max_pos][rope_dim]: rope_dim/2 cosines, then
+ *               rope_dim/2 sines; NULL when rope_dim is 0 (no rotation).
+ *   depth       (device) int32 [total_q] or NULL.
+ *   q_out       (device) bf16 [total_q][num_heads][head_dim]; may be q itself
+ *               when q_stride = num_heads * head_dim.
+ *   k_pool, v_pool (device) bf16, row r at r * pool_stride elements (a multiple
+ *               of 8, at least num_kv_heads * head_dim).
+ * All pointers 16-byte aligned (weights, cos_sin too).  Supported: head_dim 64
+ * or 128; rope_dim a multiple of 16 up to head_dim; num_heads a multiple of
+ * num_kv_heads, at most DDT_GQA_MAX_HEADS; batch and total_q up to 2^31 - 1.
+ * Device checks: offsets (DDT_DEVERR_QO_INDPTR, _KV_INDPTR), a slot outside
+ * the pool (DDT_DEVERR_KV_INDEX: the token's k and v are not written), a
+ * position outside [0, max_pos) (DDT_DEVERR_POSITION: nothing of the token is
+ * written).  No two tokens may share a slot.
+ */
+ddt_status ddt_gqa_norm_rope_append(
+    const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride, const uint16_t *v,
+    int64_t v_stride, const uint16_t *q_weight, const uint16_t *k_weight, float eps,
+    const float *cos_sin, int64_t max_pos, int32_t rope_dim, int32_t interleaved,
+    const int32_t *depth, const int32_t *qo_indptr, const int32_t *kv_indices,
+    const int32_t *kv_indptr, int32_t batch, int32_t total_q, int32_t total_kv, int32_t num_heads,
+    int32_t num_kv_heads, int32_t head_dim, uint16_t *q_out, uint16_t *k_pool, uint16_t *v_pool,
+    int64_t pool_stride, int64_t pool_rows, void *stream);
+
+/*
+ * ddt_gqa_verify_attn -- ddt_verify_attn for a grouped-query layer: for row
+ * (token t of request b = node i, head h), with g = h / (num_heads /
+ * num_kv_heads) and row_j = kv_indices[kv_indptr[b] + j],
+ *   s_j = scale * <q[t,h,:], k_pool[row_j][g,:]> over the columns j of [0,
+ *         kv_len_b) whose mask bit (i, j) is set,
+ *   out[t,h,:] = sum_j softmax(s)_j * v_pool[row_j][g,:],
+ *   lse[t,h]   = log(sum_j exp(s_j))   (natural log).
+ * Every mask bit is honoured: a column that a row does not see does not reach
+ * it, whatever its K and V rows hold (infinities and NaN included).  A row with
+ * no visible column gets out = 0 and lse = -inf.  Decode is q_len 1, a prefill
+ * chunk the mask of ddt_build_chain_visibility.
+ *
+ *   q           (device) bf16 [total_q][num_heads][head_dim], 16-byte aligned.
+ *   k_pool, v_pool (device) bf16, row r at r * pool_stride elements (a multiple
+ *               of 8, at least num_kv_heads * head_dim), 16-byte aligned.
+ *   kv_indices, kv_indptr, qo_indptr, mask, mask_indptr (device) as in
+ *               ddt_verify_attn.
+ *   num_splits  0 = choose among the counts whose partial results fit
+ *               workspace_bytes (1 needs none), else 1..128.
+ *   out         (device) bf16 [total_q][num_heads][head_dim], 16-byte aligned:
+ *               what the layer's output projection reads.
+ *   lse         (device) float [total_q][num_heads] or NULL.
+ *   workspace   (device) 256-byte aligned; ddt_gqa_verify_attn_workspace_size
+ *               (total_q, num_heads, head_dim, splits) bytes for an explicit
+ *               num_splits; may be NULL for one split.  Calls that may overlap
+ *               on the GPU need a workspace each.
+ * Supported: head_dim 64 or 128, num_heads a multiple of num_kv_heads and at
+ * most DDT_GQA_MAX_HEADS, max_q_len <= 128, pool_rows <= 2^31 - 1.
+ * Device checks (latched, the request's rows left unwritten): q_len outside
+ * [0, max_q_len] or offsets outside [0, total_q] (DDT_DEVERR_QO_INDPTR),
+ * kv_len outside [q_len, max_kv_len] or offsets outside [0, total_kv]
+ * (DDT_DEVERR_KV_INDPTR), mask words that do not number q_len * ceil(kv_len /
+ * 32) or lie outside [0, total_mask_words] (DDT_DEVERR_MASK_INDPTR), a slot
+ * outside the pool (DDT_DEVERR_KV_INDEX: row 0 is read instead).
+ *
+ * ddt_gqa_verify_attn_num_splits() returns the count chosen for these bounds
+ * with an unlimited workspace, on num_sms SMs (<= 0: the current device's).
+ */
+int32_t ddt_gqa_verify_attn_num_splits(int32_t batch, int32_t num_heads, int32_t num_kv_heads,
+                                       int32_t max_q_len, int32_t max_kv_len, int32_t num_sms);
+size_t ddt_gqa_verify_attn_workspace_size(int32_t total_q, int32_t num_heads, int32_t head_dim,
+                                          int32_t num_splits);
+ddt_status ddt_gqa_verify_attn(
+    const uint16_t *q, const uint16_t *k_pool, const uint16_t *v_pool, int64_t pool_stride,
+    int64_t pool_rows, const int32_t *kv_indices, const int32_t *kv_indptr,
+    const int32_t *qo_indptr, const uint32_t *mask, const int32_t *mask_indptr, int32_t batch,
+    int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t total_q, int32_t total_kv,
+    int32_t total_mask_words, int32_t max_q_len, int32_t max_kv_len, float scale,
+    int32_t num_splits, uint16_t *out, float *lse, void *workspace, size_t workspace_bytes,
+    void *stream);
+
+/*
+ * Cache rows of every layer at once.  The layers' pools are one slab: pool p
+ * (p < num_pools: one per layer for a latent cache, one for K and one for V
+ * per layer for a grouped-query one) starts at p * pool_bytes bytes and holds
+ * pool_rows rows of row_bytes bytes; a slot names the same row in all of them.
+ * row_bytes and pool_bytes are multiples of 16, pool_bytes at least pool_rows *
+ * row_bytes, the slab 16-byte aligned.
+ *
+ * ddt_cache_copy -- row dst[i] of every dst pool <- row src[i] of the same src
+ * pool, for i < n: a request's rows forked or moved, within one slab or into
+ * another.  A row may be copied to several places.  Destinations are distinct,
+ * and none is the source of another pair (src[i] = dst[i] is allowed).
+ *   src, dst    (device) int32 [n].
+ * Device check: a slot outside its pool (DDT_DEVERR_KV_INDEX: the pair is
+ * skipped).
+ */
+ddt_status ddt_cache_copy(const void *src_slab, int64_t src_pool_bytes, int64_t src_pool_rows,
+                          void *dst_slab, int64_t dst_pool_bytes, int64_t dst_pool_rows,
+                          int32_t num_pools, int64_t row_bytes, const int32_t *src,
+                          const int32_t *dst, int32_t n, void *stream);
+
+/*
+ * ddt_cache_commit -- ddt_commit_kv (the same rows, checks and error bits) in
+ * every pool of a slab: for k < accept_len[b]
+ *   row(P_b + k) <- row(P_b + accepted_nodes[b][k]), every source read before
+ * any destination is written; new_len[b] = P_b + accept_len[b].  A request with
+ * q_len_b = 0 has accept_len 0 and nothing moves.
+ */
+ddt_status ddt_cache_commit(void *slab, int64_t pool_bytes, int64_t pool_rows, int32_t num_pools,
+                            int64_t row_bytes, const int32_t *kv_indices, const int32_t *kv_indptr,
+                            const int32_t *qo_indptr, const int32_t *accept_len,
+                            const int32_t *accepted_nodes, int32_t batch, int32_t total_kv,
+                            int32_t max_depth, int32_t *new_len, void *stream);
+
+/*
+ * ddt_cache_compact -- the rows that kv_indices names (n different ones; rows
+ * shared by several requests are one) moved into rows 0 .. n - 1 of every pool:
+ * the k-th unnamed row below n takes the k-th named row at or above n, other
+ * rows stay where they are.  Rows n .. pool_rows - 1 are free afterwards; a
+ * request is freed by leaving its slots out of kv_indices.
+ *   kv_indices  (device) int32 [total].
+ *   new_indices (device) int32 [total]: the slots after the move; may be
+ *               kv_indices itself.
+ *   live        (device) int32 [1]: n.
+ *   workspace   (device) ddt_cache_compact_workspace_size(pool_rows) bytes,
+ *               256-byte aligned; calls that may overlap need one each.
+ * Supported: pool_rows <= DDT_CACHE_MAX_ROWS.  Device check: a slot outside the
+ * pool (DDT_DEVERR_KV_INDEX: it names no row and is copied unchanged).
+ */
+size_t ddt_cache_compact_workspace_size(int64_t pool_rows);
+ddt_status ddt_cache_compact(void *slab, int64_t pool_bytes, int64_t pool_rows, int32_t num_pools,
+                             int64_t row_bytes, const int32_t *kv_indices, int32_t total,
+                             int32_t *new_indices, int32_t *live, void *workspace,
+                             size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

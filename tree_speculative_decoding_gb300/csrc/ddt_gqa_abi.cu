@@ -1,0 +1,239 @@
+// ddt_gqa_abi.cu -- the extern "C" entry points of the grouped-query layer and
+// of the cache-row calls: host-side argument checks, sizing and launches.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "ddt_internal.cuh"
+
+namespace {
+
+inline cudaStream_t as_stream(void *s) { return static_cast<cudaStream_t>(s); }
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+inline bool misaligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
+inline ddt_status launched(cudaError_t e) { return e == cudaSuccess ? DDT_OK : DDT_ERR_CUDA; }
+
+// head layout of a grouped-query call
+ddt_status check_heads(int32_t num_heads, int32_t num_kv_heads, int32_t head_dim) {
+    if (num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads) return DDT_ERR_INVALID_ARG;
+    if (num_heads > DDT_GQA_MAX_HEADS || (head_dim != 64 && head_dim != 128)) return DDT_ERR_UNSUPPORTED;
+    return DDT_OK;
+}
+bool bad_pool_stride(int64_t stride, int32_t num_kv_heads, int32_t head_dim) {
+    return stride < (int64_t)num_kv_heads * head_dim || stride % 8;
+}
+
+// layout of a slab of pools
+bool bad_slab(const void *slab, int64_t pool_bytes, int64_t pool_rows, int32_t num_pools, int64_t row_bytes) {
+    if (!slab || misaligned(slab, 16) || pool_rows < 1 || num_pools < 1 || row_bytes < 16 || row_bytes % 16 ||
+        pool_bytes % 16 || row_bytes / 16 > INT32_MAX)
+        return true;
+    return pool_rows > INT64_MAX / row_bytes || pool_bytes < pool_rows * row_bytes;
+}
+
+}  // namespace
+
+extern "C" {
+
+ddt_status ddt_gqa_norm_rope_append(
+    const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride, const uint16_t *v,
+    int64_t v_stride, const uint16_t *q_weight, const uint16_t *k_weight, float eps,
+    const float *cos_sin, int64_t max_pos, int32_t rope_dim, int32_t interleaved,
+    const int32_t *depth, const int32_t *qo_indptr, const int32_t *kv_indices,
+    const int32_t *kv_indptr, int32_t batch, int32_t total_q, int32_t total_kv, int32_t num_heads,
+    int32_t num_kv_heads, int32_t head_dim, uint16_t *q_out, uint16_t *k_pool, uint16_t *v_pool,
+    int64_t pool_stride, int64_t pool_rows, void *stream) {
+    if (!q || !k || !v || !qo_indptr || !kv_indices || !kv_indptr || !q_out || !k_pool || !v_pool || batch < 0 ||
+        total_q < 0 || total_kv < 0 || pool_rows < 1 || !(eps >= 0.f) || !isfinite(eps) || rope_dim < 0 || max_pos < 0 ||
+        (rope_dim > 0 && !cos_sin))
+        return DDT_ERR_INVALID_ARG;
+    const ddt_status heads = check_heads(num_heads, num_kv_heads, head_dim);
+    if (heads != DDT_OK) return heads;
+    if (rope_dim % 16 || rope_dim > head_dim) return DDT_ERR_UNSUPPORTED;
+    const int64_t qw = (int64_t)num_heads * head_dim, kw = (int64_t)num_kv_heads * head_dim;
+    if (q_stride < qw || k_stride < kw || v_stride < kw || q_stride % 8 || k_stride % 8 || v_stride % 8 ||
+        bad_pool_stride(pool_stride, num_kv_heads, head_dim))
+        return DDT_ERR_INVALID_ARG;
+    // in place only where a token's rows stay where they are
+    if (q_out == q && q_stride != qw) return DDT_ERR_INVALID_ARG;
+    const void *aligned[] = {q, k, v, q_weight, k_weight, cos_sin, q_out, k_pool, v_pool};
+    for (const void *p : aligned)
+        if (misaligned(p, 16)) return DDT_ERR_INVALID_ARG;
+    if (batch == 0 || total_q == 0) return DDT_OK;
+    unsigned int *err = ddt::device_error_word();
+    if (!err) return DDT_ERR_CUDA;
+    ddt::AppendArgs a;
+    memset(&a, 0, sizeof a);
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.eps = eps;
+    a.cos_sin = cos_sin;
+    a.max_pos = max_pos;
+    a.rope_dim = rope_dim;
+    a.interleaved = interleaved != 0;
+    a.depth = depth;
+    a.qo_indptr = qo_indptr;
+    a.kv_indices = kv_indices;
+    a.kv_indptr = kv_indptr;
+    a.batch = batch;
+    a.total_q = total_q;
+    a.total_kv = total_kv;
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.q_out = q_out;
+    a.k_pool = k_pool;
+    a.v_pool = v_pool;
+    a.pool_stride = pool_stride;
+    a.pool_rows = pool_rows;
+    a.err = err;
+    return launched(ddt::launch_norm_rope_append(a, ddt::device_sm_count(), as_stream(stream)));
+}
+
+int32_t ddt_gqa_verify_attn_num_splits(int32_t batch, int32_t num_heads, int32_t num_kv_heads,
+                                       int32_t max_q_len, int32_t max_kv_len, int32_t num_sms) {
+    if (batch < 1 || num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads || max_q_len < 1 ||
+        max_kv_len < 1)
+        return 1;
+    if (num_sms <= 0) num_sms = ddt::device_sm_count();
+    return ddt::gqa_choose_splits(batch, num_heads, num_kv_heads, max_q_len, max_kv_len, num_sms, DDT_MAX_SPLITS);
+}
+
+size_t ddt_gqa_verify_attn_workspace_size(int32_t total_q, int32_t num_heads, int32_t head_dim,
+                                          int32_t num_splits) {
+    if (total_q < 1 || num_heads < 1 || head_dim < 1 || num_splits <= 1) return 0;
+    const size_t rows = (size_t)total_q * num_heads;
+    return align256(rows * num_splits * head_dim * sizeof(float)) + align256(rows * num_splits * sizeof(float));
+}
+
+ddt_status ddt_gqa_verify_attn(
+    const uint16_t *q, const uint16_t *k_pool, const uint16_t *v_pool, int64_t pool_stride,
+    int64_t pool_rows, const int32_t *kv_indices, const int32_t *kv_indptr,
+    const int32_t *qo_indptr, const uint32_t *mask, const int32_t *mask_indptr, int32_t batch,
+    int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t total_q, int32_t total_kv,
+    int32_t total_mask_words, int32_t max_q_len, int32_t max_kv_len, float scale,
+    int32_t num_splits, uint16_t *out, float *lse, void *workspace, size_t workspace_bytes,
+    void *stream) {
+    if (!q || !k_pool || !v_pool || !kv_indices || !kv_indptr || !qo_indptr || !mask || !mask_indptr || !out ||
+        batch < 0 || total_q < 0 || total_kv < 0 || total_mask_words < 0 || pool_rows < 1 || max_q_len < 0 ||
+        max_kv_len < max_q_len || !isfinite(scale) || num_splits < 0)
+        return DDT_ERR_INVALID_ARG;
+    const ddt_status heads = check_heads(num_heads, num_kv_heads, head_dim);
+    if (heads != DDT_OK) return heads;
+    if (max_q_len > DDT_MAX_Q_LEN || num_splits > DDT_MAX_SPLITS || pool_rows > INT32_MAX || batch > 65535)
+        return DDT_ERR_UNSUPPORTED;
+    if (misaligned(q, 16) || misaligned(k_pool, 16) || misaligned(v_pool, 16) || misaligned(out, 16) ||
+        misaligned(workspace, 256) || bad_pool_stride(pool_stride, num_kv_heads, head_dim))
+        return DDT_ERR_INVALID_ARG;
+    if (batch == 0 || total_q == 0 || max_q_len == 0) return DDT_OK;
+    unsigned int *err = ddt::device_error_word();
+    if (!err) return DDT_ERR_CUDA;
+
+    int requested = num_splits;
+    if (requested == 0) {
+        int cap = 1;
+        if (workspace)
+            for (cap = DDT_MAX_SPLITS; cap > 1; --cap)
+                if (ddt_gqa_verify_attn_workspace_size(total_q, num_heads, head_dim, cap) <= workspace_bytes) break;
+        requested = ddt::gqa_choose_splits(batch, num_heads, num_kv_heads, max_q_len, max_kv_len,
+                                           ddt::device_sm_count(), cap);
+    }
+    ddt::GqaArgs a;
+    memset(&a, 0, sizeof a);
+    ddt::gqa_split_layout(max_kv_len, requested, &a.split_cols, &a.num_splits);
+    a.q = q;
+    a.k_pool = k_pool;
+    a.v_pool = v_pool;
+    a.pool_stride = pool_stride;
+    a.pool_rows = pool_rows;
+    a.kv_indices = kv_indices;
+    a.kv_indptr = kv_indptr;
+    a.qo_indptr = qo_indptr;
+    a.mask = mask;
+    a.mask_indptr = mask_indptr;
+    a.batch = batch;
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.total_q = total_q;
+    a.total_kv = total_kv;
+    a.total_mask_words = total_mask_words;
+    a.max_q_len = max_q_len;
+    a.max_kv_len = max_kv_len;
+    a.scale = scale;
+    a.out = out;
+    a.lse = lse;
+    a.err = err;
+    if (a.num_splits > 1) {
+        if (!workspace ||
+            workspace_bytes < ddt_gqa_verify_attn_workspace_size(total_q, num_heads, head_dim, a.num_splits))
+            return DDT_ERR_WORKSPACE;
+        const size_t rows = (size_t)total_q * num_heads;
+        a.o_part = static_cast<float *>(workspace);
+        a.lse_part = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                               align256(rows * a.num_splits * head_dim * sizeof(float)));
+    }
+    return launched(ddt::launch_gqa_attn(a, as_stream(stream)));
+}
+
+ddt_status ddt_cache_copy(const void *src_slab, int64_t src_pool_bytes, int64_t src_pool_rows,
+                          void *dst_slab, int64_t dst_pool_bytes, int64_t dst_pool_rows,
+                          int32_t num_pools, int64_t row_bytes, const int32_t *src,
+                          const int32_t *dst, int32_t n, void *stream) {
+    if (bad_slab(src_slab, src_pool_bytes, src_pool_rows, num_pools, row_bytes) ||
+        bad_slab(dst_slab, dst_pool_bytes, dst_pool_rows, num_pools, row_bytes) || n < 0 || (n > 0 && (!src || !dst)))
+        return DDT_ERR_INVALID_ARG;
+    if (n == 0) return DDT_OK;
+    unsigned int *err = ddt::device_error_word();
+    if (!err) return DDT_ERR_CUDA;
+    return launched(ddt::launch_cache_copy(src_slab, src_pool_bytes, src_pool_rows, dst_slab, dst_pool_bytes,
+                                           dst_pool_rows, num_pools, row_bytes, src, dst, n, err, as_stream(stream)));
+}
+
+ddt_status ddt_cache_commit(void *slab, int64_t pool_bytes, int64_t pool_rows, int32_t num_pools,
+                            int64_t row_bytes, const int32_t *kv_indices, const int32_t *kv_indptr,
+                            const int32_t *qo_indptr, const int32_t *accept_len,
+                            const int32_t *accepted_nodes, int32_t batch, int32_t total_kv,
+                            int32_t max_depth, int32_t *new_len, void *stream) {
+    if (bad_slab(slab, pool_bytes, pool_rows, num_pools, row_bytes) || !kv_indices || !kv_indptr || !qo_indptr ||
+        !accept_len || !accepted_nodes || batch < 0 || total_kv < 0)
+        return DDT_ERR_INVALID_ARG;
+    if (max_depth < 1 || max_depth > DDT_MAX_DEPTH) return DDT_ERR_UNSUPPORTED;
+    if (batch == 0) return DDT_OK;
+    unsigned int *err = ddt::device_error_word();
+    if (!err) return DDT_ERR_CUDA;
+    return launched(ddt::launch_cache_commit(slab, pool_bytes, pool_rows, num_pools, row_bytes, kv_indices, kv_indptr,
+                                             qo_indptr, accept_len, accepted_nodes, batch, total_kv, max_depth, new_len,
+                                             ddt::device_sm_count(), err, as_stream(stream)));
+}
+
+size_t ddt_cache_compact_workspace_size(int64_t pool_rows) {
+    if (pool_rows < 1 || pool_rows > DDT_CACHE_MAX_ROWS) return 0;
+    return ddt::cache_compact_workspace(pool_rows);
+}
+
+ddt_status ddt_cache_compact(void *slab, int64_t pool_bytes, int64_t pool_rows, int32_t num_pools,
+                             int64_t row_bytes, const int32_t *kv_indices, int32_t total,
+                             int32_t *new_indices, int32_t *live, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+    if (bad_slab(slab, pool_bytes, pool_rows, num_pools, row_bytes) || total < 0 ||
+        (total > 0 && (!kv_indices || !new_indices)) || !live)
+        return DDT_ERR_INVALID_ARG;
+    if (pool_rows > DDT_CACHE_MAX_ROWS) return DDT_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < ddt::cache_compact_workspace(pool_rows) || misaligned(workspace, 256))
+        return DDT_ERR_WORKSPACE;
+    unsigned int *err = ddt::device_error_word();
+    if (!err) return DDT_ERR_CUDA;
+    return launched(ddt::launch_cache_compact(slab, pool_bytes, pool_rows, num_pools, row_bytes, kv_indices, total,
+                                              new_indices, live, workspace, ddt::device_sm_count(), err,
+                                              as_stream(stream)));
+}
+
+}  // extern "C"

@@ -134,6 +134,83 @@ cudaError_t tree_prepare_device();
 cudaError_t commit_prepare_device();
 cudaError_t sample_prepare_device();
 
+// Arguments of one norm + rotation + append call as seen by the kernel.
+struct AppendArgs {
+    const uint16_t *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements per token
+    const uint16_t *q_weight, *k_weight;   // or null
+    float eps;
+    const float *cos_sin;  // [max_pos][rope_dim]: cosines, then sines
+    int64_t max_pos;
+    int rope_dim;
+    int interleaved;
+    const int32_t *depth;  // or null: the token's index in its request
+    const int32_t *qo_indptr;
+    const int32_t *kv_indices;
+    const int32_t *kv_indptr;
+    int batch;
+    int total_q;
+    int total_kv;
+    int num_heads;
+    int num_kv_heads;
+    int head_dim;
+    uint16_t *q_out;
+    uint16_t *k_pool, *v_pool;
+    int64_t pool_stride;  // elements per row
+    int64_t pool_rows;
+    unsigned int *err;
+};
+cudaError_t launch_norm_rope_append(const AppendArgs &a, int num_sms, cudaStream_t s);
+
+// Arguments of one grouped-query attention call as seen by the kernels.
+struct GqaArgs {
+    const uint16_t *q;
+    const uint16_t *k_pool, *v_pool;
+    int64_t pool_stride;  // elements per row
+    int64_t pool_rows;
+    const int32_t *kv_indices;
+    const int32_t *kv_indptr;
+    const int32_t *qo_indptr;
+    const uint32_t *mask;
+    const int32_t *mask_indptr;
+    int batch;
+    int num_heads;
+    int num_kv_heads;
+    int head_dim;
+    int total_q;
+    int total_kv;
+    int total_mask_words;
+    int max_q_len;
+    int max_kv_len;
+    float scale;
+    int num_splits;
+    int split_cols;   // kv columns per split (a multiple of the kv block)
+    uint16_t *out;    // [total_q, H, D] bf16
+    float *lse;       // [total_q, H] or null
+    float *o_part;    // [splits, total_q*H, D] when num_splits > 1
+    float *lse_part;  // [splits, total_q*H]
+    unsigned int *err;
+};
+cudaError_t launch_gqa_attn(const GqaArgs &a, cudaStream_t s);
+// the split count for these bounds, at most max_splits (>= 1)
+int gqa_choose_splits(int batch, int num_heads, int num_kv_heads, int max_q_len, int max_kv_len, int num_sms,
+                      int max_splits);
+// kv columns per split of a requested count (>= 1), in whole kv blocks, and the
+// splits that then cover max_kv_len
+void gqa_split_layout(int max_kv_len, int requested, int *split_cols, int *splits);
+
+cudaError_t launch_cache_copy(const void *src_slab, int64_t src_pool_bytes, int64_t src_rows, void *dst_slab,
+                              int64_t dst_pool_bytes, int64_t dst_rows, int num_pools, int64_t row_bytes,
+                              const int32_t *src, const int32_t *dst, int n, unsigned int *err, cudaStream_t s);
+cudaError_t launch_cache_commit(void *slab, int64_t pool_bytes, int64_t pool_rows, int num_pools, int64_t row_bytes,
+                                const int32_t *kv_indices, const int32_t *kv_indptr, const int32_t *qo_indptr,
+                                const int32_t *accept_len, const int32_t *accepted_nodes, int batch, int total_kv,
+                                int max_depth, int32_t *new_len, int num_sms, unsigned int *err, cudaStream_t s);
+size_t cache_compact_workspace(int64_t pool_rows);
+cudaError_t launch_cache_compact(void *slab, int64_t pool_bytes, int64_t pool_rows, int num_pools, int64_t row_bytes,
+                                 const int32_t *kv_indices, int total, int32_t *new_indices, int32_t *live,
+                                 void *workspace, int num_sms, unsigned int *err, cudaStream_t s);
+
 // A kernel whose bounded mbarrier wait can never succeed: it latches
 // DDT_DEVERR_TIMEOUT and exits (the failure path, exercised without a fault).
 cudaError_t launch_wait_timeout_selftest(uint32_t poll_limit, unsigned int *err, cudaStream_t s);

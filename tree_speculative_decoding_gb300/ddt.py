@@ -55,6 +55,16 @@ def _load():
         "ddt_tree_links": ([P, P, i32, P, P, P, P], i32),
         "ddt_accept_sampled": ([P, P, P, P, P, i32, P, P, P, P, i32, i32, i32, P, P, P, P, P],
                                i32),
+        "ddt_gqa_norm_rope_append": ([P, i64, P, i64, P, i64, P, P, f32, P, i64, i32, i32, P, P, P, P,
+                                      i32, i32, i32, i32, i32, i32, P, P, P, i64, i64, P], i32),
+        "ddt_gqa_verify_attn_num_splits": ([i32, i32, i32, i32, i32, i32], i32),
+        "ddt_gqa_verify_attn_workspace_size": ([i32, i32, i32, i32], sz),
+        "ddt_gqa_verify_attn": ([P, P, P, i64, i64, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32,
+                                 i32, i32, f32, i32, P, P, P, sz, P], i32),
+        "ddt_cache_copy": ([P, i64, i64, P, i64, i64, i32, i64, P, P, i32, P], i32),
+        "ddt_cache_commit": ([P, i64, i64, i32, i64, P, P, P, P, P, i32, i32, i32, P, P], i32),
+        "ddt_cache_compact_workspace_size": ([i64], sz),
+        "ddt_cache_compact": ([P, i64, i64, i32, i64, P, i32, P, P, P, sz, P], i32),
         "ddt_get_error": ([P, P], i32),
         "ddt_selftest_wait_timeout": ([ctypes.c_uint32, P], i32),
         "ddt_verify_step": ([P, P], i32),
@@ -403,6 +413,231 @@ def ddt_accept_sampled(node_token, first_child, next_sibling, qo_indptr, target_
         target_logits.shape[1], _p(temperature), _p(top_k), _p(top_p), _p(coins), coins.shape[1], B,
         int(max_depth), _p(accept_len), _p(accepted_nodes), _p(commit_tokens), _p(bonus),
         _stream(stream)))
+
+
+# ---------------------------------------------------------------- grouped-query layers, cache rows
+def _on_device(first, name):
+    """The CUDA device a call runs on: its first tensor's, which has to be the current one."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {dev}, which is not the current device")
+    return dev
+
+
+def _like(t, dtype, dev, name):
+    if t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {dev}")
+    return t.data_ptr()
+
+
+def _mask_ptr(mask, dev):
+    if mask.dtype not in (torch.int32, torch.uint32) or mask.device != dev or not mask.is_contiguous():
+        raise ValueError(f"mask must be a contiguous 32-bit tensor on {dev}")
+    return mask.data_ptr()
+
+
+def _heads(t, dev, name, heads=None):
+    """Pointer, row stride, rows, heads and head_dim of a [rows, heads, head_dim] bf16 tensor
+    whose rows are contiguous (the rows themselves may be apart)."""
+    if t.dtype != torch.bfloat16 or t.device != dev or t.dim() != 3:
+        raise ValueError(f"{name} must be a [rows, heads, head_dim] bfloat16 tensor on {dev}")
+    n, h, d = t.shape
+    sn, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and h > 1):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    if heads is not None and (h, d) != heads:
+        raise ValueError(f"{name} must have {heads[0]} heads of {heads[1]} values")
+    return t.data_ptr(), (sn if n > 1 else h * d), n, h, d
+
+
+def _pools(k_pool, v_pool, dev):
+    kp, stride, rows, G, D = _heads(k_pool, dev, "k_pool")
+    vp, vstride, vrows, _, _ = _heads(v_pool, dev, "v_pool", (G, D))
+    if vrows != rows or vstride != stride:
+        raise ValueError("k_pool and v_pool must have the same rows at the same stride")
+    return kp, vp, stride, rows, G, D
+
+
+def _raw_stream(stream, dev):
+    return (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+
+
+def ddt_gqa_norm_rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, depth, qo_indptr, kv_indices,
+                             kv_indptr, q_out, k_pool, v_pool, interleaved=False, stream=None):
+    """Norm, rotation and cache append of a grouped-query layer in one pass.
+
+    q [total_q, H, D], k and v [total_q, G, D] bf16 (rows contiguous; slices of one projection
+    will do); q_weight / k_weight bf16 [D] or None (no norm); cos_sin float32 [max_pos, rope_dim]
+    (cosines, then sines) or None (no rotation); depth int32 [total_q] or None (a chain);
+    q_out [total_q, H, D] contiguous, may be q; k_pool, v_pool [pool_rows, G, D]."""
+    dev = _on_device(q, "q")
+    qp, qs, total_q, H, D = _heads(q, dev, "q")
+    kp, ks, nk, G, _ = _heads(k, dev, "k")
+    vp, vs, nv, _, _ = _heads(v, dev, "v", (G, D))
+    kpp, vpp, stride, rows, Gp, Dp = _pools(k_pool, v_pool, dev)
+    if nk != total_q or nv != total_q or k.shape[2] != D or (Gp, Dp) != (G, D):
+        raise ValueError("q, k, v and the pools must agree in tokens, K/V heads and head_dim")
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    for n, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and w.numel() != D:
+            raise ValueError(f"{n} must hold head_dim values")
+    max_pos, rope_dim = 0, 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [max_pos, rope_dim]")
+        max_pos, rope_dim = cos_sin.shape
+    B = qo_indptr.numel() - 1
+    if kv_indptr.numel() != B + 1:
+        raise ValueError("qo_indptr and kv_indptr must both hold batch + 1 entries")
+    if depth is not None and depth.numel() < total_q:
+        raise ValueError("depth must hold an entry per token")
+    if total_q == 0 or B == 0:
+        return
+    i32, bf16 = torch.int32, torch.bfloat16
+    _check("ddt_gqa_norm_rope_append", lib.ddt_gqa_norm_rope_append(
+        qp, qs, kp, ks, vp, vs,
+        None if q_weight is None else _like(q_weight, bf16, dev, "q_weight"),
+        None if k_weight is None else _like(k_weight, bf16, dev, "k_weight"), eps,
+        None if cos_sin is None else _like(cos_sin, torch.float32, dev, "cos_sin"), max_pos, rope_dim,
+        int(bool(interleaved)), None if depth is None else _like(depth, i32, dev, "depth"),
+        _like(qo_indptr, i32, dev, "qo_indptr"), _like(kv_indices, i32, dev, "kv_indices"),
+        _like(kv_indptr, i32, dev, "kv_indptr"), B, total_q, kv_indices.numel(), H, G, D,
+        _like(q_out, bf16, dev, "q_out"), kpp, vpp, stride, rows, _raw_stream(stream, dev)))
+
+
+def ddt_gqa_verify_attn_num_splits(batch, num_heads, num_kv_heads, max_q_len, max_kv_len, num_sms=0):
+    return lib.ddt_gqa_verify_attn_num_splits(batch, num_heads, num_kv_heads, max_q_len, max_kv_len, num_sms)
+
+
+def ddt_gqa_verify_attn_workspace_size(total_q, num_heads, head_dim, num_splits):
+    return lib.ddt_gqa_verify_attn_workspace_size(total_q, num_heads, head_dim, num_splits)
+
+
+def ddt_gqa_verify_attn(q, k_pool, v_pool, kv_indices, kv_indptr, qo_indptr, mask, mask_indptr, scale,
+                        out, lse=None, max_q_len=None, max_kv_len=None, num_splits=0, workspace=None,
+                        stream=None):
+    """Tree-verify attention over grouped-query rows.  q, out: [total_q, H, D] bf16; k_pool, v_pool:
+    [pool_rows, G, D] bf16 (rows may be apart: slices of one [pool_rows, 2, G, D] pool will do);
+    lse: float32 [total_q, H] or None.
+
+    max_q_len / max_kv_len are host-side bounds; when omitted they are read from the indptrs (a
+    device->host copy).  With num_splits = 0 the split count is chosen among those that fit
+    `workspace`; without one, the chosen count's workspace is allocated here."""
+    dev = _on_device(q, "q")
+    qp, qs, total_q, H, D = _heads(q, dev, "q")
+    kp, vp, stride, rows, G, Dp = _pools(k_pool, v_pool, dev)
+    if Dp != D:
+        raise ValueError("q and the pools must have the same head_dim")
+    if qs != H * D:
+        raise ValueError("q must be contiguous")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is not None and lse.shape != q.shape[:2]:
+        raise ValueError("lse must be [total_q, H]")
+    B = qo_indptr.numel() - 1
+    if kv_indptr.numel() != B + 1 or mask_indptr.numel() != B + 1:
+        raise ValueError("qo_indptr, kv_indptr and mask_indptr must all hold batch + 1 entries")
+    if total_q == 0 or B == 0:
+        return
+    if max_q_len is None or max_kv_len is None:
+        max_q_len = int((qo_indptr[1:] - qo_indptr[:-1]).max())
+        max_kv_len = int((kv_indptr[1:] - kv_indptr[:-1]).max())
+    if workspace is None:
+        splits = num_splits or lib.ddt_gqa_verify_attn_num_splits(B, H, G, max_q_len, max_kv_len, 0)
+        nbytes = lib.ddt_gqa_verify_attn_workspace_size(total_q, H, D, splits)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        num_splits = splits
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(),
+                                                        workspace.numel() * workspace.element_size())
+    i32, bf16 = torch.int32, torch.bfloat16
+    _check("ddt_gqa_verify_attn", lib.ddt_gqa_verify_attn(
+        qp, kp, vp, stride, rows, _like(kv_indices, i32, dev, "kv_indices"),
+        _like(kv_indptr, i32, dev, "kv_indptr"), _like(qo_indptr, i32, dev, "qo_indptr"),
+        _mask_ptr(mask, dev), _like(mask_indptr, i32, dev, "mask_indptr"), B, H, G, D, total_q,
+        kv_indices.numel(), mask.numel(), max_q_len, max_kv_len, scale, num_splits,
+        _like(out, bf16, dev, "out"), None if lse is None else _like(lse, torch.float32, dev, "lse"),
+        ws, ws_bytes, _raw_stream(stream, dev)))
+
+
+def _slab(t, dev, name):
+    """Pointer, bytes between pools, rows, pools and row bytes of a [pools, rows, ...] tensor whose
+    pools are contiguous (the pools themselves may be apart)."""
+    if t.dim() < 3 or t.device != dev:
+        raise ValueError(f"{name} must be a [pools, rows, ...] tensor on {dev}")
+    if t.shape[0] == 0 or t.shape[1] == 0 or not t[0].is_contiguous():
+        raise ValueError(f"{name}: every pool must be contiguous and hold a row")
+    es = t.element_size()
+    row = t[0, 0].numel() * es
+    gap = t.stride(0) * es if t.shape[0] > 1 else t.shape[1] * row
+    return t.data_ptr(), gap, t.shape[1], t.shape[0], row
+
+
+def ddt_cache_copy(src_pool, dst_pool, src, dst, stream=None):
+    """Row dst[i] of every dst pool <- row src[i] of the same src pool.  src_pool, dst_pool:
+    [pools, rows, ...] (one pool per layer, or one for K and one for V per layer; may be the same
+    tensor); src, dst: int32 [n]."""
+    dev = _on_device(src_pool, "src_pool")
+    sp, sgap, srows, pools, row = _slab(src_pool, dev, "src_pool")
+    dp, dgap, drows, dpools, drow = _slab(dst_pool, dev, "dst_pool")
+    if dpools != pools or drow != row or src_pool.dtype != dst_pool.dtype:
+        raise ValueError("src_pool and dst_pool must agree in pools, row and type")
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst must have the same length")
+    if src.numel() == 0:
+        return
+    _check("ddt_cache_copy", lib.ddt_cache_copy(
+        sp, sgap, srows, dp, dgap, drows, pools, row, _like(src, torch.int32, dev, "src"),
+        _like(dst, torch.int32, dev, "dst"), src.numel(), _raw_stream(stream, dev)))
+
+
+def ddt_cache_commit(pool, kv_indices, kv_indptr, qo_indptr, accept_len, accepted_nodes, max_depth,
+                     new_len=None, stream=None):
+    """KV commit in every pool of a [pools, rows, ...] tensor: each request's accepted rows gathered
+    into positions P .. P + accept_len - 1 of its sequence, in place."""
+    dev = _on_device(pool, "pool")
+    pp, gap, rows, pools, row = _slab(pool, dev, "pool")
+    B = qo_indptr.numel() - 1
+    if kv_indptr.numel() != B + 1 or accept_len.numel() != B or accepted_nodes.numel() != B * (max_depth + 1):
+        raise ValueError("kv_indptr, accept_len and accepted_nodes must match the batch and max_depth")
+    if new_len is not None and new_len.numel() != B:
+        raise ValueError("new_len must hold one value per request")
+    if B == 0:
+        return
+    i32 = torch.int32
+    _check("ddt_cache_commit", lib.ddt_cache_commit(
+        pp, gap, rows, pools, row, _like(kv_indices, i32, dev, "kv_indices"),
+        _like(kv_indptr, i32, dev, "kv_indptr"), _like(qo_indptr, i32, dev, "qo_indptr"),
+        _like(accept_len, i32, dev, "accept_len"), _like(accepted_nodes, i32, dev, "accepted_nodes"),
+        B, kv_indices.numel(), max_depth, None if new_len is None else _like(new_len, i32, dev, "new_len"),
+        _raw_stream(stream, dev)))
+
+
+def ddt_cache_compact_workspace_size(pool_rows):
+    return lib.ddt_cache_compact_workspace_size(pool_rows)
+
+
+def ddt_cache_compact(pool, kv_indices, new_indices, live, workspace=None, stream=None):
+    """The rows named by kv_indices moved to the front of every pool of a [pools, rows, ...] tensor;
+    new_indices (may be kv_indices) receives their numbers, live (int32 [1]) how many they are."""
+    dev = _on_device(pool, "pool")
+    pp, gap, rows, pools, row = _slab(pool, dev, "pool")
+    if new_indices.numel() != kv_indices.numel() or live.numel() != 1:
+        raise ValueError("new_indices must have kv_indices' length, live one entry")
+    if workspace is None:
+        workspace = torch.empty(max(1, lib.ddt_cache_compact_workspace_size(rows)), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    i32 = torch.int32
+    _check("ddt_cache_compact", lib.ddt_cache_compact(
+        pp, gap, rows, pools, row, _like(kv_indices, i32, dev, "kv_indices"), kv_indices.numel(),
+        _like(new_indices, i32, dev, "new_indices"), _like(live, i32, dev, "live"), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)))
 
 
 def ddt_get_error(stream=None):
