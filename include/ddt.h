@@ -682,8 +682,8 @@ ddt_status ddt_gqa_norm_rope_append(
  *               (total_q, num_heads, head_dim, splits) bytes for an explicit
  *               num_splits; may be NULL for one split.  Calls that may overlap
  *               on the GPU need a workspace each.
- * Supported: head_dim 64 or 128, num_heads a multiple of num_kv_heads and at
- * most DDT_GQA_MAX_HEADS, max_q_len <= 128, pool_rows <= 2^31 - 1.
+ * Supported: scale > 0, head_dim 64 or 128, num_heads a multiple of
+ * num_kv_heads and at most DDT_GQA_MAX_HEADS, max_q_len <= 128, pool_rows <= 2^31 - 1.
  * Device checks (latched, the request's rows left unwritten): q_len outside
  * [0, max_q_len] or offsets outside [0, total_q] (DDT_DEVERR_QO_INDPTR),
  * kv_len outside [q_len, max_kv_len] or offsets outside [0, total_kv]

@@ -40,7 +40,7 @@ def test_attention_host_checks(lib):
         assert f(**{name: ctypes.c_void_p(264)}) == INVALID, name    # not 16-byte aligned
     assert f(ws=ctypes.c_void_p(128)) == INVALID                     # not 256-byte aligned
     for bad in (dict(batch=-1), dict(total_q=-1), dict(total_kv=-1), dict(words=-1), dict(rows=0), dict(max_kv=8),
-                dict(scale=float("nan")), dict(scale=float("inf")), dict(splits=-1), dict(H=63), dict(G=0), dict(H=0),
+                dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=0.0), dict(scale=-0.1), dict(splits=-1), dict(H=63), dict(G=0), dict(H=0),
                 dict(G=128), dict(stride=1016), dict(stride=1028), dict(max_q=-1)):
         assert f(**bad) == INVALID, bad
     for bad in (dict(D=96), dict(D=256, stride=2048), dict(H=136), dict(max_q=129, max_kv=129), dict(splits=129),

@@ -123,7 +123,7 @@ ddt_status ddt_gqa_verify_attn(
     void *stream) {
     if (!q || !k_pool || !v_pool || !kv_indices || !kv_indptr || !qo_indptr || !mask || !mask_indptr || !out ||
         batch < 0 || total_q < 0 || total_kv < 0 || total_mask_words < 0 || pool_rows < 1 || max_q_len < 0 ||
-        max_kv_len < max_q_len || !isfinite(scale) || num_splits < 0)
+        max_kv_len < max_q_len || !isfinite(scale) || !(scale > 0.f) || num_splits < 0)
         return DDT_ERR_INVALID_ARG;
     const ddt_status heads = check_heads(num_heads, num_kv_heads, head_dim);
     if (heads != DDT_OK) return heads;

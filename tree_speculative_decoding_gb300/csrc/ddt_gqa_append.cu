@@ -19,6 +19,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "ddt_gqa.cuh"
 #include "ddt_internal.cuh"
 
 namespace ddt {
@@ -26,22 +27,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBatchRows = 4;  // head rows in flight per group
-
-// The last request b in [0, batch] with qo_indptr[b] <= t, by a 32-way search
-// of the whole warp (two rounds of loads up to 1024 requests).  b == batch:
-// the token is behind the last request.
-__device__ __forceinline__ int find_request(const int32_t *qo_indptr, int batch, int t, int lane) {
-    int64_t lo = 0, hi = batch;
-    while (hi > lo) {
-        const int64_t step = (hi - lo + 31) >> 5;
-        const int64_t probe = lo + (lane + 1) * step;
-        const bool below = probe <= hi && qo_indptr[probe] <= t;
-        const int64_t c = __popc(__ballot_sync(0xffffffffu, below));
-        lo += c * step;
-        if (lo + step - 1 < hi) hi = lo + step - 1;
-    }
-    return (int)lo;
-}
 
 __device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};

@@ -191,6 +191,8 @@ struct GqaArgs {
     float *lse_part;  // [splits, total_q*H]
     unsigned int *err;
 };
+// kernel attributes, once per device (see attn_prepare_device)
+cudaError_t gqa_prepare_device();
 cudaError_t launch_gqa_attn(const GqaArgs &a, cudaStream_t s);
 // the split count for these bounds, at most max_splits (>= 1)
 int gqa_choose_splits(int batch, int num_heads, int num_kv_heads, int max_q_len, int max_kv_len, int num_sms,
