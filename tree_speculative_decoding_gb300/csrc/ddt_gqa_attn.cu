@@ -39,7 +39,6 @@
 // for its own copies and MMAs and leaves.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -64,7 +63,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct GqaParams {
-    CUtensorMap k_map, v_map;  // [pool_rows][kv_heads * D] bf16, boxes of one row x 64 columns
     GqaArgs a;
     int group;     // query heads per K/V head
 };
@@ -79,7 +77,8 @@ struct Cfg {
     static constexpr int kQBytes = kBoxes * kQBoxBytes;  // one tile of q
     static constexpr int kKStages = D == 128 ? (kTiles == 2 ? 3 : 2) : 4;
     static constexpr int kVStages = D == 128 ? 2 : 4;
-    static constexpr int kThreads = 128 * kTiles + 64;
+    static constexpr int kLoadWarps = 2 * kTiles;        // for K, and as many for V: 32 rows of a block each
+    static constexpr int kThreads = 32 * (4 * kTiles + 2 * kLoadWarps + 1);
     static constexpr uint32_t kTmemCols = kTiles == 2 ? 512 : 256;
     static constexpr uint32_t kColS = 0, kColO = 2 * NB;
     static constexpr int kOffQ = 0;
@@ -141,7 +140,7 @@ __device__ __noinline__ void row_again(const GqaArgs &a, const uint16_t *q, cons
 }
 
 template <int D, int kTiles>
-__global__ void __launch_bounds__(128 * kTiles + 64, kTiles == 2 ? 1 : 2)
+__global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, kTiles == 2 ? 1 : 2)
 gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
     using C = Cfg<D, kTiles>;
     constexpr int NB = C::NB;
@@ -154,11 +153,7 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffHolder + 4);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kMmaWarp = 4 * kTiles, kLoadWarp = kMmaWarp + 1;
-    if (warp == kLoadWarp && lane == 0) {
-        tma_prefetch_map(&prm.k_map);
-        tma_prefetch_map(&prm.v_map);
-    }
+    constexpr int kMmaWarp = 4 * kTiles, kFirstLoad = kMmaWarp + 1;
     // everything read below may be the previous kernel's output (q, the appended rows, the mask)
     pdl_wait();
 
@@ -192,12 +187,13 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
         // P of a slot: one arrival per softmax warp that has rows in the slot's tile
         const int w0 = (min(rows, kRows) + 31) >> 5, w1 = tiles == 2 ? (rows - kRows + 31) >> 5 : w0;
         for (int i = 0; i < C::bCount; ++i)
-            mbar_init(bar(i), i == C::bPFull ? w0 : i == C::bPFull + 1 ? w1 : i == C::bQFull ? (tiles == 2 ? w0 + w1 : w0) : 1);
+            mbar_init(bar(i), i < C::bKFull + C::kKStages || (i >= C::bVFull && i < C::bVFull + C::kVStages) ? 32 * C::kLoadWarps
+                      : i == C::bPFull ? w0 : i == C::bPFull + 1 ? w1 : i == C::bQFull ? (tiles == 2 ? w0 + w1 : w0) : 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
     __syncwarp();
-    if (warp == kLoadWarp) tmem_alloc(smem_u32(holder), C::kTmemCols);
+    if (warp == kMmaWarp) tmem_alloc(smem_u32(holder), C::kTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -207,73 +203,55 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
     // memory that this one still needs while it waits for this one's end.
     pdl_trigger();
 
-    if (warp == kLoadWarp) {
-        // ================= gather: K(0) K(1) V(0) K(2) V(1) ... =================
-        // lane l moves rows [4 l, 4 l + 4) of a block
-        const bool mine = lane < NB / 4;
-        auto fetch = [&](int j, int (&s)[4]) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c = min(c_begin + j * NB + 4 * lane + e, c_end - 1);  // past the end: a valid row again
-                s[e] = mine ? a.kv_indices[kv0 + c] : 0;
-            }
+    if (warp >= kFirstLoad) {
+        // ================= gather: kLoadWarps warps for K, kLoadWarps for V =================
+        // A warp moves 32 rows of every block, 16 bytes a lane: an instruction
+        // covers 512 / (2 D) rows.  The slots of the next block are loaded while
+        // this one's rows are copied.
+        const int lw = warp - kFirstLoad;
+        const bool is_v = lw >= C::kLoadWarps;
+        const int first = 32 * (is_v ? lw - C::kLoadWarps : lw);  // its rows: [first, first + 32) of a block
+        const int stages = is_v ? C::kVStages : C::kKStages;
+        const int full = is_v ? C::bVFull : C::bKFull, empty = is_v ? C::bVEmpty : C::bKEmpty;
+        constexpr int kChunks = D / 8, kPer = 32 / kChunks;  // 16-byte pieces of a row; rows an instruction
+        const int c = lane % kChunks, sub = lane / kChunks;
+        const char *pool = reinterpret_cast<const char *>(is_v ? a.v_pool : a.k_pool) + ((int64_t)g * D + c * 8) * 2;
+        const int64_t pitch = a.pool_stride * 2;
+        const uint32_t base = sbase + (is_v ? C::kOffV : C::kOffK) + (c >> 3) * C::kBoxBytes + first * 128;
+        auto fetch = [&](int j) {  // past the end: a valid row again
+            return a.kv_indices[kv0 + min(c_begin + j * NB + first + lane, c_end - 1)];
         };
-        auto load = [&](uint32_t dst, const CUtensorMap *map, const int (&s)[4], uint32_t full) {
-            if (lane == 0) mbar_arrive_expect_tx(full, C::kBlockBytes);
-            __syncwarp();
-            if (mine) {
-#pragma unroll
-                for (int x = 0; x < C::kBoxes; ++x)
-                    tma_gather4(dst + x * C::kBoxBytes + lane * 512, map, g * D + 64 * x, s[0], s[1], s[2], s[3], full);
+        int ahead = fetch(0), s = 0;
+        uint32_t phase = 1;  // of the stage's "empty": the first round finds it free
+        for (int j = 0; j < nblk; ++j) {
+            int slot = ahead;
+            if (slot < 0 || slot >= a.pool_rows) {
+                latch(a.err, DDT_DEVERR_KV_INDEX);
+                slot = 0;
             }
-        };
-        // slots of blocks j - 1 (its V), j, and two ahead
-        int prev[4] = {0, 0, 0, 0}, cur[4], next[4], next2[4];
-        fetch(0, cur);
-        fetch(min(1, nblk - 1), next);
-        bool ok = true;
-        int nk = 0, nv = 0;  // blocks issued
-        for (int j = 0; j <= nblk && ok; ++j) {
-            if (j < nblk) {
-                fetch(min(j + 2, nblk - 1), next2);
+            if (j + 1 < nblk) ahead = fetch(j + 1);
+            if (!warp_wait(bar(empty + s), phase, abort_flag, a.err)) break;
+            const uint32_t stage = base + s * C::kBlockBytes;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (cur[e] < 0 || cur[e] >= a.pool_rows) {
-                        latch(a.err, DDT_DEVERR_KV_INDEX);
-                        cur[e] = 0;
-                    }
-                const int s = j % C::kKStages, u = j / C::kKStages;
-                if (u > 0) ok = warp_wait(bar(C::bKEmpty + s), (u - 1) & 1, abort_flag, a.err);
-                if (!ok) break;
-                load(sbase + C::kOffK + s * C::kBlockBytes, &prm.k_map, cur, bar(C::bKFull + s));
-                ++nk;
+            for (int i = 0; i < 32 / kPer; ++i) {
+                const int k = i * kPer + sub;  // first is a multiple of 8: the swizzle goes by k alone
+                cp_async_16(stage + k * 128 + (((c & 7) ^ (k & 7)) << 4),
+                            pool + __shfl_sync(0xffffffffu, slot, k) * pitch);
             }
-            if (j > 0) {
-                const int s = (j - 1) % C::kVStages, u = (j - 1) / C::kVStages;
-                if (u > 0) ok = warp_wait(bar(C::bVEmpty + s), (u - 1) & 1, abort_flag, a.err);
-                if (!ok) break;
-                load(sbase + C::kOffV + s * C::kBlockBytes, &prm.v_map, prev, bar(C::bVFull + s));
-                ++nv;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                prev[e] = cur[e];
-                cur[e] = next[e];
-                next[e] = next2[e];
+            cp_async_arrive(bar(full + s));
+            if (++s == stages) {
+                s = 0;
+                phase ^= 1;
             }
         }
-        if (*abort_flag) {  // nothing may land after the CTA has left
-            for (int j = max(0, nk - C::kKStages); j < nk; ++j)
-                mbar_wait(bar(C::bKFull + j % C::kKStages), (j / C::kKStages) & 1, kWaitLimit);
-            for (int j = max(0, nv - C::kVStages); j < nv; ++j)
-                mbar_wait(bar(C::bVFull + j % C::kVStages), (j / C::kVStages) & 1, kWaitLimit);
-        }
+        asm volatile("cp.async.wait_all;" ::: "memory");  // nothing may land after the CTA has left
     } else if (warp == kMmaWarp) {
         // ================= MMA =================
         if (lane == 0) {
             auto issue_s = [&](int w) -> bool {
                 const int j = w / tiles, t = w - j * tiles, s = j % C::kKStages;
                 if (!wait_or_abort(bar(C::bKFull + s), (j / C::kKStages) & 1, abort_flag, a.err)) return false;
+                fence_proxy_async_smem();  // written by cp.async, read by the tensor core
                 tc_fence_after();
                 const uint32_t qb = sbase + C::kOffQ + t * C::kQBytes, kb = sbase + C::kOffK + s * C::kBlockBytes;
                 const uint32_t d = tmem + C::kColS + NB * (w & 1);
@@ -289,6 +267,7 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                 const int j = w / tiles, t = w - j * tiles, s = j % C::kVStages;
                 if (!wait_or_abort(bar(C::bVFull + s), (j / C::kVStages) & 1, abort_flag, a.err)) return false;
                 if (!wait_or_abort(bar(C::bPFull + (w & 1)), (w >> 1) & 1, abort_flag, a.err)) return false;
+                fence_proxy_async_smem();
                 tc_fence_after();
                 const uint32_t vb = sbase + C::kOffV + s * C::kBlockBytes;
                 const uint32_t p = tmem + C::kColS + NB * (w & 1), d = tmem + C::kColO + D * t;
@@ -370,25 +349,30 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                 ok = warp_wait(bar(C::bSFull + slot), (w >> 1) & 1, abort_flag, a.err);
                 if (!ok) break;
                 tc_fence_after();
-                float sv[NB];
+                uint32_t all = mw[0];
 #pragma unroll
-                for (int k = 0; k < kW; ++k) {
+                for (int k = 1; k < kW; ++k) all &= mw[k];
+                // 32 scores of the row, unseen columns at -inf; read twice (maximum, then weights)
+                // so that a block's scores need not stay in registers
+                auto scores = [&](int k, float (&sv)[32]) {
                     uint32_t t32[32];
                     tmem_ld32(col + 32 * k, t32);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) sv[32 * k + e] = __uint_as_float(t32[e]);
+                    for (int e = 0; e < 32; ++e) sv[e] = __uint_as_float(t32[e]);
+                    if (all != 0xffffffffu) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) sv[e] = ((mw[k] >> e) & 1u) ? sv[e] : -INFINITY;
+                    }
+                };
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int k = 0; k < kW; ++k) {
+                    float sv[32];
+                    scores(k, sv);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) mx[(e >> 1) & 3] = fmaxf(mx[(e >> 1) & 3], fmaxf(sv[e], sv[e + 1]));
                 }
-                uint32_t all = mw[0];
-#pragma unroll
-                for (int k = 1; k < kW; ++k) all &= mw[k];
-                if (all != 0xffffffffu) {
-#pragma unroll
-                    for (int k = 0; k < NB; ++k) sv[k] = ((mw[k >> 5] >> (k & 31)) & 1u) ? sv[k] : -INFINITY;
-                }
-                float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
-#pragma unroll
-                for (int k = 4; k < NB; ++k) mx[k & 3] = fmaxf(mx[k & 3], sv[k]);
                 float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
                 float alpha = 1.0f;
                 if (mb > m_ref + kRescaleLog2) {  // also the first visible block (m_ref = -inf)
@@ -403,13 +387,18 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                 for (int h = 0; h < NB / 64; ++h) {
                     uint32_t pw[32];
 #pragma unroll
-                    for (int k = 0; k < 64; k += 2) {
-                        const float2 x = f2fma(make_float2(sv[64 * h + k], sv[64 * h + k + 1]), scv, nmv);
-                        const float p0 = ex2(x.x), p1 = ex2(x.y);
-                        acc = f2add(acc, make_float2(p0, p1));
-                        pw[k / 2] = pack_bf16(p0, p1);
+                    for (int k = 0; k < 2; ++k) {
+                        float sv[32];
+                        scores(2 * h + k, sv);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float2 x = f2fma(make_float2(sv[e], sv[e + 1]), scv, nmv);
+                            const float p0 = ex2(x.x), p1 = ex2(x.y);
+                            acc = f2add(acc, make_float2(p0, p1));
+                            pw[16 * k + e / 2] = pack_bf16(p0, p1);
+                        }
                     }
-                    tmem_st32(col + 32 * h, pw);
+                    tmem_st32(col + 32 * h, pw);  // over scores that have been read
                 }
                 l += acc.x + acc.y;
                 // The output so far shrinks before PV(w).  With two tiles S(w) was issued behind
@@ -505,7 +494,7 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
     // ---- teardown ----
     tc_fence_before();
     __syncthreads();
-    if (warp == kLoadWarp) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmemCols);
     }
@@ -586,31 +575,6 @@ __global__ void __launch_bounds__(32 * kCombineWarps) gqa_combine_kernel(const G
     if (a.lse && lane == 0) a.lse[row] = den == 0.f ? -INFINITY : m + log2f(den) * kLn2;
 }
 
-// cuTensorMapEncodeTiled from the driver, looked up once through the runtime
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }();
-    return fn;
-}
-
-bool encode_pool_map(CUtensorMap *map, const uint16_t *pool, const GqaArgs &a) {
-    const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    if (!enc) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)a.num_kv_heads * a.head_dim, (cuuint64_t)a.pool_rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)a.pool_stride * 2};
-    const cuuint32_t box[2] = {64, 1};
-    const cuuint32_t elem[2] = {1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(pool), dims, strides, box, elem,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 int tiles_per_cta(int max_q_len, int group) { return max_q_len * group > kRows ? 2 : 1; }
 
 template <int D, int kTiles>
@@ -666,7 +630,6 @@ cudaError_t launch_gqa_attn(const GqaArgs &a, cudaStream_t s) {
     GqaParams prm;
     prm.a = a;
     prm.group = a.num_heads / a.num_kv_heads;
-    if (!encode_pool_map(&prm.k_map, a.k_pool, a) || !encode_pool_map(&prm.v_map, a.v_pool, a)) return cudaErrorInvalidValue;
     const int tiles = tiles_per_cta(a.max_q_len, prm.group);
     cudaError_t e = a.head_dim == 128 ? (tiles == 2 ? launch_partial<128, 2>(prm, s) : launch_partial<128, 1>(prm, s))
                                       : (tiles == 2 ? launch_partial<64, 2>(prm, s) : launch_partial<64, 1>(prm, s));
