@@ -77,8 +77,9 @@ struct Cfg {
     static constexpr int kQBytes = kBoxes * kQBoxBytes;  // one tile of q
     static constexpr int kKStages = D == 128 ? (kTiles == 2 ? 3 : 2) : 4;
     static constexpr int kVStages = D == 128 ? 2 : 4;
-    static constexpr int kLoadWarps = 2 * kTiles;        // for K, and as many for V: 32 rows of a block each
-    static constexpr int kThreads = 32 * (4 * kTiles + 2 * kLoadWarps + 1);
+    static constexpr int kUnits = NB / 32;               // 32-row units of a block
+    static constexpr int kLoadWarps = 4 * kTiles - 1;    // with the MMA warp: whole warpgroups
+    static constexpr int kThreads = 256 * kTiles;
     static constexpr uint32_t kTmemCols = kTiles == 2 ? 512 : 256;
     static constexpr uint32_t kColS = 0, kColO = 2 * NB;
     static constexpr int kOffQ = 0;
@@ -113,7 +114,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 // warp: lane l keeps values [l D / 32, (l + 1) D / 32).  m is the row's running
 // maximum in log2 units.
 template <int D>
-__device__ __noinline__ void row_again(const GqaArgs &a, const uint16_t *q, const uint32_t *words, int kv0, int c_begin,
+__device__ __forceinline__ void row_again(const GqaArgs &a, const uint16_t *q, const uint32_t *words, int kv0, int c_begin,
                                        int c_end, int g, float m, float (&o)[D / 32]) {
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
@@ -187,7 +188,7 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
         // P of a slot: one arrival per softmax warp that has rows in the slot's tile
         const int w0 = (min(rows, kRows) + 31) >> 5, w1 = tiles == 2 ? (rows - kRows + 31) >> 5 : w0;
         for (int i = 0; i < C::bCount; ++i)
-            mbar_init(bar(i), i < C::bKFull + C::kKStages || (i >= C::bVFull && i < C::bVFull + C::kVStages) ? 32 * C::kLoadWarps
+            mbar_init(bar(i), i < C::bKFull + C::kKStages || (i >= C::bVFull && i < C::bVFull + C::kVStages) ? 32 * C::kUnits
                       : i == C::bPFull ? w0 : i == C::bPFull + 1 ? w1 : i == C::bQFull ? (tiles == 2 ? w0 + w1 : w0) : 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -202,94 +203,102 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
     // it.  After the allocation: a CTA that starts early cannot take the tensor
     // memory that this one still needs while it waits for this one's end.
     pdl_trigger();
-
-    if (warp >= kFirstLoad) {
-        // ================= gather: kLoadWarps warps for K, kLoadWarps for V =================
-        // A warp moves 32 rows of every block, 16 bytes a lane: an instruction
-        // covers 512 / (2 D) rows.  The slots of the next block are loaded while
-        // this one's rows are copied.
-        const int lw = warp - kFirstLoad;
-        const bool is_v = lw >= C::kLoadWarps;
-        const int first = 32 * (is_v ? lw - C::kLoadWarps : lw);  // its rows: [first, first + 32) of a block
-        const int stages = is_v ? C::kVStages : C::kKStages;
-        const int full = is_v ? C::bVFull : C::bKFull, empty = is_v ? C::bVEmpty : C::bKEmpty;
-        constexpr int kChunks = D / 8, kPer = 32 / kChunks;  // 16-byte pieces of a row; rows an instruction
-        const int c = lane % kChunks, sub = lane / kChunks;
-        const char *pool = reinterpret_cast<const char *>(is_v ? a.v_pool : a.k_pool) + ((int64_t)g * D + c * 8) * 2;
-        const int64_t pitch = a.pool_stride * 2;
-        const uint32_t base = sbase + (is_v ? C::kOffV : C::kOffK) + (c >> 3) * C::kBoxBytes + first * 128;
-        auto fetch = [&](int j) {  // past the end: a valid row again
-            return a.kv_indices[kv0 + min(c_begin + j * NB + first + lane, c_end - 1)];
-        };
-        int ahead = fetch(0), s = 0;
-        uint32_t phase = 1;  // of the stage's "empty": the first round finds it free
-        for (int j = 0; j < nblk; ++j) {
-            int slot = ahead;
-            if (slot < 0 || slot >= a.pool_rows) {
-                latch(a.err, DDT_DEVERR_KV_INDEX);
-                slot = 0;
-            }
-            if (j + 1 < nblk) ahead = fetch(j + 1);
-            if (!warp_wait(bar(empty + s), phase, abort_flag, a.err)) break;
-            const uint32_t stage = base + s * C::kBlockBytes;
-#pragma unroll
-            for (int i = 0; i < 32 / kPer; ++i) {
-                const int k = i * kPer + sub;  // first is a multiple of 8: the swizzle goes by k alone
-                cp_async_16(stage + k * 128 + (((c & 7) ^ (k & 7)) << 4),
-                            pool + __shfl_sync(0xffffffffu, slot, k) * pitch);
-            }
-            cp_async_arrive(bar(full + s));
-            if (++s == stages) {
-                s = 0;
-                phase ^= 1;
-            }
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");  // nothing may land after the CTA has left
-    } else if (warp == kMmaWarp) {
-        // ================= MMA =================
-        if (lane == 0) {
-            auto issue_s = [&](int w) -> bool {
-                const int j = w / tiles, t = w - j * tiles, s = j % C::kKStages;
-                if (!wait_or_abort(bar(C::bKFull + s), (j / C::kKStages) & 1, abort_flag, a.err)) return false;
-                fence_proxy_async_smem();  // written by cp.async, read by the tensor core
-                tc_fence_after();
-                const uint32_t qb = sbase + C::kOffQ + t * C::kQBytes, kb = sbase + C::kOffK + s * C::kBlockBytes;
-                const uint32_t d = tmem + C::kColS + NB * (w & 1);
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    mma_ss(d, smem_desc(qb + (ks >> 2) * C::kQBoxBytes + (ks & 3) * 32, 16, 1024),
-                           smem_desc(kb + (ks >> 2) * C::kBoxBytes + (ks & 3) * 32, 16, 1024), C::kIdescS, ks > 0);
-                mma_commit(bar(C::bSFull + (w & 1)));
-                if (t == tiles - 1) mma_commit(bar(C::bKEmpty + s));
-                return true;
+    // Registers of the two-tile kernel: 512 threads x 128 at launch = 256 x 184 (softmax: a block's
+    // scores of a row) + 256 x 72.
+    if (warp >= kMmaWarp) {
+        if constexpr (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");  // one instruction for the warpgroup
+        if (warp >= kFirstLoad) {
+            // ================= gather =================
+            // The warps take units of 32 rows in turn, in the order K(0) K(1) V(0)
+            // K(2) V(1) ... V(nblk - 1): a unit's fixed cost (its waits) and its copies
+            // overlap those of the other warps' units.  A copy instruction moves 512
+            // bytes; the next unit's slots are loaded while this one's rows are copied.
+            constexpr int kChunks = D / 8, kPer = 32 / kChunks;  // 16-byte pieces of a row; rows an instruction
+            const int c = lane % kChunks, sub = lane / kChunks;
+            const int64_t at = ((int64_t)g * D + c * 8) * 2, pitch = a.pool_stride * 2;
+            const char *kp = reinterpret_cast<const char *>(a.k_pool) + at, *vp = reinterpret_cast<const char *>(a.v_pool) + at;
+            const int last = 2 * nblk - 1, end = 2 * nblk * C::kUnits;
+            // block of the sequence's group q, and whether it is its V
+            auto block_of = [&](int q, bool &is_v) {
+                is_v = q == last || (q > 0 && !(q & 1));
+                return q == last ? nblk - 1 : is_v ? q / 2 - 1 : (q + 1) / 2;
             };
-            auto issue_pv = [&](int w) -> bool {
-                const int j = w / tiles, t = w - j * tiles, s = j % C::kVStages;
-                if (!wait_or_abort(bar(C::bVFull + s), (j / C::kVStages) & 1, abort_flag, a.err)) return false;
-                if (!wait_or_abort(bar(C::bPFull + (w & 1)), (w >> 1) & 1, abort_flag, a.err)) return false;
-                fence_proxy_async_smem();
-                tc_fence_after();
-                const uint32_t vb = sbase + C::kOffV + s * C::kBlockBytes;
-                const uint32_t p = tmem + C::kColS + NB * (w & 1), d = tmem + C::kColO + D * t;
-#pragma unroll
-                for (int ks = 0; ks < NB / 16; ++ks)
-                    mma_ts(d, p + 8 * ks, smem_desc(vb + ks * 2048, C::kBoxBytes, 1024), C::kIdescPV, j > 0 || ks > 0);
-                if (t == tiles - 1) mma_commit(bar(C::bVEmpty + s));
-                if (tiles == 1) mma_commit(bar(C::bODone));
-                return true;
+            auto fetch = [&](int n) {
+                bool is_v;
+                const int j = block_of(n / C::kUnits, is_v);
+                return a.kv_indices[kv0 + min(c_begin + j * NB + 32 * (n % C::kUnits) + lane, c_end - 1)];  // past the end: a valid row again
             };
-            bool ok = wait_or_abort(bar(C::bQFull), 0, abort_flag, a.err) && issue_s(0);
-            if (ok && items > 1) ok = issue_s(1);
-            for (int w = 0; w < items && ok; ++w) {
-                ok = issue_pv(w);
-                if (ok && w + 2 < items) ok = issue_s(w + 2);
+            int n = warp - kFirstLoad;
+            int ahead = n < end ? fetch(n) : 0;
+            for (; n < end; n += C::kLoadWarps) {
+                int slot = ahead;
+                if (slot < 0 || slot >= a.pool_rows) {
+                    latch(a.err, DDT_DEVERR_KV_INDEX);
+                    slot = 0;
+                }
+                if (n + C::kLoadWarps < end) ahead = fetch(n + C::kLoadWarps);
+                bool is_v;
+                const int j = block_of(n / C::kUnits, is_v);
+                const int s = is_v ? j % C::kVStages : j % C::kKStages, u = is_v ? j / C::kVStages : j / C::kKStages;
+                if (u > 0 && !warp_wait(bar((is_v ? C::bVEmpty : C::bKEmpty) + s), (u - 1) & 1, abort_flag, a.err)) break;
+                const uint32_t to = sbase + (is_v ? C::kOffV : C::kOffK) + s * C::kBlockBytes + (c >> 3) * C::kBoxBytes +
+                                    (n % C::kUnits) * 32 * 128;
+                const char *pool = is_v ? vp : kp;
+#pragma unroll
+                for (int i = 0; i < 32 / kPer; ++i) {
+                    const int k = i * kPer + sub;
+                    cp_async_16(to + k * 128 + (((c & 7) ^ (k & 7)) << 4), pool + __shfl_sync(0xffffffffu, slot, k) * pitch);
+                }
+                cp_async_arrive(bar((is_v ? C::bVFull : C::bKFull) + s));
             }
-            // completes when every MMA issued has: the epilogue (and, after a timeout, the exit) waits for it
-            mma_commit(bar(C::bOFin));
-            mbar_wait(bar(C::bOFin), 0, kWaitLimit);
+            asm volatile("cp.async.wait_all;" ::: "memory");  // nothing may land after the CTA has left
+        } else {
+            // ================= MMA =================
+            if (lane == 0) {
+                auto issue_s = [&](int w) -> bool {
+                    const int j = w / tiles, t = w - j * tiles, s = j % C::kKStages;
+                    if (!wait_or_abort(bar(C::bKFull + s), (j / C::kKStages) & 1, abort_flag, a.err)) return false;
+                    fence_proxy_async_smem();  // written by cp.async, read by the tensor core
+                    tc_fence_after();
+                    const uint32_t qb = sbase + C::kOffQ + t * C::kQBytes, kb = sbase + C::kOffK + s * C::kBlockBytes;
+                    const uint32_t d = tmem + C::kColS + NB * (w & 1);
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        mma_ss(d, smem_desc(qb + (ks >> 2) * C::kQBoxBytes + (ks & 3) * 32, 16, 1024),
+                               smem_desc(kb + (ks >> 2) * C::kBoxBytes + (ks & 3) * 32, 16, 1024), C::kIdescS, ks > 0);
+                    mma_commit(bar(C::bSFull + (w & 1)));
+                    if (t == tiles - 1) mma_commit(bar(C::bKEmpty + s));
+                    return true;
+                };
+                auto issue_pv = [&](int w) -> bool {
+                    const int j = w / tiles, t = w - j * tiles, s = j % C::kVStages;
+                    if (!wait_or_abort(bar(C::bVFull + s), (j / C::kVStages) & 1, abort_flag, a.err)) return false;
+                    if (!wait_or_abort(bar(C::bPFull + (w & 1)), (w >> 1) & 1, abort_flag, a.err)) return false;
+                    fence_proxy_async_smem();
+                    tc_fence_after();
+                    const uint32_t vb = sbase + C::kOffV + s * C::kBlockBytes;
+                    const uint32_t p = tmem + C::kColS + NB * (w & 1), d = tmem + C::kColO + D * t;
+#pragma unroll
+                    for (int ks = 0; ks < NB / 16; ++ks)
+                        mma_ts(d, p + 8 * ks, smem_desc(vb + ks * 2048, C::kBoxBytes, 1024), C::kIdescPV, j > 0 || ks > 0);
+                    if (t == tiles - 1) mma_commit(bar(C::bVEmpty + s));
+                    if (tiles == 1) mma_commit(bar(C::bODone));
+                    return true;
+                };
+                bool ok = wait_or_abort(bar(C::bQFull), 0, abort_flag, a.err) && issue_s(0);
+                if (ok && items > 1) ok = issue_s(1);
+                for (int w = 0; w < items && ok; ++w) {
+                    ok = issue_pv(w);
+                    if (ok && w + 2 < items) ok = issue_s(w + 2);
+                }
+                // completes when every MMA issued has: the epilogue (and, after a timeout, the exit) waits for it
+                mma_commit(bar(C::bOFin));
+                mbar_wait(bar(C::bOFin), 0, kWaitLimit);
+            }
+            __syncwarp();
         }
-        __syncwarp();
     } else {
+        if constexpr (kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         // ================= softmax (thread = row = TMEM lane of its tile) =================
         const int t = warp >> 2, wq = warp & 3;
         const int r = 32 * wq + lane;  // row within the tile
@@ -352,28 +361,27 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                 uint32_t all = mw[0];
 #pragma unroll
                 for (int k = 1; k < kW; ++k) all &= mw[k];
-                // 32 scores of the row, unseen columns at -inf; read twice (maximum, then weights)
-                // so that a block's scores need not stay in registers
-                auto scores = [&](int k, float (&sv)[32]) {
-                    uint32_t t32[32];
-                    tmem_ld32(col + 32 * k, t32);
+                float sv[NB];
+                {
+                    uint32_t t32[kW][32];
+#pragma unroll
+                    for (int k = 0; k < kW; ++k) tmem_ld32(col + 32 * k, t32[k]);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) sv[e] = __uint_as_float(t32[e]);
-                    if (all != 0xffffffffu) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) sv[e] = ((mw[k] >> e) & 1u) ? sv[e] : -INFINITY;
-                    }
-                };
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int k = 0; k < kW; ++k) {
-                    float sv[32];
-                    scores(k, sv);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) mx[(e >> 1) & 3] = fmaxf(mx[(e >> 1) & 3], fmaxf(sv[e], sv[e + 1]));
+                    for (int k = 0; k < NB; ++k) sv[k] = __uint_as_float(t32[k >> 5][k & 31]);
                 }
-                float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+                if (all != 0xffffffffu) {
+#pragma unroll
+                    for (int k = 0; k < NB; ++k) sv[k] = ((mw[k >> 5] >> (k & 31)) & 1u) ? sv[k] : -INFINITY;
+                }
+                float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+                for (int k = 4; k < NB; k += 8) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        mx[e] = k + 4 + e < NB ? fmaxf(fmaxf(mx[e], sv[k + e]), sv[k + 4 + e]) : fmaxf(mx[e], sv[k + e]);
+                }
+                const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
                 float alpha = 1.0f;
                 if (mb > m_ref + kRescaleLog2) {  // also the first visible block (m_ref = -inf)
                     alpha = ex2(m_ref - mb);
@@ -387,16 +395,11 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                 for (int h = 0; h < NB / 64; ++h) {
                     uint32_t pw[32];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float sv[32];
-                        scores(2 * h + k, sv);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float2 x = f2fma(make_float2(sv[e], sv[e + 1]), scv, nmv);
-                            const float p0 = ex2(x.x), p1 = ex2(x.y);
-                            acc = f2add(acc, make_float2(p0, p1));
-                            pw[16 * k + e / 2] = pack_bf16(p0, p1);
-                        }
+                    for (int k = 0; k < 64; k += 2) {
+                        const float2 x = f2fma(make_float2(sv[64 * h + k], sv[64 * h + k + 1]), scv, nmv);
+                        const float p0 = ex2(x.x), p1 = ex2(x.y);
+                        acc = f2add(acc, make_float2(p0, p1));
+                        pw[k / 2] = pack_bf16(p0, p1);
                     }
                     tmem_st32(col + 32 * h, pw);  // over scores that have been read
                 }
