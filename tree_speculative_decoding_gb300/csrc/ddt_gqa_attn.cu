@@ -42,6 +42,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "ddt_gqa.cuh"
 #include "ddt_internal.cuh"
 #include "ddt_sm100.cuh"
@@ -99,13 +101,20 @@ struct Cfg {
     static_assert(kSmemBytes <= (kTiles == 2 ? 232448 : 115712), "shared memory");
 };
 
+// The waits try the barrier first: the abort flag is read only where the phase
+// is still open.
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *err) {
-    if (*abort) return false;
-    if (mbar_wait(bar, parity, kWaitLimit)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+    }
     *abort = 1;
     latch(err, DDT_DEVERR_TIMEOUT);
     return false;
 }
+// The same for a whole warp: it succeeds for every lane or for none, so the warp
+// stays converged for the warp-collective instructions after it.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *err) {
     return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, err));
 }
@@ -255,41 +264,81 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
         } else {
             // ================= MMA =================
             if (lane == 0) {
-                auto issue_s = [&](int w) -> bool {
-                    const int j = w / tiles, t = w - j * tiles, s = j % C::kKStages;
-                    if (!wait_or_abort(bar(C::bKFull + s), (j / C::kKStages) & 1, abort_flag, a.err)) return false;
-                    fence_proxy_async_smem();  // written by cp.async, read by the tensor core
-                    tc_fence_after();
-                    const uint32_t qb = sbase + C::kOffQ + t * C::kQBytes, kb = sbase + C::kOffK + s * C::kBlockBytes;
-                    const uint32_t d = tmem + C::kColS + NB * (w & 1);
+                const uint64_t q0 = smem_desc(sbase + C::kOffQ, 16, 1024), k0 = smem_desc(sbase + C::kOffK, 16, 1024),
+                               v0 = smem_desc(sbase + C::kOffV, C::kBoxBytes, 1024);  // + bytes >> 4
+                bool ok = wait_or_abort(bar(C::bQFull), 0, abort_flag, a.err);
+                // The tensor pipe is idle while this thread waits or computes: the loop is
+                // unrolled over the two slots and keeps its stages and phases in counters.
+                auto run = [&](auto tile_count) {
+                    constexpr int A = decltype(tile_count)::value;  // tiles of the CTA
+                    int ks = 0, vs = 0, w = 0;
+                    uint32_t kph = 0, vph = 0, pph = 0;
+                    auto issue_s = [&](int slot) {
+                        const int t = A == 2 ? slot : 0;
+                        if (t == 0) {
+                            ok = wait_or_abort(bar(C::bKFull + ks), kph, abort_flag, a.err);
+                            if (!ok) return;
+                            fence_proxy_async_smem();  // written by cp.async, read by the tensor core
+                        }
+                        tc_fence_after();
+                        const uint64_t qd = q0 + t * (C::kQBytes >> 4), kd = k0 + (uint32_t)ks * (C::kBlockBytes >> 4);
+                        const uint32_t d = tmem + C::kColS + NB * slot;
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        mma_ss(d, smem_desc(qb + (ks >> 2) * C::kQBoxBytes + (ks & 3) * 32, 16, 1024),
-                               smem_desc(kb + (ks >> 2) * C::kBoxBytes + (ks & 3) * 32, 16, 1024), C::kIdescS, ks > 0);
-                    mma_commit(bar(C::bSFull + (w & 1)));
-                    if (t == tiles - 1) mma_commit(bar(C::bKEmpty + s));
-                    return true;
-                };
-                auto issue_pv = [&](int w) -> bool {
-                    const int j = w / tiles, t = w - j * tiles, s = j % C::kVStages;
-                    if (!wait_or_abort(bar(C::bVFull + s), (j / C::kVStages) & 1, abort_flag, a.err)) return false;
-                    if (!wait_or_abort(bar(C::bPFull + (w & 1)), (w >> 1) & 1, abort_flag, a.err)) return false;
-                    fence_proxy_async_smem();
-                    tc_fence_after();
-                    const uint32_t vb = sbase + C::kOffV + s * C::kBlockBytes;
-                    const uint32_t p = tmem + C::kColS + NB * (w & 1), d = tmem + C::kColO + D * t;
+                        for (int i = 0; i < D / 16; ++i)
+                            mma_ss(d, qd + (((i >> 2) * C::kQBoxBytes + (i & 3) * 32) >> 4),
+                                   kd + (((i >> 2) * C::kBoxBytes + (i & 3) * 32) >> 4), C::kIdescS, i > 0);
+                        mma_commit(bar(C::bSFull + slot));
+                        if (t == A - 1) {
+                            mma_commit(bar(C::bKEmpty + ks));
+                            if (++ks == C::kKStages) {
+                                ks = 0;
+                                kph ^= 1;
+                            }
+                        }
+                    };
+                    auto issue_pv = [&](int slot) {
+                        const int t = A == 2 ? slot : 0;
+                        if (t == 0) {
+                            ok = wait_or_abort(bar(C::bVFull + vs), vph, abort_flag, a.err);
+                            if (!ok) return;
+                            fence_proxy_async_smem();
+                        }
+                        ok = wait_or_abort(bar(C::bPFull + slot), pph, abort_flag, a.err);
+                        if (!ok) return;
+                        tc_fence_after();
+                        const uint64_t vd = v0 + (uint32_t)vs * (C::kBlockBytes >> 4);
+                        const uint32_t p = tmem + C::kColS + NB * slot, d = tmem + C::kColO + D * t;
+                        const uint32_t later = w >= A;  // the first block's product overwrites
 #pragma unroll
-                    for (int ks = 0; ks < NB / 16; ++ks)
-                        mma_ts(d, p + 8 * ks, smem_desc(vb + ks * 2048, C::kBoxBytes, 1024), C::kIdescPV, j > 0 || ks > 0);
-                    if (t == tiles - 1) mma_commit(bar(C::bVEmpty + s));
-                    if (tiles == 1) mma_commit(bar(C::bODone));
-                    return true;
+                        for (int i = 0; i < NB / 16; ++i)
+                            mma_ts(d, p + 8 * i, vd + i * (2048 >> 4), C::kIdescPV, i > 0 ? 1u : later);
+                        if (A == 1) mma_commit(bar(C::bODone));
+                        if (t == A - 1) {
+                            mma_commit(bar(C::bVEmpty + vs));
+                            if (++vs == C::kVStages) {
+                                vs = 0;
+                                vph ^= 1;
+                            }
+                        }
+                    };
+                    if (ok) issue_s(0);
+                    if (ok && items > 1) issue_s(1);
+                    while (ok && w < items) {
+#pragma unroll
+                        for (int slot = 0; slot < 2; ++slot) {
+                            if (!ok || w >= items) break;
+                            issue_pv(slot);
+                            if (ok && w + 2 < items) issue_s(slot);
+                            ++w;
+                        }
+                        pph ^= 1;
+                    }
                 };
-                bool ok = wait_or_abort(bar(C::bQFull), 0, abort_flag, a.err) && issue_s(0);
-                if (ok && items > 1) ok = issue_s(1);
-                for (int w = 0; w < items && ok; ++w) {
-                    ok = issue_pv(w);
-                    if (ok && w + 2 < items) ok = issue_s(w + 2);
+                if constexpr (kTiles == 2) {
+                    if (tiles == 2) run(std::integral_constant<int, 2>{});
+                    else run(std::integral_constant<int, 1>{});
+                } else {
+                    run(std::integral_constant<int, 1>{});
                 }
                 // completes when every MMA issued has: the epilogue (and, after a timeout, the exit) waits for it
                 mma_commit(bar(C::bOFin));
