@@ -79,6 +79,7 @@ struct Cfg {
     static constexpr int kQBytes = kBoxes * kQBoxBytes;  // one tile of q
     static constexpr int kKStages = D == 128 ? (kTiles == 2 ? 3 : 2) : 4;
     static constexpr int kVStages = D == 128 ? 2 : 4;
+    static constexpr int kHalves = NB / 64;              // parts of P that PV may start on
     static constexpr int kUnits = NB / 32;               // 32-row units of a block
     static constexpr int kLoadWarps = 4 * kTiles - 1;    // with the MMA warp: whole warpgroups
     static constexpr int kThreads = 256 * kTiles;
@@ -91,7 +92,7 @@ struct Cfg {
     // barriers
     static constexpr int bKFull = 0, bKEmpty = bKFull + kKStages, bVFull = bKEmpty + kKStages,
                          bVEmpty = bVFull + kVStages, bSFull = bVEmpty + kVStages, bPFull = bSFull + 2,
-                         bQFull = bPFull + 2, bODone = bQFull + 1, bOFin = bODone + 1, bCount = bOFin + 1;
+                         bQFull = bPFull + 2 * kHalves, bODone = bQFull + 1, bOFin = bODone + 1, bCount = bOFin + 1;
     static constexpr int kOffHolder = kOffBar + 8 * bCount;
     static constexpr int kSmemUsed = kOffHolder + 8;
     static constexpr int kSmemBytes = kSmemUsed + 1024;  // slack for the 1024-byte alignment of swizzle atoms
@@ -198,7 +199,7 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
         const int w0 = (min(rows, kRows) + 31) >> 5, w1 = tiles == 2 ? (rows - kRows + 31) >> 5 : w0;
         for (int i = 0; i < C::bCount; ++i)
             mbar_init(bar(i), i < C::bKFull + C::kKStages || (i >= C::bVFull && i < C::bVFull + C::kVStages) ? 32 * C::kUnits
-                      : i == C::bPFull ? w0 : i == C::bPFull + 1 ? w1 : i == C::bQFull ? (tiles == 2 ? w0 + w1 : w0) : 1);
+                      : i >= C::bPFull && i < C::bPFull + C::kHalves ? w0 : i >= C::bPFull + C::kHalves && i < C::bQFull ? w1 : i == C::bQFull ? (tiles == 2 ? w0 + w1 : w0) : 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -263,7 +264,7 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
             asm volatile("cp.async.wait_all;" ::: "memory");  // nothing may land after the CTA has left
         } else {
             // ================= MMA =================
-            if (lane == 0) {
+            if (elect_one()) {
                 const uint64_t q0 = smem_desc(sbase + C::kOffQ, 16, 1024), k0 = smem_desc(sbase + C::kOffK, 16, 1024),
                                v0 = smem_desc(sbase + C::kOffV, C::kBoxBytes, 1024);  // + bytes >> 4
                 bool ok = wait_or_abort(bar(C::bQFull), 0, abort_flag, a.err);
@@ -303,15 +304,18 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                             if (!ok) return;
                             fence_proxy_async_smem();
                         }
-                        ok = wait_or_abort(bar(C::bPFull + slot), pph, abort_flag, a.err);
-                        if (!ok) return;
-                        tc_fence_after();
                         const uint64_t vd = v0 + (uint32_t)vs * (C::kBlockBytes >> 4);
                         const uint32_t p = tmem + C::kColS + NB * slot, d = tmem + C::kColO + D * t;
                         const uint32_t later = w >= A;  // the first block's product overwrites
 #pragma unroll
-                        for (int i = 0; i < NB / 16; ++i)
-                            mma_ts(d, p + 8 * i, vd + i * (2048 >> 4), C::kIdescPV, i > 0 ? 1u : later);
+                        for (int h = 0; h < C::kHalves; ++h) {
+                            ok = wait_or_abort(bar(C::bPFull + C::kHalves * slot + h), pph, abort_flag, a.err);
+                            if (!ok) return;
+                            tc_fence_after();
+#pragma unroll
+                            for (int i = 4 * h; i < 4 * h + 4; ++i)
+                                mma_ts(d, p + 8 * i, vd + i * (2048 >> 4), C::kIdescPV, i > 0 ? 1u : later);
+                        }
                         if (A == 1) mma_commit(bar(C::bODone));
                         if (t == A - 1) {
                             mma_commit(bar(C::bVEmpty + vs));
@@ -437,22 +441,6 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                     l *= alpha;
                     m_ref = mb;
                 }
-                const float mref = m_ref == -INFINITY ? 0.f : m_ref;  // nothing seen yet: every p is 0
-                const float2 scv = make_float2(sc, sc), nmv = make_float2(-mref, -mref);
-                float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int h = 0; h < NB / 64; ++h) {
-                    uint32_t pw[32];
-#pragma unroll
-                    for (int k = 0; k < 64; k += 2) {
-                        const float2 x = f2fma(make_float2(sv[64 * h + k], sv[64 * h + k + 1]), scv, nmv);
-                        const float p0 = ex2(x.x), p1 = ex2(x.y);
-                        acc = f2add(acc, make_float2(p0, p1));
-                        pw[k / 2] = pack_bf16(p0, p1);
-                    }
-                    tmem_st32(col + 32 * h, pw);  // over scores that have been read
-                }
-                l += acc.x + acc.y;
                 // The output so far shrinks before PV(w).  With two tiles S(w) was issued behind
                 // this tile's last PV, so that is done; with one it has to be waited for.
                 if (j > 0 && __any_sync(0xffffffffu, row_on && alpha != 1.0f)) {
@@ -472,10 +460,26 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                         tmem_st32(oc + 32 * q, t32);
                     }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::bPFull + slot));
+                const float mref = m_ref == -INFINITY ? 0.f : m_ref;  // nothing seen yet: every p is 0
+                const float2 scv = make_float2(sc, sc), nmv = make_float2(-mref, -mref);
+                float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int h = 0; h < NB / 64; ++h) {
+                    uint32_t pw[32];
+#pragma unroll
+                    for (int k = 0; k < 64; k += 2) {
+                        const float2 x = f2fma(make_float2(sv[64 * h + k], sv[64 * h + k + 1]), scv, nmv);
+                        const float p0 = ex2(x.x), p1 = ex2(x.y);
+                        acc = f2add(acc, make_float2(p0, p1));
+                        pw[k / 2] = pack_bf16(p0, p1);
+                    }
+                    tmem_st32(col + 32 * h, pw);  // over scores that have been read
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::bPFull + C::kHalves * slot + h));
+                }
+                l += acc.x + acc.y;
             }
             // ---- epilogue ----
             ok = ok && warp_wait(bar(C::bOFin), 0, abort_flag, a.err) && *abort_flag == 0;
