@@ -7,54 +7,82 @@
 // prefix, node n at its depth below it: "The Architecture of a Speculative
 // Decoding Engine", section "The Final Resolution: A Concrete Trace").
 //
-// Bound by memory: 2 bytes in and 2 out per value, some twenty fp32 operations.
-// A group of head_dim / 8 lanes holds one head row, 16 bytes a lane; the sum of
-// squares and the far half of a pair come by shuffles inside the group, so the
-// row is read once and written once.  One CTA takes a token (its request, slot
-// and angles are looked up once) and its groups walk the token's q, k and v
-// rows four at a time, loads first.  With few tokens several CTAs share one.
-// The angles are read from the caller's table: sine and cosine of far
-// positions need more than fp32, once per position and not per token.
+// Bound by memory: 2 bytes in and 2 out per value, some ten fp32 instructions
+// per pair of values.  A group of head_dim / 8 lanes holds one head row.  A lane
+// holds both halves of its pairs (two pieces of four values, rope_dim / 2
+// apart), so the rotation needs no exchange between lanes; only the sum of
+// squares crosses the group.  Weight, cosine and sine are folded into four
+// factors per pair once per token.  A CTA takes a token and its groups walk the
+// token's rows; the first rows are loaded before the token's request, slot and
+// angles are looked up, a chain of four dependent loads.  With few tokens several
+// CTAs share one.  The angles are read from the caller's table: sine and cosine
+// of far positions need more than fp32, once per position and not per token.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "ddt_gqa.cuh"
 #include "ddt_internal.cuh"
+#include "ddt_sm100.cuh"
 
 namespace ddt {
 namespace {
 
-constexpr int kThreads = 256;
+using namespace sm100;
+
+constexpr int kThreads = 128;
 constexpr int kBatchRows = 4;  // head rows in flight per group
 
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+struct Row {  // a lane's two pieces of four values
+    uint2 a, b;
+};
+__device__ __forceinline__ Row load_row(const uint16_t *p, int off0, int off1) {
+    Row r;
+    r.a = *reinterpret_cast<const uint2 *>(p + off0);
+    r.b = *reinterpret_cast<const uint2 *>(p + off1);
+    return r;
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ void store_row(uint16_t *p, int off0, int off1, const Row &r) {
+    *reinterpret_cast<uint2 *>(p + off0) = r.a;
+    *reinterpret_cast<uint2 *>(p + off1) = r.b;
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
+// The factors of a token's rows: out_a = a * aa + b * ab, out_b = b * bb + a * ba
+// for the values a, b of a pair, times the row's 1 / rms.  With split pairs the
+// two pieces are the two sides; with adjacent pairs the sides alternate inside
+// each piece, and (a, b) are the values of one float2.
+struct Factors {
+    float2 aa[2], ab[2], bb[2], ba[2];
+};
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 8) norm_rope_append_kernel(const AppendArgs a) {
     constexpr int kLanes = D / 8;               // lanes of one head row
     constexpr int kGroups = kThreads / kLanes;  // head rows of a CTA at a time
     const int lane = threadIdx.x & 31;
-    const int sub = threadIdx.x & (kLanes - 1);  // this lane's 8 values: [8 sub, 8 sub + 8)
+    const int sub = threadIdx.x & (kLanes - 1);
     const int t = blockIdx.x;
+    const int H = a.num_heads, G = a.num_kv_heads;
+    const int group = blockIdx.y * kGroups + threadIdx.x / kLanes;
+    const int stride = gridDim.y * kGroups;
+    // the lane's pieces: a pair's two sides, or eight values in a row (adjacent pairs, or not rotated)
+    const int half = a.rope_dim >> 1;
+    const bool turn = 8 * sub < a.rope_dim, split = turn && !a.interleaved;
+    const int off0 = split ? 4 * sub : 8 * sub, off1 = split ? half + 4 * sub : 8 * sub + 4;
     pdl_wait();
     pdl_trigger();  // after the wait: whatever runs next sees everything before this kernel
+
+    const uint16_t *q = a.q + t * a.q_stride;
+    Row in[kBatchRows];
+    auto load_batch = [&](int r0) {
+#pragma unroll
+        for (int u = 0; u < kBatchRows; ++u)
+            if (r0 + u * stride < H) in[u] = load_row(q + (int64_t)(r0 + u * stride) * D, off0, off1);
+    };
+    load_batch(group);
 
     const int b = find_request(a.qo_indptr, a.batch, t, lane);
     if (b >= a.batch) return;  // behind the last request: left as it is
@@ -71,89 +99,116 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const Append
     const int64_t slot = a.kv_indices[kv0 + P + i];
     const bool slot_ok = slot >= 0 && slot < a.pool_rows;
     if (!slot_ok && threadIdx.x == 0) latch(a.err, DDT_DEVERR_KV_INDEX);
-    // this lane's angles: first half of a split pair, second half, or (interleaved) four whole pairs
-    const int half = a.rope_dim >> 4;  // lanes of half the rotated values
-    const bool turn = sub < 2 * half;
-    float cs[8], sn[8];
+    float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};  // of the lane's four pairs
     if (a.rope_dim > 0) {
         const int64_t pos = (int64_t)P + (a.depth ? a.depth[t] : i);
         if (pos < 0 || pos >= a.max_pos) {
             if (threadIdx.x == 0) latch(a.err, DDT_DEVERR_POSITION);
             return;
         }
-        const float *row = a.cos_sin + pos * a.rope_dim;
         if (turn) {
-            const int first = a.interleaved ? 4 * sub : 8 * (sub < half ? sub : sub - half);
+            const float *row = a.cos_sin + pos * a.rope_dim + 4 * sub;
+            const float4 c = *reinterpret_cast<const float4 *>(row), s = *reinterpret_cast<const float4 *>(row + half);
+            cs[0] = c.x; cs[1] = c.y; cs[2] = c.z; cs[3] = c.w;
+            sn[0] = s.x; sn[1] = s.y; sn[2] = s.z; sn[3] = s.w;
+        }
+    }
+    auto factors = [&](const uint16_t *weight) {
+        float2 w0[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)}, w1[2] = {w0[0], w0[1]};
+        if (weight) {
+            const Row w = load_row(weight, off0, off1);
+            w0[0] = unpack2(w.a.x); w0[1] = unpack2(w.a.y);
+            w1[0] = unpack2(w.b.x); w1[1] = unpack2(w.b.y);
+        }
+        Factors f;
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                if (v == 1 && a.interleaved) break;
-                const float4 c = *reinterpret_cast<const float4 *>(row + first + 4 * v);
-                const float4 s = *reinterpret_cast<const float4 *>(row + (a.rope_dim >> 1) + first + 4 * v);
-                cs[4 * v] = c.x; cs[4 * v + 1] = c.y; cs[4 * v + 2] = c.z; cs[4 * v + 3] = c.w;
-                sn[4 * v] = s.x; sn[4 * v + 1] = s.y; sn[4 * v + 2] = s.z; sn[4 * v + 3] = s.w;
+        for (int p = 0; p < 2; ++p) {
+            if (a.interleaved) {  // pairs 2 p' and 2 p' + 1 of piece p: (x, y) = (a, b)
+                const float c0 = cs[2 * p], c1 = cs[2 * p + 1], s0 = sn[2 * p], s1 = sn[2 * p + 1];
+                const float2 wa = p ? w1[0] : w0[0], wb = p ? w1[1] : w0[1];
+                f.aa[p] = make_float2(wa.x * c0, wb.x * c1);
+                f.ab[p] = make_float2(-wa.y * s0, -wb.y * s1);
+                f.bb[p] = make_float2(wa.y * c0, wb.y * c1);
+                f.ba[p] = make_float2(wa.x * s0, wb.x * s1);
+            } else {
+                const float2 c = make_float2(cs[2 * p], cs[2 * p + 1]), s = make_float2(sn[2 * p], sn[2 * p + 1]);
+                f.aa[p] = make_float2(w0[p].x * c.x, w0[p].y * c.y);
+                f.ab[p] = make_float2(-w1[p].x * s.x, -w1[p].y * s.y);
+                f.bb[p] = make_float2(w1[p].x * c.x, w1[p].y * c.y);
+                f.ba[p] = make_float2(w0[p].x * s.x, w0[p].y * s.y);
+            }
+        }
+        return f;
+    };
+    // one row; the whole warp calls it (lanes without a row pass anything)
+    auto apply = [&](const Row &r, const Factors &f, bool norm) {
+        float2 x[2][2] = {{unpack2(r.a.x), unpack2(r.a.y)}, {unpack2(r.b.x), unpack2(r.b.y)}};
+        float inv = 1.f;
+        if (norm) {
+            float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) ss = f2fma(x[p][e], x[p][e], ss);
+            float s = ss.x + ss.y;
+#pragma unroll
+            for (int o = kLanes / 2; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o, kLanes);
+            inv = rsqrtf(s * (1.0f / D) + a.eps);
+        }
+        const float2 z = make_float2(0.f, 0.f), iv = make_float2(inv, inv);
+        Row y;
+        if (a.interleaved) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {  // the piece's two pairs
+                const float2 xa = make_float2(x[p][0].x, x[p][1].x), xb = make_float2(x[p][0].y, x[p][1].y);
+                const float2 ya = f2fma(f2fma(xa, f.aa[p], turn ? f2fma(xb, f.ab[p], z) : z), iv, z);
+                const float2 yb = f2fma(f2fma(xb, f.bb[p], turn ? f2fma(xa, f.ba[p], z) : z), iv, z);
+                (p ? y.b : y.a) = make_uint2(pack_bf16(ya.x, yb.x), pack_bf16(ya.y, yb.y));
+            }
+        } else {
+            uint32_t wa[2], wb[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const float2 ya = f2fma(f2fma(x[0][p], f.aa[p], turn ? f2fma(x[1][p], f.ab[p], z) : z), iv, z);
+                const float2 yb = f2fma(f2fma(x[1][p], f.bb[p], turn ? f2fma(x[0][p], f.ba[p], z) : z), iv, z);
+                wa[p] = pack_bf16(ya.x, ya.y);
+                wb[p] = pack_bf16(yb.x, yb.y);
+            }
+            y.a = make_uint2(wa[0], wa[1]);
+            y.b = make_uint2(wb[0], wb[1]);
+        }
+        return y;
+    };
+
+    uint16_t *q_out = a.q_out + (int64_t)t * H * D;
+    {
+        const Factors f = factors(a.q_weight);
+        // groups of a warp walk the same number of rows: the sums above need all its lanes
+        for (int r0 = group; __any_sync(0xffffffffu, r0 < H); r0 += kBatchRows * stride) {
+            if (r0 != group) load_batch(r0);
+#pragma unroll
+            for (int u = 0; u < kBatchRows; ++u) {
+                const int r = r0 + u * stride;
+                if (!__any_sync(0xffffffffu, r < H)) break;
+                const Row y = apply(in[u], f, a.q_weight != nullptr);
+                if (r < H) store_row(q_out + (int64_t)r * D, off0, off1, y);
             }
         }
     }
-    float wq[8], wk[8];
-    if (a.q_weight) unpack8(reinterpret_cast<const uint4 *>(a.q_weight)[sub], wq);
-    if (a.k_weight) unpack8(reinterpret_cast<const uint4 *>(a.k_weight)[sub], wk);
-
-    const int H = a.num_heads, G = a.num_kv_heads;
-    const int rows = H + 2 * G;
-    const int group = blockIdx.y * kGroups + threadIdx.x / kLanes;
-    const int stride = gridDim.y * kGroups;
-    // lanes of a warp walk the same number of batches: the shuffles below need them all
-    for (int base = group; __any_sync(0xffffffffu, base < rows); base += kBatchRows * stride) {
-        uint4 in[kBatchRows];
-#pragma unroll
-        for (int u = 0; u < kBatchRows; ++u) {
-            const int r = base + u * stride;
-            const uint16_t *src = r < H ? a.q + t * a.q_stride + (int64_t)r * D
-                : r < H + G ? a.k + t * a.k_stride + (int64_t)(r - H) * D
-                            : a.v + t * a.v_stride + (int64_t)(r - H - G) * D;
-            if (r < rows) in[u] = reinterpret_cast<const uint4 *>(src)[sub];
+    if (!slot_ok) return;  // the whole CTA
+    const Factors f = factors(a.k_weight);
+    const uint16_t *k = a.k + t * a.k_stride, *v = a.v + t * a.v_stride;
+    uint16_t *kp = a.k_pool + slot * a.pool_stride, *vp = a.v_pool + slot * a.pool_stride;
+    for (int r = group; __any_sync(0xffffffffu, r < G); r += stride) {
+        Row kr{}, vr{};
+        if (r < G) {
+            kr = load_row(k + (int64_t)r * D, off0, off1);
+            vr = load_row(v + (int64_t)r * D, off0, off1);
         }
-#pragma unroll
-        for (int u = 0; u < kBatchRows; ++u) {
-            const int r = base + u * stride;
-            if (!__any_sync(0xffffffffu, r < rows)) break;
-            const bool is_q = r < H, is_v = r >= H + G;
-            float x[8];
-            unpack8(r < rows ? in[u] : make_uint4(0, 0, 0, 0), x);
-            float ss = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-            for (int o = kLanes / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, kLanes);
-            if (is_q ? a.q_weight != nullptr : a.k_weight != nullptr) {
-                const float inv = rsqrtf(ss * (1.0f / D) + a.eps);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] *= inv * (is_q ? wq[e] : wk[e]);
-            }
-            if (a.rope_dim > 0) {
-                if (a.interleaved) {
-                    if (turn) {
-#pragma unroll
-                        for (int p = 0; p < 4; ++p) {
-                            const float lo = x[2 * p], hi = x[2 * p + 1];
-                            x[2 * p] = lo * cs[p] - hi * sn[p];
-                            x[2 * p + 1] = hi * cs[p] + lo * sn[p];
-                        }
-                    }
-                } else {
-                    const int other = !turn ? sub : sub < half ? sub + half : sub - half;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float y = __shfl_sync(0xffffffffu, x[e], other, kLanes);
-                        if (turn) x[e] = sub < half ? x[e] * cs[e] - y * sn[e] : x[e] * cs[e] + y * sn[e];
-                    }
-                }
-            }
-            if (r < rows && (is_q || slot_ok)) {
-                uint16_t *dst = is_q ? a.q_out + ((int64_t)t * H + r) * D
-                    : (is_v ? a.v_pool + (int64_t)(r - H - G) * D : a.k_pool + (int64_t)(r - H) * D) + slot * a.pool_stride;
-                reinterpret_cast<uint4 *>(dst)[sub] = is_v ? in[u] : pack8(x);
-            }
+        kr = apply(kr, f, a.k_weight != nullptr);
+        if (r < G) {
+            store_row(kp + (int64_t)r * D, off0, off1, kr);
+            store_row(vp + (int64_t)r * D, off0, off1, vr);
         }
     }
 }
@@ -162,10 +217,9 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const Append
 
 cudaError_t launch_norm_rope_append(const AppendArgs &a, int num_sms, cudaStream_t s) {
     const int groups = kThreads / (a.head_dim / 8);
-    const int rows = a.num_heads + 2 * a.num_kv_heads;
-    // CTAs per token: one when the tokens alone fill the SMs, else down to one head row per group
-    int split = (rows + groups - 1) / groups;
-    const int64_t room = (4LL * num_sms + a.total_q - 1) / a.total_q;
+    // CTAs per token: one when the tokens alone fill the SMs, else down to one query row per group
+    int split = (a.num_heads + groups - 1) / groups;
+    const int64_t room = (8LL * num_sms + a.total_q - 1) / a.total_q;
     if (split > room) split = (int)room;
     const dim3 grid((unsigned)a.total_q, (unsigned)split);
     return a.head_dim == 128 ? launch_pdl(norm_rope_append_kernel<128>, grid, dim3(kThreads), 0, s, a)

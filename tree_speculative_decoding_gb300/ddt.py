@@ -570,12 +570,17 @@ def _slab(t, dev, name):
     pools are contiguous (the pools themselves may be apart)."""
     if t.dim() < 3 or t.device != dev:
         raise ValueError(f"{name} must be a [pools, rows, ...] tensor on {dev}")
-    if t.shape[0] == 0 or t.shape[1] == 0 or not t[0].is_contiguous():
+    shape, strides, es = t.shape, t.stride(), t.element_size()
+    size = 1   # values of the dimensions walked so far, innermost first
+    for n, s in zip(shape[:1:-1], strides[:1:-1]):
+        if n != 1 and s != size:
+            raise ValueError(f"{name}: every pool must be contiguous")
+        size *= n
+    pools, rows = shape[0], shape[1]
+    if pools == 0 or rows == 0 or size == 0 or (rows != 1 and strides[1] != size):
         raise ValueError(f"{name}: every pool must be contiguous and hold a row")
-    es = t.element_size()
-    row = t[0, 0].numel() * es
-    gap = t.stride(0) * es if t.shape[0] > 1 else t.shape[1] * row
-    return t.data_ptr(), gap, t.shape[1], t.shape[0], row
+    row = size * es
+    return t.data_ptr(), (strides[0] * es if pools > 1 else rows * row), rows, pools, row
 
 
 def ddt_cache_copy(src_pool, dst_pool, src, dst, stream=None):
