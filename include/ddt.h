@@ -88,6 +88,7 @@ extern "C" {
 #define DDT_MAX_SPLITS 128
 #define DDT_MAX_VOCAB 262144 /* ddt_accept_sampled */
 #define DDT_GQA_MAX_HEADS 128 /* query heads of the grouped-query calls */
+#define DDT_GQA_MAX_CTAS 512  /* ddt_gqa_verify_attn: CTAs that the work is dealt to */
 #define DDT_CACHE_MAX_ROWS (1 << 24) /* ddt_cache_compact: rows of a pool */
 
 typedef enum {
@@ -673,14 +674,17 @@ ddt_status ddt_gqa_norm_rope_append(
  *               of 8, at least num_kv_heads * head_dim), 16-byte aligned.
  *   kv_indices, kv_indptr, qo_indptr, mask, mask_indptr (device) as in
  *               ddt_verify_attn.
- *   num_splits  0 = choose among the counts whose partial results fit
- *               workspace_bytes (1 needs none), else 1..128.
+ *   num_ctas    the cached columns of all requests and heads are dealt to this
+ *               many CTAs in equal shares, and what a share's ends cut is joined
+ *               afterwards: 1..DDT_GQA_MAX_CTAS (batch <= 256), or 0 = choose what
+ *               the device holds at once, less where workspace_bytes is too small
+ *               for that; without a workspace, for batch > 256 and for short
+ *               caches each request and K/V head has a CTA of its own.
  *   out         (device) bf16 [total_q][num_heads][head_dim], 16-byte aligned:
  *               what the layer's output projection reads.
  *   lse         (device) float [total_q][num_heads] or NULL.
  *   workspace   (device) 256-byte aligned; ddt_gqa_verify_attn_workspace_size
- *               (total_q, num_heads, head_dim, splits) bytes for an explicit
- *               num_splits; may be NULL for one split.  Calls that may overlap
+ *               bytes for num_ctas, or NULL when that is 0.  Calls that may overlap
  *               on the GPU need a workspace each.
  * Supported: scale > 0, head_dim 64 or 128, num_heads a multiple of
  * num_kv_heads and at most DDT_GQA_MAX_HEADS, max_q_len <= 128, pool_rows <= 2^31 - 1.
@@ -691,20 +695,21 @@ ddt_status ddt_gqa_norm_rope_append(
  * 32) or lie outside [0, total_mask_words] (DDT_DEVERR_MASK_INDPTR), a slot
  * outside the pool (DDT_DEVERR_KV_INDEX: row 0 is read instead).
  *
- * ddt_gqa_verify_attn_num_splits() returns the count chosen for these bounds
- * with an unlimited workspace, on num_sms SMs (<= 0: the current device's).
+ * ddt_gqa_verify_attn_num_ctas() returns the count chosen for these bounds with
+ * a workspace that holds it, on num_sms SMs (<= 0: the current device's); 0: no
+ * workspace is used.
  */
-int32_t ddt_gqa_verify_attn_num_splits(int32_t batch, int32_t num_heads, int32_t num_kv_heads,
-                                       int32_t max_q_len, int32_t max_kv_len, int32_t num_sms);
-size_t ddt_gqa_verify_attn_workspace_size(int32_t total_q, int32_t num_heads, int32_t head_dim,
-                                          int32_t num_splits);
+int32_t ddt_gqa_verify_attn_num_ctas(int32_t batch, int32_t num_heads, int32_t num_kv_heads,
+                                     int32_t max_q_len, int32_t max_kv_len, int32_t num_sms);
+size_t ddt_gqa_verify_attn_workspace_size(int32_t batch, int32_t num_heads, int32_t num_kv_heads,
+                                          int32_t head_dim, int32_t max_q_len, int32_t num_ctas);
 ddt_status ddt_gqa_verify_attn(
     const uint16_t *q, const uint16_t *k_pool, const uint16_t *v_pool, int64_t pool_stride,
     int64_t pool_rows, const int32_t *kv_indices, const int32_t *kv_indptr,
     const int32_t *qo_indptr, const uint32_t *mask, const int32_t *mask_indptr, int32_t batch,
     int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t total_q, int32_t total_kv,
     int32_t total_mask_words, int32_t max_q_len, int32_t max_kv_len, float scale,
-    int32_t num_splits, uint16_t *out, float *lse, void *workspace, size_t workspace_bytes,
+    int32_t num_ctas, uint16_t *out, float *lse, void *workspace, size_t workspace_bytes,
     void *stream);
 
 /*

@@ -27,7 +27,7 @@ def call(lib, name, good, **changes):
 
 
 ATTN = dict(q=P, k=P, v=P, stride=1024, rows=100, idx=P, kvp=P, qop=P, mask=P, mip=P, batch=1, H=64, G=8, D=128,
-            total_q=0, total_kv=40, words=18, max_q=9, max_kv=40, scale=0.1, splits=0, out=P, lse=None, ws=None, wsb=0,
+            total_q=0, total_kv=40, words=18, max_q=9, max_kv=40, scale=0.1, ctas=0, out=P, lse=None, ws=None, wsb=0,
             stream=None)
 
 
@@ -40,25 +40,30 @@ def test_attention_host_checks(lib):
         assert f(**{name: ctypes.c_void_p(264)}) == INVALID, name    # not 16-byte aligned
     assert f(ws=ctypes.c_void_p(128)) == INVALID                     # not 256-byte aligned
     for bad in (dict(batch=-1), dict(total_q=-1), dict(total_kv=-1), dict(words=-1), dict(rows=0), dict(max_kv=8),
-                dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=0.0), dict(scale=-0.1), dict(splits=-1), dict(H=63), dict(G=0), dict(H=0),
+                dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=0.0), dict(scale=-0.1), dict(ctas=-1), dict(H=63), dict(G=0), dict(H=0),
                 dict(G=128), dict(stride=1016), dict(stride=1028), dict(max_q=-1)):
         assert f(**bad) == INVALID, bad
-    for bad in (dict(D=96), dict(D=256, stride=2048), dict(H=136), dict(max_q=129, max_kv=129), dict(splits=129),
+    for bad in (dict(D=96), dict(D=256, stride=2048), dict(H=136), dict(max_q=129, max_kv=129), dict(ctas=513),
+                dict(ctas=2, batch=257),
                 dict(rows=2 ** 31), dict(batch=65536)):
         assert f(**bad) == UNSUPPORTED, bad
 
 
 def test_attention_sizing(lib):
     size = lib.ddt_gqa_verify_attn_workspace_size
-    assert size(33, 64, 128, 1) == 0 and size(0, 64, 128, 4) == 0
+    assert size(1, 64, 8, 128, 33, 0) == 0 and size(0, 64, 8, 128, 33, 4) == 0 and size(1, 64, 7, 128, 33, 4) == 0
     up = lambda x: (x + 255) // 256 * 256  # noqa: E731
-    for tq, h, d, s in ((33, 64, 128, 4), (1, 1, 64, 2), (128, 128, 128, 128)):
-        assert size(tq, h, d, s) == up(tq * h * s * d * 4) + up(tq * h * s * 4)
-    splits = lib.ddt_gqa_verify_attn_num_splits
+    # two parts per CTA of as many rows as an item has: q_len x group, at most 128 or (two tiles) 256
+    for b, h, g, d, t, c, rows in ((1, 64, 8, 128, 1, 304, 8), (3, 64, 8, 128, 16, 9, 128), (2, 64, 8, 64, 17, 5, 136),
+                                   (256, 128, 1, 128, 128, 512, 256)):
+        assert size(b, h, g, d, t, c) == up(8 * (b + 2)) + up(2 * c * rows * d * 4) + up(2 * c * rows * 4)
+    ctas = lib.ddt_gqa_verify_attn_num_ctas
     for args in ((1, 64, 8, 33, 4129, 152), (64, 64, 8, 1, 16384, 152), (1, 8, 2, 9, 30, 152), (1, 1, 1, 1, 1, 152),
-                 (1, 64, 8, 65, 131137, 152), (32, 32, 4, 33, 8225, 152), (65535, 128, 1, 128, 2 ** 31 - 1, 152)):
-        assert 1 <= splits(*args) <= 128, args
-    assert splits(0, 64, 8, 33, 4129, 152) == 1 and splits(1, 64, 7, 33, 4129, 152) == 1
+                 (1, 64, 8, 65, 131137, 152), (32, 32, 4, 33, 8225, 1000), (65535, 128, 1, 128, 2 ** 31 - 1, 152)):
+        assert 0 <= ctas(*args) <= 512, args
+    assert ctas(1, 64, 8, 65, 131137, 152) == 152 and ctas(64, 64, 8, 1, 16384, 152) == 304
+    assert ctas(257, 64, 8, 1, 16384, 152) == 0 and ctas(1, 8, 2, 9, 30, 152) == 0
+    assert ctas(0, 64, 8, 33, 4129, 152) == 0 and ctas(1, 64, 7, 33, 4129, 152) == 0
 
 
 APPEND = dict(q=P, qs=1536, k=P, ks=1536, v=P, vs=1536, qw=P, kw=P, eps=1e-6, table=P, max_pos=64, rope=128, il=0,

@@ -41,13 +41,13 @@ def attn_inputs(batch, H, G, D, seed, strided=False, q_scale=1.5):
     return q, k, v, k.to(DEV), v.to(DEV)
 
 
-def run_attn(ddt, batch, q, kd, vd, scale, num_splits=0, lse=True, **kw):
+def run_attn(ddt, batch, q, kd, vd, scale, num_ctas=0, lse=True, **kw):
     d = batch.device()
     out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device=DEV)
     ls = torch.full(q.shape[:2], 7.0, dtype=torch.float32, device=DEV) if lse else None
     ddt.ddt_gqa_verify_attn(q.to(DEV), kd, vd, d["kv_indices"], d["kv_indptr"], d["qo_indptr"], d["mask"],
                             d["mask_indptr"], scale, out, ls, max_q_len=batch.max_q, max_kv_len=batch.max_kv,
-                            num_splits=num_splits, **kw)
+                            num_ctas=num_ctas, **kw)
     return out, ls
 
 
@@ -82,22 +82,22 @@ ATTN = [
 
 
 @pytest.mark.parametrize("H,G,D,lens,mask", ATTN)
-@pytest.mark.parametrize("splits", [0, 1, 3])
-def test_attention(ddt, H, G, D, lens, mask, splits):
+@pytest.mark.parametrize("ctas", [0, 1, 3, 29])
+def test_attention(ddt, H, G, D, lens, mask, ctas):
     batch = ref.Batch(lens, 11 + H + len(lens), mask)
     q, k, v, kd, vd = attn_inputs(batch, H, G, D, 5 * H + D)
-    out, ls = run_attn(ddt, batch, q, kd, vd, D ** -0.5, splits)
+    out, ls = run_attn(ddt, batch, q, kd, vd, D ** -0.5, ctas)
     clean(ddt)
     check_attn(out, ls, q, k, v, batch, D ** -0.5)
 
 
-@pytest.mark.parametrize("splits", [2, 5, 16, 128])
-@pytest.mark.parametrize("H,T", [(8, 1), (16, 20)])
-def test_attention_forced_splits(ddt, splits, H, T):
-    # a long and a short request: splits past the short one's end see no column
-    batch = ref.Batch([(1900, T), (40, T)], 3, "tree")
-    q, k, v, kd, vd = attn_inputs(batch, H, 2, 128, 9)
-    out, ls = run_attn(ddt, batch, q, kd, vd, 0.1, splits)
+@pytest.mark.parametrize("ctas", [2, 5, 7, 16, 64, 128, 512])
+@pytest.mark.parametrize("H,T,D", [(8, 1, 128), (16, 20, 128), (16, 33, 64)])
+def test_attention_dealt_to_any_number_of_ctas(ddt, ctas, H, T, D):
+    # shares that cut the long request many times, and that hold its end, whole requests and a start
+    batch = ref.Batch([(1900, T), (40, T), (0, T), (700, max(1, T // 2))], 3, "tree")
+    q, k, v, kd, vd = attn_inputs(batch, H, 2, D, 9)
+    out, ls = run_attn(ddt, batch, q, kd, vd, 0.1, ctas)
     clean(ddt)
     check_attn(out, ls, q, k, v, batch, 0.1)
 
@@ -109,8 +109,8 @@ def test_attention_peaked_scores_and_a_rising_maximum(ddt):
     ramp = torch.linspace(0.0, 6.0, batch.total_kv).to(torch.bfloat16)
     k[torch.from_numpy(batch.slots.astype(np.int64))] *= ramp[:, None, None]
     kd.copy_(k)
-    for splits in (1, 3):
-        out, ls = run_attn(ddt, batch, q, kd, vd, 1.0, splits)
+    for ctas in (1, 3):
+        out, ls = run_attn(ddt, batch, q, kd, vd, 1.0, ctas)
         clean(ddt)
         check_attn(out, ls, q, k, v, batch, 1.0)
 
@@ -125,8 +125,8 @@ def test_attention_strided_pool_and_no_lse(ddt):
 
 
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("splits", [1, 2])
-def test_attention_unseen_rows_may_hold_anything(ddt, D, splits):
+@pytest.mark.parametrize("ctas,H", [(0, 8), (3, 8), (0, 64), (5, 64)])
+def test_attention_unseen_rows_may_hold_anything(ddt, D, ctas, H):
     # prefix columns hidden from every row, others from some, with NaN and infinities in their K
     # and V rows and in the pool's unnamed rows; one row sees nothing
     batch = ref.Batch([(180, 6), (70, 1)], 21, "tree")
@@ -135,7 +135,7 @@ def test_attention_unseen_rows_may_hold_anything(ddt, D, splits):
         batch.vis[b][0, 60] = False
     batch.vis[0][4] = False
     batch.words = np.concatenate([ref.pack_bits(x) for x in batch.vis])
-    q, k, v, kd, vd = attn_inputs(batch, 8, 2, D, 6)
+    q, k, v, kd, vd = attn_inputs(batch, H, 2, D, 6)
     clean_k, clean_v = k.clone(), v.clone()
     named = torch.from_numpy(batch.slots.astype(np.int64))
     unnamed = torch.ones(batch.rows, dtype=torch.bool)
@@ -147,14 +147,14 @@ def test_attention_unseen_rows_may_hold_anything(ddt, D, splits):
     # the column hidden from one row only: finite for the rows that see it, so its K may not be NaN
     kd.copy_(k)
     vd.copy_(v)
-    out, ls = run_attn(ddt, batch, q, kd, vd, 0.125, splits)
+    out, ls = run_attn(ddt, batch, q, kd, vd, 0.125, ctas)
     clean(ddt)
     assert torch.isfinite(out).all()
     check_attn(out, ls, q, clean_k, clean_v, batch, 0.125)
     # a V row with NaN that one node sees: that node's rows are NaN, the others' are not
     r = named[int(batch.kv[0]) + 60]
     vd[r] = float("nan")
-    out2, ls2 = run_attn(ddt, batch, q, kd, vd, 0.125, splits)
+    out2, ls2 = run_attn(ddt, batch, q, kd, vd, 0.125, ctas)
     clean(ddt)
     assert torch.equal(ls2, ls)
     assert torch.isfinite(out2[0]).all() and torch.isfinite(out2[4]).all() and torch.isfinite(out2[6]).all()
@@ -168,8 +168,8 @@ def test_attention_padded_batch_leaves_the_rest_alone(ddt):
     batch = ref.Batch([(40, 3), (12, 0), (0, 0), (9, 5)], 31, "tree")
     q, k, v, kd, vd = attn_inputs(batch, 8, 4, 128, 14)
     pad = torch.cat([q, torch.full((6, 8, 128), float("nan"), dtype=torch.bfloat16)])
-    for splits in (1, 2):
-        out, ls = run_attn(ddt, batch, pad, kd, vd, 0.1, splits)
+    for ctas in (0, 1, 5):
+        out, ls = run_attn(ddt, batch, pad, kd, vd, 0.1, ctas)
         clean(ddt)
         check_attn(out[: batch.total_q], ls[: batch.total_q], q, k, v, batch, 0.1)
         assert (out[batch.total_q:] == 7).all() and (ls[batch.total_q:] == 7).all()
@@ -210,7 +210,7 @@ def test_attention_is_the_same_on_every_run_on_a_stream_and_in_a_graph(ddt):
     d = batch.device()
     qd = q.to(DEV)
     out, ls = torch.zeros_like(qd), torch.zeros(q.shape[:2], device=DEV)
-    ws = torch.empty(1 << 22, dtype=torch.uint8, device=DEV)
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device=DEV)
     # the longer bounds of a graph that is replayed for growing requests
     call = lambda stream=None: ddt.ddt_gqa_verify_attn(  # noqa: E731
         qd, kd, vd, d["kv_indices"], d["kv_indptr"], d["qo_indptr"], d["mask"], d["mask_indptr"], 0.1, out, ls,
@@ -253,8 +253,8 @@ def test_attention_rows_past_32_bit_offsets(ddt):
     kd = torch.zeros(rows, G, D, dtype=torch.bfloat16, device=DEV)
     vd = torch.zeros(rows, G, D, dtype=torch.bfloat16, device=DEV)
     kd[lo:], vd[lo:] = k.to(DEV), v.to(DEV)
-    for splits in (1, 2):
-        out, ls = run_attn(ddt, batch, q, kd, vd, 0.1, splits)
+    for ctas in (0, 1, 5):
+        out, ls = run_attn(ddt, batch, q, kd, vd, 0.1, ctas)
         clean(ddt)
         check_attn(out, ls, q, k, v, small, 0.1)
 

@@ -97,20 +97,23 @@ ddt_status ddt_gqa_norm_rope_append(
     return launched(ddt::launch_norm_rope_append(a, ddt::device_sm_count(), as_stream(stream)));
 }
 
-int32_t ddt_gqa_verify_attn_num_splits(int32_t batch, int32_t num_heads, int32_t num_kv_heads,
-                                       int32_t max_q_len, int32_t max_kv_len, int32_t num_sms) {
+int32_t ddt_gqa_verify_attn_num_ctas(int32_t batch, int32_t num_heads, int32_t num_kv_heads,
+                                     int32_t max_q_len, int32_t max_kv_len, int32_t num_sms) {
     if (batch < 1 || num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads || max_q_len < 1 ||
         max_kv_len < 1)
-        return 1;
+        return 0;
     if (num_sms <= 0) num_sms = ddt::device_sm_count();
-    return ddt::gqa_choose_splits(batch, num_heads, num_kv_heads, max_q_len, max_kv_len, num_sms, DDT_MAX_SPLITS);
+    return ddt::gqa_choose_ctas(batch, num_heads, num_kv_heads, max_q_len, max_kv_len, num_sms);
 }
 
-size_t ddt_gqa_verify_attn_workspace_size(int32_t total_q, int32_t num_heads, int32_t head_dim,
-                                          int32_t num_splits) {
-    if (total_q < 1 || num_heads < 1 || head_dim < 1 || num_splits <= 1) return 0;
-    const size_t rows = (size_t)total_q * num_heads;
-    return align256(rows * num_splits * head_dim * sizeof(float)) + align256(rows * num_splits * sizeof(float));
+size_t ddt_gqa_verify_attn_workspace_size(int32_t batch, int32_t num_heads, int32_t num_kv_heads,
+                                          int32_t head_dim, int32_t max_q_len, int32_t num_ctas) {
+    if (batch < 1 || num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads || head_dim < 1 || max_q_len < 1 ||
+        num_ctas < 1)
+        return 0;
+    const size_t rows = (size_t)2 * num_ctas * ddt::gqa_part_rows(max_q_len, num_heads / num_kv_heads);
+    return align256(((size_t)batch + 2) * sizeof(int64_t)) + align256(rows * head_dim * sizeof(float)) +
+           align256(rows * sizeof(float));
 }
 
 ddt_status ddt_gqa_verify_attn(
@@ -119,15 +122,16 @@ ddt_status ddt_gqa_verify_attn(
     const int32_t *qo_indptr, const uint32_t *mask, const int32_t *mask_indptr, int32_t batch,
     int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t total_q, int32_t total_kv,
     int32_t total_mask_words, int32_t max_q_len, int32_t max_kv_len, float scale,
-    int32_t num_splits, uint16_t *out, float *lse, void *workspace, size_t workspace_bytes,
+    int32_t num_ctas, uint16_t *out, float *lse, void *workspace, size_t workspace_bytes,
     void *stream) {
     if (!q || !k_pool || !v_pool || !kv_indices || !kv_indptr || !qo_indptr || !mask || !mask_indptr || !out ||
         batch < 0 || total_q < 0 || total_kv < 0 || total_mask_words < 0 || pool_rows < 1 || max_q_len < 0 ||
-        max_kv_len < max_q_len || !isfinite(scale) || !(scale > 0.f) || num_splits < 0)
+        max_kv_len < max_q_len || !isfinite(scale) || !(scale > 0.f) || num_ctas < 0)
         return DDT_ERR_INVALID_ARG;
     const ddt_status heads = check_heads(num_heads, num_kv_heads, head_dim);
     if (heads != DDT_OK) return heads;
-    if (max_q_len > DDT_MAX_Q_LEN || num_splits > DDT_MAX_SPLITS || pool_rows > INT32_MAX || batch > 65535)
+    if (max_q_len > DDT_MAX_Q_LEN || num_ctas > DDT_GQA_MAX_CTAS || pool_rows > INT32_MAX || batch > 65535 ||
+        (num_ctas > 0 && batch > ddt::kGqaMaxDealtBatch))
         return DDT_ERR_UNSUPPORTED;
     if (misaligned(q, 16) || misaligned(k_pool, 16) || misaligned(v_pool, 16) || misaligned(out, 16) ||
         misaligned(workspace, 256) || bad_pool_stride(pool_stride, num_kv_heads, head_dim))
@@ -136,18 +140,21 @@ ddt_status ddt_gqa_verify_attn(
     unsigned int *err = ddt::device_error_word();
     if (!err) return DDT_ERR_CUDA;
 
-    int requested = num_splits;
-    if (requested == 0) {
-        int cap = 1;
-        if (workspace)
-            for (cap = DDT_MAX_SPLITS; cap > 1; --cap)
-                if (ddt_gqa_verify_attn_workspace_size(total_q, num_heads, head_dim, cap) <= workspace_bytes) break;
-        requested = ddt::gqa_choose_splits(batch, num_heads, num_kv_heads, max_q_len, max_kv_len,
-                                           ddt::device_sm_count(), cap);
+    auto need = [&](int ctas) {
+        return ddt_gqa_verify_attn_workspace_size(batch, num_heads, num_kv_heads, head_dim, max_q_len, ctas);
+    };
+    int ctas = num_ctas;
+    if (num_ctas == 0) {  // the choice, or what the workspace holds of it
+        ctas = ddt::gqa_choose_ctas(batch, num_heads, num_kv_heads, max_q_len, max_kv_len, ddt::device_sm_count());
+        if (!workspace) ctas = 0;
+        while (ctas > 0 && need(ctas) > workspace_bytes) --ctas;
+    } else if (!workspace || workspace_bytes < need(ctas)) {
+        return DDT_ERR_WORKSPACE;
     }
     ddt::GqaArgs a;
     memset(&a, 0, sizeof a);
-    ddt::gqa_split_layout(max_kv_len, requested, &a.split_cols, &a.num_splits);
+    a.num_ctas = ctas;
+    a.forced = num_ctas > 0;
     a.q = q;
     a.k_pool = k_pool;
     a.v_pool = v_pool;
@@ -171,14 +178,13 @@ ddt_status ddt_gqa_verify_attn(
     a.out = out;
     a.lse = lse;
     a.err = err;
-    if (a.num_splits > 1) {
-        if (!workspace ||
-            workspace_bytes < ddt_gqa_verify_attn_workspace_size(total_q, num_heads, head_dim, a.num_splits))
-            return DDT_ERR_WORKSPACE;
-        const size_t rows = (size_t)total_q * num_heads;
-        a.o_part = static_cast<float *>(workspace);
-        a.lse_part = reinterpret_cast<float *>(static_cast<char *>(workspace) +
-                                               align256(rows * a.num_splits * head_dim * sizeof(float)));
+    if (ctas > 0) {
+        const size_t rows = (size_t)2 * ctas * ddt::gqa_part_rows(max_q_len, num_heads / num_kv_heads);
+        char *p = static_cast<char *>(workspace);
+        a.plan = reinterpret_cast<int64_t *>(p);
+        p += align256(((size_t)batch + 2) * sizeof(int64_t));
+        a.o_part = reinterpret_cast<float *>(p);
+        a.lse_part = reinterpret_cast<float *>(p + align256(rows * head_dim * sizeof(float)));
     }
     return launched(ddt::launch_gqa_attn(a, as_stream(stream)));
 }

@@ -7,27 +7,37 @@
 //   lse = log sum_j e^{s_j}
 // in one pass over the columns with a running maximum and sum.
 //
-// Work of a CTA: one K/V head of one request, one split of its columns, and up
-// to kTiles tiles of 128 consecutive rows (node-major, the group's heads inside
-// a node: the rows that share the K/V head).  The K and V rows of a block are
-// gathered once for all its tiles.
+// Work.  An item is one K/V head of one request and up to kTiles tiles of 128
+// consecutive rows (node-major, the group's heads inside a node: the rows that
+// share the K/V head); its K and V rows are gathered once for all its tiles, a
+// block of columns at a time.
 //   * kTiles = 1: blocks of 64 columns, 256 tensor-memory columns and under half
 //     of the shared memory, so two CTAs share an SM: one's prologue, softmax and
 //     epilogue run under the other's loads.  Taken when a request's rows per K/V
 //     head fit one tile (decode, small trees): the loads bound it.
 //   * kTiles = 2: blocks of 128 columns, all of tensor memory; the tensor core
 //     works on one tile while the softmax of the other runs.
-// Score slots: two buffers of one block's scores in tensor memory.  Work item w
-// (block-major, tiles inside a block) uses slot w mod 2: with two tiles each has
-// its own, with one tile blocks alternate.  The MMA warp issues
+// The blocks of all items, weighted by what they cost, form one line that is
+// dealt to the resident CTAs in equal shares: a CTA takes the end of one item,
+// whole items, and the start of another, whatever the requests' lengths are.
+// Items that were cut leave partial results (at most two per CTA) in the
+// workspace for the combine kernel.  Every CTA and the combine find the same
+// cuts from the offsets.
+//
+// Score slots: two buffers of one block's scores in tensor memory.  Work unit w
+// of a segment (block-major, tiles inside a block) uses slot w mod 2: with two
+// tiles each has its own, with one tile blocks alternate.  The MMA warp issues
 //   S(0) S(1) | PV(0) S(2) | PV(1) S(3) | ...
 // so the scores of w + 1 are being computed, or done, while the softmax of w
 // runs.  P (bf16) overwrites the scores in place and is the A operand of PV
 // from tensor memory; V is read as an MN-major operand from its gathered rows.
 //
-// Warps: four softmax warps per tile (thread = row = TMEM lane), one that issues
-// MMAs, one that gathers rows by TMA (tile::gather4: four 128-byte row pieces an
-// instruction, 128-byte swizzle, the layout the MMA descriptors expect).
+// Warps: softmax warps of 32 rows x 64 columns (thread = row = TMEM lane; with
+// blocks of 128 columns two of them share a row, and PV starts on the half that
+// is ready), one warp that issues MMAs, and load warps that copy row pieces with
+// 16-byte cp.async into the 128-byte-swizzled layout of the MMA descriptors.
+// (A TMA row gather costs its warp ~57 clk for 512 bytes and measured half the
+// rate.)
 //
 // Columns that a row does not see get p = 0, but 0 * NaN is NaN: a V row that
 // holds NaN or infinities reaches the output rows that do not see it.  A row
@@ -53,8 +63,7 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kRows = 128;      // rows per tile (TMEM lanes)
-constexpr int kSplitUnit = 128; // a split is a whole number of these columns
+constexpr int kRows = 128;  // rows per tile (TMEM lanes)
 constexpr uint32_t kWaitLimit = 1u << 22;
 // Lazy rescale: the running maximum (log2 units) moves only when a block's
 // exceeds it by more than this, so p <= 2^48; the fp32 sums stay finite for
@@ -66,12 +75,14 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 struct GqaParams {
     GqaArgs a;
-    int group;     // query heads per K/V head
+    int group;      // query heads per K/V head
+    int part_rows;  // rows of a partial result
 };
 
 template <int D, int kTiles>
 struct Cfg {
     static constexpr int NB = kTiles == 2 ? 128 : 64;    // columns per block
+    static constexpr int kHalves = NB / 64;              // softmax warps that share a row
     static constexpr int kBoxes = D / 64;                // 128-byte pieces of a row
     static constexpr int kBoxBytes = NB * 128;           // one piece of a block's rows
     static constexpr int kBlockBytes = kBoxes * kBoxBytes;
@@ -79,10 +90,10 @@ struct Cfg {
     static constexpr int kQBytes = kBoxes * kQBoxBytes;  // one tile of q
     static constexpr int kKStages = D == 128 ? (kTiles == 2 ? 3 : 2) : 4;
     static constexpr int kVStages = D == 128 ? 2 : 4;
-    static constexpr int kHalves = NB / 64;              // parts of P that PV may start on
     static constexpr int kUnits = NB / 32;               // 32-row units of a block
+    static constexpr int kSoftWarps = 4 * kTiles * kHalves;
     static constexpr int kLoadWarps = 4 * kTiles - 1;    // with the MMA warp: whole warpgroups
-    static constexpr int kThreads = 256 * kTiles;
+    static constexpr int kThreads = 32 * (kSoftWarps + kLoadWarps + 1);
     static constexpr uint32_t kTmemCols = kTiles == 2 ? 512 : 256;
     static constexpr uint32_t kColS = 0, kColO = 2 * NB;
     static constexpr int kOffQ = 0;
@@ -92,12 +103,24 @@ struct Cfg {
     // barriers
     static constexpr int bKFull = 0, bKEmpty = bKFull + kKStages, bVFull = bKEmpty + kKStages,
                          bVEmpty = bVFull + kVStages, bSFull = bVEmpty + kVStages, bPFull = bSFull + 2,
-                         bQFull = bPFull + 2 * kHalves, bODone = bQFull + 1, bOFin = bODone + 1, bCount = bOFin + 1;
+                         bQFull = bPFull + 2 * kHalves, bODone = bQFull + 1, bOFin = bODone + 1, bDrain = bOFin + 1,
+                         bSegFull = bDrain + 1, bSegEmpty = bSegFull + 2, bCount = bSegEmpty + 2;
     static constexpr int kOffHolder = kOffBar + 8 * bCount;
-    static constexpr int kSmemUsed = kOffHolder + 8;
+    static constexpr int kOffWalk = kOffHolder + 8;  // 128 bytes: the walk; 2 x 48: the segments it has given
+    static constexpr int kOffPlan = kOffWalk + 128 + 2 * 48;  // a sum per warp, then where the CTA's share starts
+    // what the two warps of a row tell each other: [kTiles][128] floats
+    static constexpr int kOffXch = kOffPlan + 8 * (kThreads / 32);
+    static constexpr int kSmemUsed = kOffXch + (kHalves == 2 ? kTiles * kRows * 4 : 0);
     static constexpr int kSmemBytes = kSmemUsed + 1024;  // slack for the 1024-byte alignment of swizzle atoms
     static constexpr uint32_t kIdescS = idesc_bf16(kRows, NB, 0, 0);
     static constexpr uint32_t kIdescPV = idesc_bf16(kRows, D, 0, 1);
+    // cost of a block with all tiles and with one, and of an item besides its blocks
+    // (its q, the latency of its first loads, its epilogue), in one unit; blocks
+    // that a CTA gets at least
+    static constexpr int kCostFull = kTiles == 2 ? 16 : 8, kCostOne = kTiles == 2 ? 10 : 8, kCostItem = 24;
+    static constexpr int kMinBlocks = kTiles == 2 ? 2 : 4;
+    static_assert(kTiles == 2 ? kLoadWarps > kUnits : kKStages >= 2 && kVStages >= 2 && kKStages <= kVStages, "see the load warps");
+    static_assert(kOffPlan % 8 == 0 && kOffXch % 4 == 0, "alignment");
     static_assert(kColO + kTiles * D <= kTmemCols, "tensor memory");
     static_assert(kSmemBytes <= (kTiles == 2 ? 232448 : 115712), "shared memory");
 };
@@ -150,6 +173,170 @@ __device__ __forceinline__ void row_again(const GqaArgs &a, const uint16_t *q, c
     }
 }
 
+// ---------------------------------------------------------------- the deal
+// A request's offsets, checked, and the size of its items.
+struct Request {
+    int qo0, T, kv0, N, m0;
+    int tgs;        // tile groups: items per K/V head (0: nothing to do)
+    int blocks;     // blocks of columns
+    bool last_one;  // the last tile group has one tile of two
+};
+
+template <class C>
+__device__ __forceinline__ int64_t item_cost(const Request &r, int tg) {
+    return C::kCostItem + (int64_t)r.blocks * (tg == r.tgs - 1 && r.last_one ? C::kCostOne : C::kCostFull);
+}
+template <class C>
+__device__ __forceinline__ int64_t request_cost(const Request &r, int num_kv_heads) {
+    return r.tgs > 0 ? ((r.tgs - 1) * item_cost<C>(r, 0) * (r.tgs > 1) + item_cost<C>(r, r.tgs - 1)) * num_kv_heads : 0;
+}
+
+// kTiles: tiles of an item.  err: where a bad request is reported, or null.
+template <class C, int kTiles>
+__device__ __forceinline__ Request load_request(const GqaArgs &a, int group, int b, unsigned int *err) {
+    Request r;
+    r.qo0 = a.qo_indptr[b];
+    const int qo1 = a.qo_indptr[b + 1];
+    r.kv0 = a.kv_indptr[b];
+    const int kv1 = a.kv_indptr[b + 1];
+    r.m0 = a.mask_indptr[b];
+    const int m1 = a.mask_indptr[b + 1];
+    r.T = qo1 - r.qo0;
+    r.N = kv1 - r.kv0;
+    const bool bad_qo = r.T < 0 || r.T > a.max_q_len || r.qo0 < 0 || qo1 > a.total_q;
+    const bool bad_kv = r.N < r.T || r.N > a.max_kv_len || r.kv0 < 0 || kv1 > a.total_kv;
+    const bool bad_mask =
+        !bad_qo && !bad_kv && (r.m0 < 0 || m1 - r.m0 != r.T * ((r.N + 31) >> 5) || m1 > a.total_mask_words);
+    if (bad_qo || bad_kv || bad_mask) {
+        latch(err, (bad_qo ? DDT_DEVERR_QO_INDPTR : 0u) | (bad_kv ? DDT_DEVERR_KV_INDPTR : 0u) |
+                       (bad_mask ? DDT_DEVERR_MASK_INDPTR : 0u));
+        r.T = 0;
+    }
+    const int rows = r.T * group, per = kTiles * kRows;
+    r.tgs = (rows + per - 1) / per;
+    r.blocks = r.tgs > 0 ? (r.N + C::NB - 1) / C::NB : 0;
+    r.last_one = kTiles == 2 && rows - (r.tgs - 1) * per <= kRows;
+    return r;
+}
+
+// CTA c of `ctas` takes the positions [share(c), share(c + 1)) of the line.
+__device__ __forceinline__ int64_t share_start(int64_t total, int ctas, int c) { return total * c / ctas; }
+__device__ __forceinline__ int share_owner(int64_t total, int ctas, int64_t pos) {
+    int c = (int)(pos * ctas / total);
+    while (share_start(total, ctas, c + 1) <= pos) ++c;
+    return c;
+}
+// the item's blocks that start before position x (block k starts kCostItem + k unit behind the item)
+template <class C>
+__device__ __forceinline__ int blocks_before(int64_t item, int64_t x, int unit, int blocks) {
+    const int64_t d = x - (item + C::kCostItem);
+    if (d <= 0) return 0;
+    const int64_t k = (d + unit - 1) / unit;
+    return k < blocks ? (int)k : blocks;
+}
+
+// What a CTA does in one go: `blocks` blocks of an item, from column c_begin on.
+struct Segment {
+    int row0, rows, tiles;  // rows of the request from row0 on; tiles of 128
+    int g, c_begin, c_end, blocks;
+    int qo0, kv0, m0, W;    // of the request
+    int part;               // -1: the whole item, else the place of the partial result
+};
+
+// The walk over the CTA's segments.  It lives in shared memory: one thread steps
+// it and hands the segments to the warps through a ring of two.
+template <class C, int kTiles>
+struct Walk {
+    int64_t pos, lo, hi;  // the item's position on the line; the CTA's share of it
+    Request r;
+    int b, tg, g, cta;
+    int dealt, more;
+
+    // one item, whole
+    __device__ __forceinline__ void start_item(const Request &req, int b_, int tg_, int g_) {
+        r = req;
+        b = b_;
+        tg = tg_;
+        g = g_;
+        pos = lo = hi = 0;
+        cta = 0;
+        dealt = 0;
+        more = 1;
+    }
+    // share [lo_, hi_), which starts inside request b_, whose items start at pos_
+    __device__ __forceinline__ void start_share(const Request &req, int heads, int cta_, int b_, int64_t pos_, int64_t lo_,
+                                                int64_t hi_) {
+        r = req;
+        cta = cta_;
+        b = b_;
+        lo = lo_;
+        hi = hi_;
+        dealt = more = 1;
+        const int64_t full = item_cost<C>(r, 0), before_last = r.tgs > 1 ? (r.tgs - 1) * full * heads : 0;
+        const int64_t off = lo - pos_;
+        if (off < before_last) {
+            const int64_t k = off / full;
+            tg = (int)(k / heads);
+            g = (int)(k - (int64_t)tg * heads);
+            pos = pos_ + k * full;
+        } else {
+            const int64_t last = item_cost<C>(r, r.tgs - 1);
+            tg = r.tgs - 1;
+            g = (int)((off - before_last) / last);
+            pos = pos_ + before_last + g * last;
+        }
+    }
+    // the next segment; one without blocks when the share is done
+    __device__ __forceinline__ Segment next(const GqaArgs &a, int group) {
+        Segment s;
+        s.blocks = 0;
+        while (more && s.blocks == 0) {
+            const int unit = tg == r.tgs - 1 && r.last_one ? C::kCostOne : C::kCostFull;
+            const int b0 = dealt ? blocks_before<C>(pos, lo, unit, r.blocks) : 0;
+            const int b1 = dealt ? blocks_before<C>(pos, hi, unit, r.blocks) : r.blocks;
+            s.row0 = tg * kTiles * kRows;
+            s.rows = min(kTiles * kRows, r.T * group - s.row0);
+            s.tiles = (s.rows + kRows - 1) / kRows;
+            s.g = g;
+            s.c_begin = b0 * C::NB;
+            s.c_end = min(r.N, b1 * C::NB);
+            s.blocks = b1 - b0;
+            s.qo0 = r.qo0;
+            s.kv0 = r.kv0;
+            s.m0 = r.m0;
+            s.W = (r.N + 31) >> 5;
+            // at most one item of a share starts before it, and at most one ends behind it
+            s.part = s.blocks == r.blocks ? -1 : 2 * cta + (lo > pos ? 0 : 1);
+            if (!dealt) {
+                more = 0;
+            } else {
+                pos += item_cost<C>(r, tg);
+                if (++g == a.num_kv_heads) {
+                    g = 0;
+                    ++tg;
+                }
+                while (tg >= r.tgs && pos < hi && ++b < a.batch) {  // the next request with items
+                    r = load_request<C, kTiles>(a, group, b, nullptr);
+                    tg = 0;
+                }
+                more = pos < hi && b < a.batch;
+            }
+        }
+        return s;
+    }
+};
+
+// a barrier of the two warps that share a row; true when any of their threads says so
+__device__ __forceinline__ bool pair_any(int id, bool x) {
+    uint32_t any;
+    asm volatile(
+        "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, %2, 64, p; selp.u32 %0, 1, 0, q; }"
+        : "=r"(any)
+        : "r"((uint32_t)x), "r"(id)
+        : "memory");
+    return any != 0;
+}
+
 template <int D, int kTiles>
 __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, kTiles == 2 ? 1 : 2)
 gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
@@ -162,48 +349,69 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
     auto bar = [&](int i) { return sbase + C::kOffBar + 8u * i; };
     uint32_t *holder = reinterpret_cast<uint32_t *>(smem + C::kOffHolder);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffHolder + 4);
+    int64_t *plan = reinterpret_cast<int64_t *>(smem + C::kOffPlan);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kMmaWarp = 4 * kTiles, kFirstLoad = kMmaWarp + 1;
-    // everything read below may be the previous kernel's output (q, the appended rows, the mask)
-    pdl_wait();
-
-    // ---- the CTA's work: K/V head g of request b, rows [row0, row0 + rows), columns [c_begin, c_end) ----
-    const int g = blockIdx.x % a.num_kv_heads, tile_group = blockIdx.x / a.num_kv_heads;
-    const int split = blockIdx.y, b = blockIdx.z;
-    const int qo0 = a.qo_indptr[b], qo1 = a.qo_indptr[b + 1];
-    const int kv0 = a.kv_indptr[b], kv1 = a.kv_indptr[b + 1];
-    const int m0 = a.mask_indptr[b], m1 = a.mask_indptr[b + 1];
-    const int T = qo1 - qo0, N = kv1 - kv0, W = (N + 31) >> 5;
-    const bool bad_qo = T < 0 || T > a.max_q_len || qo0 < 0 || qo1 > a.total_q;
-    const bool bad_kv = N < T || N > a.max_kv_len || kv0 < 0 || kv1 > a.total_kv;
-    const bool bad_mask = !bad_qo && !bad_kv && (m0 < 0 || m1 - m0 != T * W || m1 > a.total_mask_words);
-    if (bad_qo || bad_kv || bad_mask) {
-        if (tid == 0)
-            latch(a.err, (bad_qo ? DDT_DEVERR_QO_INDPTR : 0u) | (bad_kv ? DDT_DEVERR_KV_INDPTR : 0u) |
-                             (bad_mask ? DDT_DEVERR_MASK_INDPTR : 0u));
-        return;
-    }
-    const int row0 = tile_group * kTiles * kRows;
-    const int rows = min(kTiles * kRows, T * prm.group - row0);
-    const int c_begin = split * a.split_cols;
-    const int c_end = min(N, c_begin + a.split_cols);
-    if (rows <= 0 || c_begin >= c_end) return;  // the combine knows which splits of a request exist
-    const int nblk = (c_end - c_begin + NB - 1) / NB;
-    const int tiles = (rows + kRows - 1) / kRows;  // 1 .. kTiles
-    const int items = nblk * tiles;
-
-    // ---- barriers and tensor memory ----
+    constexpr int kMmaWarp = C::kSoftWarps, kFirstLoad = kMmaWarp + 1;
     if (warp == kMmaWarp && lane == 0) {
-        // P of a slot: one arrival per softmax warp that has rows in the slot's tile
-        const int w0 = (min(rows, kRows) + 31) >> 5, w1 = tiles == 2 ? (rows - kRows + 31) >> 5 : w0;
         for (int i = 0; i < C::bCount; ++i)
-            mbar_init(bar(i), i < C::bKFull + C::kKStages || (i >= C::bVFull && i < C::bVFull + C::kVStages) ? 32 * C::kUnits
-                      : i >= C::bPFull && i < C::bPFull + C::kHalves ? w0 : i >= C::bPFull + C::kHalves && i < C::bQFull ? w1 : i == C::bQFull ? (tiles == 2 ? w0 + w1 : w0) : 1);
+            mbar_init(bar(i), i < C::bKEmpty || (i >= C::bVFull && i < C::bVEmpty) ? 32 * C::kUnits  // load lanes
+                      : i >= C::bPFull && i < C::bQFull                            ? 4               // row quarters
+                      : i == C::bQFull                                             ? C::kSoftWarps
+                      : i >= C::bSegEmpty                                          ? C::kThreads / 32
+                                                                                   : 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
-    __syncwarp();
+    // everything read below may be the previous kernel's output (q, the appended rows, the mask)
+    pdl_wait();
+
+    // ---- this CTA's work ----
+    const bool dealt = a.num_ctas > 0;
+    Walk<C, kTiles> *walk = reinterpret_cast<Walk<C, kTiles> *>(smem + C::kOffWalk);
+    static_assert(sizeof(Walk<C, kTiles>) <= 128 && sizeof(Segment) <= 48, "the walk's room");
+    if (dealt) {  // batch <= kThreads: thread i sizes request i, and a scan places it on the line
+        constexpr int kWarps = C::kThreads / 32;
+        Request req;
+        int64_t cost = 0;
+        if (tid < a.batch) {
+            req = load_request<C, kTiles>(a, prm.group, tid, blockIdx.x == 0 ? a.err : nullptr);
+            cost = request_cost<C>(req, a.num_kv_heads);
+        }
+        int64_t sum = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += x;
+        }
+        if (lane == 31) plan[warp] = sum;
+        __syncthreads();
+        int64_t total = 0, at = sum - cost;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) at += plan[w];
+            total += plan[w];
+        }
+        // CTAs that take a share: as many as get a few blocks at least
+        const int64_t most = total / (C::kCostItem + (a.forced ? 1 : C::kMinBlocks) * C::kCostFull);
+        const int ctas = most < 1 ? 1 : most < a.num_ctas ? (int)most : a.num_ctas;
+        if (blockIdx.x == 0) {  // for the combine
+            if (tid < a.batch) a.plan[tid] = at;
+            if (tid == 0) {
+                a.plan[a.batch] = total;
+                a.plan[a.batch + 1] = ctas;
+            }
+        }
+        if (total == 0 || (int)blockIdx.x >= ctas) return;
+        const int64_t lo = share_start(total, ctas, blockIdx.x), hi = share_start(total, ctas, blockIdx.x + 1);
+        if (at <= lo && lo < at + cost) walk->start_share(req, a.num_kv_heads, blockIdx.x, tid, at, lo, hi);
+    } else {
+        const int b = blockIdx.z, tg = blockIdx.x / a.num_kv_heads;
+        const Request req = load_request<C, kTiles>(a, prm.group, b, blockIdx.x == 0 && tid == 0 ? a.err : nullptr);
+        if (tg >= req.tgs) return;
+        if (tid == 0) walk->start_item(req, b, tg, blockIdx.x - tg * a.num_kv_heads);
+    }
+
     if (warp == kMmaWarp) tmem_alloc(smem_u32(holder), C::kTmemCols);
     tc_fence_before();
     __syncthreads();
@@ -213,53 +421,122 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
     // it.  After the allocation: a CTA that starts early cannot take the tensor
     // memory that this one still needs while it waits for this one's end.
     pdl_trigger();
-    // Registers of the two-tile kernel: 512 threads x 128 at launch = 256 x 184 (softmax: a block's
-    // scores of a row) + 256 x 72.
+    volatile Segment *ring = reinterpret_cast<volatile Segment *>(smem + C::kOffWalk + 128);
+    // segment n of the CTA (its fields, or blocks = 0 behind the last); the caller's thread or warp
+    // reads it once
+    auto read_segment = [&](int n, Segment &s) {
+        volatile Segment &x = ring[n & 1];
+        s.row0 = x.row0;
+        s.rows = x.rows;
+        s.tiles = x.tiles;
+        s.g = x.g;
+        s.c_begin = x.c_begin;
+        s.c_end = x.c_end;
+        s.blocks = x.blocks;
+        s.qo0 = x.qo0;
+        s.kv0 = x.kv0;
+        s.m0 = x.m0;
+        s.W = x.W;
+        s.part = x.part;
+    };
+    auto warp_segment = [&](int n, Segment &s) -> bool {  // false: the wait ran out
+        if (!warp_wait(bar(C::bSegFull + (n & 1)), (n >> 1) & 1, abort_flag, a.err)) return false;
+        read_segment(n, s);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::bSegEmpty + (n & 1)));
+        return true;
+    };
+    Segment sg;
+
+    // Registers of the two-tile kernel: 768 threads x 80 at launch = 512 x 96 (softmax) + 256 x 48.
     if (warp >= kMmaWarp) {
-        if constexpr (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");  // one instruction for the warpgroup
+        if constexpr (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");  // one instruction for the warpgroup
         if (warp >= kFirstLoad) {
             // ================= gather =================
-            // The warps take units of 32 rows in turn, in the order K(0) K(1) V(0)
-            // K(2) V(1) ... V(nblk - 1): a unit's fixed cost (its waits) and its copies
-            // overlap those of the other warps' units.  A copy instruction moves 512
-            // bytes; the next unit's slots are loaded while this one's rows are copied.
+            // A unit is 32 rows of a block of K or V.  Two-tile kernel: four warps take
+            // a unit each of every block of K, three take the units of V in turn.
+            // One-tile kernel: three warps take the units in turn in the order K(0) K(1)
+            // V(0) K(2) V(1) ... V(blocks - 1).  A unit's fixed cost (its waits) and its
+            // copies overlap those of the other warps' units.  A copy instruction moves
+            // 512 bytes; the next unit's slots are loaded while this one's rows are copied.
+            //
+            // An "empty" wait goes by the phase's parity, so a warp may not reach a use of
+            // a stage while the use two before is still to be read.  Where a warp has a
+            // unit of every block its own last wait excludes that.  In the one-tile order
+            // the unit before one of V(j) is of K(j) at the earliest (whose wait implies
+            // PV(j - 4) is done, with two stages), the one before K(j) of V(j - 3) (S(j - 4)
+            // done, since S(w + 1) is issued before PV(w)).
             constexpr int kChunks = D / 8, kPer = 32 / kChunks;  // 16-byte pieces of a row; rows an instruction
             const int c = lane % kChunks, sub = lane / kChunks;
-            const int64_t at = ((int64_t)g * D + c * 8) * 2, pitch = a.pool_stride * 2;
-            const char *kp = reinterpret_cast<const char *>(a.k_pool) + at, *vp = reinterpret_cast<const char *>(a.v_pool) + at;
-            const int last = 2 * nblk - 1, end = 2 * nblk * C::kUnits;
-            // block of the sequence's group q, and whether it is its V
-            auto block_of = [&](int q, bool &is_v) {
-                is_v = q == last || (q > 0 && !(q & 1));
-                return q == last ? nblk - 1 : is_v ? q / 2 - 1 : (q + 1) / 2;
-            };
-            auto fetch = [&](int n) {
-                bool is_v;
-                const int j = block_of(n / C::kUnits, is_v);
-                return a.kv_indices[kv0 + min(c_begin + j * NB + 32 * (n % C::kUnits) + lane, c_end - 1)];  // past the end: a valid row again
-            };
-            int n = warp - kFirstLoad;
-            int ahead = n < end ? fetch(n) : 0;
-            for (; n < end; n += C::kLoadWarps) {
-                int slot = ahead;
-                if (slot < 0 || slot >= a.pool_rows) {
-                    latch(a.err, DDT_DEVERR_KV_INDEX);
-                    slot = 0;
+            const int64_t pitch = a.pool_stride * 2;
+            int base = 0;  // blocks of the segments before
+            bool ok = true;
+            auto give_segment = [&](int n) {  // by the first load warp
+                if (warp != kFirstLoad) return;
+                if (n >= 2) ok = warp_wait(bar(C::bSegEmpty + (n & 1)), ((n >> 1) - 1) & 1, abort_flag, a.err);
+                if (ok && lane == 0) {
+                    const Segment s = walk->next(a, prm.group);
+                    const_cast<Segment &>(ring[n & 1]) = s;
+                    mbar_arrive(bar(C::bSegFull + (n & 1)));
                 }
-                if (n + C::kLoadWarps < end) ahead = fetch(n + C::kLoadWarps);
-                bool is_v;
-                const int j = block_of(n / C::kUnits, is_v);
-                const int s = is_v ? j % C::kVStages : j % C::kKStages, u = is_v ? j / C::kVStages : j / C::kKStages;
-                if (u > 0 && !warp_wait(bar((is_v ? C::bVEmpty : C::bKEmpty) + s), (u - 1) & 1, abort_flag, a.err)) break;
-                const uint32_t to = sbase + (is_v ? C::kOffV : C::kOffK) + s * C::kBlockBytes + (c >> 3) * C::kBoxBytes +
-                                    (n % C::kUnits) * 32 * 128;
-                const char *pool = is_v ? vp : kp;
+                __syncwarp();
+            };
+            give_segment(0);
+            for (int seg = 0; ok; ++seg) {
+                ok = warp_segment(seg, sg);
+                if (!ok || sg.blocks == 0) break;
+                give_segment(seg + 1);
+                if (!ok) break;
+                const int64_t at = ((int64_t)sg.g * D + c * 8) * 2;
+                const char *kp = reinterpret_cast<const char *>(a.k_pool) + at, *vp = reinterpret_cast<const char *>(a.v_pool) + at;
+                const int32_t *slots = a.kv_indices + sg.kv0 + sg.c_begin;
+                const int cols = sg.c_end - sg.c_begin;
+                constexpr bool kApart = kTiles == 2;
+                constexpr int kKWarps = C::kUnits;  // of the two-tile kernel
+                const int lw = warp - kFirstLoad;
+                const bool v_warp = kApart && lw >= kKWarps;
+                const int last = 2 * sg.blocks - 1, end = (kApart ? 1 : 2) * sg.blocks * C::kUnits;
+                const int step = !kApart ? C::kLoadWarps : v_warp ? C::kLoadWarps - kKWarps : kKWarps;
+                // block of unit n, and whether it is its V
+                auto block_of = [&](int n, bool &is_v) {
+                    const int q = n / C::kUnits;
+                    if constexpr (kApart) {
+                        is_v = v_warp;
+                        return q;
+                    }
+                    is_v = q == last || (q > 0 && !(q & 1));
+                    return q == last ? sg.blocks - 1 : is_v ? q / 2 - 1 : (q + 1) / 2;
+                };
+                auto fetch = [&](int n) {
+                    bool is_v;
+                    const int j = block_of(n, is_v);
+                    return slots[min(j * NB + 32 * (n % C::kUnits) + lane, cols - 1)];  // past the end: a valid row again
+                };
+                int n = v_warp ? lw - kKWarps : lw;
+                int ahead = n < end ? fetch(n) : 0;
+                for (; n < end; n += step) {
+                    int slot = ahead;
+                    if (slot < 0 || slot >= a.pool_rows) {
+                        latch(a.err, DDT_DEVERR_KV_INDEX);
+                        slot = 0;
+                    }
+                    if (n + step < end) ahead = fetch(n + step);
+                    bool is_v;
+                    const int j = base + block_of(n, is_v);
+                    const int s = is_v ? j % C::kVStages : j % C::kKStages, u = is_v ? j / C::kVStages : j / C::kKStages;
+                    if (u > 0) ok = warp_wait(bar((is_v ? C::bVEmpty : C::bKEmpty) + s), (u - 1) & 1, abort_flag, a.err);
+                    if (!ok) break;
+                    const uint32_t to = sbase + (is_v ? C::kOffV : C::kOffK) + s * C::kBlockBytes +
+                                        (c >> 3) * C::kBoxBytes + (n % C::kUnits) * 32 * 128;
+                    const char *pool = is_v ? vp : kp;
 #pragma unroll
-                for (int i = 0; i < 32 / kPer; ++i) {
-                    const int k = i * kPer + sub;
-                    cp_async_16(to + k * 128 + (((c & 7) ^ (k & 7)) << 4), pool + __shfl_sync(0xffffffffu, slot, k) * pitch);
+                    for (int i = 0; i < 32 / kPer; ++i) {
+                        const int k = i * kPer + sub;
+                        cp_async_16(to + k * 128 + (((c & 7) ^ (k & 7)) << 4), pool + __shfl_sync(0xffffffffu, slot, k) * pitch);
+                    }
+                    cp_async_arrive(bar((is_v ? C::bVFull : C::bKFull) + s));
                 }
-                cp_async_arrive(bar((is_v ? C::bVFull : C::bKFull) + s));
+                base += sg.blocks;
             }
             asm volatile("cp.async.wait_all;" ::: "memory");  // nothing may land after the CTA has left
         } else {
@@ -267,13 +544,14 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
             if (elect_one()) {
                 const uint64_t q0 = smem_desc(sbase + C::kOffQ, 16, 1024), k0 = smem_desc(sbase + C::kOffK, 16, 1024),
                                v0 = smem_desc(sbase + C::kOffV, C::kBoxBytes, 1024);  // + bytes >> 4
-                bool ok = wait_or_abort(bar(C::bQFull), 0, abort_flag, a.err);
+                bool ok = true;
+                int ks = 0, vs = 0;
+                uint32_t kph = 0, vph = 0, pph[2] = {0, 0};
                 // The tensor pipe is idle while this thread waits or computes: the loop is
                 // unrolled over the two slots and keeps its stages and phases in counters.
-                auto run = [&](auto tile_count) {
-                    constexpr int A = decltype(tile_count)::value;  // tiles of the CTA
-                    int ks = 0, vs = 0, w = 0;
-                    uint32_t kph = 0, vph = 0, pph = 0;
+                auto run = [&](auto tile_count, int items) {
+                    constexpr int A = decltype(tile_count)::value;  // tiles of the segment
+                    int w = 0;
                     auto issue_s = [&](int slot) {
                         const int t = A == 2 ? slot : 0;
                         if (t == 0) {
@@ -309,13 +587,14 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                         const uint32_t later = w >= A;  // the first block's product overwrites
 #pragma unroll
                         for (int h = 0; h < C::kHalves; ++h) {
-                            ok = wait_or_abort(bar(C::bPFull + C::kHalves * slot + h), pph, abort_flag, a.err);
+                            ok = wait_or_abort(bar(C::bPFull + C::kHalves * slot + h), pph[slot], abort_flag, a.err);
                             if (!ok) return;
                             tc_fence_after();
 #pragma unroll
                             for (int i = 4 * h; i < 4 * h + 4; ++i)
                                 mma_ts(d, p + 8 * i, vd + i * (2048 >> 4), C::kIdescPV, i > 0 ? 1u : later);
                         }
+                        pph[slot] ^= 1;
                         if (A == 1) mma_commit(bar(C::bODone));
                         if (t == A - 1) {
                             mma_commit(bar(C::bVEmpty + vs));
@@ -325,7 +604,7 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                             }
                         }
                     };
-                    if (ok) issue_s(0);
+                    issue_s(0);
                     if (ok && items > 1) issue_s(1);
                     while (ok && w < items) {
 #pragma unroll
@@ -335,43 +614,73 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                             if (ok && w + 2 < items) issue_s(slot);
                             ++w;
                         }
-                        pph ^= 1;
                     }
                 };
-                if constexpr (kTiles == 2) {
-                    if (tiles == 2) run(std::integral_constant<int, 2>{});
-                    else run(std::integral_constant<int, 1>{});
-                } else {
-                    run(std::integral_constant<int, 1>{});
+                for (int seg = 0; ok; ++seg) {
+                    ok = wait_or_abort(bar(C::bSegFull + (seg & 1)), (seg >> 1) & 1, abort_flag, a.err);
+                    if (!ok) break;
+                    read_segment(seg, sg);
+                    mbar_arrive(bar(C::bSegEmpty + (seg & 1)));
+                    if (sg.blocks == 0) break;
+                    ok = wait_or_abort(bar(C::bQFull), seg & 1, abort_flag, a.err);
+                    if (!ok) break;
+                    if constexpr (kTiles == 2) {
+                        if (sg.tiles == 2) run(std::integral_constant<int, 2>{}, 2 * sg.blocks);
+                        else run(std::integral_constant<int, 1>{}, sg.blocks);
+                    } else {
+                        run(std::integral_constant<int, 1>{}, sg.blocks);
+                    }
+                    mma_commit(bar(C::bOFin));  // completes when the segment's MMAs have
                 }
-                // completes when every MMA issued has: the epilogue (and, after a timeout, the exit) waits for it
-                mma_commit(bar(C::bOFin));
-                mbar_wait(bar(C::bOFin), 0, kWaitLimit);
+                mma_commit(bar(C::bDrain));  // every MMA issued has to be done before the exit
+                mbar_wait(bar(C::bDrain), 0, kWaitLimit);
             }
             __syncwarp();
         }
     } else {
-        if constexpr (kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         // ================= softmax (thread = row = TMEM lane of its tile) =================
-        const int t = warp >> 2, wq = warp & 3;
+        if constexpr (kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+        const int t = warp / (4 * C::kHalves), hf = C::kHalves == 2 ? (warp >> 2) & 1 : 0, wq = warp & 3;
         const int r = 32 * wq + lane;  // row within the tile
-        const int rows_t = rows - t * kRows;
-        const bool warp_on = t < tiles && 32 * wq < rows_t;
-        if (warp_on) {
-            const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
-            // ---- q rows of this warp into the swizzled operand layout ----
-            {
+        const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
+        const int pair = 1 + 4 * t + wq;  // barrier of the row's two warps
+        volatile float *xch = reinterpret_cast<float *>(smem + C::kOffXch) + t * kRows + r;
+        // a value that both warps of a row hold afterwards: the second warp hands its own over, the first joins them
+        auto join = [&](float x, auto op) {
+            if (hf) *xch = x;
+            pair_any(pair, false);
+            if (!hf) *xch = op(x, *xch);
+            pair_any(pair, false);
+            return *xch;
+        };
+        const float sc = a.scale * kLog2e;
+        uint32_t sph[2] = {0, 0}, odone = 0;
+        bool ok = true;
+        // A wait that runs out in one warp of a pair takes both out at the next of their
+        // barriers: neither may be left waiting for the other.
+        auto failed = [&]() {
+            if constexpr (C::kHalves == 2) return pair_any(pair, !ok);
+            else return !ok;
+        };
+        for (int seg = 0;; ++seg) {
+            ok = ok && warp_segment(seg, sg);
+            if (failed() || sg.blocks == 0) break;
+            const int rows_t = sg.rows - t * kRows;  // rows of this warp's tile
+            const int tiles = sg.tiles;
+            // ---- q rows of the tile into the swizzled operand layout (the row's two warps take half each) ----
+            if (32 * wq < rows_t) {
                 constexpr int kChunks = D / 8, kPer = 32 / kChunks;  // 16-byte pieces of a row; rows per step
                 const int c = lane % kChunks, sub = lane / kChunks;
                 const uint32_t qb = sbase + C::kOffQ + t * C::kQBytes;
-#pragma unroll 8
-                for (int i = 0; i < 32 / kPer; ++i) {
+                constexpr int kSteps = 32 / kPer / C::kHalves;
+#pragma unroll 4
+                for (int i = hf * kSteps; i < (hf + 1) * kSteps; ++i) {
                     const int rt = 32 * wq + i * kPer + sub;
                     if (rt < rows_t) {
-                        const int rr = row0 + t * kRows + rt;
+                        const int rr = sg.row0 + t * kRows + rt;
                         const int node = rr / prm.group, hg = rr - node * prm.group;
                         const uint4 v = reinterpret_cast<const uint4 *>(
-                            a.q + ((int64_t)(qo0 + node) * a.num_heads + g * prm.group + hg) * D)[c];
+                            a.q + ((int64_t)(sg.qo0 + node) * a.num_heads + sg.g * prm.group + hg) * D)[c];
                         const uint32_t at = qb + (c >> 3) * C::kQBoxBytes + (rt >> 3) * 1024 + (rt & 7) * 128 +
                                             (((c & 7) ^ (rt & 7)) << 4);
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z),
@@ -380,123 +689,161 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                     }
                 }
                 fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::bQFull));
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::bQFull));
+            const bool mine = t < tiles;             // the segment has this tile
+            const bool warp_on = 32 * wq < rows_t;   // ... and rows of this warp (mine is implied)
             const bool row_on = r < rows_t;
-            const int rr = row0 + t * kRows + (row_on ? r : 0);
-            const int node = rr / prm.group, head = g * prm.group + rr - node * prm.group;
-            const uint32_t *words = a.mask + m0 + (int64_t)node * W;
-            const float sc = a.scale * kLog2e;
+            const int rr = sg.row0 + (row_on ? t * kRows + r : 0);
+            const int node = rr / prm.group;
+            const uint32_t *words = a.mask + sg.m0 + (int64_t)node * sg.W;
             float m_ref = -INFINITY, l = 0.f;
-            constexpr int kW = NB / 32;
-            auto mask_words = [&](int j, uint32_t (&mw)[kW]) {
+            // the two mask words of this warp's 64 columns of block j
+            auto mask_words = [&](int j, uint32_t (&mw)[2]) {
 #pragma unroll
-                for (int k = 0; k < kW; ++k) {
-                    const int c0 = c_begin + j * NB + 32 * k;
-                    uint32_t x = c0 < c_end ? words[c0 >> 5] : 0u;
-                    if (c0 < c_end && c_end - c0 < 32) x &= (1u << (c_end - c0)) - 1u;
+                for (int k = 0; k < 2; ++k) {
+                    const int c0 = sg.c_begin + j * NB + 64 * hf + 32 * k;
+                    uint32_t x = c0 < sg.c_end ? words[c0 >> 5] : 0u;
+                    if (c0 < sg.c_end && sg.c_end - c0 < 32) x &= (1u << (sg.c_end - c0)) - 1u;
                     mw[k] = x;
                 }
             };
-            uint32_t mw[kW], mnext[kW];
-            mask_words(0, mnext);
-            bool ok = true;
-            for (int j = 0; j < nblk; ++j) {
-                const int w = j * tiles + t, slot = w & 1;
+            uint32_t mnext[2] = {0, 0};
+            if (warp_on) mask_words(0, mnext);
+            for (int j = 0; mine && j < sg.blocks; ++j) {
+                const int slot = tiles == 2 ? t : j & 1;
                 const uint32_t col = tmem + lane_off + C::kColS + NB * slot;
-#pragma unroll
-                for (int k = 0; k < kW; ++k) mw[k] = mnext[k];
-                if (j + 1 < nblk) mask_words(j + 1, mnext);
-                ok = warp_wait(bar(C::bSFull + slot), (w >> 1) & 1, abort_flag, a.err);
-                if (!ok) break;
-                tc_fence_after();
-                uint32_t all = mw[0];
-#pragma unroll
-                for (int k = 1; k < kW; ++k) all &= mw[k];
-                float sv[NB];
-                {
-                    uint32_t t32[kW][32];
-#pragma unroll
-                    for (int k = 0; k < kW; ++k) tmem_ld32(col + 32 * k, t32[k]);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < NB; ++k) sv[k] = __uint_as_float(t32[k >> 5][k & 31]);
-                }
-                if (all != 0xffffffffu) {
-#pragma unroll
-                    for (int k = 0; k < NB; ++k) sv[k] = ((mw[k >> 5] >> (k & 31)) & 1u) ? sv[k] : -INFINITY;
-                }
-                float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
-#pragma unroll
-                for (int k = 4; k < NB; k += 8) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mx[e] = k + 4 + e < NB ? fmaxf(fmaxf(mx[e], sv[k + e]), sv[k + 4 + e]) : fmaxf(mx[e], sv[k + e]);
-                }
-                const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-                float alpha = 1.0f;
-                if (mb > m_ref + kRescaleLog2) {  // also the first visible block (m_ref = -inf)
-                    alpha = ex2(m_ref - mb);
-                    l *= alpha;
-                    m_ref = mb;
-                }
-                // The output so far shrinks before PV(w).  With two tiles S(w) was issued behind
-                // this tile's last PV, so that is done; with one it has to be waited for.
-                if (j > 0 && __any_sync(0xffffffffu, row_on && alpha != 1.0f)) {
-                    if (tiles == 1 && !warp_wait(bar(C::bODone), (j - 1) & 1, abort_flag, a.err)) {
-                        ok = false;
-                        break;
-                    }
+                uint32_t mw[2] = {mnext[0], mnext[1]};
+                if (warp_on && j + 1 < sg.blocks) mask_words(j + 1, mnext);
+                ok = warp_wait(bar(C::bSFull + slot), sph[slot], abort_flag, a.err);
+                sph[slot] ^= 1;
+                if (!ok && !(warp_on && C::kHalves == 2)) break;  // a pair leaves together, below
+                if (warp_on) {
                     tc_fence_after();
-                    const uint32_t oc = tmem + lane_off + C::kColO + D * t;
+                    // The weights are taken against the maximum so far while the block's own is
+                    // being found: it moves the reference only when it is more than 2^48 above,
+                    // and the weights are then taken again.
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float2 acc = make_float2(0.f, 0.f);
+                    uint32_t pw[32];  // the weights as bf16 pairs
+                    const float2 scv = make_float2(sc, sc);
+                    auto pass = [&](float m, bool find) {
+                        const float2 nmv = make_float2(-m, -m);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t t32[32];
+                            tmem_ld32(col + 64 * hf + 32 * k, t32);
+                            tmem_wait_ld();
+                            float sv[32];  // scores, unseen columns at -inf
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) sv[e] = __uint_as_float(t32[e]);
+                            if (mw[k] != 0xffffffffu) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) sv[e] = ((mw[k] >> e) & 1u) ? sv[e] : -INFINITY;
+                            }
+                            if (find) {
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2)
+                                    mx[(e >> 1) & 3] = fmaxf(fmaxf(mx[(e >> 1) & 3], sv[e]), sv[e + 1]);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                const float2 x = f2fma(make_float2(sv[e], sv[e + 1]), scv, nmv);
+                                const float p0 = ex2(x.x), p1 = ex2(x.y);
+                                acc = f2add(acc, make_float2(p0, p1));
+                                pw[16 * k + e / 2] = pack_bf16(p0, p1);
+                            }
+                        }
+                    };
+                    auto reference = [&]() { return m_ref == -INFINITY ? 0.f : m_ref; };  // nothing seen: every p is 0
+                    if (ok) pass(reference(), true);
+                    float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+                    bool moves = row_on && mb > m_ref + kRescaleLog2;  // also the first visible block (m_ref = -inf)
+                    bool any;
+                    if constexpr (C::kHalves == 2) {
+                        // the pair has read its scores before either half of P goes over them
+                        tc_fence_before();
+                        any = pair_any(pair, moves || !ok);
+                        if (any && failed()) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                    } else {
+                        any = __any_sync(0xffffffffu, moves);
+                    }
+                    if (any) {
+                        if constexpr (C::kHalves == 2) {
+                            mb = join(mb, [](float x, float y) { return fmaxf(x, y); });
+                            moves = row_on && mb > m_ref + kRescaleLog2;
+                        }
+                        const float alpha = moves ? ex2(m_ref - mb) : 1.0f;
+                        l *= alpha;
+                        if (moves) m_ref = mb;
+                        acc = make_float2(0.f, 0.f);
+                        pass(reference(), false);
+                        // The output so far shrinks before PV(w).  With two tiles S(w) was issued behind
+                        // this tile's last PV, so that is done; with one it has to be waited for.
+                        if (j > 0) {
+                            if (tiles == 1) ok = warp_wait(bar(C::bODone), (odone + j - 1) & 1, abort_flag, a.err);
+                            tc_fence_after();
+                            const uint32_t oc = tmem + lane_off + C::kColO + D * t + hf * (D / C::kHalves);
 #pragma unroll 1
-                    for (int q = 0; q < D / 32; ++q) {
-                        uint32_t t32[32];
-                        tmem_ld32(oc + 32 * q, t32);
-                        tmem_wait_ld();
+                            for (int q = 0; ok && q < D / C::kHalves / 32; ++q) {
+                                uint32_t t32[32];
+                                tmem_ld32(oc + 32 * q, t32);
+                                tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) t32[e] = __float_as_uint(__uint_as_float(t32[e]) * alpha);
-                        tmem_st32(oc + 32 * q, t32);
+                                for (int e = 0; e < 32; ++e) t32[e] = __float_as_uint(__uint_as_float(t32[e]) * alpha);
+                                tmem_st32(oc + 32 * q, t32);
+                            }
+                        }
+                        tc_fence_before();
+                        if (failed()) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
                     }
-                }
-                const float mref = m_ref == -INFINITY ? 0.f : m_ref;  // nothing seen yet: every p is 0
-                const float2 scv = make_float2(sc, sc), nmv = make_float2(-mref, -mref);
-                float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int h = 0; h < NB / 64; ++h) {
-                    uint32_t pw[32];
-#pragma unroll
-                    for (int k = 0; k < 64; k += 2) {
-                        const float2 x = f2fma(make_float2(sv[64 * h + k], sv[64 * h + k + 1]), scv, nmv);
-                        const float p0 = ex2(x.x), p1 = ex2(x.y);
-                        acc = f2add(acc, make_float2(p0, p1));
-                        pw[k / 2] = pack_bf16(p0, p1);
-                    }
-                    tmem_st32(col + 32 * h, pw);  // over scores that have been read
+                    l += acc.x + acc.y;
+                    tmem_st32(col + 32 * hf, pw);
                     tmem_wait_st();
                     tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(C::bPFull + C::kHalves * slot + h));
                 }
-                l += acc.x + acc.y;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::bPFull + C::kHalves * slot + hf));
+            }
+            // uses of the slots by the other tile's warps
+            if (tiles == 2) {
+                sph[1 - t] ^= sg.blocks & 1;
+            } else {
+                if (!mine) {
+                    sph[0] ^= ((sg.blocks + 1) >> 1) & 1;
+                    sph[1] ^= (sg.blocks >> 1) & 1;
+                }
+                odone += sg.blocks;
             }
             // ---- epilogue ----
-            ok = ok && warp_wait(bar(C::bOFin), 0, abort_flag, a.err) && *abort_flag == 0;
-            if (__all_sync(0xffffffffu, ok)) {
+            ok = ok && warp_wait(bar(C::bOFin), seg & 1, abort_flag, a.err);
+            if (warp_on && failed()) {
+                ok = false;
+            } else if (warp_on) {
                 tc_fence_after();
-                const int64_t row = (int64_t)(qo0 + node) * a.num_heads + head;
-                const int64_t all_rows = (int64_t)a.total_q * a.num_heads;
-                const bool part = a.num_splits > 1;
-                float *op = part ? a.o_part + ((int64_t)split * all_rows + row) * D : nullptr;
-                uint16_t *ob = a.out + row * D;
+                if constexpr (C::kHalves == 2) l = join(l, [](float x, float y) { return x + y; });
+                const int head = sg.g * prm.group + rr - node * prm.group;
+                const int64_t row = (int64_t)(sg.qo0 + node) * a.num_heads + head;
+                const bool part = sg.part >= 0;
+                const int64_t prow = (int64_t)sg.part * prm.part_rows + t * kRows + r;
                 const float inv = 1.f / l;
                 const bool none = l == 0.f;
                 bool finite = true;
+                constexpr int kCols = D / C::kHalves;  // of this warp
 #pragma unroll 1
-                for (int q = 0; q < D / 32; ++q) {
+                for (int q = 0; q < kCols / 32; ++q) {
+                    const int c0 = hf * kCols + 32 * q;
                     uint32_t t32[32];
-                    tmem_ld32(tmem + lane_off + C::kColO + D * t + 32 * q, t32);
+                    tmem_ld32(tmem + lane_off + C::kColO + D * t + c0, t32);
                     tmem_wait_ld();
                     float o[32];
 #pragma unroll
@@ -505,44 +852,55 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                         o[e] = none ? 0.f : __uint_as_float(t32[e]) * inv;
                     }
                     if (row_on && part) {
+                        float4 *op = reinterpret_cast<float4 *>(a.o_part + prow * D + c0);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            reinterpret_cast<float4 *>(op)[8 * q + e] =
-                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        for (int e = 0; e < 8; ++e) op[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     } else if (row_on) {
+                        uint4 *ob = reinterpret_cast<uint4 *>(a.out + row * D + c0);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            reinterpret_cast<uint4 *>(ob)[4 * q + e] =
-                                make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
-                                           pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+                            ob[e] = make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                                               pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
                     }
                 }
-                if (row_on) {
+                if (row_on && hf == 0) {
                     const float lse = none ? -INFINITY : (m_ref + log2f(l)) * kLn2;
-                    if (part) a.lse_part[(int64_t)split * all_rows + row] = lse;
+                    if (part) a.lse_part[prow] = lse;
                     else if (a.lse) a.lse[row] = lse;
                 }
                 // rows that something unseen may have reached (a NaN sum stays one whatever V holds)
                 uint32_t again = __ballot_sync(0xffffffffu, row_on && !finite && l > 0.f);
+                bool any = again != 0;
+                if constexpr (C::kHalves == 2) {
+                    any = pair_any(pair, any);
+                    if (any) {  // the first of the two does the rows
+                        if (hf) *xch = __uint_as_float(again);
+                        pair_any(pair, false);
+                        again = hf ? 0u : again | __float_as_uint(*xch);
+                    }
+                }
                 while (again) {
                     const int from = __ffs(again) - 1;
                     again &= again - 1;
                     const int n2 = __shfl_sync(0xffffffffu, node, from);
                     const int64_t row2 = __shfl_sync(0xffffffffu, (long long)row, from);
+                    const int64_t prow2 = __shfl_sync(0xffffffffu, (long long)prow, from);
                     const float m2 = __shfl_sync(0xffffffffu, m_ref, from), inv2 = __shfl_sync(0xffffffffu, inv, from);
                     float o[D / 32];
-                    row_again<D>(a, a.q + row2 * D, a.mask + m0 + (int64_t)n2 * W, kv0, c_begin, c_end, g, m2, o);
+                    row_again<D>(a, a.q + row2 * D, a.mask + sg.m0 + (int64_t)n2 * sg.W, sg.kv0, sg.c_begin, sg.c_end, sg.g,
+                                 m2, o);
 #pragma unroll
                     for (int e = 0; e < D / 32; ++e) {
                         const float x = o[e] * inv2;
                         if (part) {
-                            a.o_part[((int64_t)split * all_rows + row2) * D + lane * (D / 32) + e] = x;
+                            a.o_part[prow2 * D + lane * (D / 32) + e] = x;
                         } else {
                             const __nv_bfloat16 y = __float2bfloat16_rn(x);
                             a.out[row2 * D + lane * (D / 32) + e] = *reinterpret_cast<const uint16_t *>(&y);
                         }
                     }
                 }
+                tc_fence_before();  // the output has been read before the next segment's first product
             }
         }
     }
@@ -556,15 +914,17 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
     }
 }
 
-// out = sum_s e^{lse_s - LSE} o_s over the splits that the row's request has
-// (columns [s * split_cols, ...) below its length), LSE = log sum_s e^{lse_s}.
-// One warp per (token, head) row: lane s, s + 32, ... holds split s's weight,
-// then the lanes sum D / 32 values each.
+// out = sum_s e^{lse_s - LSE} o_s over the parts s of the row's item, LSE = log
+// sum_s e^{lse_s}.  One warp per (token, head) row: lane s holds part s's
+// weight, 32 parts at a time, then the lanes sum D / 32 values each.  Items that
+// one CTA did are in place already.
 constexpr int kCombineWarps = 8;
 
-template <int D>
-__global__ void __launch_bounds__(32 * kCombineWarps) gqa_combine_kernel(const GqaArgs a) {
+template <int D, int kTiles>
+__global__ void __launch_bounds__(32 * kCombineWarps) gqa_combine_kernel(const GqaParams prm) {
+    using C = Cfg<D, kTiles>;
     constexpr int E = D / 32;
+    const GqaArgs &a = prm.a;
     const int lane = threadIdx.x & 31;
     const int t = blockIdx.x, h = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
     pdl_wait();
@@ -572,73 +932,87 @@ __global__ void __launch_bounds__(32 * kCombineWarps) gqa_combine_kernel(const G
     if (h >= a.num_heads) return;
     const int b = find_request(a.qo_indptr, a.batch, t, lane);
     if (b >= a.batch) return;
-    const int qo0 = a.qo_indptr[b], T = a.qo_indptr[b + 1] - qo0;
-    const int kv0 = a.kv_indptr[b], N = a.kv_indptr[b + 1] - kv0;
-    const int m0 = a.mask_indptr[b], m1 = a.mask_indptr[b + 1];
-    // a request that the attention refused has no partial results
-    if (T < 1 || T > a.max_q_len || qo0 < 0 || qo0 + T > a.total_q || t - qo0 >= T || N < T || N > a.max_kv_len || kv0 < 0 ||
-        kv0 + N > a.total_kv || m0 < 0 || m1 - m0 != T * ((N + 31) >> 5) || m1 > a.total_mask_words)
-        return;
-    const int splits = min(a.num_splits, (N + a.split_cols - 1) / a.split_cols);
-    const int64_t rows = (int64_t)a.total_q * a.num_heads, row = (int64_t)t * a.num_heads + h;
-    constexpr int kL = DDT_MAX_SPLITS / 32;
-    float ls[kL], m = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kL; ++k) {
-        const int s = lane + 32 * k;
-        ls[k] = s < splits ? a.lse_part[(int64_t)s * rows + row] : -INFINITY;
-        m = fmaxf(m, ls[k]);
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float den = 0.f;
-#pragma unroll
-    for (int k = 0; k < kL; ++k) {
-        ls[k] = ls[k] == -INFINITY ? 0.f : ex2((ls[k] - m) * kLog2e);  // now the split's weight (NaN stays)
-        den += ls[k];
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-    float acc[E];
+    const Request r = load_request<C, kTiles>(a, prm.group, b, nullptr);
+    if (r.tgs == 0 || t - r.qo0 >= r.T) return;  // nothing to do, or refused
+    const int64_t total = a.plan[a.batch];
+    const int ctas = (int)a.plan[a.batch + 1];
+    const int g = h / prm.group, rr = (t - r.qo0) * prm.group + h - g * prm.group;  // row of the request
+    const int tg = rr / (kTiles * kRows);
+    const int64_t full = item_cost<C>(r, 0), cost = item_cost<C>(r, tg);
+    const int64_t pos = a.plan[b] + (int64_t)tg * full * a.num_kv_heads + g * cost;
+    const int unit = tg == r.tgs - 1 && r.last_one ? C::kCostOne : C::kCostFull;
+    // owners of the item's first and last block
+    const int c0 = share_owner(total, ctas, pos + C::kCostItem);
+    const int c1 = share_owner(total, ctas, pos + C::kCostItem + (int64_t)(r.blocks - 1) * unit);
+    if (c0 == c1) return;
+    const int prow = rr - tg * kTiles * kRows;
+    const int parts = c1 - c0 + 1;
+    float m = -INFINITY, den = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int s0 = 0; s0 < parts; s0 += 32) {
+        const int c = c0 + s0 + lane;
+        int64_t at = 0;
+        float ls = -INFINITY;
+        if (s0 + lane < parts) {
+            at = (int64_t)(2 * c + (share_start(total, ctas, c) > pos ? 0 : 1)) * prm.part_rows + prow;
+            ls = a.lse_part[at];
+        }
+        float mg = fmaxf(m, ls);
 #pragma unroll
-    for (int k = 0; k < kL; ++k) {
-        const int left = min(32, splits - 32 * k);
+        for (int o = 16; o >= 1; o >>= 1) mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, o));
+        const float keep = m == -INFINITY ? 0.f : ex2((m - mg) * kLog2e);
+        const float w = ls == -INFINITY ? 0.f : ex2((ls - mg) * kLog2e);  // NaN stays
+        float sum = w;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        den = den * keep + sum;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= keep;
+        m = mg;
+        const int n = min(32, parts - s0);
 #pragma unroll 4
-        for (int s = 0; s < left; ++s) {
-            const float wgt = __shfl_sync(0xffffffffu, ls[k], s);
-            const float *o = a.o_part + ((int64_t)(32 * k + s) * rows + row) * D + lane * E;
-            float v[E];
+        for (int s = 0; s < n; ++s) {
+            const float ws = __shfl_sync(0xffffffffu, w, s);
+            const float *o = a.o_part + __shfl_sync(0xffffffffu, (long long)at, s) * D + lane * E;
             if constexpr (E == 4) {
                 const float4 x = *reinterpret_cast<const float4 *>(o);
-                v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+                acc[0] = fmaf(ws, x.x, acc[0]);
+                acc[1] = fmaf(ws, x.y, acc[1]);
+                acc[2] = fmaf(ws, x.z, acc[2]);
+                acc[3] = fmaf(ws, x.w, acc[3]);
             } else {
                 const float2 x = *reinterpret_cast<const float2 *>(o);
-                v[0] = x.x; v[1] = x.y;
+                acc[0] = fmaf(ws, x.x, acc[0]);
+                acc[1] = fmaf(ws, x.y, acc[1]);
             }
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(wgt, v[e], acc[e]);
         }
     }
+    const int64_t row = (int64_t)t * a.num_heads + h;
     const float inv = den == 0.f ? 0.f : 1.f / den;
-    uint32_t w[E / 2];
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e) w[e] = pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv);
     uint16_t *dst = a.out + row * D + lane * E;
-    if constexpr (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint32_t *>(dst) = w[0];
+    if constexpr (E == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+    else
+        *reinterpret_cast<uint32_t *>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
     if (a.lse && lane == 0) a.lse[row] = den == 0.f ? -INFINITY : m + log2f(den) * kLn2;
 }
 
-int tiles_per_cta(int max_q_len, int group) { return max_q_len * group > kRows ? 2 : 1; }
+int tiles_per_item(int max_q_len, int group) { return max_q_len * group > kRows ? 2 : 1; }
 
 template <int D, int kTiles>
-cudaError_t launch_partial(const GqaParams &prm, cudaStream_t s) {
-    const GqaArgs &a = prm.a;
+cudaError_t launch(GqaParams &prm, cudaStream_t s) {
+    using C = Cfg<D, kTiles>;
+    GqaArgs &a = prm.a;
     const int groups = (a.max_q_len * prm.group + kTiles * kRows - 1) / (kTiles * kRows);
-    const dim3 grid((unsigned)(groups * a.num_kv_heads), (unsigned)a.num_splits, (unsigned)a.batch);
-    return launch_pdl(gqa_attn_kernel<D, kTiles>, grid, dim3(Cfg<D, kTiles>::kThreads), Cfg<D, kTiles>::kSmemBytes, s, prm);
+    const dim3 grid = a.num_ctas > 0 ? dim3((unsigned)a.num_ctas)
+                                     : dim3((unsigned)(groups * a.num_kv_heads), 1, (unsigned)a.batch);
+    cudaError_t e = launch_pdl(gqa_attn_kernel<D, kTiles>, grid, dim3(C::kThreads), C::kSmemBytes, s, prm);
+    if (e == cudaSuccess && a.num_ctas > 0) {
+        const dim3 rows((unsigned)a.total_q, (unsigned)((a.num_heads + kCombineWarps - 1) / kCombineWarps));
+        e = launch_pdl(gqa_combine_kernel<D, kTiles>, rows, dim3(32 * kCombineWarps), 0, s, prm);
+    }
+    return e;
 }
 
 template <int D, int kTiles>
@@ -660,41 +1034,27 @@ cudaError_t gqa_prepare_device() {
     return e;
 }
 
-int gqa_choose_splits(int batch, int num_heads, int num_kv_heads, int max_q_len, int max_kv_len, int num_sms,
-                      int max_splits) {
-    const int group = num_heads / num_kv_heads;
-    const int tiles = tiles_per_cta(max_q_len, group);
-    const long long ctas = (long long)batch * num_kv_heads * ((max_q_len * group + tiles * kRows - 1) / (tiles * kRows));
-    const long long slots = (long long)num_sms * (tiles == 2 ? 1 : 2);
-    const long long units = ((long long)max_kv_len + kSplitUnit - 1) / kSplitUnit;
-    long long want = (2 * slots + ctas - 1) / ctas;
-    if (want > (units + 1) / 2) want = (units + 1) / 2;
-    if (want > max_splits) want = max_splits;
-    return want < 1 ? 1 : (int)want;
+int gqa_choose_ctas(int batch, int num_heads, int num_kv_heads, int max_q_len, int max_kv_len, int num_sms) {
+    const int tiles = tiles_per_item(max_q_len, num_heads / num_kv_heads);
+    if (batch > kGqaMaxDealtBatch) return 0;
+    if (max_kv_len <= 256) return 0;
+    const int slots = num_sms * (tiles == 2 ? 1 : 2);
+    return slots < DDT_GQA_MAX_CTAS ? slots : DDT_GQA_MAX_CTAS;
 }
 
-void gqa_split_layout(int max_kv_len, int requested, int *split_cols, int *splits) {
-    const int64_t want = requested < 1 ? 1 : requested;
-    int64_t cols = (max_kv_len + want - 1) / want;
-    cols = (cols + kSplitUnit - 1) / kSplitUnit * kSplitUnit;
-    *splits = (int)((max_kv_len + cols - 1) / cols);
-    *split_cols = *splits <= 1 ? max_kv_len : (int)cols;
-    if (*splits < 1) *splits = 1;
+int gqa_part_rows(int max_q_len, int group) {
+    const int rows = max_q_len * group, most = tiles_per_item(max_q_len, group) * kRows;
+    return rows < most ? rows : most;
 }
 
 cudaError_t launch_gqa_attn(const GqaArgs &a, cudaStream_t s) {
     GqaParams prm;
     prm.a = a;
     prm.group = a.num_heads / a.num_kv_heads;
-    const int tiles = tiles_per_cta(a.max_q_len, prm.group);
-    cudaError_t e = a.head_dim == 128 ? (tiles == 2 ? launch_partial<128, 2>(prm, s) : launch_partial<128, 1>(prm, s))
-                                      : (tiles == 2 ? launch_partial<64, 2>(prm, s) : launch_partial<64, 1>(prm, s));
-    if (e == cudaSuccess && a.num_splits > 1) {
-        const dim3 grid((unsigned)a.total_q, (unsigned)((a.num_heads + kCombineWarps - 1) / kCombineWarps));
-        e = a.head_dim == 128 ? launch_pdl(gqa_combine_kernel<128>, grid, dim3(32 * kCombineWarps), 0, s, a)
-                              : launch_pdl(gqa_combine_kernel<64>, grid, dim3(32 * kCombineWarps), 0, s, a);
-    }
-    return e;
+    prm.part_rows = gqa_part_rows(a.max_q_len, prm.group);
+    const bool two = tiles_per_item(a.max_q_len, prm.group) == 2;
+    if (a.head_dim == 128) return two ? launch<128, 2>(prm, s) : launch<128, 1>(prm, s);
+    return two ? launch<64, 2>(prm, s) : launch<64, 1>(prm, s);
 }
 
 }  // namespace ddt

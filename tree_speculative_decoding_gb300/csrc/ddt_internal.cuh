@@ -183,23 +183,26 @@ struct GqaArgs {
     int max_q_len;
     int max_kv_len;
     float scale;
-    int num_splits;
-    int split_cols;   // kv columns per split (a multiple of the kv block)
+    // CTAs that the blocks of columns are dealt to (batch <= kGqaMaxDealtBatch),
+    // or 0: one CTA per item, no workspace
+    int num_ctas;
+    int forced;       // the caller gave the count: a CTA may get a single block
     uint16_t *out;    // [total_q, H, D] bf16
     float *lse;       // [total_q, H] or null
-    float *o_part;    // [splits, total_q*H, D] when num_splits > 1
-    float *lse_part;  // [splits, total_q*H]
+    // dealt: where each request's items start on the line, its length, the CTAs that took a share
+    int64_t *plan;    // [batch + 2]
+    float *o_part;    // [2 * num_ctas, gqa_part_rows(), D]
+    float *lse_part;  // [2 * num_ctas, gqa_part_rows()]
     unsigned int *err;
 };
+constexpr int kGqaMaxDealtBatch = 256;  // a thread per request sizes the line
 // kernel attributes, once per device (see attn_prepare_device)
 cudaError_t gqa_prepare_device();
 cudaError_t launch_gqa_attn(const GqaArgs &a, cudaStream_t s);
-// the split count for these bounds, at most max_splits (>= 1)
-int gqa_choose_splits(int batch, int num_heads, int num_kv_heads, int max_q_len, int max_kv_len, int num_sms,
-                      int max_splits);
-// kv columns per split of a requested count (>= 1), in whole kv blocks, and the
-// splits that then cover max_kv_len
-void gqa_split_layout(int max_kv_len, int requested, int *split_cols, int *splits);
+// the CTAs that the work is dealt to for these bounds, or 0 (see GqaArgs)
+int gqa_choose_ctas(int batch, int num_heads, int num_kv_heads, int max_q_len, int max_kv_len, int num_sms);
+// rows of a partial result
+int gqa_part_rows(int max_q_len, int group);
 
 cudaError_t launch_cache_copy(const void *src_slab, int64_t src_pool_bytes, int64_t src_rows, void *dst_slab,
                               int64_t dst_pool_bytes, int64_t dst_rows, int num_pools, int64_t row_bytes,

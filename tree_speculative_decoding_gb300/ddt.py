@@ -57,8 +57,8 @@ def _load():
                                i32),
         "ddt_gqa_norm_rope_append": ([P, i64, P, i64, P, i64, P, P, f32, P, i64, i32, i32, P, P, P, P,
                                       i32, i32, i32, i32, i32, i32, P, P, P, i64, i64, P], i32),
-        "ddt_gqa_verify_attn_num_splits": ([i32, i32, i32, i32, i32, i32], i32),
-        "ddt_gqa_verify_attn_workspace_size": ([i32, i32, i32, i32], sz),
+        "ddt_gqa_verify_attn_num_ctas": ([i32, i32, i32, i32, i32, i32], i32),
+        "ddt_gqa_verify_attn_workspace_size": ([i32, i32, i32, i32, i32, i32], sz),
         "ddt_gqa_verify_attn": ([P, P, P, i64, i64, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32,
                                  i32, i32, f32, i32, P, P, P, sz, P], i32),
         "ddt_cache_copy": ([P, i64, i64, P, i64, i64, i32, i64, P, P, i32, P], i32),
@@ -508,24 +508,24 @@ def ddt_gqa_norm_rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, depth, q
         _like(q_out, bf16, dev, "q_out"), kpp, vpp, stride, rows, _raw_stream(stream, dev)))
 
 
-def ddt_gqa_verify_attn_num_splits(batch, num_heads, num_kv_heads, max_q_len, max_kv_len, num_sms=0):
-    return lib.ddt_gqa_verify_attn_num_splits(batch, num_heads, num_kv_heads, max_q_len, max_kv_len, num_sms)
+def ddt_gqa_verify_attn_num_ctas(batch, num_heads, num_kv_heads, max_q_len, max_kv_len, num_sms=0):
+    return lib.ddt_gqa_verify_attn_num_ctas(batch, num_heads, num_kv_heads, max_q_len, max_kv_len, num_sms)
 
 
-def ddt_gqa_verify_attn_workspace_size(total_q, num_heads, head_dim, num_splits):
-    return lib.ddt_gqa_verify_attn_workspace_size(total_q, num_heads, head_dim, num_splits)
+def ddt_gqa_verify_attn_workspace_size(batch, num_heads, num_kv_heads, head_dim, max_q_len, num_ctas):
+    return lib.ddt_gqa_verify_attn_workspace_size(batch, num_heads, num_kv_heads, head_dim, max_q_len, num_ctas)
 
 
 def ddt_gqa_verify_attn(q, k_pool, v_pool, kv_indices, kv_indptr, qo_indptr, mask, mask_indptr, scale,
-                        out, lse=None, max_q_len=None, max_kv_len=None, num_splits=0, workspace=None,
+                        out, lse=None, max_q_len=None, max_kv_len=None, num_ctas=0, workspace=None,
                         stream=None):
     """Tree-verify attention over grouped-query rows.  q, out: [total_q, H, D] bf16; k_pool, v_pool:
     [pool_rows, G, D] bf16 (rows may be apart: slices of one [pool_rows, 2, G, D] pool will do);
     lse: float32 [total_q, H] or None.
 
     max_q_len / max_kv_len are host-side bounds; when omitted they are read from the indptrs (a
-    device->host copy).  With num_splits = 0 the split count is chosen among those that fit
-    `workspace`; without one, the chosen count's workspace is allocated here."""
+    device->host copy).  num_ctas: the CTAs that the cached columns are dealt to (0 = choose, within
+    what `workspace` holds); without a workspace, the count's workspace is allocated here."""
     dev = _on_device(q, "q")
     qp, qs, total_q, H, D = _heads(q, dev, "q")
     kp, vp, stride, rows, G, Dp = _pools(k_pool, v_pool, dev)
@@ -546,11 +546,10 @@ def ddt_gqa_verify_attn(q, k_pool, v_pool, kv_indices, kv_indptr, qo_indptr, mas
         max_q_len = int((qo_indptr[1:] - qo_indptr[:-1]).max())
         max_kv_len = int((kv_indptr[1:] - kv_indptr[:-1]).max())
     if workspace is None:
-        splits = num_splits or lib.ddt_gqa_verify_attn_num_splits(B, H, G, max_q_len, max_kv_len, 0)
-        nbytes = lib.ddt_gqa_verify_attn_workspace_size(total_q, H, D, splits)
+        ctas = num_ctas or lib.ddt_gqa_verify_attn_num_ctas(B, H, G, max_q_len, max_kv_len, 0)
+        nbytes = lib.ddt_gqa_verify_attn_workspace_size(B, H, G, D, max_q_len, ctas)
         if nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        num_splits = splits
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(),
@@ -560,7 +559,7 @@ def ddt_gqa_verify_attn(q, k_pool, v_pool, kv_indices, kv_indptr, qo_indptr, mas
         qp, kp, vp, stride, rows, _like(kv_indices, i32, dev, "kv_indices"),
         _like(kv_indptr, i32, dev, "kv_indptr"), _like(qo_indptr, i32, dev, "qo_indptr"),
         _mask_ptr(mask, dev), _like(mask_indptr, i32, dev, "mask_indptr"), B, H, G, D, total_q,
-        kv_indices.numel(), mask.numel(), max_q_len, max_kv_len, scale, num_splits,
+        kv_indices.numel(), mask.numel(), max_q_len, max_kv_len, scale, num_ctas,
         _like(out, bf16, dev, "out"), None if lse is None else _like(lse, torch.float32, dev, "lse"),
         ws, ws_bytes, _raw_stream(stream, dev)))
 
