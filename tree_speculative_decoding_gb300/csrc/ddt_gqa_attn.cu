@@ -5,7 +5,7 @@
 // columns j that mask row i makes visible:
 //   s_j = scale <q[i,h], k[idx_j][g]>,  out[i,h] = sum_j softmax(s)_j v[idx_j][g],
 //   lse = log sum_j e^{s_j}
-// in one pass over the columns with a running maximum and sum.
+// in one pass over the columns with a running reference and sum.
 //
 // Work.  An item is one K/V head of one request and up to kTiles tiles of 128
 // consecutive rows (node-major, the group's heads inside a node: the rows that
@@ -32,12 +32,17 @@
 // runs.  P (bf16) overwrites the scores in place and is the A operand of PV
 // from tensor memory; V is read as an MN-major operand from its gathered rows.
 //
-// Warps: softmax warps of 32 rows x 64 columns (thread = row = TMEM lane; with
-// blocks of 128 columns two of them share a row, and PV starts on the half that
-// is ready), one warp that issues MMAs, and load warps that copy row pieces with
-// 16-byte cp.async into the 128-byte-swizzled layout of the MMA descriptors.
-// (A TMA row gather costs its warp ~57 clk for 512 bytes and measured half the
-// rate.)
+// Warps: four softmax warps per tile (thread = row = TMEM lane), one warp that
+// issues MMAs, and load warps that copy row pieces with 16-byte cp.async into the
+// 128-byte-swizzled layout of the MMA descriptors.  (A TMA row gather costs its
+// warp ~57 clk for 512 bytes and measured half the rate.)
+//
+// The softmax does not look for a block's maximum: the weights of 64 columns are
+// taken against the row's reference, the maximum of the first columns it saw.
+// Only where their sum passes 2^40 (or the row had seen nothing) the maximum is
+// found, the reference moves, and the sums so far are scaled.  fp32 sums stay
+// finite for |v| below ~2^67 at a million columns, and bf16 weights keep their
+// relative precision at any scale.
 //
 // Columns that a row does not see get p = 0, but 0 * NaN is NaN: a V row that
 // holds NaN or infinities reaches the output rows that do not see it.  A row
@@ -65,11 +70,7 @@ using namespace sm100;
 
 constexpr int kRows = 128;  // rows per tile (TMEM lanes)
 constexpr uint32_t kWaitLimit = 1u << 22;
-// Lazy rescale: the running maximum (log2 units) moves only when a block's
-// exceeds it by more than this, so p <= 2^48; the fp32 sums stay finite for
-// |v| below ~2^59 at a million columns, and bf16 weights keep their relative
-// precision at any scale.
-constexpr float kRescaleLog2 = 48.0f;
+constexpr float kSumLimit = 1099511627776.0f;  // 2^40: weights of 64 columns that sum to more move the reference
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -82,7 +83,7 @@ struct GqaParams {
 template <int D, int kTiles>
 struct Cfg {
     static constexpr int NB = kTiles == 2 ? 128 : 64;    // columns per block
-    static constexpr int kHalves = NB / 64;              // softmax warps that share a row
+    static constexpr int kHalves = NB / 64;              // parts of P that PV may start on
     static constexpr int kBoxes = D / 64;                // 128-byte pieces of a row
     static constexpr int kBoxBytes = NB * 128;           // one piece of a block's rows
     static constexpr int kBlockBytes = kBoxes * kBoxBytes;
@@ -91,7 +92,7 @@ struct Cfg {
     static constexpr int kKStages = D == 128 ? (kTiles == 2 ? 3 : 2) : 4;
     static constexpr int kVStages = D == 128 ? 2 : 4;
     static constexpr int kUnits = NB / 32;               // 32-row units of a block
-    static constexpr int kSoftWarps = 4 * kTiles * kHalves;
+    static constexpr int kSoftWarps = 4 * kTiles;
     static constexpr int kLoadWarps = 4 * kTiles - 1;    // with the MMA warp: whole warpgroups
     static constexpr int kThreads = 32 * (kSoftWarps + kLoadWarps + 1);
     static constexpr uint32_t kTmemCols = kTiles == 2 ? 512 : 256;
@@ -103,24 +104,22 @@ struct Cfg {
     // barriers
     static constexpr int bKFull = 0, bKEmpty = bKFull + kKStages, bVFull = bKEmpty + kKStages,
                          bVEmpty = bVFull + kVStages, bSFull = bVEmpty + kVStages, bPFull = bSFull + 2,
-                         bQFull = bPFull + 2 * kHalves, bODone = bQFull + 1, bOFin = bODone + 1, bDrain = bOFin + 1,
+                         bQFull = bPFull + 2 * kHalves, bHalf = bQFull + 1, bODone = bHalf + 2, bOFin = bODone + 1, bDrain = bOFin + 1,
                          bSegFull = bDrain + 1, bSegEmpty = bSegFull + 2, bCount = bSegEmpty + 2;
     static constexpr int kOffHolder = kOffBar + 8 * bCount;
     static constexpr int kOffWalk = kOffHolder + 8;  // 128 bytes: the walk; 2 x 48: the segments it has given
     static constexpr int kOffPlan = kOffWalk + 128 + 2 * 48;  // a sum per warp, then where the CTA's share starts
-    // what the two warps of a row tell each other: [kTiles][128] floats
-    static constexpr int kOffXch = kOffPlan + 8 * (kThreads / 32);
-    static constexpr int kSmemUsed = kOffXch + (kHalves == 2 ? kTiles * kRows * 4 : 0);
+    static constexpr int kSmemUsed = kOffPlan + 8 * (kThreads / 32);
     static constexpr int kSmemBytes = kSmemUsed + 1024;  // slack for the 1024-byte alignment of swizzle atoms
     static constexpr uint32_t kIdescS = idesc_bf16(kRows, NB, 0, 0);
     static constexpr uint32_t kIdescPV = idesc_bf16(kRows, D, 0, 1);
     // cost of a block with all tiles and with one, and of an item besides its blocks
-    // (its q, the latency of its first loads, its epilogue), in one unit; blocks
+    // (its q, the latency of its first loads, its epilogue), in one unit; the share
     // that a CTA gets at least
     static constexpr int kCostFull = kTiles == 2 ? 16 : 8, kCostOne = kTiles == 2 ? 10 : 8, kCostItem = 24;
-    static constexpr int kMinBlocks = kTiles == 2 ? 2 : 4;
+    static constexpr int kMinShare = kTiles == 2 ? 32 : 24;
     static_assert(kTiles == 2 ? kLoadWarps > kUnits : kKStages >= 2 && kVStages >= 2 && kKStages <= kVStages, "see the load warps");
-    static_assert(kOffPlan % 8 == 0 && kOffXch % 4 == 0, "alignment");
+    static_assert(kOffPlan % 8 == 0, "alignment");
     static_assert(kColO + kTiles * D <= kTmemCols, "tensor memory");
     static_assert(kSmemBytes <= (kTiles == 2 ? 232448 : 115712), "shared memory");
 };
@@ -231,7 +230,7 @@ template <class C>
 __device__ __forceinline__ int blocks_before(int64_t item, int64_t x, int unit, int blocks) {
     const int64_t d = x - (item + C::kCostItem);
     if (d <= 0) return 0;
-    const int64_t k = (d + unit - 1) / unit;
+    const int64_t k = unit == C::kCostFull ? (d + C::kCostFull - 1) / C::kCostFull : (d + C::kCostOne - 1) / C::kCostOne;
     return k < blocks ? (int)k : blocks;
 }
 
@@ -326,17 +325,6 @@ struct Walk {
     }
 };
 
-// a barrier of the two warps that share a row; true when any of their threads says so
-__device__ __forceinline__ bool pair_any(int id, bool x) {
-    uint32_t any;
-    asm volatile(
-        "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, %2, 64, p; selp.u32 %0, 1, 0, q; }"
-        : "=r"(any)
-        : "r"((uint32_t)x), "r"(id)
-        : "memory");
-    return any != 0;
-}
-
 template <int D, int kTiles>
 __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, kTiles == 2 ? 1 : 2)
 gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
@@ -393,7 +381,7 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
             total += plan[w];
         }
         // CTAs that take a share: as many as get a few blocks at least
-        const int64_t most = total / (C::kCostItem + (a.forced ? 1 : C::kMinBlocks) * C::kCostFull);
+        const int64_t most = total / (a.forced ? C::kCostFull : C::kMinShare);
         const int ctas = most < 1 ? 1 : most < a.num_ctas ? (int)most : a.num_ctas;
         if (blockIdx.x == 0) {  // for the combine
             if (tid < a.batch) a.plan[tid] = at;
@@ -448,9 +436,9 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
     };
     Segment sg;
 
-    // Registers of the two-tile kernel: 768 threads x 80 at launch = 512 x 96 (softmax) + 256 x 48.
+    // Registers of the two-tile kernel: 512 threads x 128 at launch = 256 x 184 (softmax) + 256 x 72.
     if (warp >= kMmaWarp) {
-        if constexpr (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");  // one instruction for the warpgroup
+        if constexpr (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");  // one instruction for the warpgroup
         if (warp >= kFirstLoad) {
             // ================= gather =================
             // A unit is 32 rows of a block of K or V.  Two-tile kernel: four warps take
@@ -593,6 +581,7 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
 #pragma unroll
                             for (int i = 4 * h; i < 4 * h + 4; ++i)
                                 mma_ts(d, p + 8 * i, vd + i * (2048 >> 4), C::kIdescPV, i > 0 ? 1u : later);
+                            if (h + 1 < C::kHalves) mma_commit(bar(C::bHalf + slot));
                         }
                         pph[slot] ^= 1;
                         if (A == 1) mma_commit(bar(C::bODone));
@@ -639,181 +628,152 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
         }
     } else {
         // ================= softmax (thread = row = TMEM lane of its tile) =================
-        if constexpr (kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
-        const int t = warp / (4 * C::kHalves), hf = C::kHalves == 2 ? (warp >> 2) & 1 : 0, wq = warp & 3;
+        if constexpr (kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        const int t = warp >> 2, wq = warp & 3;
         const int r = 32 * wq + lane;  // row within the tile
         const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
-        const int pair = 1 + 4 * t + wq;  // barrier of the row's two warps
-        volatile float *xch = reinterpret_cast<float *>(smem + C::kOffXch) + t * kRows + r;
-        // a value that both warps of a row hold afterwards: the second warp hands its own over, the first joins them
-        auto join = [&](float x, auto op) {
-            if (hf) *xch = x;
-            pair_any(pair, false);
-            if (!hf) *xch = op(x, *xch);
-            pair_any(pair, false);
-            return *xch;
-        };
         const float sc = a.scale * kLog2e;
-        uint32_t sph[2] = {0, 0}, odone = 0;
+        uint32_t sph[2] = {0, 0}, odone = 0;  // phases of the slots; one-tile blocks so far
         bool ok = true;
-        // A wait that runs out in one warp of a pair takes both out at the next of their
-        // barriers: neither may be left waiting for the other.
-        auto failed = [&]() {
-            if constexpr (C::kHalves == 2) return pair_any(pair, !ok);
-            else return !ok;
-        };
-        for (int seg = 0;; ++seg) {
-            ok = ok && warp_segment(seg, sg);
-            if (failed() || sg.blocks == 0) break;
+        for (int seg = 0; ok; ++seg) {
+            ok = warp_segment(seg, sg);
+            if (!ok || sg.blocks == 0) break;
             const int rows_t = sg.rows - t * kRows;  // rows of this warp's tile
             const int tiles = sg.tiles;
-            // ---- q rows of the tile into the swizzled operand layout (the row's two warps take half each) ----
+            // ---- q rows of this warp into the swizzled operand layout ----
             if (32 * wq < rows_t) {
                 constexpr int kChunks = D / 8, kPer = 32 / kChunks;  // 16-byte pieces of a row; rows per step
                 const int c = lane % kChunks, sub = lane / kChunks;
-                const uint32_t qb = sbase + C::kOffQ + t * C::kQBytes;
-                constexpr int kSteps = 32 / kPer / C::kHalves;
+                const uint32_t qb = sbase + C::kOffQ + t * C::kQBytes + (c >> 3) * C::kQBoxBytes;
+                const uint16_t *q = a.q + ((int64_t)sg.qo0 * a.num_heads + sg.g * prm.group) * D + c * 8;
 #pragma unroll 4
-                for (int i = hf * kSteps; i < (hf + 1) * kSteps; ++i) {
+                for (int i = 0; i < 32 / kPer; ++i) {
                     const int rt = 32 * wq + i * kPer + sub;
                     if (rt < rows_t) {
                         const int rr = sg.row0 + t * kRows + rt;
                         const int node = rr / prm.group, hg = rr - node * prm.group;
-                        const uint4 v = reinterpret_cast<const uint4 *>(
-                            a.q + ((int64_t)(sg.qo0 + node) * a.num_heads + sg.g * prm.group + hg) * D)[c];
-                        const uint32_t at = qb + (c >> 3) * C::kQBoxBytes + (rt >> 3) * 1024 + (rt & 7) * 128 +
-                                            (((c & 7) ^ (rt & 7)) << 4);
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z),
-                                     "r"(v.w)
-                                     : "memory");
+                        cp_async_16(qb + (rt >> 3) * 1024 + (rt & 7) * 128 + (((c & 7) ^ (rt & 7)) << 4),
+                                    q + ((int64_t)node * a.num_heads + hg) * D);
                     }
                 }
+                asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_proxy_async_smem();
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::bQFull));
-            const bool mine = t < tiles;             // the segment has this tile
-            const bool warp_on = 32 * wq < rows_t;   // ... and rows of this warp (mine is implied)
+            const bool mine = t < tiles;            // the segment has this tile
+            const bool warp_on = 32 * wq < rows_t;  // ... and rows of this warp
             const bool row_on = r < rows_t;
             const int rr = sg.row0 + (row_on ? t * kRows + r : 0);
             const int node = rr / prm.group;
             const uint32_t *words = a.mask + sg.m0 + (int64_t)node * sg.W;
-            float m_ref = -INFINITY, l = 0.f;
-            // the two mask words of this warp's 64 columns of block j
-            auto mask_words = [&](int j, uint32_t (&mw)[2]) {
+            float m_ref = -INFINITY, l = 0.f;  // the reference in log2 units, the sum against it
+            constexpr int kW = NB / 32;
+            auto mask_words = [&](int j, uint32_t (&mw)[kW]) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int c0 = sg.c_begin + j * NB + 64 * hf + 32 * k;
+                for (int k = 0; k < kW; ++k) {
+                    const int c0 = sg.c_begin + j * NB + 32 * k;
                     uint32_t x = c0 < sg.c_end ? words[c0 >> 5] : 0u;
                     if (c0 < sg.c_end && sg.c_end - c0 < 32) x &= (1u << (sg.c_end - c0)) - 1u;
                     mw[k] = x;
                 }
             };
-            uint32_t mnext[2] = {0, 0};
+            uint32_t mnext[kW];
             if (warp_on) mask_words(0, mnext);
             for (int j = 0; mine && j < sg.blocks; ++j) {
                 const int slot = tiles == 2 ? t : j & 1;
                 const uint32_t col = tmem + lane_off + C::kColS + NB * slot;
-                uint32_t mw[2] = {mnext[0], mnext[1]};
-                if (warp_on && j + 1 < sg.blocks) mask_words(j + 1, mnext);
+                uint32_t mw[kW];
+                if (warp_on) {
+#pragma unroll
+                    for (int k = 0; k < kW; ++k) mw[k] = mnext[k];
+                    if (j + 1 < sg.blocks) mask_words(j + 1, mnext);
+                }
                 ok = warp_wait(bar(C::bSFull + slot), sph[slot], abort_flag, a.err);
-                sph[slot] ^= 1;
-                if (!ok && !(warp_on && C::kHalves == 2)) break;  // a pair leaves together, below
+                if (!ok) break;
                 if (warp_on) {
                     tc_fence_after();
-                    // The weights are taken against the maximum so far while the block's own is
-                    // being found: it moves the reference only when it is more than 2^48 above,
-                    // and the weights are then taken again.
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    float2 acc = make_float2(0.f, 0.f);
-                    uint32_t pw[32];  // the weights as bf16 pairs
                     const float2 scv = make_float2(sc, sc);
-                    auto pass = [&](float m, bool find) {
-                        const float2 nmv = make_float2(-m, -m);
+                    uint32_t s[kW][32];  // the block's scores of the row
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            uint32_t t32[32];
-                            tmem_ld32(col + 64 * hf + 32 * k, t32);
-                            tmem_wait_ld();
-                            float sv[32];  // scores, unseen columns at -inf
+                    for (int k = 0; k < kW; ++k) tmem_ld32(col + 32 * k, s[k]);
+                    tmem_wait_ld();
+                    // unseen columns at -inf; a branch, not selects: most blocks are seen whole
+                    uint32_t all = mw[0];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) sv[e] = __uint_as_float(t32[e]);
-                            if (mw[k] != 0xffffffffu) {
+                    for (int k = 1; k < kW; ++k) all &= mw[k];
+                    if (!__all_sync(0xffffffffu, all == 0xffffffffu)) {
+                        asm volatile("");
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) sv[e] = ((mw[k] >> e) & 1u) ? sv[e] : -INFINITY;
-                            }
-                            if (find) {
-#pragma unroll
-                                for (int e = 0; e < 32; e += 2)
-                                    mx[(e >> 1) & 3] = fmaxf(fmaxf(mx[(e >> 1) & 3], sv[e]), sv[e + 1]);
-                            }
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                const float2 x = f2fma(make_float2(sv[e], sv[e + 1]), scv, nmv);
-                                const float p0 = ex2(x.x), p1 = ex2(x.y);
-                                acc = f2add(acc, make_float2(p0, p1));
-                                pw[16 * k + e / 2] = pack_bf16(p0, p1);
-                            }
-                        }
-                    };
-                    auto reference = [&]() { return m_ref == -INFINITY ? 0.f : m_ref; };  // nothing seen: every p is 0
-                    if (ok) pass(reference(), true);
-                    float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-                    bool moves = row_on && mb > m_ref + kRescaleLog2;  // also the first visible block (m_ref = -inf)
-                    bool any;
-                    if constexpr (C::kHalves == 2) {
-                        // the pair has read its scores before either half of P goes over them
-                        tc_fence_before();
-                        any = pair_any(pair, moves || !ok);
-                        if (any && failed()) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                    } else {
-                        any = __any_sync(0xffffffffu, moves);
+                        for (int k = 0; k < NB; ++k) s[k >> 5][k & 31] = ((mw[k >> 5] >> (k & 31)) & 1u) ? s[k >> 5][k & 31] : 0xff800000u;
                     }
-                    if (any) {
-                        if constexpr (C::kHalves == 2) {
-                            mb = join(mb, [](float x, float y) { return fmaxf(x, y); });
-                            moves = row_on && mb > m_ref + kRescaleLog2;
-                        }
-                        const float alpha = moves ? ex2(m_ref - mb) : 1.0f;
-                        l *= alpha;
-                        if (moves) m_ref = mb;
-                        acc = make_float2(0.f, 0.f);
-                        pass(reference(), false);
-                        // The output so far shrinks before PV(w).  With two tiles S(w) was issued behind
-                        // this tile's last PV, so that is done; with one it has to be waited for.
-                        if (j > 0) {
-                            if (tiles == 1) ok = warp_wait(bar(C::bODone), (odone + j - 1) & 1, abort_flag, a.err);
-                            tc_fence_after();
-                            const uint32_t oc = tmem + lane_off + C::kColO + D * t + hf * (D / C::kHalves);
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h) {
+                        float2 acc;
+                        while (true) {
+                            const float m = m_ref == -INFINITY ? 0.f : m_ref;  // nothing seen: every weight is 0
+                            const float2 nmv = make_float2(-m, -m);
+                            acc = make_float2(0.f, 0.f);
+#pragma unroll
+                            for (int k = 2 * h; k < 2 * h + 2; ++k) {
+                                uint32_t pw[16];  // the weights of 32 columns as bf16 pairs
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2) {
+                                    const float2 x = f2fma(make_float2(__uint_as_float(s[k][e]), __uint_as_float(s[k][e + 1])), scv, nmv);
+                                    const float p0 = ex2(x.x), p1 = ex2(x.y);
+                                    acc = f2add(acc, make_float2(p0, p1));
+                                    pw[e / 2] = pack_bf16(p0, p1);
+                                }
+                                tmem_st16(col + 16 * k, pw);  // over scores that have been read
+                            }
+                            const bool moves = row_on && (acc.x + acc.y > kSumLimit || (m_ref == -INFINITY && (mw[2 * h] | mw[2 * h + 1])));
+                            if (!__any_sync(0xffffffffu, moves)) break;
+                            // The reference moves to the largest of these scores, and what was summed
+                            // against the old one shrinks; then the weights are taken again.
+                            float mx = -INFINITY;
+#pragma unroll
+                            for (int e = 0; e < 64; ++e) mx = fmaxf(mx, __uint_as_float(s[2 * h + e / 32][e & 31]));
+                            mx *= sc;
+                            const bool up = moves && mx > m_ref;
+                            const float alpha = up ? ex2(m_ref - mx) : 1.0f;
+                            if (up) m_ref = mx;
+                            l *= alpha;
+                            // The products so far have to be done before the output is scaled: of this
+                            // block's first half; or of the last block (with two tiles S(w) was issued
+                            // behind it, so it is done).
+                            if (h > 0) ok = warp_wait(bar(C::bHalf + slot), sph[slot], abort_flag, a.err);
+                            else if (j > 0 && tiles == 1) ok = warp_wait(bar(C::bODone), (odone + j - 1) & 1, abort_flag, a.err);
+                            if (ok && (h > 0 || j > 0)) {
+                                tc_fence_after();
+                                const uint32_t oc = tmem + lane_off + C::kColO + D * t;
 #pragma unroll 1
-                            for (int q = 0; ok && q < D / C::kHalves / 32; ++q) {
-                                uint32_t t32[32];
-                                tmem_ld32(oc + 32 * q, t32);
-                                tmem_wait_ld();
+                                for (int q = 0; q < D / 8; ++q) {
+                                    uint32_t o8[8];
+                                    tmem_ld8(oc + 8 * q, o8);
+                                    tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) t32[e] = __float_as_uint(__uint_as_float(t32[e]) * alpha);
-                                tmem_st32(oc + 32 * q, t32);
+                                    for (int e = 0; e < 8; ++e) o8[e] = __float_as_uint(__uint_as_float(o8[e]) * alpha);
+                                    tmem_st8(oc + 8 * q, o8);
+                                }
                             }
+                            if (!ok || !__any_sync(0xffffffffu, up)) break;  // (scores of -inf or NaN move nothing)
                         }
+                        if (!ok) break;
+                        l += acc.x + acc.y;
+                        tmem_wait_st();
                         tc_fence_before();
-                        if (failed()) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(C::bPFull + C::kHalves * slot + h));
                     }
-                    l += acc.x + acc.y;
-                    tmem_st32(col + 32 * hf, pw);
-                    tmem_wait_st();
-                    tc_fence_before();
+                    if (!ok) break;
+                } else {
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h)
+                        if (lane == 0) mbar_arrive(bar(C::bPFull + C::kHalves * slot + h));
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::bPFull + C::kHalves * slot + hf));
+                sph[slot] ^= 1;
             }
+            if (!ok) break;
             // uses of the slots by the other tile's warps
             if (tiles == 2) {
                 sph[1 - t] ^= sg.blocks & 1;
@@ -825,12 +785,9 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                 odone += sg.blocks;
             }
             // ---- epilogue ----
-            ok = ok && warp_wait(bar(C::bOFin), seg & 1, abort_flag, a.err);
-            if (warp_on && failed()) {
-                ok = false;
-            } else if (warp_on) {
+            ok = warp_wait(bar(C::bOFin), seg & 1, abort_flag, a.err);
+            if (ok && warp_on) {
                 tc_fence_after();
-                if constexpr (C::kHalves == 2) l = join(l, [](float x, float y) { return x + y; });
                 const int head = sg.g * prm.group + rr - node * prm.group;
                 const int64_t row = (int64_t)(sg.qo0 + node) * a.num_heads + head;
                 const bool part = sg.part >= 0;
@@ -838,12 +795,10 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                 const float inv = 1.f / l;
                 const bool none = l == 0.f;
                 bool finite = true;
-                constexpr int kCols = D / C::kHalves;  // of this warp
 #pragma unroll 1
-                for (int q = 0; q < kCols / 32; ++q) {
-                    const int c0 = hf * kCols + 32 * q;
+                for (int q = 0; q < D / 32; ++q) {
                     uint32_t t32[32];
-                    tmem_ld32(tmem + lane_off + C::kColO + D * t + c0, t32);
+                    tmem_ld32(tmem + lane_off + C::kColO + D * t + 32 * q, t32);
                     tmem_wait_ld();
                     float o[32];
 #pragma unroll
@@ -852,33 +807,24 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                         o[e] = none ? 0.f : __uint_as_float(t32[e]) * inv;
                     }
                     if (row_on && part) {
-                        float4 *op = reinterpret_cast<float4 *>(a.o_part + prow * D + c0);
+                        float4 *op = reinterpret_cast<float4 *>(a.o_part + prow * D + 32 * q);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) op[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     } else if (row_on) {
-                        uint4 *ob = reinterpret_cast<uint4 *>(a.out + row * D + c0);
+                        uint4 *ob = reinterpret_cast<uint4 *>(a.out + row * D + 32 * q);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             ob[e] = make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
                                                pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
                     }
                 }
-                if (row_on && hf == 0) {
+                if (row_on) {
                     const float lse = none ? -INFINITY : (m_ref + log2f(l)) * kLn2;
                     if (part) a.lse_part[prow] = lse;
                     else if (a.lse) a.lse[row] = lse;
                 }
                 // rows that something unseen may have reached (a NaN sum stays one whatever V holds)
                 uint32_t again = __ballot_sync(0xffffffffu, row_on && !finite && l > 0.f);
-                bool any = again != 0;
-                if constexpr (C::kHalves == 2) {
-                    any = pair_any(pair, any);
-                    if (any) {  // the first of the two does the rows
-                        if (hf) *xch = __uint_as_float(again);
-                        pair_any(pair, false);
-                        again = hf ? 0u : again | __float_as_uint(*xch);
-                    }
-                }
                 while (again) {
                     const int from = __ffs(again) - 1;
                     again &= again - 1;
