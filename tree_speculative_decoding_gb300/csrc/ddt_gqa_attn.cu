@@ -16,17 +16,20 @@
 //     epilogue run under the other's loads.  Taken when a request's rows per K/V
 //     head fit one tile (decode, small trees): the loads bound it.
 //   * kTiles = 2: blocks of 128 columns, all of tensor memory; the tensor core
-//     works on one tile while the softmax of the other runs.
-// The blocks of all items, weighted by what they cost, form one line that is
-// dealt to the resident CTAs in equal shares: a CTA takes the end of one item,
+//     works on one tile while the softmax of the other runs.  An item's last rows
+//     may fill one tile only: its blocks then alternate between the two tiles'
+//     warps and outputs, each with a reference and sum of its own, and the two
+//     are joined at the end.
+// The blocks of all items, weighted by what they cost, form one line (request,
+// K/V head, rows, columns) that is dealt to the resident CTAs in equal shares: a CTA takes the end of one item,
 // whole items, and the start of another, whatever the requests' lengths are.
 // Items that were cut leave partial results (at most two per CTA) in the
 // workspace for the combine kernel.  Every CTA and the combine find the same
 // cuts from the offsets.
 //
 // Score slots: two buffers of one block's scores in tensor memory.  Work unit w
-// of a segment (block-major, tiles inside a block) uses slot w mod 2: with two
-// tiles each has its own, with one tile blocks alternate.  The MMA warp issues
+// of a segment (block-major, tiles inside a block) uses slot w mod 2.  The MMA
+// warp issues
 //   S(0) S(1) | PV(0) S(2) | PV(1) S(3) | ...
 // so the scores of w + 1 are being computed, or done, while the softmax of w
 // runs.  P (bf16) overwrites the scores in place and is the A operand of PV
@@ -89,12 +92,19 @@ struct Cfg {
     static constexpr int kBlockBytes = kBoxes * kBoxBytes;
     static constexpr int kQBoxBytes = kRows * 128;
     static constexpr int kQBytes = kBoxes * kQBoxBytes;  // one tile of q
-    static constexpr int kKStages = D == 128 ? (kTiles == 2 ? 3 : 2) : 4;
-    static constexpr int kVStages = D == 128 ? 2 : 4;
+    static constexpr int kKStages = D == 128 ? 2 : 4;
+    static constexpr int kVStages = D == 128 ? (kTiles == 2 ? 3 : 2) : 4;  // V waits for the softmax, K does not
     static constexpr int kUnits = NB / 32;               // 32-row units of a block
     static constexpr int kSoftWarps = 4 * kTiles;
-    static constexpr int kLoadWarps = 4 * kTiles - 1;    // with the MMA warp: whole warpgroups
-    static constexpr int kThreads = 32 * (kSoftWarps + kLoadWarps + 1);
+    // two tiles: warps 8..11 load K, 12..15 V, 16 issues MMAs (its warpgroup's others
+    // are idle); one tile: warp 4 issues MMAs, 5..7 load
+    static constexpr int kLoadWarps = kTiles == 2 ? 2 * kUnits : 3;
+    static constexpr int kFirstLoad = kTiles == 2 ? kSoftWarps : kSoftWarps + 1;
+    static constexpr int kMmaWarp = kTiles == 2 ? kSoftWarps + kLoadWarps : kSoftWarps;
+    static constexpr int kThreads = kTiles == 2 ? 640 : 256;
+    // registers of the two-tile kernel: a softmax thread's, another's; together no more than at launch
+    static constexpr int kSoftRegs = 144, kOtherRegs = 64, kLaunchRegs = 96;
+    static_assert(32 * kSoftWarps * kSoftRegs + (640 - 32 * kSoftWarps) * kOtherRegs <= 640 * kLaunchRegs || kTiles == 1, "registers");
     static constexpr uint32_t kTmemCols = kTiles == 2 ? 512 : 256;
     static constexpr uint32_t kColS = 0, kColO = 2 * NB;
     static constexpr int kOffQ = 0;
@@ -104,21 +114,22 @@ struct Cfg {
     // barriers
     static constexpr int bKFull = 0, bKEmpty = bKFull + kKStages, bVFull = bKEmpty + kKStages,
                          bVEmpty = bVFull + kVStages, bSFull = bVEmpty + kVStages, bPFull = bSFull + 2,
-                         bQFull = bPFull + 2 * kHalves, bHalf = bQFull + 1, bODone = bHalf + 2, bOFin = bODone + 1, bDrain = bOFin + 1,
+                         bQFull = bPFull + 2 * kHalves, bHalf = bQFull + 1, bODone = bHalf + 2, bOFin = bODone + 1, bJoin = bOFin + 1, bDrain = bJoin + 1,
                          bSegFull = bDrain + 1, bSegEmpty = bSegFull + 2, bCount = bSegEmpty + 2;
     static constexpr int kOffHolder = kOffBar + 8 * bCount;
     static constexpr int kOffWalk = kOffHolder + 8;  // 128 bytes: the walk; 2 x 48: the segments it has given
     static constexpr int kOffPlan = kOffWalk + 128 + 2 * 48;  // a sum per warp, then where the CTA's share starts
-    static constexpr int kSmemUsed = kOffPlan + 8 * (kThreads / 32);
+    static constexpr int kOffJoin = kOffPlan + 8 * (kThreads / 32);  // the second tile's references and sums
+    static constexpr int kSmemUsed = kOffJoin + (kTiles == 2 ? kRows * 8 : 0);
     static constexpr int kSmemBytes = kSmemUsed + 1024;  // slack for the 1024-byte alignment of swizzle atoms
     static constexpr uint32_t kIdescS = idesc_bf16(kRows, NB, 0, 0);
     static constexpr uint32_t kIdescPV = idesc_bf16(kRows, D, 0, 1);
     // cost of a block with all tiles and with one, and of an item besides its blocks
     // (its q, the latency of its first loads, its epilogue), in one unit; the share
     // that a CTA gets at least
-    static constexpr int kCostFull = kTiles == 2 ? 16 : 8, kCostOne = kTiles == 2 ? 10 : 8, kCostItem = 24;
+    static constexpr int kCostFull = kTiles == 2 ? 16 : 8, kCostOne = kTiles == 2 ? 11 : 8, kCostItem = 24;
     static constexpr int kMinShare = kTiles == 2 ? 32 : 24;
-    static_assert(kTiles == 2 ? kLoadWarps > kUnits : kKStages >= 2 && kVStages >= 2 && kKStages <= kVStages, "see the load warps");
+    static_assert(kTiles == 2 || (kKStages >= 2 && kKStages <= kVStages), "see the load warps");
     static_assert(kOffPlan % 8 == 0, "alignment");
     static_assert(kColO + kTiles * D <= kTmemCols, "tensor memory");
     static_assert(kSmemBytes <= (kTiles == 2 ? 232448 : 115712), "shared memory");
@@ -185,9 +196,14 @@ template <class C>
 __device__ __forceinline__ int64_t item_cost(const Request &r, int tg) {
     return C::kCostItem + (int64_t)r.blocks * (tg == r.tgs - 1 && r.last_one ? C::kCostOne : C::kCostFull);
 }
+// of the items of one K/V head
+template <class C>
+__device__ __forceinline__ int64_t head_cost(const Request &r) {
+    return r.tgs > 0 ? (r.tgs - 1) * (C::kCostItem + (int64_t)r.blocks * C::kCostFull) + item_cost<C>(r, r.tgs - 1) : 0;
+}
 template <class C>
 __device__ __forceinline__ int64_t request_cost(const Request &r, int num_kv_heads) {
-    return r.tgs > 0 ? ((r.tgs - 1) * item_cost<C>(r, 0) * (r.tgs > 1) + item_cost<C>(r, r.tgs - 1)) * num_kv_heads : 0;
+    return head_cost<C>(r) * num_kv_heads;
 }
 
 // kTiles: tiles of an item.  err: where a bad request is reported, or null.
@@ -263,27 +279,18 @@ struct Walk {
         more = 1;
     }
     // share [lo_, hi_), which starts inside request b_, whose items start at pos_
-    __device__ __forceinline__ void start_share(const Request &req, int heads, int cta_, int b_, int64_t pos_, int64_t lo_,
-                                                int64_t hi_) {
+    __device__ __forceinline__ void start_share(const Request &req, int cta_, int b_, int64_t pos_, int64_t lo_, int64_t hi_) {
         r = req;
         cta = cta_;
         b = b_;
         lo = lo_;
         hi = hi_;
         dealt = more = 1;
-        const int64_t full = item_cost<C>(r, 0), before_last = r.tgs > 1 ? (r.tgs - 1) * full * heads : 0;
-        const int64_t off = lo - pos_;
-        if (off < before_last) {
-            const int64_t k = off / full;
-            tg = (int)(k / heads);
-            g = (int)(k - (int64_t)tg * heads);
-            pos = pos_ + k * full;
-        } else {
-            const int64_t last = item_cost<C>(r, r.tgs - 1);
-            tg = r.tgs - 1;
-            g = (int)((off - before_last) / last);
-            pos = pos_ + before_last + g * last;
-        }
+        const int64_t head = head_cost<C>(r), full = C::kCostItem + (int64_t)r.blocks * C::kCostFull;
+        g = (int)((lo - pos_) / head);
+        pos = pos_ + g * head;
+        tg = min((int)((lo - pos) / full), r.tgs - 1);
+        pos += tg * full;
     }
     // the next segment; one without blocks when the share is done
     __device__ __forceinline__ Segment next(const GqaArgs &a, int group) {
@@ -310,13 +317,13 @@ struct Walk {
                 more = 0;
             } else {
                 pos += item_cost<C>(r, tg);
-                if (++g == a.num_kv_heads) {
-                    g = 0;
-                    ++tg;
-                }
-                while (tg >= r.tgs && pos < hi && ++b < a.batch) {  // the next request with items
-                    r = load_request<C, kTiles>(a, group, b, nullptr);
+                if (++tg == r.tgs) {
                     tg = 0;
+                    ++g;
+                }
+                while ((g >= a.num_kv_heads || r.tgs == 0) && pos < hi && ++b < a.batch) {  // the next request with items
+                    r = load_request<C, kTiles>(a, group, b, nullptr);
+                    tg = g = 0;
                 }
                 more = pos < hi && b < a.batch;
             }
@@ -340,13 +347,14 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
     int64_t *plan = reinterpret_cast<int64_t *>(smem + C::kOffPlan);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kMmaWarp = C::kSoftWarps, kFirstLoad = kMmaWarp + 1;
+    constexpr int kMmaWarp = C::kMmaWarp, kFirstLoad = C::kFirstLoad;
     if (warp == kMmaWarp && lane == 0) {
         for (int i = 0; i < C::bCount; ++i)
             mbar_init(bar(i), i < C::bKEmpty || (i >= C::bVFull && i < C::bVEmpty) ? 32 * C::kUnits  // load lanes
                       : i >= C::bPFull && i < C::bQFull                            ? 4               // row quarters
                       : i == C::bQFull                                             ? C::kSoftWarps
-                      : i >= C::bSegEmpty                                          ? C::kThreads / 32
+                      : i == C::bJoin                                              ? 4
+                      : i >= C::bSegEmpty                                          ? C::kSoftWarps + C::kLoadWarps + 1
                                                                                    : 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -392,7 +400,7 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
         }
         if (total == 0 || (int)blockIdx.x >= ctas) return;
         const int64_t lo = share_start(total, ctas, blockIdx.x), hi = share_start(total, ctas, blockIdx.x + 1);
-        if (at <= lo && lo < at + cost) walk->start_share(req, a.num_kv_heads, blockIdx.x, tid, at, lo, hi);
+        if (at <= lo && lo < at + cost) walk->start_share(req, blockIdx.x, tid, at, lo, hi);
     } else {
         const int b = blockIdx.z, tg = blockIdx.x / a.num_kv_heads;
         const Request req = load_request<C, kTiles>(a, prm.group, b, blockIdx.x == 0 && tid == 0 ? a.err : nullptr);
@@ -436,13 +444,12 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
     };
     Segment sg;
 
-    // Registers of the two-tile kernel: 512 threads x 128 at launch = 256 x 184 (softmax) + 256 x 72.
-    if (warp >= kMmaWarp) {
-        if constexpr (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");  // one instruction for the warpgroup
-        if (warp >= kFirstLoad) {
+    if (warp >= C::kSoftWarps) {
+        if constexpr (kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));  // one instruction for each warpgroup
+        if (warp >= kFirstLoad && warp < kFirstLoad + C::kLoadWarps) {
             // ================= gather =================
-            // A unit is 32 rows of a block of K or V.  Two-tile kernel: four warps take
-            // a unit each of every block of K, three take the units of V in turn.
+            // A unit is 32 rows of a block of K or V.  Two-tile kernel: a warp has the same
+            // unit of every block of K, or of V.
             // One-tile kernel: three warps take the units in turn in the order K(0) K(1)
             // V(0) K(2) V(1) ... V(blocks - 1).  A unit's fixed cost (its waits) and its
             // copies overlap those of the other warps' units.  A copy instruction moves
@@ -480,11 +487,10 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                 const int32_t *slots = a.kv_indices + sg.kv0 + sg.c_begin;
                 const int cols = sg.c_end - sg.c_begin;
                 constexpr bool kApart = kTiles == 2;
-                constexpr int kKWarps = C::kUnits;  // of the two-tile kernel
                 const int lw = warp - kFirstLoad;
-                const bool v_warp = kApart && lw >= kKWarps;
+                const bool v_warp = kApart && lw >= C::kUnits;
                 const int last = 2 * sg.blocks - 1, end = (kApart ? 1 : 2) * sg.blocks * C::kUnits;
-                const int step = !kApart ? C::kLoadWarps : v_warp ? C::kLoadWarps - kKWarps : kKWarps;
+                const int step = kApart ? C::kUnits : C::kLoadWarps;
                 // block of unit n, and whether it is its V
                 auto block_of = [&](int n, bool &is_v) {
                     const int q = n / C::kUnits;
@@ -500,7 +506,7 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                     const int j = block_of(n, is_v);
                     return slots[min(j * NB + 32 * (n % C::kUnits) + lane, cols - 1)];  // past the end: a valid row again
                 };
-                int n = v_warp ? lw - kKWarps : lw;
+                int n = v_warp ? lw - C::kUnits : lw;
                 int ahead = n < end ? fetch(n) : 0;
                 for (; n < end; n += step) {
                     int slot = ahead;
@@ -527,7 +533,7 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                 base += sg.blocks;
             }
             asm volatile("cp.async.wait_all;" ::: "memory");  // nothing may land after the CTA has left
-        } else {
+        } else if (warp == kMmaWarp) {
             // ================= MMA =================
             if (elect_one()) {
                 const uint64_t q0 = smem_desc(sbase + C::kOffQ, 16, 1024), k0 = smem_desc(sbase + C::kOffK, 16, 1024),
@@ -539,6 +545,7 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                 // unrolled over the two slots and keeps its stages and phases in counters.
                 auto run = [&](auto tile_count, int items) {
                     constexpr int A = decltype(tile_count)::value;  // tiles of the segment
+                    constexpr int kOuts = kTiles;                   // outputs that work units alternate between
                     int w = 0;
                     auto issue_s = [&](int slot) {
                         const int t = A == 2 ? slot : 0;
@@ -571,8 +578,8 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                             fence_proxy_async_smem();
                         }
                         const uint64_t vd = v0 + (uint32_t)vs * (C::kBlockBytes >> 4);
-                        const uint32_t p = tmem + C::kColS + NB * slot, d = tmem + C::kColO + D * t;
-                        const uint32_t later = w >= A;  // the first block's product overwrites
+                        const uint32_t p = tmem + C::kColS + NB * slot, d = tmem + C::kColO + D * (kOuts == 2 ? slot : 0);
+                        const uint32_t later = w >= kOuts;  // an output's first product overwrites
 #pragma unroll
                         for (int h = 0; h < C::kHalves; ++h) {
                             ok = wait_or_abort(bar(C::bPFull + C::kHalves * slot + h), pph[slot], abort_flag, a.err);
@@ -584,7 +591,7 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                             if (h + 1 < C::kHalves) mma_commit(bar(C::bHalf + slot));
                         }
                         pph[slot] ^= 1;
-                        if (A == 1) mma_commit(bar(C::bODone));
+                        if (kOuts == 1) mma_commit(bar(C::bODone));
                         if (t == A - 1) {
                             mma_commit(bar(C::bVEmpty + vs));
                             if (++vs == C::kVStages) {
@@ -628,20 +635,22 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
         }
     } else {
         // ================= softmax (thread = row = TMEM lane of its tile) =================
-        if constexpr (kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        if constexpr (kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
         const int t = warp >> 2, wq = warp & 3;
         const int r = 32 * wq + lane;  // row within the tile
         const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
         const float sc = a.scale * kLog2e;
-        uint32_t sph[2] = {0, 0}, odone = 0;  // phases of the slots; one-tile blocks so far
+        // phases of the slots that this warp serves (two tiles: its own one); blocks, and joins, so far
+        uint32_t sph[2] = {0, 0}, done = 0, joins = 0;
         bool ok = true;
         for (int seg = 0; ok; ++seg) {
             ok = warp_segment(seg, sg);
             if (!ok || sg.blocks == 0) break;
-            const int rows_t = sg.rows - t * kRows;  // rows of this warp's tile
-            const int tiles = sg.tiles;
+            const bool lone = kTiles == 2 && sg.tiles == 1;  // one tile, served by both tiles' warps
+            const int first = lone ? 0 : t * kRows;          // the tile's first row in the item
+            const int rows_t = sg.rows - first;
             // ---- q rows of this warp into the swizzled operand layout ----
-            if (32 * wq < rows_t) {
+            if (32 * wq < rows_t && !(lone && t == 1)) {
                 constexpr int kChunks = D / 8, kPer = 32 / kChunks;  // 16-byte pieces of a row; rows per step
                 const int c = lane % kChunks, sub = lane / kChunks;
                 const uint32_t qb = sbase + C::kOffQ + t * C::kQBytes + (c >> 3) * C::kQBoxBytes;
@@ -650,7 +659,7 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                 for (int i = 0; i < 32 / kPer; ++i) {
                     const int rt = 32 * wq + i * kPer + sub;
                     if (rt < rows_t) {
-                        const int rr = sg.row0 + t * kRows + rt;
+                        const int rr = sg.row0 + first + rt;
                         const int node = rr / prm.group, hg = rr - node * prm.group;
                         cp_async_16(qb + (rt >> 3) * 1024 + (rt & 7) * 128 + (((c & 7) ^ (rt & 7)) << 4),
                                     q + ((int64_t)node * a.num_heads + hg) * D);
@@ -661,10 +670,9 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::bQFull));
-            const bool mine = t < tiles;            // the segment has this tile
-            const bool warp_on = 32 * wq < rows_t;  // ... and rows of this warp
+            const bool warp_on = 32 * wq < rows_t;  // the warp has rows
             const bool row_on = r < rows_t;
-            const int rr = sg.row0 + (row_on ? t * kRows + r : 0);
+            const int rr = sg.row0 + (row_on ? first + r : 0);
             const int node = rr / prm.group;
             const uint32_t *words = a.mask + sg.m0 + (int64_t)node * sg.W;
             float m_ref = -INFINITY, l = 0.f;  // the reference in log2 units, the sum against it
@@ -679,71 +687,97 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                 }
             };
             uint32_t mnext[kW];
-            if (warp_on) mask_words(0, mnext);
-            for (int j = 0; mine && j < sg.blocks; ++j) {
-                const int slot = tiles == 2 ? t : j & 1;
+            const int j0 = lone ? t : 0, step = lone ? 2 : 1;
+            if (warp_on && j0 < sg.blocks) mask_words(j0, mnext);
+            for (int j = j0; j < sg.blocks; j += step) {
+                const int slot = kTiles == 2 ? t : j & 1;
                 const uint32_t col = tmem + lane_off + C::kColS + NB * slot;
                 uint32_t mw[kW];
                 if (warp_on) {
 #pragma unroll
                     for (int k = 0; k < kW; ++k) mw[k] = mnext[k];
-                    if (j + 1 < sg.blocks) mask_words(j + 1, mnext);
+                    if (j + step < sg.blocks) mask_words(j + step, mnext);
                 }
                 ok = warp_wait(bar(C::bSFull + slot), sph[slot], abort_flag, a.err);
                 if (!ok) break;
                 if (warp_on) {
                     tc_fence_after();
-                    const float2 scv = make_float2(sc, sc);
-                    uint32_t s[kW][32];  // the block's scores of the row
-#pragma unroll
-                    for (int k = 0; k < kW; ++k) tmem_ld32(col + 32 * k, s[k]);
-                    tmem_wait_ld();
-                    // unseen columns at -inf; a branch, not selects: most blocks are seen whole
                     uint32_t all = mw[0];
 #pragma unroll
                     for (int k = 1; k < kW; ++k) all &= mw[k];
-                    if (!__all_sync(0xffffffffu, all == 0xffffffffu)) {
-                        asm volatile("");
-#pragma unroll
-                        for (int k = 0; k < NB; ++k) s[k >> 5][k & 31] = ((mw[k >> 5] >> (k & 31)) & 1u) ? s[k >> 5][k & 31] : 0xff800000u;
-                    }
+                    const bool whole = __all_sync(0xffffffffu, all == 0xffffffffu);
 #pragma unroll
                     for (int h = 0; h < C::kHalves; ++h) {
-                        float2 acc;
-                        while (true) {
-                            const float m = m_ref == -INFINITY ? 0.f : m_ref;  // nothing seen: every weight is 0
-                            const float2 nmv = make_float2(-m, -m);
-                            acc = make_float2(0.f, 0.f);
+                        // The one-tile kernel keeps the 64 scores until the weights are sure and stores
+                        // these as it goes; the two-tile kernel, short of registers, reads the scores
+                        // again when the reference moves and stores the weights at the end (the other
+                        // way round measured 2% and 12% slower).
+                        constexpr bool kKeep = kTiles == 1;
+                        uint32_t s[2][32];  // the scores
+                        auto take = [&]() {
+                            tmem_ld32(col + 64 * h, s[0]);
+                            tmem_ld32(col + 64 * h + 32, s[1]);
+                            tmem_wait_ld();
+                            if (!whole) {  // unseen columns at -inf; a branch, not selects: most blocks are seen whole
+                                asm volatile("");
 #pragma unroll
-                            for (int k = 2 * h; k < 2 * h + 2; ++k) {
-                                uint32_t pw[16];  // the weights of 32 columns as bf16 pairs
+                                for (int e = 0; e < 64; ++e)
+                                    s[e >> 5][e & 31] = ((mw[2 * h + (e >> 5)] >> (e & 31)) & 1u) ? s[e >> 5][e & 31] : 0xff800000u;
+                            }
+                        };
+                        if (kKeep) take();
+                        uint32_t pw[2][16];  // the weights as bf16 pairs
+                        float sum;
+                        while (true) {
+                            if (!kKeep) take();
+                            const float m = m_ref == -INFINITY ? 0.f : m_ref;  // nothing seen: every weight is 0
+                            const float2 scv = make_float2(sc, sc), nmv = make_float2(-m, -m);
+                            float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
 #pragma unroll
                                 for (int e = 0; e < 32; e += 2) {
                                     const float2 x = f2fma(make_float2(__uint_as_float(s[k][e]), __uint_as_float(s[k][e + 1])), scv, nmv);
                                     const float p0 = ex2(x.x), p1 = ex2(x.y);
                                     acc = f2add(acc, make_float2(p0, p1));
-                                    pw[e / 2] = pack_bf16(p0, p1);
+                                    pw[k][e / 2] = pack_bf16(p0, p1);
                                 }
-                                tmem_st16(col + 16 * k, pw);  // over scores that have been read
+                                if (kKeep) tmem_st16(col + 32 * h + 16 * k, pw[k]);  // over scores that have been read
                             }
-                            const bool moves = row_on && (acc.x + acc.y > kSumLimit || (m_ref == -INFINITY && (mw[2 * h] | mw[2 * h + 1])));
+                            sum = acc.x + acc.y;
+                            const bool moves = row_on && (sum > kSumLimit || (m_ref == -INFINITY && (mw[2 * h] | mw[2 * h + 1])));
                             if (!__any_sync(0xffffffffu, moves)) break;
                             // The reference moves to the largest of these scores, and what was summed
                             // against the old one shrinks; then the weights are taken again.
                             float mx = -INFINITY;
+                            if (kKeep) {
 #pragma unroll
-                            for (int e = 0; e < 64; ++e) mx = fmaxf(mx, __uint_as_float(s[2 * h + e / 32][e & 31]));
+                                for (int e = 0; e < 64; ++e) mx = fmaxf(mx, __uint_as_float(s[e >> 5][e & 31]));
+                            } else {
+#pragma unroll 1
+                                for (int q = 0; q < 8; ++q) {
+                                    uint32_t o8[8];
+                                    tmem_ld8(col + 64 * h + 8 * q, o8);
+                                    tmem_wait_ld();
+                                    const uint32_t seen = (q < 4 ? mw[2 * h] : mw[2 * h + 1]) >> (8 * (q & 3));
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e)
+                                        if ((seen >> e) & 1u) mx = fmaxf(mx, __uint_as_float(o8[e]));
+                                }
+                            }
                             mx *= sc;
                             const bool up = moves && mx > m_ref;
+                            if (!__any_sync(0xffffffffu, up)) break;  // scores of -inf or NaN move nothing
                             const float alpha = up ? ex2(m_ref - mx) : 1.0f;
                             if (up) m_ref = mx;
                             l *= alpha;
                             // The products so far have to be done before the output is scaled: of this
-                            // block's first half; or of the last block (with two tiles S(w) was issued
-                            // behind it, so it is done).
+                            // block's first half; or of the output's last block (with two outputs S(w)
+                            // was issued behind it, so it is done).
                             if (h > 0) ok = warp_wait(bar(C::bHalf + slot), sph[slot], abort_flag, a.err);
-                            else if (j > 0 && tiles == 1) ok = warp_wait(bar(C::bODone), (odone + j - 1) & 1, abort_flag, a.err);
-                            if (ok && (h > 0 || j > 0)) {
+                            else if (kTiles == 1 && j > 0) ok = warp_wait(bar(C::bODone), (done + j - 1) & 1, abort_flag, a.err);
+                            if (!ok) break;
+                            if (h > 0 || j > j0) {
                                 tc_fence_after();
                                 const uint32_t oc = tmem + lane_off + C::kColO + D * t;
 #pragma unroll 1
@@ -756,10 +790,13 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                                     tmem_st8(oc + 8 * q, o8);
                                 }
                             }
-                            if (!ok || !__any_sync(0xffffffffu, up)) break;  // (scores of -inf or NaN move nothing)
                         }
                         if (!ok) break;
-                        l += acc.x + acc.y;
+                        l += sum;
+                        if (!kKeep) {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) tmem_st16(col + 32 * h + 16 * k, pw[k]);
+                        }
                         tmem_wait_st();
                         tc_fence_before();
                         __syncwarp();
@@ -774,24 +811,35 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                 sph[slot] ^= 1;
             }
             if (!ok) break;
-            // uses of the slots by the other tile's warps
-            if (tiles == 2) {
-                sph[1 - t] ^= sg.blocks & 1;
-            } else {
-                if (!mine) {
-                    sph[0] ^= ((sg.blocks + 1) >> 1) & 1;
-                    sph[1] ^= (sg.blocks >> 1) & 1;
-                }
-                odone += sg.blocks;
-            }
+            done += sg.blocks;
             // ---- epilogue ----
             ok = warp_wait(bar(C::bOFin), seg & 1, abort_flag, a.err);
-            if (ok && warp_on) {
+            float keep0 = 1.f, keep1 = 0.f;  // what the two outputs of a lone tile count
+            if (ok && lone) {
+                // The wait above: the first tile's warps have left the segment before (its q is
+                // theirs), so these places are free.
+                volatile float *place = reinterpret_cast<volatile float *>(smem + C::kOffJoin) + 2 * r;
+                if (t == 1) {
+                    place[0] = m_ref;
+                    place[1] = l;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::bJoin));
+                } else {
+                    ok = warp_wait(bar(C::bJoin), joins & 1, abort_flag, a.err);
+                    const float m1 = place[0], l1 = place[1], m = fmaxf(m_ref, m1);
+                    keep0 = m_ref == -INFINITY ? 0.f : ex2(m_ref - m);
+                    keep1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
+                    l = (keep0 != 0.f ? l * keep0 : 0.f) + (keep1 != 0.f ? l1 * keep1 : 0.f);
+                    m_ref = m;
+                }
+                ++joins;
+            }
+            if (ok && warp_on && !(lone && t == 1)) {
                 tc_fence_after();
                 const int head = sg.g * prm.group + rr - node * prm.group;
                 const int64_t row = (int64_t)(sg.qo0 + node) * a.num_heads + head;
                 const bool part = sg.part >= 0;
-                const int64_t prow = (int64_t)sg.part * prm.part_rows + t * kRows + r;
+                const int64_t prow = (int64_t)sg.part * prm.part_rows + first + r;
                 const float inv = 1.f / l;
                 const bool none = l == 0.f;
                 bool finite = true;
@@ -802,9 +850,17 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                     tmem_wait_ld();
                     float o[32];
 #pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = keep0 != 0.f ? __uint_as_float(t32[e]) * keep0 : 0.f;
+                    if (lone) {
+                        tmem_ld32(tmem + lane_off + C::kColO + D + 32 * q, t32);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] += keep1 != 0.f ? __uint_as_float(t32[e]) * keep1 : 0.f;
+                    }
+#pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        finite = finite && (t32[e] & 0x7f800000u) != 0x7f800000u;
-                        o[e] = none ? 0.f : __uint_as_float(t32[e]) * inv;
+                        finite = finite && (__float_as_uint(o[e]) & 0x7f800000u) != 0x7f800000u;
+                        o[e] = none ? 0.f : o[e] * inv;
                     }
                     if (row_on && part) {
                         float4 *op = reinterpret_cast<float4 *>(a.o_part + prow * D + 32 * q);
@@ -884,8 +940,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps) gqa_combine_kernel(const G
     const int ctas = (int)a.plan[a.batch + 1];
     const int g = h / prm.group, rr = (t - r.qo0) * prm.group + h - g * prm.group;  // row of the request
     const int tg = rr / (kTiles * kRows);
-    const int64_t full = item_cost<C>(r, 0), cost = item_cost<C>(r, tg);
-    const int64_t pos = a.plan[b] + (int64_t)tg * full * a.num_kv_heads + g * cost;
+    const int64_t full = C::kCostItem + (int64_t)r.blocks * C::kCostFull;
+    const int64_t pos = a.plan[b] + g * head_cost<C>(r) + tg * full;
     const int unit = tg == r.tgs - 1 && r.last_one ? C::kCostOne : C::kCostFull;
     // owners of the item's first and last block
     const int c0 = share_owner(total, ctas, pos + C::kCostItem);
@@ -963,6 +1019,12 @@ cudaError_t launch(GqaParams &prm, cudaStream_t s) {
 
 template <int D, int kTiles>
 cudaError_t prepare() {
+    if (kTiles == 2) {  // the softmax warps would wait for registers that the launch does not have
+        cudaFuncAttributes attr;
+        const cudaError_t e = cudaFuncGetAttributes(&attr, gqa_attn_kernel<D, kTiles>);
+        if (e != cudaSuccess) return e;
+        if (attr.numRegs < Cfg<D, kTiles>::kLaunchRegs) return cudaErrorInvalidConfiguration;
+    }
     const cudaError_t e = cudaFuncSetAttribute(gqa_attn_kernel<D, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                Cfg<D, kTiles>::kSmemBytes);
     if (e != cudaSuccess) return e;
