@@ -56,7 +56,8 @@ def test_attention_sizing(lib):
     # two parts per CTA of as many rows as an item has: q_len x group, at most 128 or (two tiles) 256
     for b, h, g, d, t, c, rows in ((1, 64, 8, 128, 1, 304, 8), (3, 64, 8, 128, 16, 9, 128), (2, 64, 8, 64, 17, 5, 136),
                                    (256, 128, 1, 128, 128, 512, 256)):
-        assert size(b, h, g, d, t, c) == up(8 * (b + 2)) + up(2 * c * rows * d * 4) + up(2 * c * rows * 4)
+        notes = 8 * b * g * -(-t * (h // g) // (256 if t * (h // g) > 128 else 128))
+        assert size(b, h, g, d, t, c) == up(notes) + up(2 * c * rows * d * 4) + up(2 * c * rows * 4)
     ctas = lib.ddt_gqa_verify_attn_num_ctas
     for args in ((1, 64, 8, 33, 4129, 152), (64, 64, 8, 1, 16384, 152), (1, 8, 2, 9, 30, 152), (1, 1, 1, 1, 1, 152),
                  (1, 64, 8, 65, 131137, 152), (32, 32, 4, 33, 8225, 1000), (65535, 128, 1, 128, 2 ** 31 - 1, 152)):

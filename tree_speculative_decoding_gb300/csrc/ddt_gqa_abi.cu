@@ -9,6 +9,11 @@
 
 namespace {
 
+// bytes of the notes on a call's items (256-byte aligned), at the workspace's start
+size_t notes_bytes(int32_t batch, int32_t num_kv_heads, int32_t group, int32_t max_q_len) {
+    return ((size_t)batch * num_kv_heads * ddt::gqa_tile_groups(max_q_len, group) * sizeof(int2) + 255) & ~size_t(255);
+}
+
 inline cudaStream_t as_stream(void *s) { return static_cast<cudaStream_t>(s); }
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 inline bool misaligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
@@ -111,8 +116,9 @@ size_t ddt_gqa_verify_attn_workspace_size(int32_t batch, int32_t num_heads, int3
     if (batch < 1 || num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads || head_dim < 1 || max_q_len < 1 ||
         num_ctas < 1)
         return 0;
-    const size_t rows = (size_t)2 * num_ctas * ddt::gqa_part_rows(max_q_len, num_heads / num_kv_heads);
-    return align256(((size_t)batch + 2) * sizeof(int64_t)) + align256(rows * head_dim * sizeof(float)) +
+    const int group = num_heads / num_kv_heads;
+    const size_t rows = (size_t)2 * num_ctas * ddt::gqa_part_rows(max_q_len, group);
+    return notes_bytes(batch, num_kv_heads, group, max_q_len) + align256(rows * head_dim * sizeof(float)) +
            align256(rows * sizeof(float));
 }
 
@@ -181,8 +187,8 @@ ddt_status ddt_gqa_verify_attn(
     if (ctas > 0) {
         const size_t rows = (size_t)2 * ctas * ddt::gqa_part_rows(max_q_len, num_heads / num_kv_heads);
         char *p = static_cast<char *>(workspace);
-        a.plan = reinterpret_cast<int64_t *>(p);
-        p += align256(((size_t)batch + 2) * sizeof(int64_t));
+        a.notes = reinterpret_cast<int2 *>(p);
+        p += notes_bytes(batch, num_kv_heads, num_heads / num_kv_heads, max_q_len);
         a.o_part = reinterpret_cast<float *>(p);
         a.lse_part = reinterpret_cast<float *>(p + align256(rows * head_dim * sizeof(float)));
     }

@@ -24,8 +24,8 @@
 // K/V head, rows, columns) that is dealt to the resident CTAs in equal shares: a CTA takes the end of one item,
 // whole items, and the start of another, whatever the requests' lengths are.
 // Items that were cut leave partial results (at most two per CTA) in the
-// workspace for the combine kernel.  Every CTA and the combine find the same
-// cuts from the offsets.
+// workspace for the combine kernel, and a note of where they are.  Every CTA finds
+// the same cuts from the offsets.
 //
 // Score slots: two buffers of one block's scores in tensor memory.  Work unit w
 // of a segment (block-major, tiles inside a block) uses slot w mod 2.  The MMA
@@ -81,6 +81,7 @@ struct GqaParams {
     GqaArgs a;
     int group;      // query heads per K/V head
     int part_rows;  // rows of a partial result
+    int tgs_most;   // items per K/V head of the longest request
 };
 
 template <int D, int kTiles>
@@ -234,12 +235,8 @@ __device__ __forceinline__ Request load_request(const GqaArgs &a, int group, int
     return r;
 }
 
-// CTA c of `ctas` takes the positions [share(c), share(c + 1)) of the line.
-__device__ __forceinline__ int64_t share_start(int64_t total, int ctas, int c) { return total * c / ctas; }
-__device__ __forceinline__ int share_owner(int64_t total, int ctas, int64_t pos) {
-    int c = (int)(pos * ctas / total);
-    while (share_start(total, ctas, c + 1) <= pos) ++c;
-    return c;
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {  // a, b >= 0; nearly always small enough for 32 bits
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 // the item's blocks that start before position x (block k starts kCostItem + k unit behind the item)
 template <class C>
@@ -287,13 +284,13 @@ struct Walk {
         hi = hi_;
         dealt = more = 1;
         const int64_t head = head_cost<C>(r), full = C::kCostItem + (int64_t)r.blocks * C::kCostFull;
-        g = (int)((lo - pos_) / head);
+        g = (int)divide(lo - pos_, head);
         pos = pos_ + g * head;
-        tg = min((int)((lo - pos) / full), r.tgs - 1);
+        tg = min((int)divide(lo - pos, full), r.tgs - 1);
         pos += tg * full;
     }
     // the next segment; one without blocks when the share is done
-    __device__ __forceinline__ Segment next(const GqaArgs &a, int group) {
+    __device__ __forceinline__ Segment next(const GqaArgs &a, int group, int tgs_most) {
         Segment s;
         s.blocks = 0;
         while (more && s.blocks == 0) {
@@ -316,6 +313,13 @@ struct Walk {
             if (!dealt) {
                 more = 0;
             } else {
+                // for the combine: the place of the item's first part (the later ones are at 2 CTA) and
+                // the CTA that has its last
+                if (s.blocks > 0) {
+                    int2 &note = a.notes[((int64_t)b * a.num_kv_heads + g) * tgs_most + tg];
+                    if (b0 == 0) note.x = s.part;
+                    if (b1 == r.blocks) note.y = cta;
+                }
                 pos += item_cost<C>(r, tg);
                 if (++tg == r.tgs) {
                     tg = 0;
@@ -388,18 +392,13 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
             if (w < warp) at += plan[w];
             total += plan[w];
         }
-        // CTAs that take a share: as many as get a few blocks at least
-        const int64_t most = total / (a.forced ? C::kCostFull : C::kMinShare);
+        // CTAs that take a share: as many as get a few blocks at least; CTA c has the
+        // positions [c q + min(c, rem), ...) of the line
+        const int64_t most = a.forced ? total / C::kCostFull : total / C::kMinShare;
         const int ctas = most < 1 ? 1 : most < a.num_ctas ? (int)most : a.num_ctas;
-        if (blockIdx.x == 0) {  // for the combine
-            if (tid < a.batch) a.plan[tid] = at;
-            if (tid == 0) {
-                a.plan[a.batch] = total;
-                a.plan[a.batch + 1] = ctas;
-            }
-        }
         if (total == 0 || (int)blockIdx.x >= ctas) return;
-        const int64_t lo = share_start(total, ctas, blockIdx.x), hi = share_start(total, ctas, blockIdx.x + 1);
+        const int64_t q = divide(total, ctas), rem = total - q * ctas, c = blockIdx.x;
+        const int64_t lo = c * q + min(c, rem), hi = (c + 1) * q + min(c + 1, rem);
         if (at <= lo && lo < at + cost) walk->start_share(req, blockIdx.x, tid, at, lo, hi);
     } else {
         const int b = blockIdx.z, tg = blockIdx.x / a.num_kv_heads;
@@ -470,7 +469,7 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                 if (warp != kFirstLoad) return;
                 if (n >= 2) ok = warp_wait(bar(C::bSegEmpty + (n & 1)), ((n >> 1) - 1) & 1, abort_flag, a.err);
                 if (ok && lane == 0) {
-                    const Segment s = walk->next(a, prm.group);
+                    const Segment s = walk->next(a, prm.group, prm.tgs_most);
                     const_cast<Segment &>(ring[n & 1]) = s;
                     mbar_arrive(bar(C::bSegFull + (n & 1)));
                 }
@@ -936,19 +935,11 @@ __global__ void __launch_bounds__(32 * kCombineWarps) gqa_combine_kernel(const G
     if (b >= a.batch) return;
     const Request r = load_request<C, kTiles>(a, prm.group, b, nullptr);
     if (r.tgs == 0 || t - r.qo0 >= r.T) return;  // nothing to do, or refused
-    const int64_t total = a.plan[a.batch];
-    const int ctas = (int)a.plan[a.batch + 1];
     const int g = h / prm.group, rr = (t - r.qo0) * prm.group + h - g * prm.group;  // row of the request
-    const int tg = rr / (kTiles * kRows);
-    const int64_t full = C::kCostItem + (int64_t)r.blocks * C::kCostFull;
-    const int64_t pos = a.plan[b] + g * head_cost<C>(r) + tg * full;
-    const int unit = tg == r.tgs - 1 && r.last_one ? C::kCostOne : C::kCostFull;
-    // owners of the item's first and last block
-    const int c0 = share_owner(total, ctas, pos + C::kCostItem);
-    const int c1 = share_owner(total, ctas, pos + C::kCostItem + (int64_t)(r.blocks - 1) * unit);
-    if (c0 == c1) return;
-    const int prow = rr - tg * kTiles * kRows;
-    const int parts = c1 - c0 + 1;
+    const int tg = rr / (kTiles * kRows), prow = rr - tg * kTiles * kRows;
+    const int2 note = a.notes[((int64_t)b * a.num_kv_heads + g) * prm.tgs_most + tg];
+    if (note.x < 0) return;
+    const int c0 = note.x >> 1, parts = note.y - c0 + 1;
     float m = -INFINITY, den = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -957,7 +948,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) gqa_combine_kernel(const G
         int64_t at = 0;
         float ls = -INFINITY;
         if (s0 + lane < parts) {
-            at = (int64_t)(2 * c + (share_start(total, ctas, c) > pos ? 0 : 1)) * prm.part_rows + prow;
+            at = (int64_t)(c == c0 ? note.x : 2 * c) * prm.part_rows + prow;
             ls = a.lse_part[at];
         }
         float mg = fmaxf(m, ls);
@@ -973,7 +964,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) gqa_combine_kernel(const G
         for (int e = 0; e < E; ++e) acc[e] *= keep;
         m = mg;
         const int n = min(32, parts - s0);
-#pragma unroll 4
+#pragma unroll 8
         for (int s = 0; s < n; ++s) {
             const float ws = __shfl_sync(0xffffffffu, w, s);
             const float *o = a.o_part + __shfl_sync(0xffffffffu, (long long)at, s) * D + lane * E;
@@ -1006,9 +997,8 @@ template <int D, int kTiles>
 cudaError_t launch(GqaParams &prm, cudaStream_t s) {
     using C = Cfg<D, kTiles>;
     GqaArgs &a = prm.a;
-    const int groups = (a.max_q_len * prm.group + kTiles * kRows - 1) / (kTiles * kRows);
     const dim3 grid = a.num_ctas > 0 ? dim3((unsigned)a.num_ctas)
-                                     : dim3((unsigned)(groups * a.num_kv_heads), 1, (unsigned)a.batch);
+                                     : dim3((unsigned)(prm.tgs_most * a.num_kv_heads), 1, (unsigned)a.batch);
     cudaError_t e = launch_pdl(gqa_attn_kernel<D, kTiles>, grid, dim3(C::kThreads), C::kSmemBytes, s, prm);
     if (e == cudaSuccess && a.num_ctas > 0) {
         const dim3 rows((unsigned)a.total_q, (unsigned)((a.num_heads + kCombineWarps - 1) / kCombineWarps));
@@ -1055,11 +1045,17 @@ int gqa_part_rows(int max_q_len, int group) {
     return rows < most ? rows : most;
 }
 
+int gqa_tile_groups(int max_q_len, int group) {
+    const int per = tiles_per_item(max_q_len, group) * kRows;
+    return (max_q_len * group + per - 1) / per;
+}
+
 cudaError_t launch_gqa_attn(const GqaArgs &a, cudaStream_t s) {
     GqaParams prm;
     prm.a = a;
     prm.group = a.num_heads / a.num_kv_heads;
     prm.part_rows = gqa_part_rows(a.max_q_len, prm.group);
+    prm.tgs_most = gqa_tile_groups(a.max_q_len, prm.group);
     const bool two = tiles_per_item(a.max_q_len, prm.group) == 2;
     if (a.head_dim == 128) return two ? launch<128, 2>(prm, s) : launch<128, 1>(prm, s);
     return two ? launch<64, 2>(prm, s) : launch<64, 1>(prm, s);

@@ -189,8 +189,8 @@ struct GqaArgs {
     int forced;       // the caller gave the count: a CTA may get a single block
     uint16_t *out;    // [total_q, H, D] bf16
     float *lse;       // [total_q, H] or null
-    // dealt: where each request's items start on the line, its length, the CTAs that took a share
-    int64_t *plan;    // [batch + 2]
+    // dealt: per item the place of its first part (-1: whole) and the CTA with its last
+    int2 *notes;      // [batch][num_kv_heads][gqa_tile_groups()]
     float *o_part;    // [2 * num_ctas, gqa_part_rows(), D]
     float *lse_part;  // [2 * num_ctas, gqa_part_rows()]
     unsigned int *err;
@@ -201,8 +201,9 @@ cudaError_t gqa_prepare_device();
 cudaError_t launch_gqa_attn(const GqaArgs &a, cudaStream_t s);
 // the CTAs that the work is dealt to for these bounds, or 0 (see GqaArgs)
 int gqa_choose_ctas(int batch, int num_heads, int num_kv_heads, int max_q_len, int max_kv_len, int num_sms);
-// rows of a partial result
+// rows of a partial result; most items per K/V head of a request
 int gqa_part_rows(int max_q_len, int group);
+int gqa_tile_groups(int max_q_len, int group);
 
 cudaError_t launch_cache_copy(const void *src_slab, int64_t src_pool_bytes, int64_t src_rows, void *dst_slab,
                               int64_t dst_pool_bytes, int64_t dst_rows, int num_pools, int64_t row_bytes,
