@@ -134,7 +134,7 @@ struct Cfg {
     // (its q, the latency of its first loads, its epilogue), in one unit; the share
     // that a CTA gets at least
     static constexpr int kCostFull = kTiles == 2 ? 16 : 8, kCostOne = kTiles == 2 ? 11 : 8, kCostItem = 24;
-    static constexpr int kMinShare = kTiles == 2 ? 32 : 24;
+    static constexpr int kMinShare = kTiles == 2 ? 80 : 36;
     static_assert(kTiles == 2 || (kKStages >= 2 && kKStages <= kVStages), "see the load warps");
     static_assert(kOffPlan % 8 == 0, "alignment");
     static_assert(kColO + kTiles * D <= kTmemCols, "tensor memory");

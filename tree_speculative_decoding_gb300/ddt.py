@@ -427,7 +427,7 @@ def _on_device(first, name):
 
 
 def _like(t, dtype, dev, name):
-    if t.dtype != dtype or t.device != dev or not t.is_contiguous():
+    if t.dtype is not dtype or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor on {dev}")
     return t.data_ptr()
 
@@ -441,7 +441,7 @@ def _mask_ptr(mask, dev):
 def _heads(t, dev, name, heads=None):
     """Pointer, row stride, rows, heads and head_dim of a [rows, heads, head_dim] bf16 tensor
     whose rows are contiguous (the rows themselves may be apart)."""
-    if t.dtype != torch.bfloat16 or t.device != dev or t.dim() != 3:
+    if t.dtype is not torch.bfloat16 or t.device != dev or t.dim() != 3:
         raise ValueError(f"{name} must be a [rows, heads, head_dim] bfloat16 tensor on {dev}")
     n, h, d = t.shape
     sn, sh, sd = t.stride()
@@ -461,7 +461,8 @@ def _pools(k_pool, v_pool, dev):
 
 
 def _raw_stream(stream, dev):
-    return (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+    # the raw handle of the current stream without a Stream object around it
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def ddt_gqa_norm_rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, depth, qo_indptr, kv_indices,
