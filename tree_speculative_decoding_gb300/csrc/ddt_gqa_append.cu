@@ -13,13 +13,17 @@
 // apart), so the rotation needs no exchange between lanes; only the sum of
 // squares crosses the group.  Weight, cosine and sine are folded into four
 // factors per pair once per token.  A CTA takes a token and its groups walk the
-// token's rows; the first rows are loaded before the token's request, slot and
-// angles are looked up, a chain of four dependent loads.  With few tokens several
-// CTAs share one.  The angles are read from the caller's table: sine and cosine
+// token's rows.  What bounds a CTA is its chain of dependent loads, so the first
+// rows, the weights and the depth are loaded before the token's request is looked
+// up, and its slot and angles at once behind that.  4096 tokens of 32 query and 8
+// K/V heads of 128 in 32 requests take 30.3 us, 5.6 TB/s (33.5 us with 128 threads
+// and 8 CTAs per SM, 35.3 us with 12 of these and 32.7 us with 16).  The angles are read from the caller's table: sine and cosine
 // of far positions need more than fp32, once per position and not per token.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "ddt_gqa.cuh"
 #include "ddt_internal.cuh"
@@ -30,7 +34,8 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 64;
+constexpr int kCtasPerSm = 14;
 constexpr int kBatchRows = 4;  // head rows in flight per group
 
 struct Row {  // a lane's two pieces of four values
@@ -59,7 +64,7 @@ struct Factors {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 8) norm_rope_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_append_kernel(const AppendArgs a) {
     constexpr int kLanes = D / 8;               // lanes of one head row
     constexpr int kGroups = kThreads / kLanes;  // head rows of a CTA at a time
     const int lane = threadIdx.x & 31;
@@ -83,13 +88,33 @@ __global__ void __launch_bounds__(kThreads, 8) norm_rope_append_kernel(const App
             if (r0 + u * stride < H) in[u] = load_row(q + (int64_t)(r0 + u * stride) * D, off0, off1);
     };
     load_batch(group);
+    Row w_q{}, w_k{};  // the weights of the lane's values
+    if (a.q_weight) w_q = load_row(a.q_weight, off0, off1);
+    if (a.k_weight) w_k = load_row(a.k_weight, off0, off1);
+    const int depth = a.depth ? a.depth[t] : 0;
 
-    const int b = find_request(a.qo_indptr, a.batch, t, lane);
-    if (b >= a.batch) return;  // behind the last request: left as it is
-    const int q0 = a.qo_indptr[b], T = a.qo_indptr[b + 1] - q0;
-    const int kv0 = a.kv_indptr[b], kv1 = a.kv_indptr[b + 1];
-    const int P = kv1 - kv0 - T;
-    const bool bad_q = q0 < 0 || t - q0 >= T || q0 + T > a.total_q;
+    // The token's request: up to 31 requests one round of loads gives every offset
+    // there is, else the search comes first.
+    int b, q0, q1, kv0, kv1;
+    if (a.batch < 32) {
+        const int i = min(lane, a.batch);
+        const int qo = a.qo_indptr[i], kv = a.kv_indptr[i];
+        b = __popc(__ballot_sync(0xffffffffu, lane >= 1 && lane <= a.batch && qo <= t));
+        q0 = __shfl_sync(0xffffffffu, qo, b);
+        q1 = __shfl_sync(0xffffffffu, qo, b + 1);
+        kv0 = __shfl_sync(0xffffffffu, kv, b);
+        kv1 = __shfl_sync(0xffffffffu, kv, b + 1);
+        if (b >= a.batch) return;  // behind the last request: left as it is
+    } else {
+        b = find_request(a.qo_indptr, a.batch, t, lane);
+        if (b >= a.batch) return;
+        q0 = a.qo_indptr[b];
+        q1 = a.qo_indptr[b + 1];
+        kv0 = a.kv_indptr[b];
+        kv1 = a.kv_indptr[b + 1];
+    }
+    const int T = q1 - q0, P = kv1 - kv0 - T;
+    const bool bad_q = q0 < 0 || t - q0 >= T || q1 > a.total_q;
     const bool bad_kv = kv0 < 0 || kv1 > a.total_kv || P < 0;
     if (bad_q || bad_kv) {
         if (threadIdx.x == 0) latch(a.err, bad_q ? DDT_DEVERR_QO_INDPTR : DDT_DEVERR_KV_INDPTR);
@@ -97,11 +122,9 @@ __global__ void __launch_bounds__(kThreads, 8) norm_rope_append_kernel(const App
     }
     const int i = t - q0;
     const int64_t slot = a.kv_indices[kv0 + P + i];
-    const bool slot_ok = slot >= 0 && slot < a.pool_rows;
-    if (!slot_ok && threadIdx.x == 0) latch(a.err, DDT_DEVERR_KV_INDEX);
     float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};  // of the lane's four pairs
     if (a.rope_dim > 0) {
-        const int64_t pos = (int64_t)P + (a.depth ? a.depth[t] : i);
+        const int64_t pos = (int64_t)P + (a.depth ? depth : i);
         if (pos < 0 || pos >= a.max_pos) {
             if (threadIdx.x == 0) latch(a.err, DDT_DEVERR_POSITION);
             return;
@@ -113,10 +136,11 @@ __global__ void __launch_bounds__(kThreads, 8) norm_rope_append_kernel(const App
             sn[0] = s.x; sn[1] = s.y; sn[2] = s.z; sn[3] = s.w;
         }
     }
-    auto factors = [&](const uint16_t *weight) {
+    const bool slot_ok = slot >= 0 && slot < a.pool_rows;
+    if (!slot_ok && threadIdx.x == 0) latch(a.err, DDT_DEVERR_KV_INDEX);
+    auto factors = [&](bool weighted, const Row &w) {
         float2 w0[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)}, w1[2] = {w0[0], w0[1]};
-        if (weight) {
-            const Row w = load_row(weight, off0, off1);
+        if (weighted) {
             w0[0] = unpack2(w.a.x); w0[1] = unpack2(w.a.y);
             w1[0] = unpack2(w.b.x); w1[1] = unpack2(w.b.y);
         }
@@ -182,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 8) norm_rope_append_kernel(const App
 
     uint16_t *q_out = a.q_out + (int64_t)t * H * D;
     {
-        const Factors f = factors(a.q_weight);
+        const Factors f = factors(a.q_weight != nullptr, w_q);
         // groups of a warp walk the same number of rows: the sums above need all its lanes
         for (int r0 = group; __any_sync(0xffffffffu, r0 < H); r0 += kBatchRows * stride) {
             if (r0 != group) load_batch(r0);
@@ -196,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 8) norm_rope_append_kernel(const App
         }
     }
     if (!slot_ok) return;  // the whole CTA
-    const Factors f = factors(a.k_weight);
+    const Factors f = factors(a.k_weight != nullptr, w_k);
     const uint16_t *k = a.k + t * a.k_stride, *v = a.v + t * a.v_stride;
     uint16_t *kp = a.k_pool + slot * a.pool_stride, *vp = a.v_pool + slot * a.pool_stride;
     for (int r = group; __any_sync(0xffffffffu, r < G); r += stride) {
@@ -217,10 +241,12 @@ __global__ void __launch_bounds__(kThreads, 8) norm_rope_append_kernel(const App
 
 cudaError_t launch_norm_rope_append(const AppendArgs &a, int num_sms, cudaStream_t s) {
     const int groups = kThreads / (a.head_dim / 8);
-    // CTAs per token: one when the tokens alone fill the SMs, else down to one query row per group
-    int split = (a.num_heads + groups - 1) / groups;
-    const int64_t room = (8LL * num_sms + a.total_q - 1) / a.total_q;
-    if (split > room) split = (int)room;
+    // CTAs per token: as many as run at once, down to one query row per group, and one
+    // when the tokens alone fill the SMs.  1056 tokens of 32 query and 8 K/V heads of
+    // 128: two take 7.6 us, three (a second wave) 9.2 us, one 9.5 us; 128 tokens: 3.6 us
+    // with eight, 5.8 us with one.
+    const int64_t room = (int64_t)kCtasPerSm * num_sms / a.total_q;
+    const int split = (int)std::max<int64_t>(1, std::min<int64_t>((a.num_heads + groups - 1) / groups, room));
     const dim3 grid((unsigned)a.total_q, (unsigned)split);
     return a.head_dim == 128 ? launch_pdl(norm_rope_append_kernel<128>, grid, dim3(kThreads), 0, s, a)
                              : launch_pdl(norm_rope_append_kernel<64>, grid, dim3(kThreads), 0, s, a);
