@@ -626,7 +626,8 @@ ddt_status ddt_selftest_wait_timeout(uint32_t poll_limit, void *stream);
  *          kv_len_b - q_len_b (the root sits right behind the prefix);
  *   q goes to q_out, k and v to rows kv_indices[kv_indptr[b] + prefix_len_b + i]
  *          of the pools.
- * Arithmetic is fp32 with one rounding to bf16 at the end; v is copied.
+ * Arithmetic is fp32 with one rounding to bf16 at the end (a row's mean square
+ * has to be finite in fp32: values up to 2^63); v is copied.
  *
  *   q, k, v     (device) bf16 [total_q][heads][head_dim], token t at t * stride
  *               elements (q_stride, k_stride, v_stride: multiples of 8, at least
@@ -681,7 +682,7 @@ ddt_status ddt_gqa_norm_rope_append(
  *               for that; without a workspace, for batch > 256 and for short
  *               caches each request and K/V head has a CTA of its own.
  *   out         (device) bf16 [total_q][num_heads][head_dim], 16-byte aligned:
- *               what the layer's output projection reads.
+ *               what the layer's output projection reads; not q itself.
  *   lse         (device) float [total_q][num_heads] or NULL.
  *   workspace   (device) 256-byte aligned; ddt_gqa_verify_attn_workspace_size
  *               bytes for num_ctas, or NULL when that is 0.  Calls that may overlap

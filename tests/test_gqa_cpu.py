@@ -223,3 +223,7 @@ def test_norm_rope_form_keeps_lengths_and_angles():
 def test_compact_form():
     assert ref.compact([5, 1, 5, 7], 8) == ([0, 1, 0, 2], 3, [5, 1, 7, 3, 4, 5, 6, 7])
     assert ref.compact([], 3) == ([], 0, [0, 1, 2])
+
+
+def test_attention_refuses_its_query_as_output(lib):
+    assert call(lib, "ddt_gqa_verify_attn", ATTN, total_q=9) == INVALID

@@ -143,6 +143,7 @@ ddt_status ddt_gqa_verify_attn(
         misaligned(workspace, 256) || bad_pool_stride(pool_stride, num_kv_heads, head_dim))
         return DDT_ERR_INVALID_ARG;
     if (batch == 0 || total_q == 0 || max_q_len == 0) return DDT_OK;
+    if (out == q) return DDT_ERR_INVALID_ARG;  // CTAs that share an item read its q, one maybe after another's output
     unsigned int *err = ddt::device_error_word();
     if (!err) return DDT_ERR_CUDA;
 

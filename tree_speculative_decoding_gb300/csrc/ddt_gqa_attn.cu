@@ -976,7 +976,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps) gqa_combine_kernel(const G
     const int g = h / prm.group, rr = (t - r.qo0) * prm.group + h - g * prm.group;  // row of the request
     const int tg = rr / (kTiles * kRows), prow = rr - tg * kTiles * kRows;
     const int2 note = a.notes[((int64_t)b * a.num_kv_heads + g) * prm.tgs_most + tg];
-    if (note.x < 0) return;
+    if (note.x < 0) return;  // one CTA did the whole item
+    if (note.y >= a.num_ctas) return;  // nobody wrote it: the kernel before gave up (a timeout is latched)
     const int c0 = note.x >> 1, parts = note.y - c0 + 1;
     float m = -INFINITY, den = 0.f, acc[E];
 #pragma unroll

@@ -465,6 +465,15 @@ def _raw_stream(stream, dev):
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
 
 
+def _scratch(nbytes, dev, stream):
+    """A workspace of one call: the caching allocator may give its memory away again once the
+    call's own stream is past it, so it is allocated on that stream."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+
 def ddt_gqa_norm_rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, depth, qo_indptr, kv_indices,
                              kv_indptr, q_out, k_pool, v_pool, interleaved=False, stream=None):
     """Norm, rotation and cache append of a grouped-query layer in one pass.
@@ -550,7 +559,7 @@ def ddt_gqa_verify_attn(q, k_pool, v_pool, kv_indices, kv_indptr, qo_indptr, mas
         ctas = num_ctas or lib.ddt_gqa_verify_attn_num_ctas(B, H, G, max_q_len, max_kv_len, 0)
         nbytes = lib.ddt_gqa_verify_attn_workspace_size(B, H, G, D, max_q_len, ctas)
         if nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            workspace = _scratch(nbytes, dev, stream)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(),
@@ -635,7 +644,7 @@ def ddt_cache_compact(pool, kv_indices, new_indices, live, workspace=None, strea
     if new_indices.numel() != kv_indices.numel() or live.numel() != 1:
         raise ValueError("new_indices must have kv_indices' length, live one entry")
     if workspace is None:
-        workspace = torch.empty(max(1, lib.ddt_cache_compact_workspace_size(rows)), dtype=torch.uint8, device=dev)
+        workspace = _scratch(max(1, lib.ddt_cache_compact_workspace_size(rows)), dev, stream)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     i32 = torch.int32
