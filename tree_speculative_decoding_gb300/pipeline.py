@@ -214,3 +214,86 @@ class VerifyStep:
         st, bits = ddt.ddt_get_error()
         if st != 0:
             raise ddt.DDTError("device check", st, f"bits=0x{bits:x}")
+
+
+class GqaVerifyStep:
+    """One verify step of a stack of grouped-query layers for a Workload's requests, trees and
+    slots (its latent pool and queries are not used).
+
+    The model runs between the calls: ``build_tree_visibility`` once, then per layer ``layer`` on
+    the projections' q, k and v (norm and rotation, the cache rows of the new tokens, the tree
+    attention: its result is what the output projection reads), then ``accept`` on the target's
+    tokens and ``commit``, which moves the accepted rows of every layer at once.  ``kv`` is the
+    cache: [2 * num_layers, rows, num_kv_heads, head_dim], layer l's K pool at 2 l, its V pool at
+    2 l + 1.  ``compact`` moves the rows in use to the front of all of them."""
+
+    def __init__(self, wl, num_layers, num_heads, num_kv_heads, head_dim, cos_sin=None, eps=1e-6,
+                 interleaved=False, scale=None, device="cuda"):
+        self.wl, self.num_layers = wl, num_layers
+        self.device = dev = torch.device(device)
+        self.B, self.total_q = wl.B, wl.total_q
+        self.max_q_len, self.max_kv_len = int(wl.q_len.max()), int(wl.kv_len.max())
+        self.cos_sin, self.eps, self.interleaved = cos_sin, float(eps), interleaved
+        self.scale = head_dim ** -0.5 if scale is None else float(scale)
+        mip = ddt.ddt_mask_indptr(torch.from_numpy(wl.qo_indptr.astype(np.int32)),
+                                  torch.from_numpy(wl.prefix_len.astype(np.int32)))
+        T, W, i32 = self.total_q, wl.max_depth + 1, torch.int32
+        self.topk_logp = torch.from_numpy(np.ascontiguousarray(wl.topk_logp, np.float32)).to(dev)
+        for name in ("topk_ids", "root_id", "budget", "qo_indptr", "kv_indptr", "kv_indices", "prefix_len"):
+            setattr(self, name, _i32(getattr(wl, name), dev))
+        self.mask_indptr = mip.to(dev)
+        empty = lambda *shape, dtype=i32: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+        self.node_token, self.parent, self.depth = empty(T), empty(T), empty(T)
+        self.mask = empty(int(mip[-1]))
+        self.accept_len, self.bonus, self.new_len, self.live = empty(self.B), empty(self.B), empty(self.B), empty(1)
+        self.accepted_nodes, self.commit_tokens = empty(self.B, W), empty(self.B, W)
+        self.kv = torch.zeros((2 * num_layers, wl.pool_rows, num_kv_heads, head_dim), dtype=torch.bfloat16, device=dev)
+        self.q = empty(T, num_heads, head_dim, dtype=torch.bfloat16)  # normed and rotated
+        self.out = torch.empty_like(self.q)
+        ctas = ddt.ddt_gqa_verify_attn_num_ctas(self.B, num_heads, num_kv_heads, self.max_q_len, self.max_kv_len)
+        nbytes = ddt.ddt_gqa_verify_attn_workspace_size(self.B, num_heads, num_kv_heads, head_dim, self.max_q_len, ctas)
+        # the layers' attention and the compaction use it one after another
+        self.workspace = empty(max(nbytes, ddt.ddt_cache_compact_workspace_size(wl.pool_rows)), dtype=torch.uint8)
+
+    def build_tree_visibility(self, stream=None):
+        ddt.ddt_build_tree_visibility(self.topk_logp, self.topk_ids, self.root_id, self.budget,
+                                      self.qo_indptr, self.prefix_len, self.mask_indptr,
+                                      self.node_token, self.parent, self.depth, self.mask, stream)
+
+    def build_chain_visibility(self, stream=None):
+        """A causal chain in place of the tree: the layers then run a prefill chunk or a decode."""
+        ddt.ddt_build_chain_visibility(self.qo_indptr, self.prefix_len, self.mask_indptr,
+                                       self.parent, self.depth, self.mask, stream)
+
+    def layer(self, index, q, k, v, q_weight=None, k_weight=None, stream=None):
+        """Layer `index` between its projections: q [total_q, heads, head_dim], k and v [total_q,
+        K/V heads, head_dim] bf16; returns the attention's output, good until the next layer."""
+        k_pool, v_pool = self.kv[2 * index], self.kv[2 * index + 1]
+        ddt.ddt_gqa_norm_rope_append(q, k, v, q_weight, k_weight, self.eps, self.cos_sin, self.depth,
+                                     self.qo_indptr, self.kv_indices, self.kv_indptr, self.q, k_pool, v_pool,
+                                     interleaved=self.interleaved, stream=stream)
+        ddt.ddt_gqa_verify_attn(self.q, k_pool, v_pool, self.kv_indices, self.kv_indptr, self.qo_indptr, self.mask,
+                                self.mask_indptr, self.scale, self.out, max_q_len=self.max_q_len,
+                                max_kv_len=self.max_kv_len, workspace=self.workspace, stream=stream)
+        return self.out
+
+    def accept(self, target_argmax, stream=None):
+        ddt.ddt_accept(self.node_token, self.parent, self.qo_indptr, target_argmax, self.wl.max_depth,
+                       self.accept_len, self.accepted_nodes, self.commit_tokens, self.bonus, stream)
+
+    def commit(self, stream=None):
+        """The accepted rows of every layer to the positions after the prefix; new_len = prefix +
+        accept_len."""
+        ddt.ddt_cache_commit(self.kv, self.kv_indices, self.kv_indptr, self.qo_indptr, self.accept_len,
+                             self.accepted_nodes, self.wl.max_depth, self.new_len, stream)
+
+    def copy(self, src, dst, stream=None):
+        """Rows src of every layer to rows dst: a request forked or moved."""
+        ddt.ddt_cache_copy(self.kv, self.kv, src, dst, stream)
+
+    def compact(self, stream=None):
+        """The rows that kv_indices names to the front of every pool; kv_indices becomes their new
+        numbers, live their count."""
+        ddt.ddt_cache_compact(self.kv, self.kv_indices, self.kv_indices, self.live, self.workspace, stream)
+
+    check_device_errors = VerifyStep.check_device_errors
