@@ -121,6 +121,67 @@ def test_attention_values_that_are_seen_come_out(ddt, H, T, bad, ctas):
     assert ((out.double().cpu() - o).abs() <= bo)[~hit].all()
 
 
+@pytest.mark.parametrize("H,G,T,D", [(8, 2, 5, 64), (64, 2, 4, 64), (64, 2, 5, 64), (8, 1, 17, 128), (16, 2, 33, 128)])
+@pytest.mark.parametrize("ctas", [1, 4, 0])
+def test_attention_of_a_query_that_is_nan(ddt, H, G, T, D, ctas):
+    # its row is NaN whole, no other one is; in tiles, lone tiles and the few rows behind a tile
+    batch = ref.Batch([(700, T)], 101, "tree")
+    q, k, v, kd, vd = base.attn_inputs(batch, H, G, D, 102, q_scale=0.5)
+    o, l, bo, bl = ref.attention(q, k, v, batch, 0.1)
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool)
+    hit[0, 0] = hit[T - 1, H - 1] = hit[T // 2, H // 2] = True
+    q[hit] = float("nan")
+    out, ls = base.run_attn(ddt, batch, q, kd, vd, 0.1, ctas)
+    clean(ddt)
+    assert out.cpu()[hit].isnan().all() and ls.cpu()[hit].isnan().all()
+    assert ((out.double().cpu() - o).abs() <= bo)[~hit].all() and ((ls.double().cpu() - l).abs() <= bl)[~hit].all()
+
+
+FEW = [
+    # heads, kv heads, dim, (prefix, new tokens) per request: 1 to 8 rows behind one or two tiles
+    (8, 1, 128, [(300, 17), (40, 33), (1000, 33)]), (16, 2, 64, [(500, 33), (0, 17), (129, 65), (600, 3)]),
+    (1, 1, 128, [(400, 128)]), (4, 1, 64, [(700, 33), (511, 65), (200, 34), (60, 97)]), (43, 1, 128, [(300, 3), (20, 6)]),
+    (43, 1, 64, [(290, 6)]), (128, 1, 128, [(270, 1), (10, 2)]), (5, 1, 128, [(257, 26), (400, 52), (300, 27)]),
+]
+
+
+@pytest.mark.parametrize("H,G,D,lens", FEW)
+@pytest.mark.parametrize("mask", ["tree", "random"])
+@pytest.mark.parametrize("ctas", [0, 1, 2, 5, 40])
+def test_attention_of_a_few_rows_behind_a_tile(ddt, H, G, D, lens, mask, ctas):
+    batch = ref.Batch(lens, 103 + H, mask)
+    q, k, v, kd, vd = base.attn_inputs(batch, H, G, D, 104)
+    out, ls = base.run_attn(ddt, batch, q, kd, vd, D ** -0.5, ctas)
+    clean(ddt)
+    base.check_attn(out, ls, q, k, v, batch, D ** -0.5)
+
+
+@pytest.mark.parametrize("ctas", [0, 3])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_of_a_few_rows_with_unseen_nan_and_rising_scores(ddt, D, ctas):
+    batch = ref.Batch([(900, 33)], 105, "tree")
+    H = 8
+    q, k, v, kd, vd = base.attn_inputs(batch, H, 1, D, 106)
+    steps = torch.from_numpy(np.repeat(np.arange(batch.total_kv // 37 + 1), 37)[: batch.total_kv].astype(np.float32) * 2.0)
+    at = torch.from_numpy(batch.slots.astype(np.int64))
+    k[at, 0, 0] = steps.to(torch.bfloat16)
+    q[:, :, 0] = 32.0
+    kd.copy_(k)
+    # a node that the last one does not see holds anything
+    hidden = [n for n in range(33) if not batch.vis[0][32, 900 + n]]
+    for n, bad in zip(hidden, (float("nan"), float("inf"), float("-inf"))):
+        others = [i for i in range(33) if batch.vis[0][i, 900 + n]]
+        kd[int(batch.slots[900 + n])] = bad
+        vd[int(batch.slots[900 + n])] = bad
+        batch.vis[0][others] = False     # rows that see it are not compared
+    keep = torch.from_numpy(batch.vis[0].any(1))
+    assert keep[32] and int(keep.sum()) > 3
+    out, ls = base.run_attn(ddt, batch, q, kd, vd, 1.0, ctas)
+    clean(ddt)
+    o, l, bo, bl = ref.attention(q, k, v, batch, 1.0)
+    assert ((out.double().cpu() - o).abs() <= bo)[keep].all() and ((ls.double().cpu() - l).abs() <= bl)[keep].all()
+
+
 def test_attention_on_two_streams_at_once(ddt):
     batches = [ref.Batch([(3000, 9)], 73, "tree"), ref.Batch([(2500, 33)], 74, "tree")]
     made = [base.attn_inputs(b, 16, 2, 128, 75 + i) for i, b in enumerate(batches)]

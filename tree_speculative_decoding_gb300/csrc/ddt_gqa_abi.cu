@@ -193,7 +193,7 @@ ddt_status ddt_gqa_verify_attn(
         a.o_part = reinterpret_cast<float *>(p);
         a.lse_part = reinterpret_cast<float *>(p + align256(rows * head_dim * sizeof(float)));
     }
-    return launched(ddt::launch_gqa_attn(a, as_stream(stream)));
+    return launched(ddt::launch_gqa_attn(a, ddt::device_sm_count(), as_stream(stream)));
 }
 
 ddt_status ddt_cache_copy(const void *src_slab, int64_t src_pool_bytes, int64_t src_pool_rows,

@@ -130,11 +130,15 @@ struct Cfg {
     static constexpr int kSmemBytes = kSmemUsed + 1024;  // slack for the 1024-byte alignment of swizzle atoms
     static constexpr uint32_t kIdescS = idesc_bf16(kRows, NB, 0, 0);
     static constexpr uint32_t kIdescPV = idesc_bf16(kRows, D, 0, 1);
-    // cost of a block with all tiles and with one, and of an item besides its blocks
-    // (its q, the latency of its first loads, its epilogue), in one unit; the share
-    // that a CTA gets at least
-    static constexpr int kCostFull = kTiles == 2 ? 16 : 8, kCostOne = kTiles == 2 ? 11 : 8, kCostItem = 24;
-    static constexpr int kMinShare = kTiles == 2 ? 80 : 36;
+    // Cost of a block with all tiles and with one, in one unit; of an item besides its
+    // blocks: a CTA that goes on to another one writes the last one's rows, loads q and
+    // fills its pipeline anew, 6 to 10 us (two tiles) or 2 to 3 us; and the share that a CTA
+    // gets at least.  Measured with D = 128, 64 heads on 8: 8 requests of 33 tokens after
+    // 1024..16384 take 131 us with an item at 72, 149 us at 24, 135 us at 160; one request
+    // of 33 after 1024 20 us with shares of 48, 24 us of 80, 35 us of 200; one token after
+    // 600 12.2 us with an item at 48 and shares of 28, 14.0 us at 24 and 36, 15.2 us at 64 and 80.
+    static constexpr int kCostFull = kTiles == 2 ? 16 : 8, kCostOne = kTiles == 2 ? 11 : 8;
+    static constexpr int kCostItem = kTiles == 2 ? 80 : 48, kMinShare = kTiles == 2 ? 56 : 32;
     static_assert(kTiles == 2 || (kKStages >= 2 && kKStages <= kVStages), "see the load warps");
     static_assert(kOffPlan % 8 == 0, "alignment");
     static_assert(kColO + kTiles * D <= kTmemCols, "tensor memory");
@@ -831,8 +835,8 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                 } else {
                     ok = warp_wait(bar(C::bJoin), joins & 1, abort_flag, a.err);
                     const float m1 = place[0], l1 = place[1], m = fmaxf(m_ref, m1);
-                    keep0 = m_ref == -INFINITY ? 0.f : ex2(m_ref - m);
-                    keep1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
+                    keep0 = m_ref == -INFINITY ? l : ex2(m_ref - m);  // without a reference the sum is 0, or NaN
+                    keep1 = m1 == -INFINITY ? l1 : ex2(m1 - m);
                     l = (keep0 != 0.f ? l * keep0 : 0.f) + (keep1 != 0.f ? l1 * keep1 : 0.f);
                     m_ref = m;
                 }
@@ -953,102 +957,124 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
     }
 }
 
-// out = sum_s e^{lse_s - LSE} o_s over the parts s of the row's item, LSE = log
-// sum_s e^{lse_s}.  One warp per (token, head) row: lane s holds part s's
-// weight, 32 parts at a time, then the lanes sum D / 32 values each.  Items that
-// one CTA did are in place already.
+// out = sum_s e^{lse_s - LSE} o_s over the parts s of a cut item, LSE = log sum_s
+// e^{lse_s}.  A CTA has 8 kRowsOfWarp rows of an item and leaves at once where one
+// CTA did the item whole; a warp joins kRowsOfWarp rows at a time: 32 / kRowsOfWarp
+// lanes hold the weights of that many parts of each, then all lanes sum D / 32
+// values of every row.
 constexpr int kCombineWarps = 8;
 
-template <int D, int kTiles>
+template <int D, int kTiles, int kRowsOfWarp>
 __global__ void __launch_bounds__(32 * kCombineWarps) gqa_combine_kernel(const GqaParams prm) {
     using C = Cfg<D, kTiles>;
-    constexpr int E = D / 32;
+    constexpr int E = D / 32, R = kRowsOfWarp, L = 32 / R;  // lanes of a row's parts
+    constexpr int kFlight = 8 / R;                          // parts in flight
     const GqaArgs &a = prm.a;
     const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x, h = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
+    const int bg = blockIdx.x / prm.tgs_most, tg = blockIdx.x - bg * prm.tgs_most;
+    const int b = bg / a.num_kv_heads, g = bg - b * a.num_kv_heads;
+    const int first = (blockIdx.y * kCombineWarps + (threadIdx.x >> 5)) * R;  // of the item's rows
     pdl_wait();
     pdl_trigger();
-    if (h >= a.num_heads) return;
-    const int b = find_request(a.qo_indptr, a.batch, t, lane);
-    if (b >= a.batch) return;
+    const int2 note = a.notes[blockIdx.x];
     const Request r = load_request<C, kTiles>(a, prm.group, b, nullptr);
-    if (r.tgs == 0 || t - r.qo0 >= r.T) return;  // nothing to do, or refused
-    const int g = h / prm.group, rr = (t - r.qo0) * prm.group + h - g * prm.group;  // row of the request
-    const int tg = rr / (kTiles * kRows), prow = rr - tg * kTiles * kRows;
-    const int2 note = a.notes[((int64_t)b * a.num_kv_heads + g) * prm.tgs_most + tg];
-    if (note.x < 0) return;  // one CTA did the whole item
-    if (note.y >= a.num_ctas) return;  // nobody wrote it: the kernel before gave up (a timeout is latched)
+    if (tg >= r.tgs || note.x < 0) return;  // no such item, or one CTA did it whole
+    if (note.y >= a.num_ctas) return;       // nobody wrote it: the kernel before gave up (a timeout is latched)
+    const int row0 = tg * kTiles * kRows, rows = min(kTiles * kRows, r.T * prm.group - row0);
+    if (first >= rows) return;
     const int c0 = note.x >> 1, parts = note.y - c0 + 1;
-    float m = -INFINITY, den = 0.f, acc[E];
+    // row i of the warp; lanes of rows that are not there repeat the last one
+    auto place = [&](int s, int i) { return (int64_t)(s == 0 ? note.x : 2 * (c0 + s)) * prm.part_rows + min(first + i, rows - 1); };
+    float m = -INFINITY, den = 0.f;  // of the lane's row (lane / L)
+    float acc[R][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int s0 = 0; s0 < parts; s0 += 32) {
-        const int c = c0 + s0 + lane;
-        int64_t at = 0;
-        float ls = -INFINITY;
-        if (s0 + lane < parts) {
-            at = (int64_t)(c == c0 ? note.x : 2 * c) * prm.part_rows + prow;
-            ls = a.lse_part[at];
-        }
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[i][e] = 0.f;
+    for (int s0 = 0; s0 < parts; s0 += L) {
+        const int mine = s0 + lane % L;
+        const float ls = mine < parts ? a.lse_part[place(mine, lane / L)] : -INFINITY;
         float mg = fmaxf(m, ls);
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, o));
+        for (int o = L / 2; o >= 1; o >>= 1) mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, o));
         const float keep = m == -INFINITY ? 0.f : ex2((m - mg) * kLog2e);
         const float w = ls == -INFINITY ? 0.f : ex2((ls - mg) * kLog2e);  // NaN stays
         float sum = w;
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        for (int o = L / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         den = den * keep + sum;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] *= keep;
         m = mg;
-        const int n = min(32, parts - s0);
-        constexpr int kFlight = 8;  // parts' rows in flight
-        for (int s = 0; s < n; s += kFlight) {
-            float v[kFlight][E];
+        if (s0 > 0) {
 #pragma unroll
-            for (int i = 0; i < kFlight; ++i) {
-                if (s + i >= n) break;
-                const float *o = a.o_part + __shfl_sync(0xffffffffu, (long long)at, s + i) * D + lane * E;
-                if constexpr (E == 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(o);
-                    v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
-                } else {
-                    const float2 x = *reinterpret_cast<const float2 *>(o);
-                    v[i][0] = x.x; v[i][1] = x.y;
+            for (int i = 0; i < R; ++i) {
+                const float k = __shfl_sync(0xffffffffu, keep, i * L);
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[i][e] *= k;
+            }
+        }
+        const int n = min(L, parts - s0);
+        for (int s = 0; s < n; s += kFlight) {
+            float v[kFlight][R][E];
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) {
+                if (s + u >= n) break;
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const float *o = a.o_part + place(s0 + s + u, i) * D + lane * E;
+                    if constexpr (E == 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(o);
+                        v[u][i][0] = x.x; v[u][i][1] = x.y; v[u][i][2] = x.z; v[u][i][3] = x.w;
+                    } else {
+                        const float2 x = *reinterpret_cast<const float2 *>(o);
+                        v[u][i][0] = x.x; v[u][i][1] = x.y;
+                    }
                 }
             }
 #pragma unroll
-            for (int i = 0; i < kFlight; ++i) {
-                if (s + i >= n) break;
-                const float ws = __shfl_sync(0xffffffffu, w, s + i);
+            for (int u = 0; u < kFlight; ++u) {
+                if (s + u >= n) break;
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = fmaf(ws, v[i][e], acc[e]);
+                for (int i = 0; i < R; ++i) {
+                    const float ws = __shfl_sync(0xffffffffu, w, i * L + s + u);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[i][e] = fmaf(ws, v[u][i][e], acc[i][e]);
+                }
             }
         }
     }
-    const int64_t row = (int64_t)t * a.num_heads + h;
-    const float inv = den == 0.f ? 0.f : 1.f / den;
-    uint16_t *dst = a.out + row * D + lane * E;
-    if constexpr (E == 4)
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
-    else
-        *reinterpret_cast<uint32_t *>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
-    if (a.lse && lane == 0) a.lse[row] = den == 0.f ? -INFINITY : m + log2f(den) * kLn2;
+    const float inv = den == 0.f ? 0.f : 1.f / den, lse = den == 0.f ? -INFINITY : m + log2f(den) * kLn2;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const float k = __shfl_sync(0xffffffffu, inv, i * L), ls = __shfl_sync(0xffffffffu, lse, i * L);
+        if (first + i >= rows) break;
+        const int rr = row0 + first + i, node = quotient(rr, prm.group_inv);
+        const int64_t row = (int64_t)(r.qo0 + node) * a.num_heads + g * prm.group + rr - node * prm.group;
+        uint16_t *dst = a.out + row * D + lane * E;
+        if constexpr (E == 4)
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(acc[i][0] * k, acc[i][1] * k), pack_bf16(acc[i][2] * k, acc[i][3] * k));
+        else
+            *reinterpret_cast<uint32_t *>(dst) = pack_bf16(acc[i][0] * k, acc[i][1] * k);
+        if (a.lse && lane == 0) a.lse[row] = ls;
+    }
 }
 
 int tiles_per_item(int max_q_len, int group) { return max_q_len * group > kRows ? 2 : 1; }
 
 template <int D, int kTiles>
-cudaError_t launch(GqaParams &prm, cudaStream_t s) {
+cudaError_t launch(GqaParams &prm, int num_sms, cudaStream_t s) {
     using C = Cfg<D, kTiles>;
     GqaArgs &a = prm.a;
     const dim3 grid = a.num_ctas > 0 ? dim3((unsigned)a.num_ctas)
                                      : dim3((unsigned)(prm.tgs_most * a.num_kv_heads), 1, (unsigned)a.batch);
     cudaError_t e = launch_pdl(gqa_attn_kernel<D, kTiles>, grid, dim3(C::kThreads), C::kSmemBytes, s, prm);
     if (e == cudaSuccess && a.num_ctas > 0) {
-        const dim3 rows((unsigned)a.total_q, (unsigned)((a.num_heads + kCombineWarps - 1) / kCombineWarps));
-        e = launch_pdl(gqa_combine_kernel<D, kTiles>, rows, dim3(32 * kCombineWarps), 0, s, prm);
+        // four rows of a warp at once where there are many: 8448 rows (4 requests of 33 x 64)
+        // 40.1 us with the attention against 42.2 us, 25600 rows 113 against 121, 2112 rows 31.8 against 30.2
+        const int R = (int64_t)a.total_q * a.num_heads > 32LL * num_sms ? 4 : 1;
+        const dim3 items((unsigned)(a.batch * a.num_kv_heads * prm.tgs_most),
+                         (unsigned)((prm.part_rows + kCombineWarps * R - 1) / (kCombineWarps * R)));
+        e = launch_pdl(R == 4 ? gqa_combine_kernel<D, kTiles, 4> : gqa_combine_kernel<D, kTiles, 1>, items,
+                       dim3(32 * kCombineWarps), 0, s, prm);
     }
     return e;
 }
@@ -1096,7 +1122,7 @@ int gqa_tile_groups(int max_q_len, int group) {
     return (max_q_len * group + per - 1) / per;
 }
 
-cudaError_t launch_gqa_attn(const GqaArgs &a, cudaStream_t s) {
+cudaError_t launch_gqa_attn(const GqaArgs &a, int num_sms, cudaStream_t s) {
     GqaParams prm;
     prm.a = a;
     prm.group = a.num_heads / a.num_kv_heads;
@@ -1104,8 +1130,8 @@ cudaError_t launch_gqa_attn(const GqaArgs &a, cudaStream_t s) {
     prm.part_rows = gqa_part_rows(a.max_q_len, prm.group);
     prm.tgs_most = gqa_tile_groups(a.max_q_len, prm.group);
     const bool two = tiles_per_item(a.max_q_len, prm.group) == 2;
-    if (a.head_dim == 128) return two ? launch<128, 2>(prm, s) : launch<128, 1>(prm, s);
-    return two ? launch<64, 2>(prm, s) : launch<64, 1>(prm, s);
+    if (a.head_dim == 128) return two ? launch<128, 2>(prm, num_sms, s) : launch<128, 1>(prm, num_sms, s);
+    return two ? launch<64, 2>(prm, num_sms, s) : launch<64, 1>(prm, num_sms, s);
 }
 
 }  // namespace ddt

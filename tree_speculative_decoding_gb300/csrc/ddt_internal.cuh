@@ -198,7 +198,7 @@ struct GqaArgs {
 constexpr int kGqaMaxDealtBatch = 256;  // a thread per request sizes the line
 // kernel attributes, once per device (see attn_prepare_device)
 cudaError_t gqa_prepare_device();
-cudaError_t launch_gqa_attn(const GqaArgs &a, cudaStream_t s);
+cudaError_t launch_gqa_attn(const GqaArgs &a, int num_sms, cudaStream_t s);
 // the CTAs that the work is dealt to for these bounds, or 0 (see GqaArgs)
 int gqa_choose_ctas(int batch, int num_heads, int num_kv_heads, int max_q_len, int max_kv_len, int num_sms);
 // rows of a partial result; most items per K/V head of a request
