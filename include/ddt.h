@@ -768,6 +768,23 @@ ddt_status ddt_cache_compact(void *slab, int64_t pool_bytes, int64_t pool_rows, 
                              int32_t *new_indices, int32_t *live, void *workspace,
                              size_t workspace_bytes, void *stream);
 
+/*
+ * ddt_call_words -- one of the five calls above with its arguments as 64-bit
+ * words, for bindings that pay for every argument (ctypes: 0.1 us each):
+ * words[0] names the call, words[1] counts the arguments, which follow in the
+ * order of the parameters: pointers and integers as they are, floats as the
+ * bits of a double.  An integer that does not fit its parameter, another count
+ * or another name is DDT_ERR_INVALID_ARG.  words is host memory.
+ */
+enum {
+    DDT_CALL_GQA_NORM_ROPE_APPEND = 0,
+    DDT_CALL_GQA_VERIFY_ATTN = 1,
+    DDT_CALL_CACHE_COPY = 2,
+    DDT_CALL_CACHE_COMMIT = 3,
+    DDT_CALL_CACHE_COMPACT = 4
+};
+ddt_status ddt_call_words(const int64_t *words);
+
 #ifdef __cplusplus
 }
 #endif

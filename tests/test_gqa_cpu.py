@@ -225,5 +225,31 @@ def test_compact_form():
     assert ref.compact([], 3) == ([], 0, [0, 1, 2])
 
 
+def test_calls_in_words_answer_as_the_calls_do(lib):
+    import struct
+    calls = ["ddt_gqa_norm_rope_append", "ddt_gqa_verify_attn", "ddt_cache_copy", "ddt_cache_commit", "ddt_cache_compact"]
+
+    def words(name, args, count=None):
+        num = lambda x: 0 if x is None else x.value if isinstance(x, ctypes.c_void_p) else x  # noqa: E731
+        w = [struct.pack("=d" if t is ctypes.c_float else "=q", num(x)) for t, x in zip(getattr(lib, name).argtypes, args)]
+        return struct.pack("=qq", calls.index(name), len(w) if count is None else count) + b"".join(w)
+
+    for name, good in (("ddt_gqa_norm_rope_append", APPEND), ("ddt_gqa_verify_attn", ATTN)):
+        assert len(getattr(lib, name).argtypes) == len(good)
+        for changes in ({}, dict(H=63), dict(H=136), dict(D=96), dict(batch=-1), dict(out=None) if "out" in good else {},
+                        dict(scale=-1.0) if "scale" in good else dict(eps=-1.0), dict(stride=1028) if "stride" in good else {}):
+            args = list({**good, **changes}.values())
+            assert lib.ddt_call_words(words(name, args)) == getattr(lib, name)(*args), (name, changes)
+        args = list(good.values())
+        assert lib.ddt_call_words(words(name, args, len(args) - 1)) == INVALID
+        assert lib.ddt_call_words(words(name, list({**good, "H": 64 + 2 ** 32}.values()))) == INVALID   # does not fit
+    assert lib.ddt_call_words(struct.pack("=qq", 5, 0)) == INVALID and lib.ddt_call_words(None) == INVALID
+    assert lib.ddt_call_words(struct.pack("=qq", -1, 0)) == INVALID
+    # a copy of nothing, and one with a bad row width
+    args = [P, 1024, 64, P, 1024, 64, 1, 16, None, None, 0, None]
+    assert lib.ddt_call_words(words("ddt_cache_copy", args)) == 0
+    assert lib.ddt_call_words(words("ddt_cache_copy", args[:7] + [24] + args[8:])) == INVALID
+
+
 def test_attention_refuses_its_query_as_output(lib):
     assert call(lib, "ddt_gqa_verify_attn", ATTN, total_q=9) == INVALID

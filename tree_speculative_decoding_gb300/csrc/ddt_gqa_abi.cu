@@ -5,6 +5,9 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <type_traits>
+#include <utility>
+
 #include "ddt_internal.cuh"
 
 namespace {
@@ -35,6 +38,32 @@ bool bad_slab(const void *slab, int64_t pool_bytes, int64_t pool_rows, int32_t n
         pool_bytes % 16 || row_bytes / 16 > INT32_MAX)
         return true;
     return pool_rows > INT64_MAX / row_bytes || pool_bytes < pool_rows * row_bytes;
+}
+
+// a parameter of type T from its word; fits: false where it does not hold the word's value
+template <class T>
+T from_word(int64_t w, bool &fits) {
+    if constexpr (std::is_pointer_v<T>) {
+        return reinterpret_cast<T>((uintptr_t)w);
+    } else if constexpr (std::is_floating_point_v<T>) {
+        double d;
+        memcpy(&d, &w, sizeof d);
+        return (T)d;
+    } else {
+        fits = fits && (int64_t)(T)w == w;
+        return (T)w;
+    }
+}
+template <class... A, size_t... I>
+ddt_status call_with(ddt_status (*f)(A...), const int64_t *words, std::index_sequence<I...>) {
+    bool fits = words[1] == (int64_t)sizeof...(A);
+    if (!fits) return DDT_ERR_INVALID_ARG;
+    const auto go = [&](A... a) { return fits ? f(a...) : DDT_ERR_INVALID_ARG; };
+    return go(from_word<A>(words[2 + I], fits)...);
+}
+template <class... A>
+ddt_status call_words(ddt_status (*f)(A...), const int64_t *words) {
+    return call_with(f, words, std::index_sequence_for<A...>{});
 }
 
 }  // namespace
@@ -247,6 +276,18 @@ ddt_status ddt_cache_compact(void *slab, int64_t pool_bytes, int64_t pool_rows, 
     return launched(ddt::launch_cache_compact(slab, pool_bytes, pool_rows, num_pools, row_bytes, kv_indices, total,
                                               new_indices, live, workspace, ddt::device_sm_count(), err,
                                               as_stream(stream)));
+}
+
+ddt_status ddt_call_words(const int64_t *words) {
+    if (!words) return DDT_ERR_INVALID_ARG;
+    switch (words[0]) {
+        case DDT_CALL_GQA_NORM_ROPE_APPEND: return call_words(ddt_gqa_norm_rope_append, words);
+        case DDT_CALL_GQA_VERIFY_ATTN: return call_words(ddt_gqa_verify_attn, words);
+        case DDT_CALL_CACHE_COPY: return call_words(ddt_cache_copy, words);
+        case DDT_CALL_CACHE_COMMIT: return call_words(ddt_cache_commit, words);
+        case DDT_CALL_CACHE_COMPACT: return call_words(ddt_cache_compact, words);
+    }
+    return DDT_ERR_INVALID_ARG;
 }
 
 }  // extern "C"

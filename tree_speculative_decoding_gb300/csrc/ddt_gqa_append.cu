@@ -15,7 +15,7 @@
 // factors per pair once per token.  A CTA takes a token and its groups walk the
 // token's rows.  What bounds a CTA is its chain of dependent loads, so the first
 // rows, the weights and the depth are loaded before the token's request is looked
-// up, and its slot and angles at once behind that.  4096 tokens of 32 query and 8
+// up, and its slot and angles at once behind that.  4096 tokens of 64 query and 8
 // K/V heads of 128 in 32 requests take 30.3 us, 5.6 TB/s (33.5 us with 128 threads
 // and 8 CTAs per SM, 35.3 us with 12 of these and 32.7 us with 16).  The angles are read from the caller's table: sine and cosine
 // of far positions need more than fp32, once per position and not per token.
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_append_kernel(
 cudaError_t launch_norm_rope_append(const AppendArgs &a, int num_sms, cudaStream_t s) {
     const int groups = kThreads / (a.head_dim / 8);
     // CTAs per token: as many as run at once, down to one query row per group, and one
-    // when the tokens alone fill the SMs.  1056 tokens of 32 query and 8 K/V heads of
+    // when the tokens alone fill the SMs.  1056 tokens of 64 query and 8 K/V heads of
     // 128: two take 7.6 us, three (a second wave) 9.2 us, one 9.5 us; 128 tokens: 3.6 us
     // with eight, 5.8 us with one.
     const int64_t room = (int64_t)kCtasPerSm * num_sms / a.total_q;

@@ -8,13 +8,16 @@ missing or fails to load, importing this module raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
 from . import _build
 
 DL, DR, D = 512, 64, 576
+_BF16, _I32 = torch.bfloat16, torch.int32
 MAX_DEPTH, MAX_TOPK, MAX_Q_LEN, MAX_SPLITS = 7, 16, 128, 128
 
 STATUS = {0: "DDT_OK", 1: "DDT_ERR_INVALID_ARG", 2: "DDT_ERR_UNSUPPORTED", 3: "DDT_ERR_WORKSPACE",
@@ -25,6 +28,20 @@ class DDTError(RuntimeError):
     def __init__(self, fn, status, detail=""):
         self.status = status
         super().__init__(f"{fn}: {STATUS.get(status, status)}{(' ' + detail) if detail else ''}")
+
+
+# The calls that go through ddt_call_words, in the order of its numbers: their
+# arguments are packed into one buffer, which costs a fifth of what ctypes takes
+# for the 12 to 29 of them.
+_IN_WORDS = dict.fromkeys(("ddt_gqa_norm_rope_append", "ddt_gqa_verify_attn", "ddt_cache_copy", "ddt_cache_commit",
+                           "ddt_cache_compact"))
+
+
+def _call(name, *args):
+    """The call with its arguments (a null pointer is 0)."""
+    st = lib.ddt_call_words(_IN_WORDS[name](*args))
+    if st != 0:
+        raise DDTError(name, st)
 
 
 def _load():
@@ -65,6 +82,7 @@ def _load():
         "ddt_cache_commit": ([P, i64, i64, i32, i64, P, P, P, P, P, i32, i32, i32, P, P], i32),
         "ddt_cache_compact_workspace_size": ([i64], sz),
         "ddt_cache_compact": ([P, i64, i64, i32, i64, P, i32, P, P, P, sz, P], i32),
+        "ddt_call_words": ([ctypes.c_char_p], i32),
         "ddt_get_error": ([P, P], i32),
         "ddt_selftest_wait_timeout": ([ctypes.c_uint32, P], i32),
         "ddt_verify_step": ([P, P], i32),
@@ -78,6 +96,10 @@ def _load():
         f = getattr(lib, name)
         f.argtypes = args
         f.restype = res
+    for i, name in enumerate(_IN_WORDS):
+        args = sig[name][0]
+        pack = struct.Struct("=qq" + "".join("d" if a is f32 else "q" for a in args)).pack
+        _IN_WORDS[name] = functools.partial(pack, i, len(args))
     return lib
 
 
@@ -441,9 +463,10 @@ def _mask_ptr(mask, dev):
 def _heads(t, dev, name, heads=None):
     """Pointer, row stride, rows, heads and head_dim of a [rows, heads, head_dim] bf16 tensor
     whose rows are contiguous (the rows themselves may be apart)."""
-    if t.dtype is not torch.bfloat16 or t.device != dev or t.dim() != 3:
+    shape = t.shape
+    if t.dtype is not _BF16 or t.device != dev or len(shape) != 3:
         raise ValueError(f"{name} must be a [rows, heads, head_dim] bfloat16 tensor on {dev}")
-    n, h, d = t.shape
+    n, h, d = shape
     sn, sh, sd = t.stride()
     if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
@@ -489,7 +512,7 @@ def ddt_gqa_norm_rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, depth, q
     kpp, vpp, stride, rows, Gp, Dp = _pools(k_pool, v_pool, dev)
     if nk != total_q or nv != total_q or k.shape[2] != D or (Gp, Dp) != (G, D):
         raise ValueError("q, k, v and the pools must agree in tokens, K/V heads and head_dim")
-    if q_out.shape != q.shape:
+    if q_out.shape != (total_q, H, D):
         raise ValueError("q_out must have q's shape")
     for n, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is not None and w.numel() != D:
@@ -506,16 +529,16 @@ def ddt_gqa_norm_rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, depth, q
         raise ValueError("depth must hold an entry per token")
     if total_q == 0 or B == 0:
         return
-    i32, bf16 = torch.int32, torch.bfloat16
-    _check("ddt_gqa_norm_rope_append", lib.ddt_gqa_norm_rope_append(
-        qp, qs, kp, ks, vp, vs,
-        None if q_weight is None else _like(q_weight, bf16, dev, "q_weight"),
-        None if k_weight is None else _like(k_weight, bf16, dev, "k_weight"), eps,
-        None if cos_sin is None else _like(cos_sin, torch.float32, dev, "cos_sin"), max_pos, rope_dim,
-        int(bool(interleaved)), None if depth is None else _like(depth, i32, dev, "depth"),
+    i32, bf16 = _I32, _BF16
+    _call(
+        "ddt_gqa_norm_rope_append", qp, qs, kp, ks, vp, vs,
+        0 if q_weight is None else _like(q_weight, bf16, dev, "q_weight"),
+        0 if k_weight is None else _like(k_weight, bf16, dev, "k_weight"), eps,
+        0 if cos_sin is None else _like(cos_sin, torch.float32, dev, "cos_sin"), max_pos, rope_dim,
+        int(bool(interleaved)), 0 if depth is None else _like(depth, i32, dev, "depth"),
         _like(qo_indptr, i32, dev, "qo_indptr"), _like(kv_indices, i32, dev, "kv_indices"),
         _like(kv_indptr, i32, dev, "kv_indptr"), B, total_q, kv_indices.numel(), H, G, D,
-        _like(q_out, bf16, dev, "q_out"), kpp, vpp, stride, rows, _raw_stream(stream, dev)))
+        _like(q_out, bf16, dev, "q_out"), kpp, vpp, stride, rows, _raw_stream(stream, dev))
 
 
 def ddt_gqa_verify_attn_num_ctas(batch, num_heads, num_kv_heads, max_q_len, max_kv_len, num_sms=0):
@@ -543,9 +566,9 @@ def ddt_gqa_verify_attn(q, k_pool, v_pool, kv_indices, kv_indptr, qo_indptr, mas
         raise ValueError("q and the pools must have the same head_dim")
     if qs != H * D:
         raise ValueError("q must be contiguous")
-    if out.shape != q.shape:
+    if out.shape != (total_q, H, D):
         raise ValueError("out must have q's shape")
-    if lse is not None and lse.shape != q.shape[:2]:
+    if lse is not None and lse.shape != (total_q, H):
         raise ValueError("lse must be [total_q, H]")
     B = qo_indptr.numel() - 1
     if kv_indptr.numel() != B + 1 or mask_indptr.numel() != B + 1:
@@ -562,24 +585,29 @@ def ddt_gqa_verify_attn(q, k_pool, v_pool, kv_indices, kv_indptr, qo_indptr, mas
             workspace = _scratch(nbytes, dev, stream)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(),
-                                                        workspace.numel() * workspace.element_size())
-    i32, bf16 = torch.int32, torch.bfloat16
-    _check("ddt_gqa_verify_attn", lib.ddt_gqa_verify_attn(
-        qp, kp, vp, stride, rows, _like(kv_indices, i32, dev, "kv_indices"),
+    ws, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(),
+                                                     workspace.numel() * workspace.element_size())
+    i32, bf16 = _I32, _BF16
+    _call(
+        "ddt_gqa_verify_attn", qp, kp, vp, stride, rows, _like(kv_indices, i32, dev, "kv_indices"),
         _like(kv_indptr, i32, dev, "kv_indptr"), _like(qo_indptr, i32, dev, "qo_indptr"),
         _mask_ptr(mask, dev), _like(mask_indptr, i32, dev, "mask_indptr"), B, H, G, D, total_q,
         kv_indices.numel(), mask.numel(), max_q_len, max_kv_len, scale, num_ctas,
-        _like(out, bf16, dev, "out"), None if lse is None else _like(lse, torch.float32, dev, "lse"),
-        ws, ws_bytes, _raw_stream(stream, dev)))
+        _like(out, bf16, dev, "out"), 0 if lse is None else _like(lse, torch.float32, dev, "lse"),
+        ws, ws_bytes, _raw_stream(stream, dev))
 
 
 def _slab(t, dev, name):
     """Pointer, bytes between pools, rows, pools and row bytes of a [pools, rows, ...] tensor whose
     pools are contiguous (the pools themselves may be apart)."""
-    if t.dim() < 3 or t.device != dev:
+    shape, es = t.shape, t.element_size()
+    if len(shape) < 3 or t.device != dev:
         raise ValueError(f"{name} must be a [pools, rows, ...] tensor on {dev}")
-    shape, strides, es = t.shape, t.stride(), t.element_size()
+    if t.is_contiguous() and 0 not in shape:
+        pools, rows = shape[0], shape[1]
+        row = t.numel() // (pools * rows) * es
+        return t.data_ptr(), rows * row, rows, pools, row
+    strides = t.stride()
     size = 1   # values of the dimensions walked so far, innermost first
     for n, s in zip(shape[:1:-1], strides[:1:-1]):
         if n != 1 and s != size:
@@ -598,16 +626,19 @@ def ddt_cache_copy(src_pool, dst_pool, src, dst, stream=None):
     tensor); src, dst: int32 [n]."""
     dev = _on_device(src_pool, "src_pool")
     sp, sgap, srows, pools, row = _slab(src_pool, dev, "src_pool")
-    dp, dgap, drows, dpools, drow = _slab(dst_pool, dev, "dst_pool")
-    if dpools != pools or drow != row or src_pool.dtype != dst_pool.dtype:
-        raise ValueError("src_pool and dst_pool must agree in pools, row and type")
-    if src.numel() != dst.numel():
+    dp, dgap, drows = sp, sgap, srows
+    if dst_pool is not src_pool:
+        dp, dgap, drows, dpools, drow = _slab(dst_pool, dev, "dst_pool")
+        if dpools != pools or drow != row or src_pool.dtype != dst_pool.dtype:
+            raise ValueError("src_pool and dst_pool must agree in pools, row and type")
+    n = src.numel()
+    if dst.numel() != n:
         raise ValueError("src and dst must have the same length")
-    if src.numel() == 0:
+    if n == 0:
         return
-    _check("ddt_cache_copy", lib.ddt_cache_copy(
-        sp, sgap, srows, dp, dgap, drows, pools, row, _like(src, torch.int32, dev, "src"),
-        _like(dst, torch.int32, dev, "dst"), src.numel(), _raw_stream(stream, dev)))
+    _call(
+        "ddt_cache_copy", sp, sgap, srows, dp, dgap, drows, pools, row, _like(src, _I32, dev, "src"),
+        _like(dst, _I32, dev, "dst"), n, _raw_stream(stream, dev))
 
 
 def ddt_cache_commit(pool, kv_indices, kv_indptr, qo_indptr, accept_len, accepted_nodes, max_depth,
@@ -623,13 +654,13 @@ def ddt_cache_commit(pool, kv_indices, kv_indptr, qo_indptr, accept_len, accepte
         raise ValueError("new_len must hold one value per request")
     if B == 0:
         return
-    i32 = torch.int32
-    _check("ddt_cache_commit", lib.ddt_cache_commit(
-        pp, gap, rows, pools, row, _like(kv_indices, i32, dev, "kv_indices"),
+    i32 = _I32
+    _call(
+        "ddt_cache_commit", pp, gap, rows, pools, row, _like(kv_indices, i32, dev, "kv_indices"),
         _like(kv_indptr, i32, dev, "kv_indptr"), _like(qo_indptr, i32, dev, "qo_indptr"),
         _like(accept_len, i32, dev, "accept_len"), _like(accepted_nodes, i32, dev, "accepted_nodes"),
-        B, kv_indices.numel(), max_depth, None if new_len is None else _like(new_len, i32, dev, "new_len"),
-        _raw_stream(stream, dev)))
+        B, kv_indices.numel(), max_depth, 0 if new_len is None else _like(new_len, i32, dev, "new_len"),
+        _raw_stream(stream, dev))
 
 
 def ddt_cache_compact_workspace_size(pool_rows):
@@ -647,11 +678,11 @@ def ddt_cache_compact(pool, kv_indices, new_indices, live, workspace=None, strea
         workspace = _scratch(max(1, lib.ddt_cache_compact_workspace_size(rows)), dev, stream)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    i32 = torch.int32
-    _check("ddt_cache_compact", lib.ddt_cache_compact(
-        pp, gap, rows, pools, row, _like(kv_indices, i32, dev, "kv_indices"), kv_indices.numel(),
+    i32 = _I32
+    _call(
+        "ddt_cache_compact", pp, gap, rows, pools, row, _like(kv_indices, i32, dev, "kv_indices"), kv_indices.numel(),
         _like(new_indices, i32, dev, "new_indices"), _like(live, i32, dev, "live"), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)))
+        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
 
 
 def ddt_get_error(stream=None):
