@@ -677,10 +677,11 @@ ddt_status ddt_gqa_norm_rope_append(
  *               ddt_verify_attn.
  *   num_ctas    the cached columns of all requests and heads are dealt to this
  *               many CTAs in equal shares, and what a share's ends cut is joined
- *               afterwards: 1..DDT_GQA_MAX_CTAS (batch <= 256), or 0 = choose what
- *               the device holds at once, less where workspace_bytes is too small
- *               for that; without a workspace, for batch > 256 and for short
- *               caches each request and K/V head has a CTA of its own.
+ *               afterwards: 1..DDT_GQA_MAX_CTAS (batch <= 256), or 0 = choose by the
+ *               sizes (total_q and total_kv among them) between this and a CTA for
+ *               each tile of a request's K/V head, which needs no workspace.  It
+ *               deals to what the device holds at once, less where workspace_bytes
+ *               is too small for that.
  *   out         (device) bf16 [total_q][num_heads][head_dim], 16-byte aligned:
  *               what the layer's output projection reads; not q itself.
  *   lse         (device) float [total_q][num_heads] or NULL.
@@ -696,9 +697,9 @@ ddt_status ddt_gqa_norm_rope_append(
  * 32) or lie outside [0, total_mask_words] (DDT_DEVERR_MASK_INDPTR), a slot
  * outside the pool (DDT_DEVERR_KV_INDEX: row 0 is read instead).
  *
- * ddt_gqa_verify_attn_num_ctas() returns the count chosen for these bounds with
- * a workspace that holds it, on num_sms SMs (<= 0: the current device's); 0: no
- * workspace is used.
+ * ddt_gqa_verify_attn_num_ctas() returns the count whose workspace is enough for
+ * every choice within these bounds, on num_sms SMs (<= 0: the current device's);
+ * 0: no workspace is used.
  */
 int32_t ddt_gqa_verify_attn_num_ctas(int32_t batch, int32_t num_heads, int32_t num_kv_heads,
                                      int32_t max_q_len, int32_t max_kv_len, int32_t num_sms);

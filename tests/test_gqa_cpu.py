@@ -53,11 +53,17 @@ def test_attention_sizing(lib):
     size = lib.ddt_gqa_verify_attn_workspace_size
     assert size(1, 64, 8, 128, 33, 0) == 0 and size(0, 64, 8, 128, 33, 4) == 0 and size(1, 64, 7, 128, 33, 4) == 0
     up = lambda x: (x + 255) // 256 * 256  # noqa: E731
-    # two parts per CTA of as many rows as an item has: q_len x group, at most 128 or (two tiles) 256
-    for b, h, g, d, t, c, rows in ((1, 64, 8, 128, 1, 304, 8), (3, 64, 8, 128, 16, 9, 128), (2, 64, 8, 64, 17, 5, 136),
-                                   (256, 128, 1, 128, 128, 512, 256)):
-        notes = 8 * b * g * -(-t * (h // g) // (256 if t * (h // g) > 128 else 128))
-        assert size(b, h, g, d, t, c) == up(notes) + up(2 * c * rows * d * 4) + up(2 * c * rows * 4)
+    # two parts per CTA of as many rows as an item has: q_len x group, at most 128 or 256 (two tiles);
+    # with two tiles also enough for one and twice as many CTAs
+    def need(b, h, g, d, t, c, tiles):
+        rows = min(t * (h // g), 128 * tiles)
+        return up(8 * b * g * -(-t * (h // g) // (128 * tiles))) + up(2 * c * rows * d * 4) + up(2 * c * rows * 4)
+
+    for b, h, g, d, t, c in ((1, 64, 8, 128, 1, 304), (3, 64, 8, 128, 16, 9), (2, 64, 8, 64, 17, 5), (256, 128, 1, 128, 128, 512)):
+        want = need(b, h, g, d, t, c, 1)
+        if t * (h // g) > 128:
+            want = max(need(b, h, g, d, t, c, 2), need(b, h, g, d, t, 2 * c, 1))
+        assert size(b, h, g, d, t, c) == want
     ctas = lib.ddt_gqa_verify_attn_num_ctas
     for args in ((1, 64, 8, 33, 4129, 152), (64, 64, 8, 1, 16384, 152), (1, 8, 2, 9, 30, 152), (1, 1, 1, 1, 1, 152),
                  (1, 64, 8, 65, 131137, 152), (32, 32, 4, 33, 8225, 1000), (65535, 128, 1, 128, 2 ** 31 - 1, 152)):

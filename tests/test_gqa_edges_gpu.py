@@ -137,6 +137,26 @@ def test_attention_of_a_query_that_is_nan(ddt, H, G, T, D, ctas):
     assert ((out.double().cpu() - o).abs() <= bo)[~hit].all() and ((ls.double().cpu() - l).abs() <= bl)[~hit].all()
 
 
+@pytest.mark.parametrize("H,G,D,lens", [
+    # shapes that are dealt or not, with one tile of rows at a time or two
+    (64, 8, 128, [(300, 33)] * 6), (64, 8, 128, [(1500, 33)]), (32, 4, 128, [(600, 32)] * 16), (32, 4, 64, [(500, 17)] * 24),
+    (64, 8, 64, [(2500, 17), (100, 33)]), (128, 8, 64, [(400, 33), (100, 20), (700, 1)]), (16, 16, 128, [(300, 9)] * 10),
+    (32, 2, 128, [(1300, 16), (40, 5), (900, 16)]),
+])
+@pytest.mark.parametrize("room", ["none", "some", "all"])
+def test_attention_chooses_its_way(ddt, H, G, D, lens, room):
+    batch = ref.Batch(lens, 109 + H, "tree")
+    q, k, v, kd, vd = base.attn_inputs(batch, H, G, D, 110)
+    n = ddt.ddt_gqa_verify_attn_num_ctas(batch.B, H, G, batch.max_q, batch.max_kv)
+    assert n > 0
+    n = {"none": 0, "some": 9, "all": n}[room]
+    nbytes = ddt.ddt_gqa_verify_attn_workspace_size(batch.B, H, G, D, batch.max_q, n)
+    ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=DEV)[:nbytes]
+    out, ls = base.run_attn(ddt, batch, q, kd, vd, D ** -0.5, workspace=ws)
+    clean(ddt)
+    base.check_attn(out, ls, q, k, v, batch, D ** -0.5)
+
+
 FEW = [
     # heads, kv heads, dim, (prefix, new tokens) per request: 1 to 8 rows behind one or two tiles
     (8, 1, 128, [(300, 17), (40, 33), (1000, 33)]), (16, 2, 64, [(500, 33), (0, 17), (129, 65), (600, 3)]),

@@ -12,13 +12,7 @@
 
 namespace {
 
-// bytes of the notes on a call's items (256-byte aligned), at the workspace's start
-size_t notes_bytes(int32_t batch, int32_t num_kv_heads, int32_t group, int32_t max_q_len) {
-    return ((size_t)batch * num_kv_heads * ddt::gqa_tile_groups(max_q_len, group) * sizeof(int2) + 255) & ~size_t(255);
-}
-
 inline cudaStream_t as_stream(void *s) { return static_cast<cudaStream_t>(s); }
-inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 inline bool misaligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 inline ddt_status launched(cudaError_t e) { return e == cudaSuccess ? DDT_OK : DDT_ERR_CUDA; }
 
@@ -137,7 +131,7 @@ int32_t ddt_gqa_verify_attn_num_ctas(int32_t batch, int32_t num_heads, int32_t n
         max_kv_len < 1)
         return 0;
     if (num_sms <= 0) num_sms = ddt::device_sm_count();
-    return ddt::gqa_choose_ctas(batch, num_heads, num_kv_heads, max_q_len, max_kv_len, num_sms);
+    return ddt::gqa_most_ctas(batch, num_heads, num_kv_heads, max_q_len, max_kv_len, num_sms);
 }
 
 size_t ddt_gqa_verify_attn_workspace_size(int32_t batch, int32_t num_heads, int32_t num_kv_heads,
@@ -145,10 +139,23 @@ size_t ddt_gqa_verify_attn_workspace_size(int32_t batch, int32_t num_heads, int3
     if (batch < 1 || num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads || head_dim < 1 || max_q_len < 1 ||
         num_ctas < 1)
         return 0;
-    const int group = num_heads / num_kv_heads;
-    const size_t rows = (size_t)2 * num_ctas * ddt::gqa_part_rows(max_q_len, group);
-    return notes_bytes(batch, num_kv_heads, group, max_q_len) + align256(rows * head_dim * sizeof(float)) +
-           align256(rows * sizeof(float));
+    ddt::GqaArgs a;
+    memset(&a, 0, sizeof a);
+    a.batch = batch;
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.max_q_len = max_q_len;
+    a.tiles = ddt::gqa_tiles(max_q_len, num_heads / num_kv_heads);
+    a.num_ctas = num_ctas;
+    size_t bytes = ddt::gqa_layout(a, nullptr);
+    if (a.tiles == 2) {  // num_ctas = 0 may take one tile and twice as many CTAs instead
+        a.tiles = 1;
+        a.num_ctas = 2 * num_ctas;
+        const size_t other = ddt::gqa_layout(a, nullptr);
+        if (other > bytes) bytes = other;
+    }
+    return bytes;
 }
 
 ddt_status ddt_gqa_verify_attn(
@@ -176,21 +183,8 @@ ddt_status ddt_gqa_verify_attn(
     unsigned int *err = ddt::device_error_word();
     if (!err) return DDT_ERR_CUDA;
 
-    auto need = [&](int ctas) {
-        return ddt_gqa_verify_attn_workspace_size(batch, num_heads, num_kv_heads, head_dim, max_q_len, ctas);
-    };
-    int ctas = num_ctas;
-    if (num_ctas == 0) {  // the choice, or what the workspace holds of it
-        ctas = ddt::gqa_choose_ctas(batch, num_heads, num_kv_heads, max_q_len, max_kv_len, ddt::device_sm_count());
-        if (!workspace) ctas = 0;
-        while (ctas > 0 && need(ctas) > workspace_bytes) --ctas;
-    } else if (!workspace || workspace_bytes < need(ctas)) {
-        return DDT_ERR_WORKSPACE;
-    }
     ddt::GqaArgs a;
     memset(&a, 0, sizeof a);
-    a.num_ctas = ctas;
-    a.forced = num_ctas > 0;
     a.q = q;
     a.k_pool = k_pool;
     a.v_pool = v_pool;
@@ -214,15 +208,17 @@ ddt_status ddt_gqa_verify_attn(
     a.out = out;
     a.lse = lse;
     a.err = err;
-    if (ctas > 0) {
-        const size_t rows = (size_t)2 * ctas * ddt::gqa_part_rows(max_q_len, num_heads / num_kv_heads);
-        char *p = static_cast<char *>(workspace);
-        a.notes = reinterpret_cast<int2 *>(p);
-        p += notes_bytes(batch, num_kv_heads, num_heads / num_kv_heads, max_q_len);
-        a.o_part = reinterpret_cast<float *>(p);
-        a.lse_part = reinterpret_cast<float *>(p + align256(rows * head_dim * sizeof(float)));
+    const int num_sms = ddt::device_sm_count();
+    if (num_ctas > 0) {
+        a.forced = 1;
+        a.tiles = ddt::gqa_tiles(max_q_len, num_heads / num_kv_heads);
+        a.num_ctas = num_ctas;
+        if (!workspace || workspace_bytes < ddt::gqa_layout(a, nullptr)) return DDT_ERR_WORKSPACE;
+    } else {
+        ddt::gqa_choose(a, workspace ? workspace_bytes : 0, num_sms);
     }
-    return launched(ddt::launch_gqa_attn(a, ddt::device_sm_count(), as_stream(stream)));
+    if (a.num_ctas > 0) ddt::gqa_layout(a, workspace);
+    return launched(ddt::launch_gqa_attn(a, num_sms, as_stream(stream)));
 }
 
 ddt_status ddt_cache_copy(const void *src_slab, int64_t src_pool_bytes, int64_t src_pool_rows,

@@ -187,23 +187,30 @@ struct GqaArgs {
     // or 0: one CTA per item, no workspace
     int num_ctas;
     int forced;       // the caller gave the count: a CTA may get a single block
+    int tiles;        // tiles of 128 rows of an item: 1 or 2
     uint16_t *out;    // [total_q, H, D] bf16
     float *lse;       // [total_q, H] or null
     // dealt: per item the place of its first part (-1: whole) and the CTA with its last
     int2 *notes;      // [batch][num_kv_heads][gqa_tile_groups()]
-    float *o_part;    // [2 * num_ctas, gqa_part_rows(), D]
-    float *lse_part;  // [2 * num_ctas, gqa_part_rows()]
+    float *o_part;    // [2 * num_ctas][gqa_part_rows()][D]
+    float *lse_part;  // [2 * num_ctas][gqa_part_rows()]
     unsigned int *err;
 };
 constexpr int kGqaMaxDealtBatch = 256;  // a thread per request sizes the line
 // kernel attributes, once per device (see attn_prepare_device)
 cudaError_t gqa_prepare_device();
 cudaError_t launch_gqa_attn(const GqaArgs &a, int num_sms, cudaStream_t s);
-// the CTAs that the work is dealt to for these bounds, or 0 (see GqaArgs)
-int gqa_choose_ctas(int batch, int num_heads, int num_kv_heads, int max_q_len, int max_kv_len, int num_sms);
+// the most CTAs that the work may be dealt to for these bounds, or 0 (see GqaArgs)
+int gqa_most_ctas(int batch, int num_heads, int num_kv_heads, int max_q_len, int max_kv_len, int num_sms);
+// tiles of an item where the caller gives the count of CTAs
+int gqa_tiles(int max_q_len, int group);
+// a.tiles and a.num_ctas for the call's sizes, within the workspace
+void gqa_choose(GqaArgs &a, size_t workspace_bytes, int num_sms);
 // rows of a partial result; most items per K/V head of a request
-int gqa_part_rows(int max_q_len, int group);
-int gqa_tile_groups(int max_q_len, int group);
+int gqa_part_rows(int tiles, int max_q_len, int group);
+int gqa_tile_groups(int tiles, int max_q_len, int group);
+// bytes of the workspace for a.tiles and a.num_ctas; places its parts in a where base is given
+size_t gqa_layout(GqaArgs &a, void *base);
 
 cudaError_t launch_cache_copy(const void *src_slab, int64_t src_pool_bytes, int64_t src_rows, void *dst_slab,
                               int64_t dst_pool_bytes, int64_t dst_rows, int num_pools, int64_t row_bytes,
