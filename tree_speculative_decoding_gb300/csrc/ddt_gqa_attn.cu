@@ -13,19 +13,28 @@
 // block of columns at a time.
 //   * kTiles = 1: blocks of 64 columns, 256 tensor-memory columns and under half
 //     of the shared memory, so two CTAs share an SM: one's prologue, softmax and
-//     epilogue run under the other's loads.  Taken when a request's rows per K/V
-//     head fit one tile (decode, small trees): the loads bound it.
+//     epilogue run under the other's loads.  The only choice when a request's rows
+//     per K/V head fit one tile (decode, small trees): the loads bound it.
 //   * kTiles = 2: blocks of 128 columns, all of tensor memory; the tensor core
-//     works on one tile while the softmax of the other runs.  An item's last rows
-//     may fill one tile only: its blocks then alternate between the two tiles'
-//     warps and outputs, each with a reference and sum of its own, and the two
-//     are joined at the end.
-// The blocks of all items, weighted by what they cost, form one line (request,
-// K/V head, rows, columns) that is dealt to the resident CTAs in equal shares: a CTA takes the end of one item,
-// whole items, and the start of another, whatever the requests' lengths are.
-// Items that were cut leave partial results (at most two per CTA) in the
-// workspace for the combine kernel, and a note of where they are.  Every CTA finds
-// the same cuts from the offsets.
+//     works on one tile while the softmax of the other runs, and K and V are read
+//     half as often.  An item's last rows may fill one tile only: its blocks then
+//     alternate between the two tiles' warps and outputs, each with a reference and
+//     sum of its own, and the two are joined at the end.
+// A CTA takes one item; or the blocks of all items, weighted by what they cost,
+// form one line (request, K/V head, rows, columns) that is dealt to the resident
+// CTAs in equal shares: a CTA takes the end of one item, whole items, and the
+// start of another, whatever the requests' lengths are.  Items that were cut leave
+// partial results (at most two per CTA) in the workspace for the combine kernel,
+// and a note of where they are.  Every CTA finds the same cuts from the offsets.
+// estimate() weighs the four ways.
+//
+// Measured with the combine kernel, D = 128: 64 requests of one token after
+// 1024..16384, 64 heads on 8: 345 us, 6.6 TB/s, bound by memory.  32 requests of
+// 17..33 tokens after 2048..8192, 32 heads on 4: 109 us, 3.4 TB/s and 673 TFLOP/s;
+// 65 tokens after 131072, 64 heads on 8: 312 us, 894 TFLOP/s: a block of two tiles
+// takes ~3000 clk where its products take 2048, since a tile's next scores wait
+// for its softmax and its products (tensor memory is full).  Of the 109 us, 8 fill
+// the first pipeline, 6 to 10 each go to a CTA's change of item, 9 to the combine.
 //
 // Score slots: two buffers of one block's scores in tensor memory.  Work unit w
 // of a segment (block-major, tiles inside a block) uses slot w mod 2.  The MMA
