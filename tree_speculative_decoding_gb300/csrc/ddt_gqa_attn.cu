@@ -30,11 +30,12 @@
 //
 // Measured with the combine kernel, D = 128: 64 requests of one token after
 // 1024..16384, 64 heads on 8: 345 us, 6.6 TB/s, bound by memory.  32 requests of
-// 17..33 tokens after 2048..8192, 32 heads on 4: 109 us, 3.4 TB/s and 673 TFLOP/s;
-// 65 tokens after 131072, 64 heads on 8: 312 us, 894 TFLOP/s: a block of two tiles
-// takes ~3000 clk where its products take 2048, since a tile's next scores wait
-// for its softmax and its products (tensor memory is full).  Of the 109 us, 8 fill
-// the first pipeline, 6 to 10 each go to a CTA's change of item, 9 to the combine.
+// 17..33 tokens after 2048..8192, 32 heads on 4: 105 us, 3.5 TB/s and 695 TFLOP/s;
+// 65 tokens after 131072, 64 heads on 8: 296 us, 943 TFLOP/s: a block of two tiles
+// takes ~2800 clk where its products take 2048, since a tile's next scores wait
+// for its softmax and its products (tensor memory is full; a third slot at D = 64,
+// where it fits, measured 6% slower).  Of the 105 us, 8 fill the first pipeline, 6
+// to 10 each go to a CTA's change of item, 9 to the combine.
 //
 // Score slots: two buffers of one block's scores in tensor memory.  Work unit w
 // of a segment (block-major, tiles inside a block) uses slot w mod 2.  The MMA
@@ -560,7 +561,7 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                 int ks = 0, vs = 0;
                 uint32_t kph = 0, vph = 0, pph[2] = {0, 0};
                 // The tensor pipe is idle while this thread waits or computes: the loop is
-                // unrolled over the two slots and keeps its stages and phases in counters.
+                // unrolled over tiles and slots and keeps its stages and phases in counters.
                 auto run = [&](auto tile_count, int items) {
                     constexpr int A = decltype(tile_count)::value;  // tiles of the segment
                     constexpr int kOuts = kTiles;                   // outputs that work units alternate between
@@ -618,8 +619,9 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                             }
                         }
                     };
-                    issue_s(0);
-                    if (ok && items > 1) issue_s(1);
+#pragma unroll
+                    for (int slot = 0; slot < 2; ++slot)
+                        if (ok && slot < items) issue_s(slot);
                     while (ok && w < items) {
 #pragma unroll
                         for (int slot = 0; slot < 2; ++slot) {
@@ -658,8 +660,8 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
         const int r = 32 * wq + lane;  // row within the tile
         const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
         const float sc = a.scale * kLog2e;
-        // phases of the slots that this warp serves (two tiles: its own one); blocks, and joins, so far
-        uint32_t sph[2] = {0, 0}, done = 0, joins = 0;
+        // parity of the uses of the slots that this warp serves (two tiles: its own one); its blocks, and joins, so far
+        uint32_t phases = 0, done = 0, joins = 0;
         bool ok = true;
         for (int seg = 0; ok; ++seg) {
             ok = warp_segment(seg, sg);
@@ -695,28 +697,37 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
             const uint32_t *words = a.mask + sg.m0 + (int64_t)node * sg.W;
             float m_ref = -INFINITY, l = 0.f;  // the reference in log2 units, the sum against it
             constexpr int kW = NB / 32;
-            auto mask_words = [&](int j, uint32_t (&mw)[kW]) {
+            const int j0 = lone ? t : 0, step = lone ? 2 : 1;
+            const uint32_t *at = words + ((sg.c_begin + j0 * NB) >> 5);  // the next block's mask words,
+            int left = sg.c_end - sg.c_begin - j0 * NB;                  // and the columns from it on
+            auto mask_words = [&](uint32_t (&mw)[kW]) {
+                if (left >= NB) {
 #pragma unroll
-                for (int k = 0; k < kW; ++k) {
-                    const int c0 = sg.c_begin + j * NB + 32 * k;
-                    uint32_t x = c0 < sg.c_end ? words[c0 >> 5] : 0u;
-                    if (c0 < sg.c_end && sg.c_end - c0 < 32) x &= (1u << (sg.c_end - c0)) - 1u;
-                    mw[k] = x;
+                    for (int k = 0; k < kW; ++k) mw[k] = at[k];
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kW; ++k) {
+                        mw[k] = 32 * k < left ? at[k] : 0u;
+                        if (32 * k < left && left - 32 * k < 32) mw[k] &= (1u << (left - 32 * k)) - 1u;
+                    }
                 }
+                at += step * kW;
+                left -= step * NB;
             };
             uint32_t mnext[kW];
-            const int j0 = lone ? t : 0, step = lone ? 2 : 1;
-            if (warp_on && j0 < sg.blocks) mask_words(j0, mnext);
-            for (int j = j0; j < sg.blocks; j += step) {
+            if (warp_on && j0 < sg.blocks) mask_words(mnext);
+            uint32_t own = 0;  // this warp's blocks in the segment
+            for (int j = j0; j < sg.blocks; j += step, ++own) {
                 const int slot = kTiles == 2 ? t : j & 1;
+                const uint32_t phase = (phases >> slot) & 1;
                 const uint32_t col = tmem + lane_off + C::kColS + NB * slot;
                 uint32_t mw[kW];
                 if (warp_on) {
 #pragma unroll
                     for (int k = 0; k < kW; ++k) mw[k] = mnext[k];
-                    if (j + step < sg.blocks) mask_words(j + step, mnext);
+                    if (j + step < sg.blocks) mask_words(mnext);
                 }
-                ok = warp_wait(bar(C::bSFull + slot), sph[slot], abort_flag, a.err);
+                ok = warp_wait(bar(C::bSFull + slot), phase, abort_flag, a.err);
                 if (!ok) break;
                 if (warp_on) {
                     tc_fence_after();
@@ -792,8 +803,8 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                             // The products so far have to be done before the output is scaled: of this
                             // block's first half; or of the output's last block (with two outputs S(w)
                             // was issued behind it, so it is done).
-                            if (h > 0) ok = warp_wait(bar(C::bHalf + slot), sph[slot], abort_flag, a.err);
-                            else if (kTiles == 1 && j > 0) ok = warp_wait(bar(C::bODone), (done + j - 1) & 1, abort_flag, a.err);
+                            if (h > 0) ok = warp_wait(bar(C::bHalf + slot), phase, abort_flag, a.err);
+                            else if (kTiles == 1 && own > 0) ok = warp_wait(bar(C::bODone), (done + own - 1) & 1, abort_flag, a.err);
                             if (!ok) break;
                             if (h > 0 || j > j0) {
                                 tc_fence_after();
@@ -826,10 +837,10 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                     for (int h = 0; h < C::kHalves; ++h)
                         if (lane == 0) mbar_arrive(bar(C::bPFull + C::kHalves * slot + h));
                 }
-                sph[slot] ^= 1;
+                phases ^= 1u << slot;
             }
             if (!ok) break;
-            done += sg.blocks;
+            done += own;
             // ---- epilogue ----
             ok = warp_wait(bar(C::bOFin), seg & 1, abort_flag, a.err);
             float keep0 = 1.f, keep1 = 0.f;  // what the two outputs of a lone tile count
