@@ -271,6 +271,21 @@ def test_two_graphs_share_a_workspace_in_turn(ddt):
         base.check_attn(out, None, q, k, v, batch, 0.1)
 
 
+@pytest.mark.parametrize("H,T", [(4, 9), (64, 3)])
+def test_attention_ignores_bits_past_the_last_column(ddt, H, T):
+    # kv_len 309, 70, 31: the last word's bits past it are set, and the slots there are another request's
+    batch = ref.Batch([(309 - T, T), (70 - T, T), (31 - T, T)], 85, "tree")
+    q, k, v, kd, vd = base.attn_inputs(batch, H, 1, 64, 86)
+    for b in range(3):
+        W, N = -(-int(batch.P[b] + T) // 32), int(batch.P[b] + T)
+        lo = int(batch.mask_indptr[b])
+        batch.words[lo + W - 1: lo + T * W: W] |= np.uint32((0xffffffff << (N % 32)) & 0xffffffff)
+    for ctas in (0, 1, 4):
+        out, ls = base.run_attn(ddt, batch, q, kd, vd, 0.1, ctas)
+        clean(ddt)
+        base.check_attn(out, ls, q, k, v, batch, 0.1)
+
+
 def test_attention_reads_a_slot_named_twice(ddt):
     # two columns of one request, and two requests' prefixes, on the same rows
     batch = ref.Batch([(300, 4), (300, 3)], 83, "tree")
