@@ -1155,8 +1155,9 @@ int slots(int tiles, int num_sms) { return std::min(num_sms * (tiles == 2 ? 1 : 
 // (ctas = 0) with a CTA per item, which the hardware hands out as others end.  Dealing
 // costs the plan, cut items and the combine kernel, and evens out long or few items;
 // two tiles halve the reads of K and V, one tile starts and ends faster.  The constants
-// are fitted to 224 shapes measured all four ways (1 to 64 requests, 500 to 16000
-// columns even and ragged, 1 to 33 tokens, 8 to 16 K/V heads): each way within 10%.  The
+// are fitted to 224 shapes measured dealt and undealt, above 128 rows with one tile and
+// two (1 to 64 requests, 500 to 16000 columns even and ragged, 1 to 33 tokens, 4 to 16
+// K/V heads): each way within 10%.  The
 // choice costs 1% over the best on average and 20% at most, where one fixed way (two
 // tiles above 128 rows, dealt) cost 17% and 100%.  64 requests of 33 tokens x 64 heads
 // after 1000 take 230 us dealt with two tiles, 130 us undealt with one; 4 of them after
