@@ -30,11 +30,11 @@
 //
 // Measured with the combine kernel, D = 128: 64 requests of one token after
 // 1024..16384, 64 heads on 8: 345 us, 6.6 TB/s, bound by memory.  32 requests of
-// 17..33 tokens after 2048..8192, 32 heads on 4: 105 us, 3.5 TB/s and 695 TFLOP/s;
-// 65 tokens after 131072, 64 heads on 8: 296 us, 943 TFLOP/s: a block of two tiles
-// takes ~2800 clk where its products take 2048, since a tile's next scores wait
+// 17..33 tokens after 2048..8192, 32 heads on 4: 100 us, 3.7 TB/s and 730 TFLOP/s;
+// 65 tokens after 131072, 64 heads on 8: 271 us, 1030 TFLOP/s: a block of two tiles
+// takes ~2700 clk where its products take 2048, since a tile's next scores wait
 // for its softmax and its products (tensor memory is full; a third slot at D = 64,
-// where it fits, measured 6% slower).  Of the 105 us, 8 fill the first pipeline, 6
+// where it fits, measured 6% slower).  Of the 100 us, 8 fill the first pipeline, 6
 // to 10 each go to a CTA's change of item, 9 to the combine.
 //
 // Score slots: two buffers of one block's scores in tensor memory.  Work unit w
@@ -119,8 +119,10 @@ struct Cfg {
     static constexpr int kFirstLoad = kTiles == 2 ? kSoftWarps : kSoftWarps + 1;
     static constexpr int kMmaWarp = kTiles == 2 ? kSoftWarps + kLoadWarps : kSoftWarps;
     static constexpr int kThreads = kTiles == 2 ? 640 : 256;
-    // registers of the two-tile kernel: a softmax thread's, another's; together no more than at launch
-    static constexpr int kSoftRegs = 144, kOtherRegs = 64, kLaunchRegs = 96;
+    // Registers of the two-tile kernel: a softmax thread's, another's; together no more than at
+    // launch.  65 tokens after 131072: 271 us with 120 / 72, 276 us with 128 / 72, 278 us with
+    // 136 / 64, 291 us with 144 / 64 and with 120 / 80.
+    static constexpr int kSoftRegs = 120, kOtherRegs = 72, kLaunchRegs = 96;
     static_assert(32 * kSoftWarps * kSoftRegs + (640 - 32 * kSoftWarps) * kOtherRegs <= 640 * kLaunchRegs || kTiles == 1, "registers");
     static constexpr uint32_t kTmemCols = kTiles == 2 ? 512 : 256;
     static constexpr uint32_t kColS = 0, kColO = 2 * NB;
