@@ -16,9 +16,11 @@
 // token's rows.  What bounds a CTA is its chain of dependent loads, so the first
 // rows, the weights and the depth are loaded before the token's request is looked
 // up, and its slot and angles at once behind that.  4096 tokens of 64 query and 8
-// K/V heads of 128 in 32 requests take 30.3 us, 5.6 TB/s (33.5 us with 128 threads
-// and 8 CTAs per SM, 35.3 us with 12 of these and 32.7 us with 16).  The angles are read from the caller's table: sine and cosine
-// of far positions need more than fp32, once per position and not per token.
+// K/V heads of 128 in 32 requests take 29.3 us, 5.8 TB/s (30.5 us with 64 threads and
+// 14 CTAs per SM, 33.5 us with 128 and 8; 39.6 us with 24 of these, 30.5 us with 32).
+// With few tokens several CTAs share one.  The angles are read from the caller's
+// table: sine and cosine of far positions need more than fp32, once per position and
+// not per token.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -34,8 +36,8 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 64;
-constexpr int kCtasPerSm = 14;
+constexpr int kThreads = 32;
+constexpr int kCtasPerSm = 28;
 constexpr int kBatchRows = 4;  // head rows in flight per group
 
 struct Row {  // a lane's two pieces of four values
@@ -241,12 +243,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_append_kernel(
 
 cudaError_t launch_norm_rope_append(const AppendArgs &a, int num_sms, cudaStream_t s) {
     const int groups = kThreads / (a.head_dim / 8);
-    // CTAs per token: as many as run at once, down to one query row per group, and one
+    // CTAs per token: as many as run at once, down to two query rows per group, and one
     // when the tokens alone fill the SMs.  1056 tokens of 64 query and 8 K/V heads of
-    // 128: two take 7.6 us, three (a second wave) 9.2 us, one 9.5 us; 128 tokens: 3.6 us
-    // with eight, 5.8 us with one.
+    // 128: four take 7.4 us, more than one wave 9.2 us, one 9.5 us; 128 tokens: 3.0 us
+    // with sixteen, 4.6 us with thirty-two, 5.8 us with one.
     const int64_t room = (int64_t)kCtasPerSm * num_sms / a.total_q;
-    const int split = (int)std::max<int64_t>(1, std::min<int64_t>((a.num_heads + groups - 1) / groups, room));
+    const int split = (int)std::max<int64_t>(1, std::min<int64_t>((a.num_heads + 2 * groups - 1) / (2 * groups), room));
     const dim3 grid((unsigned)a.total_q, (unsigned)split);
     return a.head_dim == 128 ? launch_pdl(norm_rope_append_kernel<128>, grid, dim3(kThreads), 0, s, a)
                              : launch_pdl(norm_rope_append_kernel<64>, grid, dim3(kThreads), 0, s, a);

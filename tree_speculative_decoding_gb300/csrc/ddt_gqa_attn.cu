@@ -1159,12 +1159,11 @@ int slots(int tiles, int num_sms) { return std::min(num_sms * (tiles == 2 ? 1 : 
 // two tiles halve the reads of K and V, one tile starts and ends faster.  The constants
 // are fitted to 224 shapes measured dealt and undealt, above 128 rows with one tile and
 // two (1 to 64 requests, 500 to 16000 columns even and ragged, 1 to 33 tokens, 4 to 16
-// K/V heads): each way within 10%.  The
-// choice costs 1% over the best on average and 20% at most, where one fixed way (two
-// tiles above 128 rows, dealt) cost 17% and 100%.  64 requests of 33 tokens x 64 heads
-// after 1000 take 230 us dealt with two tiles, 130 us undealt with one; 4 of them after
-// 16000 120 us dealt and 217 us undealt; 16 of 32 tokens after 8000 122 us undealt with
-// two tiles, 140 us with one.
+// K/V heads): each way within 10%.  The choice costs 1% over the best on average and 20%
+// at most, where one fixed way (two tiles above 128 rows, dealt) cost 17% and 100%.  64
+// requests of 33 tokens x 64 heads after 1000 take 230 us dealt with two tiles, 130 us
+// undealt with one; 4 of them after 16000 120 us dealt and 217 us undealt; 16 of 32
+// tokens after 8000 122 us undealt with two tiles, 140 us with one.
 double estimate(const GqaArgs &a, int tiles, int ctas, int num_sms) {
     const double rows = std::min((double)a.total_q / a.batch, (double)a.max_q_len) * (a.num_heads / a.num_kv_heads);
     const double columns = std::min((double)a.total_kv / a.batch, (double)a.max_kv_len);
