@@ -7,7 +7,8 @@ namespace ddt {
 
 // The last request b in [0, batch] with qo_indptr[b] <= t, by a 32-way search
 // of the whole warp (two rounds of loads up to 1024 requests).  b == batch:
-// the token is behind the last request.
+// the token is behind the last request.  0 is also the answer for a token ahead of
+// the first one, and offsets that fall somewhere may give a b with qo_indptr[b] > t.
 __device__ __forceinline__ int find_request(const int32_t *qo_indptr, int batch, int t, int lane) {
     int64_t lo = 0, hi = batch;
     while (hi > lo) {

@@ -106,17 +106,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_append_kernel(
         q1 = __shfl_sync(0xffffffffu, qo, b + 1);
         kv0 = __shfl_sync(0xffffffffu, kv, b);
         kv1 = __shfl_sync(0xffffffffu, kv, b + 1);
-        if (b >= a.batch) return;  // behind the last request: left as it is
+        if (b >= a.batch || (b == 0 && t < q0)) return;  // behind the last request or ahead of the first: left as it is
     } else {
         b = find_request(a.qo_indptr, a.batch, t, lane);
         if (b >= a.batch) return;
         q0 = a.qo_indptr[b];
+        if (b == 0 && t < q0) return;
         q1 = a.qo_indptr[b + 1];
         kv0 = a.kv_indptr[b];
         kv1 = a.kv_indptr[b + 1];
     }
     const int T = q1 - q0, P = kv1 - kv0 - T;
-    const bool bad_q = q0 < 0 || t - q0 >= T || q1 > a.total_q;
+    // t < q0: offsets that fall somewhere lead the look-up to a request that starts behind the token
+    const bool bad_q = q0 < 0 || t < q0 || t - q0 >= T || q1 > a.total_q;
     const bool bad_kv = kv0 < 0 || kv1 > a.total_kv || P < 0;
     if (bad_q || bad_kv) {
         if (threadIdx.x == 0) latch(a.err, bad_q ? DDT_DEVERR_QO_INDPTR : DDT_DEVERR_KV_INDPTR);
