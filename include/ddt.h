@@ -689,10 +689,11 @@ ddt_status ddt_gqa_norm_rope_append(
  *               bytes for num_ctas, or NULL when that is 0.  Calls that may overlap
  *               on the GPU need a workspace each.
  * Supported: scale > 0, head_dim 64 or 128, num_heads a multiple of
- * num_kv_heads and at most DDT_GQA_MAX_HEADS, max_q_len <= 128, pool_rows <= 2^31 - 1.
+ * num_kv_heads and at most DDT_GQA_MAX_HEADS, max_q_len <= 128, pool_rows <= 2^31 - 1,
+ * kv_len up to 2^31 - 128.
  * Device checks (latched, the request's rows left unwritten): q_len outside
  * [0, max_q_len] or offsets outside [0, total_q] (DDT_DEVERR_QO_INDPTR),
- * kv_len outside [q_len, max_kv_len] or offsets outside [0, total_kv]
+ * kv_len outside [q_len, max_kv_len] (or too long) or offsets outside [0, total_kv]
  * (DDT_DEVERR_KV_INDPTR), mask words that do not number q_len * ceil(kv_len /
  * 32) or lie outside [0, total_mask_words] (DDT_DEVERR_MASK_INDPTR), a slot
  * outside the pool (DDT_DEVERR_KV_INDEX: row 0 is read instead).

@@ -94,12 +94,12 @@ cache_commit_kernel(uint8_t *slab, int64_t pool_bytes, int64_t pool_rows, int nu
         const int lane = threadIdx.x;
         const unsigned full = 0xffffffffu;
         const int width = max_depth + 1;
-        const int T = qo_indptr[b + 1] - qo_indptr[b];
-        const int kv0 = kv_indptr[b], kv1 = kv_indptr[b + 1];
+        const int64_t T = (int64_t)qo_indptr[b + 1] - qo_indptr[b];  // broken offsets do not fit 32 bits
+        const int64_t kv0 = kv_indptr[b], kv1 = kv_indptr[b + 1];
         const int n = accept_len[b];
         const int ak = lane < width ? accepted_nodes[(int64_t)b * width + lane] : 0;
         const int aprev = __shfl_up_sync(full, ak, 1);
-        const int P = kv1 - kv0 - T;
+        const int64_t P = kv1 - kv0 - T;
         const bool bad_entry = lane < n && (lane == 0 ? ak != 0 : (ak <= aprev || ak >= T));
         bool ok = T >= 0 && P >= 0 && kv0 >= 0 && kv1 <= total_kv && n <= width && n <= T && n >= (T > 0 ? 1 : 0) &&
                   !__any_sync(full, bad_entry);
@@ -121,7 +121,7 @@ cache_commit_kernel(uint8_t *slab, int64_t pool_bytes, int64_t pool_rows, int nu
         if (lane == 0) {
             s_n = ok ? n : 0;
             if (first && !ok) latch(err, bit);
-            if (first && ok && new_len) new_len[b] = P + n;
+            if (first && ok && new_len) new_len[b] = (int32_t)(P + n);
         }
     }
     __syncthreads();

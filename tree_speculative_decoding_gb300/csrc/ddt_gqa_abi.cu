@@ -26,6 +26,9 @@ bool bad_pool_stride(int64_t stride, int32_t num_kv_heads, int32_t head_dim) {
     return stride < (int64_t)num_kv_heads * head_dim || stride % 8;
 }
 
+// columns of a request that are counted in 32 bits, with a block behind them
+constexpr int32_t kMostColumns = INT32_MAX - 127;
+
 // layout of a slab of pools
 bool bad_slab(const void *slab, int64_t pool_bytes, int64_t pool_rows, int32_t num_pools, int64_t row_bytes) {
     if (!slab || misaligned(slab, 16) || pool_rows < 1 || num_pools < 1 || row_bytes < 16 || row_bytes % 16 ||
@@ -203,7 +206,7 @@ ddt_status ddt_gqa_verify_attn(
     a.total_kv = total_kv;
     a.total_mask_words = total_mask_words;
     a.max_q_len = max_q_len;
-    a.max_kv_len = max_kv_len;
+    a.max_kv_len = max_kv_len < kMostColumns ? max_kv_len : kMostColumns;
     a.scale = scale;
     a.out = out;
     a.lse = lse;

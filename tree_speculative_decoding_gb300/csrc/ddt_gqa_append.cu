@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_append_kernel(
         kv0 = a.kv_indptr[b];
         kv1 = a.kv_indptr[b + 1];
     }
-    const int T = q1 - q0, P = kv1 - kv0 - T;
+    const int64_t T = (int64_t)q1 - q0, P = (int64_t)kv1 - kv0 - T;  // broken offsets do not fit 32 bits
     // t < q0: offsets that fall somewhere lead the look-up to a request that starts behind the token
     const bool bad_q = q0 < 0 || t < q0 || t - q0 >= T || q1 > a.total_q;
     const bool bad_kv = kv0 < 0 || kv1 > a.total_kv || P < 0;
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_append_kernel(
     const int64_t slot = a.kv_indices[kv0 + P + i];
     float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};  // of the lane's four pairs
     if (a.rope_dim > 0) {
-        const int64_t pos = (int64_t)P + (a.depth ? depth : i);
+        const int64_t pos = P + (a.depth ? depth : i);
         if (pos < 0 || pos >= a.max_pos) {
             if (threadIdx.x == 0) latch(a.err, DDT_DEVERR_POSITION);
             return;

@@ -239,12 +239,14 @@ __device__ __forceinline__ Request load_request(const GqaArgs &a, int group, int
     const int kv1 = a.kv_indptr[b + 1];
     r.m0 = a.mask_indptr[b];
     const int m1 = a.mask_indptr[b + 1];
-    r.T = qo1 - r.qo0;
-    r.N = kv1 - r.kv0;
-    const bool bad_qo = r.T < 0 || r.T > a.max_q_len || r.qo0 < 0 || qo1 > a.total_q;
-    const bool bad_kv = r.N < r.T || r.N > a.max_kv_len || r.kv0 < 0 || kv1 > a.total_kv;
+    // broken offsets, and the words of a long request, do not fit 32 bits
+    const int64_t T = (int64_t)qo1 - r.qo0, N = (int64_t)kv1 - r.kv0;
+    const bool bad_qo = T < 0 || T > a.max_q_len || r.qo0 < 0 || qo1 > a.total_q;
+    const bool bad_kv = N < T || N > a.max_kv_len || r.kv0 < 0 || kv1 > a.total_kv;
     const bool bad_mask =
-        !bad_qo && !bad_kv && (r.m0 < 0 || m1 - r.m0 != r.T * ((r.N + 31) >> 5) || m1 > a.total_mask_words);
+        !bad_qo && !bad_kv && (r.m0 < 0 || (int64_t)m1 - r.m0 != T * ((N + 31) >> 5) || m1 > a.total_mask_words);
+    r.T = (int)T;
+    r.N = (int)N;
     if (bad_qo || bad_kv || bad_mask) {
         latch(err, (bad_qo ? DDT_DEVERR_QO_INDPTR : 0u) | (bad_kv ? DDT_DEVERR_KV_INDPTR : 0u) |
                        (bad_mask ? DDT_DEVERR_MASK_INDPTR : 0u));
