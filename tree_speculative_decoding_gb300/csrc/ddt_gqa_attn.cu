@@ -53,9 +53,10 @@
 // The softmax does not look for a block's maximum: the weights of 64 columns are
 // taken against the row's reference, the maximum of the first columns it saw.
 // Only where their sum passes 2^40 (or the row had seen nothing) the maximum is
-// found, the reference moves, and the sums so far are scaled.  fp32 sums stay
-// finite for |v| below ~2^67 at a million columns, and bf16 weights keep their
-// relative precision at any scale.
+// found, the reference moves, and the sums so far are scaled.  bf16 weights keep
+// their relative precision at any scale.  Sums against the reference overflow where
+// |v| is above ~2^67 (at a million columns): such a row is computed again with weights
+// that sum to 1, as below.
 //
 // Columns that a row does not see get p = 0, but 0 * NaN is NaN: a V row that
 // holds NaN or infinities reaches the output rows that do not see it.  A row
@@ -177,8 +178,8 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 }
 
 // Output of one row over its visible columns of [c_begin, c_end), by the whole
-// warp: lane l keeps values [l D / 32, (l + 1) D / 32).  m is the row's running
-// maximum in log2 units.
+// warp: lane l keeps values [l D / 32, (l + 1) D / 32).  m is the row's lse there in
+// log2 units: the weights sum to 1, so finite values stay finite.
 template <int D>
 __device__ __forceinline__ void row_again(const GqaArgs &a, const uint16_t *q, const uint32_t *words, int kv0, int c_begin,
                                        int c_end, int g, float m, float (&o)[D / 32]) {
@@ -953,17 +954,16 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                     const int n2 = __shfl_sync(0xffffffffu, node, from);
                     const int64_t row2 = __shfl_sync(0xffffffffu, (long long)row, from);
                     const int64_t prow2 = __shfl_sync(0xffffffffu, (long long)prow, from);
-                    const float m2 = __shfl_sync(0xffffffffu, m_ref, from), inv2 = __shfl_sync(0xffffffffu, inv, from);
+                    const float m2 = __shfl_sync(0xffffffffu, m_ref + log2f(l), from);
                     float o[D / 32];
                     row_again<D>(a, a.q + row2 * D, a.mask + sg.m0 + (int64_t)n2 * sg.W, sg.kv0, sg.c_begin, sg.c_end, sg.g,
                                  m2, o);
 #pragma unroll
                     for (int e = 0; e < D / 32; ++e) {
-                        const float x = o[e] * inv2;
                         if (part) {
-                            a.o_part[prow2 * D + lane * (D / 32) + e] = x;
+                            a.o_part[prow2 * D + lane * (D / 32) + e] = o[e];
                         } else {
-                            const __nv_bfloat16 y = __float2bfloat16_rn(x);
+                            const __nv_bfloat16 y = __float2bfloat16_rn(o[e]);
                             a.out[row2 * D + lane * (D / 32) + e] = *reinterpret_cast<const uint16_t *>(&y);
                         }
                     }
@@ -1010,33 +1010,32 @@ __global__ void __launch_bounds__(32 * kCombineWarps) gqa_combine_kernel(const G
     const int c0 = note.x >> 1, parts = note.y - c0 + 1;
     // row i of the warp; lanes of rows that are not there repeat the last one
     auto place = [&](int s, int i) { return (int64_t)(s == 0 ? note.x : 2 * (c0 + s)) * prm.part_rows + min(first + i, rows - 1); };
-    float m = -INFINITY, den = 0.f;  // of the lane's row (lane / L)
+    // The row's lse first: weights that sum to 1 keep a sum of finite parts finite.
+    float m = -INFINITY, den = 0.f, ls = -INFINITY;  // of the lane's row (lane / L); ls: of its part
+    auto part_lse = [&](int s0) {
+        const int mine = s0 + lane % L;
+        return mine < parts ? a.lse_part[place(mine, lane / L)] : -INFINITY;
+    };
+    for (int s0 = 0; s0 < parts; s0 += L) {
+        ls = part_lse(s0);
+        float mg = fmaxf(m, ls);
+#pragma unroll
+        for (int o = L / 2; o >= 1; o >>= 1) mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, o));
+        float sum = ls == -INFINITY ? 0.f : ex2((ls - mg) * kLog2e);  // NaN stays
+#pragma unroll
+        for (int o = L / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        den = den * (m == -INFINITY ? 0.f : ex2((m - mg) * kLog2e)) + sum;
+        m = mg;
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den, lse = den == 0.f ? -INFINITY : m + log2f(den) * kLn2;
     float acc[R][E];
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[i][e] = 0.f;
     for (int s0 = 0; s0 < parts; s0 += L) {
-        const int mine = s0 + lane % L;
-        const float ls = mine < parts ? a.lse_part[place(mine, lane / L)] : -INFINITY;
-        float mg = fmaxf(m, ls);
-#pragma unroll
-        for (int o = L / 2; o >= 1; o >>= 1) mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, o));
-        const float keep = m == -INFINITY ? 0.f : ex2((m - mg) * kLog2e);
-        const float w = ls == -INFINITY ? 0.f : ex2((ls - mg) * kLog2e);  // NaN stays
-        float sum = w;
-#pragma unroll
-        for (int o = L / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        den = den * keep + sum;
-        m = mg;
-        if (s0 > 0) {
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                const float k = __shfl_sync(0xffffffffu, keep, i * L);
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[i][e] *= k;
-            }
-        }
+        if (parts > L) ls = part_lse(s0);
+        const float w = ls == -INFINITY ? 0.f : ex2((ls - m) * kLog2e) * inv;
         const int n = min(L, parts - s0);
         for (int s = 0; s < n; s += kFlight) {
             float v[kFlight][R][E];
@@ -1067,19 +1066,18 @@ __global__ void __launch_bounds__(32 * kCombineWarps) gqa_combine_kernel(const G
             }
         }
     }
-    const float inv = den == 0.f ? 0.f : 1.f / den, lse = den == 0.f ? -INFINITY : m + log2f(den) * kLn2;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const float k = __shfl_sync(0xffffffffu, inv, i * L), ls = __shfl_sync(0xffffffffu, lse, i * L);
+        const float lse_i = __shfl_sync(0xffffffffu, lse, i * L);
         if (first + i >= rows) break;
         const int rr = row0 + first + i, node = quotient(rr, prm.group_inv);
         const int64_t row = (int64_t)(r.qo0 + node) * a.num_heads + g * prm.group + rr - node * prm.group;
         uint16_t *dst = a.out + row * D + lane * E;
         if constexpr (E == 4)
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(acc[i][0] * k, acc[i][1] * k), pack_bf16(acc[i][2] * k, acc[i][3] * k));
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(acc[i][0], acc[i][1]), pack_bf16(acc[i][2], acc[i][3]));
         else
-            *reinterpret_cast<uint32_t *>(dst) = pack_bf16(acc[i][0] * k, acc[i][1] * k);
-        if (a.lse && lane == 0) a.lse[row] = ls;
+            *reinterpret_cast<uint32_t *>(dst) = pack_bf16(acc[i][0], acc[i][1]);
+        if (a.lse && lane == 0) a.lse[row] = lse_i;
     }
 }
 
