@@ -59,10 +59,10 @@
 // that sum to 1, as below.
 //
 // Columns that a row does not see get p = 0, but 0 * NaN is NaN: a V row that
-// holds NaN or infinities reaches the output rows that do not see it.  A row
-// whose output is not finite is therefore computed again on the CUDA cores over
-// its visible columns only (the running maximum and sum stand: the scores were
-// selected before they were used).
+// holds NaN or infinities reaches the output rows that do not see it.  Rows whose
+// output is not finite are therefore computed again over their visible columns only,
+// after the CTA's last segment (rows_again): 16 rows at a time on the warps' own
+// products, K and V read from global memory in place of the pipeline.
 //
 // Every wait is bounded: on timeout the CTA latches DDT_DEVERR_TIMEOUT, waits
 // for its own copies and MMAs and leaves.
@@ -121,9 +121,10 @@ struct Cfg {
     static constexpr int kMmaWarp = kTiles == 2 ? kSoftWarps + kLoadWarps : kSoftWarps;
     static constexpr int kThreads = kTiles == 2 ? 640 : 256;
     // Registers of the two-tile kernel: a softmax thread's, another's; together no more than at
-    // launch.  65 tokens after 131072: 271 us with 120 / 72, 276 us with 128 / 72, 278 us with
-    // 136 / 64, 291 us with 144 / 64 and with 120 / 80.
-    static constexpr int kSoftRegs = 120, kOtherRegs = 72, kLaunchRegs = 96;
+    // launch.  65 tokens after 131072, and 32 requests of 17..33 after 2048..8192: 278 and 98.9 us
+    // with 128 / 72, 284 and 100.4 us with 120 / 72, 287 and 102.4 us with 112 / 80, 286 and
+    // 102.9 us with 136 / 64 (the last two spill).
+    static constexpr int kSoftRegs = 128, kOtherRegs = 72, kLaunchRegs = 96;
     static_assert(32 * kSoftWarps * kSoftRegs + (640 - 32 * kSoftWarps) * kOtherRegs <= 640 * kLaunchRegs || kTiles == 1, "registers");
     static constexpr uint32_t kTmemCols = kTiles == 2 ? 512 : 256;
     static constexpr uint32_t kColS = 0, kColO = 2 * NB;
@@ -137,7 +138,7 @@ struct Cfg {
                          bQFull = bPFull + 2 * kHalves, bHalf = bQFull + 1, bODone = bHalf + 2, bOFin = bODone + 1, bJoin = bOFin + 1, bDrain = bJoin + 1,
                          bSegFull = bDrain + 1, bSegEmpty = bSegFull + 2, bCount = bSegEmpty + 2;
     static constexpr int kOffHolder = kOffBar + 8 * bCount;
-    static constexpr int kOffWalk = kOffHolder + 8;  // 128 bytes: the walk; 2 x 48: the segments it has given
+    static constexpr int kOffWalk = kOffHolder + 16;  // 128 bytes: the walk; 2 x 48: the segments it has given
     static constexpr int kOffPlan = kOffWalk + 128 + 2 * 48;  // a sum per warp, then where the CTA's share starts
     static constexpr int kOffJoin = kOffPlan + 8 * (kThreads / 32);  // the second tile's references and sums
     static constexpr int kSmemUsed = kOffJoin + (kTiles == 2 ? kRows * 8 : 0);
@@ -175,36 +176,6 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
 // stays converged for the warp-collective instructions after it.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *err) {
     return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, err));
-}
-
-// Output of one row over its visible columns of [c_begin, c_end), by the whole
-// warp: lane l keeps values [l D / 32, (l + 1) D / 32).  m is the row's lse there in
-// log2 units: the weights sum to 1, so finite values stay finite.
-template <int D>
-__device__ __forceinline__ void row_again(const GqaArgs &a, const uint16_t *q, const uint32_t *words, int kv0, int c_begin,
-                                       int c_end, int g, float m, float (&o)[D / 32]) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    float x[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        x[e] = __uint_as_float((uint32_t)q[lane * E + e] << 16);
-        o[e] = 0.f;
-    }
-    for (int j = c_begin; j < c_end; ++j) {
-        if (!((words[j >> 5] >> (j & 31)) & 1u)) continue;
-        int64_t slot = a.kv_indices[kv0 + j];
-        if (slot < 0 || slot >= a.pool_rows) slot = 0;
-        const int64_t at = slot * a.pool_stride + (int64_t)g * D + lane * E;
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(x[e], __uint_as_float((uint32_t)a.k_pool[at + e] << 16), s);
-#pragma unroll
-        for (int w = 16; w >= 1; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-        const float p = ex2(s * (a.scale * kLog2e) - m);
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(p, __uint_as_float((uint32_t)a.v_pool[at + e] << 16), o[e]);
-    }
 }
 
 // ---------------------------------------------------------------- the deal
@@ -288,6 +259,8 @@ struct Walk {
     Request r;
     int b, tg, g, cta;
     int dealt, more;
+    int first_b;          // the request that the share starts in, and its position
+    int64_t first_pos;
 
     // one item, whole
     __device__ __forceinline__ void start_item(const Request &req, int b_, int tg_, int g_) {
@@ -307,12 +280,19 @@ struct Walk {
         b = b_;
         lo = lo_;
         hi = hi_;
+        first_b = b_;
+        first_pos = pos_;
         dealt = more = 1;
         const int64_t head = head_cost<C>(r), full = C::kCostItem + (int64_t)r.blocks * C::kCostFull;
         g = (int)divide(lo - pos_, head);
         pos = pos_ + g * head;
         tg = min((int)divide(lo - pos, full), r.tgs - 1);
         pos += tg * full;
+    }
+    // back to the first segment
+    __device__ __forceinline__ void restart(const GqaArgs &a, int group) {
+        if (dealt) start_share(load_request<C, kTiles>(a, group, first_b, nullptr), cta, first_b, first_pos, lo, hi);
+        else more = 1;
     }
     // the next segment; one without blocks when the share is done
     __device__ __forceinline__ Segment next(const GqaArgs &a, int group, int tgs_most) {
@@ -361,6 +341,229 @@ struct Walk {
     }
 };
 
+// ---------------------------------------------------------------- rows that are not finite
+// 16 rows of a segment (from row16 on) and 32 of the values (from e0 on), by one warp: where
+// the output written for a row holds an infinity or NaN, it is computed again over the
+// columns that the row sees.  In V infinities and NaN are replaced by 0 in the products; which
+// values they belong in, and with which sign, is kept as bits: kinds[e] has four for a pair of
+// rows (r, r + 8): seen as +inf by either, as -inf by either (NaN: both).  The weights are
+// taken against the running maximum and 2^31 below it, so that the sums stay finite: a row
+// has no 2^31 columns.  Bound by the latency of a block's slots, rows and products (few
+// warps, little in flight): one request of 33 tokens after 4096, 64 heads on 8, takes 0.33 ms
+// with a NaN in a prefix row, 0.06 without; 32 such requests with one NaN 3.3 ms, 0.24 without
+// (72 ms with one row and column at a time).  Pieces of 32 values keep the registers below what
+// the softmax needs: with 64, a quarter faster, the kernels spill and lose 3 to 12% where
+// nothing is computed again.
+constexpr int kKindWords = 32;
+
+template <int D>
+__device__ __forceinline__ void rows_again_16(const GqaParams &prm, const Segment &sg, int row16, int e0, uint32_t *kinds) {
+    constexpr uint32_t kAll = 0xffffffffu, kRow0 = 0x11111111u;
+    const GqaArgs &a = prm.a;
+    const int lane = threadIdx.x & 31, r8 = lane >> 2, c4 = lane & 3;
+    // the lane's rows r8 and r8 + 8: query, mask words, and its 8 of the 32 outputs
+    const uint16_t *q[2];
+    const uint32_t *words[2];
+    void *out[2];
+    bool bad[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int ri = row16 + r8 + 8 * i, rr = sg.row0 + min(ri, sg.rows - 1), node = quotient(rr, prm.group_inv);
+        const int64_t row = (int64_t)(sg.qo0 + node) * a.num_heads + sg.g * prm.group + rr - node * prm.group;
+        q[i] = a.q + row * D + 8 * c4;
+        words[i] = a.mask + sg.m0 + (int64_t)node * sg.W;
+        uint32_t high = 0;  // an exponent of ones among the values
+        if (sg.part >= 0) {
+            float *o = a.o_part + ((int64_t)sg.part * prm.part_rows + min(ri, sg.rows - 1)) * D + e0 + 8 * c4;
+            out[i] = o;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint4 x = reinterpret_cast<const uint4 *>(o)[k];
+                const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) high |= (v[e] & 0x7f800000u) == 0x7f800000u;
+            }
+        } else {
+            uint16_t *o = a.out + row * D + e0 + 8 * c4;
+            out[i] = o;
+            const uint4 x = *reinterpret_cast<const uint4 *>(o);
+            const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) high |= (v[e] & 0x7f80u) == 0x7f80u || (v[e] & 0x7f800000u) == 0x7f800000u;
+        }
+        bad[i] = ((__ballot_sync(kAll, high != 0 && ri < sg.rows) >> (4 * r8)) & 15u) != 0;
+    }
+    if (!__any_sync(kAll, bad[0] || bad[1])) return;
+    kinds[lane] = 0;
+    __syncwarp();
+
+    const float sc = a.scale * kLog2e;
+    float acc[4][4], ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+    const uint16_t *kp = a.k_pool + (int64_t)sg.g * D + 8 * c4, *vp = a.v_pool + (int64_t)sg.g * D + e0 + 4 * r8;
+    auto slot_of = [&](int c) {  // of column c + lane % 16
+        const int s = a.kv_indices[sg.kv0 + min(c + (lane & 15), sg.c_end - 1)];
+        return s < 0 || s >= a.pool_rows ? 0 : s;  // latched by the load warps
+    };
+    int ahead = slot_of(sg.c_begin);
+    for (int c = sg.c_begin; c < sg.c_end; c += 16) {
+        const int slot = ahead;
+        if (c + 16 < sg.c_end) ahead = slot_of(c + 16);
+        // the lane's columns: c + 2 c4, + 1, + 8, + 9
+        uint32_t seen[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t w = (words[i][c >> 5] >> (c & 31)) & 0xffffu;
+            if (sg.c_end - c < 16) w &= (1u << (sg.c_end - c)) - 1u;
+            seen[i] = w >> (2 * c4);
+        }
+        if (!__any_sync(kAll, ((seen[0] | seen[1]) & 0x303u) != 0)) continue;
+        uint2 v[4];  // 4 values from e0 + 4 r8 on of the lane's columns
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            v[k] = *reinterpret_cast<const uint2 *>(vp + __shfl_sync(kAll, slot, 2 * c4 + (k & 1) + 8 * (k >> 1)) * a.pool_stride);
+        const uint16_t *k0 = kp + __shfl_sync(kAll, slot, r8) * a.pool_stride, *k1 = kp + __shfl_sync(kAll, slot, r8 + 8) * a.pool_stride;
+        // Scores.  A lane has 8 values in a row of each 32 of q and of K: any order will do, as
+        // long as it is the same in both.
+        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int d = 0; d < D; d += 32) {
+            const uint4 q0 = *reinterpret_cast<const uint4 *>(q[0] + d), q1 = *reinterpret_cast<const uint4 *>(q[1] + d);
+            const uint4 x0 = *reinterpret_cast<const uint4 *>(k0 + d), x1 = *reinterpret_cast<const uint4 *>(k1 + d);
+            mma_16x8x16(s[0], q0.x, q1.x, q0.y, q1.y, x0.x, x0.y);
+            mma_16x8x16(s[1], q0.x, q1.x, q0.y, q1.y, x1.x, x1.y);
+            mma_16x8x16(s[0], q0.z, q1.z, q0.w, q1.w, x0.z, x0.w);
+            mma_16x8x16(s[1], q0.z, q1.z, q0.w, q1.w, x1.z, x1.w);
+        }
+        uint32_t high = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t x[2] = {v[k].x, v[k].y};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) high |= (x[e] & 0x7f80u) == 0x7f80u || (x[e] & 0x7f800000u) == 0x7f800000u;
+        }
+        if (__any_sync(kAll, high != 0)) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                // the 16 rows that see column k of the lane, at bits 4 r (+ 1 for r + 8); those whose
+                // weight there is 0 because the score is -inf: 0 times infinity is NaN
+                const int j = k >> 1, bit = (k & 1) + 8 * j;
+                uint32_t rows = 0, zero = 0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const bool sees = (seen[i] >> bit) & 1u;
+                    rows |= ((__ballot_sync(kAll, sees) >> c4) & kRow0) << i;
+                    zero |= ((__ballot_sync(kAll, sees && s[j][2 * i + (k & 1)] == -INFINITY) >> c4) & kRow0) << i;
+                }
+                uint32_t x[2] = {v[k].x, v[k].y};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t y = (x[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+                    if ((y & 0x7f80u) != 0x7f80u) continue;
+                    const bool nan = (y & 0x7fu) != 0, minus = (y >> 15) != 0;
+                    const uint32_t plus_rows = nan || !minus ? rows : zero, minus_rows = nan || minus ? rows : zero;
+                    if (rows) atomicOr(&kinds[4 * r8 + e], plus_rows | minus_rows << 2);
+                    x[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+                }
+                v[k] = make_uint2(x[0], x[1]);
+            }
+        }
+        uint32_t p[2][2];  // weights of the lane's columns: [c or c + 8][row]
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float x[4], mx = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[k] = (seen[i] >> ((k & 1) + 8 * (k >> 1))) & 1u ? s[k >> 1][2 * i + (k & 1)] * sc : -INFINITY;
+                mx = fmaxf(mx, x[k]);
+            }
+            mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2)) + 31.f;
+            if (mx > ref[i]) {
+                const float alpha = ex2(ref[i] - mx);
+                ref[i] = mx;
+                l[i] *= alpha;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    acc[n][2 * i] *= alpha;
+                    acc[n][2 * i + 1] *= alpha;
+                }
+            }
+            const float m = ref[i] == -INFINITY ? 0.f : ref[i];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[k] = ex2(x[k] - m);
+                l[i] += x[k];
+            }
+            p[0][i] = pack_bf16(x[0], x[1]);
+            p[1][i] = pack_bf16(x[2], x[3]);
+        }
+        const uint32_t w[4][2] = {{v[0].x, v[0].y}, {v[1].x, v[1].y}, {v[2].x, v[2].y}, {v[3].x, v[3].y}};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {  // column r8 of this product is value 4 r8 + n
+            const uint32_t pick = n & 1 ? 0x7632u : 0x5410u;
+            mma_16x8x16(acc[n], p[0][0], p[0][1], p[1][0], p[1][1], __byte_perm(w[0][n >> 1], w[1][n >> 1], pick),
+                        __byte_perm(w[2][n >> 1], w[3][n >> 1], pick));
+        }
+    }
+    __syncwarp();  // kinds is complete
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(kAll, l[i], 1);
+        l[i] += __shfl_xor_sync(kAll, l[i], 2);
+        if (!bad[i]) continue;
+        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float y[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                y[n] = acc[n][2 * i + j] * inv;
+                const uint32_t kind = (kinds[4 * (2 * c4 + j) + n] >> (4 * r8 + i)) & 5u;
+                if (kind) y[n] += kind == 1 ? INFINITY : kind == 4 ? -INFINITY : __uint_as_float(0x7fffffffu);
+            }
+            if (sg.part >= 0) {
+                reinterpret_cast<float4 *>(out[i])[j] = make_float4(y[0], y[1], y[2], y[3]);
+            } else {
+                reinterpret_cast<uint2 *>(out[i])[j] = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+            }
+        }
+    }
+    __syncwarp();  // kinds is read
+}
+
+// All segments of the CTA once more, after the last: each softmax warp takes its share of
+// the groups of rows.  Here nothing waits for it but the CTA's end.  room: shared memory that
+// nothing else uses any more; done: the CTA's walk, which has come to its end.
+template <class C, int D, int kTiles>
+__device__ __forceinline__ void rows_again(const GqaParams &prm, const Walk<C, kTiles> *done, uint8_t *room, int warp) {
+    constexpr int kRoom = 1024;
+    static_assert(sizeof(Walk<C, kTiles>) + sizeof(Segment) + 4 * kKindWords <= kRoom && C::kSoftWarps * kRoom <= C::kBlockBytes, "room");
+    room += warp * kRoom;
+    uint32_t *kinds = reinterpret_cast<uint32_t *>(room);
+    Walk<C, kTiles> *walk = reinterpret_cast<Walk<C, kTiles> *>(room + 4 * kKindWords);
+    Segment *place = reinterpret_cast<Segment *>(room + 4 * kKindWords + sizeof(Walk<C, kTiles>));
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) {
+        *walk = *done;
+        walk->restart(prm.a, prm.group);
+    }
+    while (true) {
+        if (lane == 0) *place = walk->next(prm.a, prm.group, prm.tgs_most);
+        __syncwarp();
+        const Segment sg = *place;
+        __syncwarp();
+        if (sg.blocks == 0) return;
+        const int units = (sg.rows + 15) / 16 * (D / 32);
+#pragma unroll 1
+        for (int u = warp; u < units; u += C::kSoftWarps)
+            rows_again_16<D>(prm, sg, u / (D / 32) * 16, u % (D / 32) * 32, kinds);
+    }
+}
+
 template <int D, int kTiles>
 __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, kTiles == 2 ? 1 : 2)
 gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
@@ -373,6 +576,7 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
     auto bar = [&](int i) { return sbase + C::kOffBar + 8u * i; };
     uint32_t *holder = reinterpret_cast<uint32_t *>(smem + C::kOffHolder);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffHolder + 4);
+    volatile int *not_finite = reinterpret_cast<volatile int *>(smem + C::kOffHolder + 8);  // a row of the CTA was not
     int64_t *plan = reinterpret_cast<int64_t *>(smem + C::kOffPlan);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -386,6 +590,7 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                       : i >= C::bSegEmpty                                          ? C::kSoftWarps + C::kLoadWarps + 1
                                                                                    : 1);
         *abort_flag = 0;
+        *not_finite = 0;
         fence_barrier_init();
     }
     // everything read below may be the previous kernel's output (q, the appended rows, the mask)
@@ -945,32 +1150,14 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                     if (part) a.lse_part[prow] = lse;
                     else if (a.lse) a.lse[row] = lse;
                 }
-                // rows that something unseen may have reached (a NaN sum stays one whatever V holds)
-                uint32_t again = __ballot_sync(0xffffffffu, row_on && check != check && l > 0.f);
-                __syncwarp();  // the rows are written (by other lanes) before any is written again
-                while (again) {
-                    const int from = __ffs(again) - 1;
-                    again &= again - 1;
-                    const int n2 = __shfl_sync(0xffffffffu, node, from);
-                    const int64_t row2 = __shfl_sync(0xffffffffu, (long long)row, from);
-                    const int64_t prow2 = __shfl_sync(0xffffffffu, (long long)prow, from);
-                    const float m2 = __shfl_sync(0xffffffffu, m_ref + log2f(l), from);
-                    float o[D / 32];
-                    row_again<D>(a, a.q + row2 * D, a.mask + sg.m0 + (int64_t)n2 * sg.W, sg.kv0, sg.c_begin, sg.c_end, sg.g,
-                                 m2, o);
-#pragma unroll
-                    for (int e = 0; e < D / 32; ++e) {
-                        if (part) {
-                            a.o_part[prow2 * D + lane * (D / 32) + e] = o[e];
-                        } else {
-                            const __nv_bfloat16 y = __float2bfloat16_rn(o[e]);
-                            a.out[row2 * D + lane * (D / 32) + e] = *reinterpret_cast<const uint16_t *>(&y);
-                        }
-                    }
-                }
+                // (a NaN sum stays one whatever V holds)
+                if (row_on && check != check && l > 0.f) *not_finite = 1;
                 tc_fence_before();  // the output has been read before the next segment's first product
             }
         }
+        // ---- rows that are not finite ----
+        named_barrier(1, 32 * C::kSoftWarps);  // every row of the CTA is written; its products have left shared memory
+        if (*not_finite && !*abort_flag) rows_again<C, D, kTiles>(prm, walk, smem + C::kOffK, warp);
     }
 
     // ---- teardown ----
@@ -1010,32 +1197,36 @@ __global__ void __launch_bounds__(32 * kCombineWarps) gqa_combine_kernel(const G
     const int c0 = note.x >> 1, parts = note.y - c0 + 1;
     // row i of the warp; lanes of rows that are not there repeat the last one
     auto place = [&](int s, int i) { return (int64_t)(s == 0 ? note.x : 2 * (c0 + s)) * prm.part_rows + min(first + i, rows - 1); };
-    // The row's lse first: weights that sum to 1 keep a sum of finite parts finite.
-    float m = -INFINITY, den = 0.f, ls = -INFINITY;  // of the lane's row (lane / L); ls: of its part
-    auto part_lse = [&](int s0) {
-        const int mine = s0 + lane % L;
-        return mine < parts ? a.lse_part[place(mine, lane / L)] : -INFINITY;
-    };
-    for (int s0 = 0; s0 < parts; s0 += L) {
-        ls = part_lse(s0);
-        float mg = fmaxf(m, ls);
-#pragma unroll
-        for (int o = L / 2; o >= 1; o >>= 1) mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, o));
-        float sum = ls == -INFINITY ? 0.f : ex2((ls - mg) * kLog2e);  // NaN stays
-#pragma unroll
-        for (int o = L / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        den = den * (m == -INFINITY ? 0.f : ex2((m - mg) * kLog2e)) + sum;
-        m = mg;
-    }
-    const float inv = den == 0.f ? 0.f : 1.f / den, lse = den == 0.f ? -INFINITY : m + log2f(den) * kLn2;
+    // weights of 2^-9 at most: those of DDT_GQA_MAX_CTAS parts sum to 1, and finite parts to a finite value
+    constexpr float kShift = 9.f;
+    static_assert(DDT_GQA_MAX_CTAS <= 512, "parts of a row");
+    float m = -INFINITY, den = 0.f;  // of the lane's row (lane / L)
     float acc[R][E];
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[i][e] = 0.f;
     for (int s0 = 0; s0 < parts; s0 += L) {
-        if (parts > L) ls = part_lse(s0);
-        const float w = ls == -INFINITY ? 0.f : ex2((ls - m) * kLog2e) * inv;
+        const int mine = s0 + lane % L;
+        const float ls = mine < parts ? a.lse_part[place(mine, lane / L)] : -INFINITY;
+        float mg = fmaxf(m, ls);
+#pragma unroll
+        for (int o = L / 2; o >= 1; o >>= 1) mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, o));
+        const float keep = m == -INFINITY ? 0.f : ex2((m - mg) * kLog2e);
+        const float w = ls == -INFINITY ? 0.f : ex2((ls - mg) * kLog2e - kShift);  // NaN stays
+        float sum = w;
+#pragma unroll
+        for (int o = L / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        den = den * keep + sum;
+        m = mg;
+        if (s0 > 0) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float k = __shfl_sync(0xffffffffu, keep, i * L);
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[i][e] *= k;
+            }
+        }
         const int n = min(L, parts - s0);
         for (int s = 0; s < n; s += kFlight) {
             float v[kFlight][R][E];
@@ -1066,18 +1257,19 @@ __global__ void __launch_bounds__(32 * kCombineWarps) gqa_combine_kernel(const G
             }
         }
     }
+    const float inv = den == 0.f ? 0.f : 1.f / den, lse = den == 0.f ? -INFINITY : m + (log2f(den) + kShift) * kLn2;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const float lse_i = __shfl_sync(0xffffffffu, lse, i * L);
+        const float k = __shfl_sync(0xffffffffu, inv, i * L), ls = __shfl_sync(0xffffffffu, lse, i * L);
         if (first + i >= rows) break;
         const int rr = row0 + first + i, node = quotient(rr, prm.group_inv);
         const int64_t row = (int64_t)(r.qo0 + node) * a.num_heads + g * prm.group + rr - node * prm.group;
         uint16_t *dst = a.out + row * D + lane * E;
         if constexpr (E == 4)
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(acc[i][0], acc[i][1]), pack_bf16(acc[i][2], acc[i][3]));
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(acc[i][0] * k, acc[i][1] * k), pack_bf16(acc[i][2] * k, acc[i][3] * k));
         else
-            *reinterpret_cast<uint32_t *>(dst) = pack_bf16(acc[i][0], acc[i][1]);
-        if (a.lse && lane == 0) a.lse[row] = lse_i;
+            *reinterpret_cast<uint32_t *>(dst) = pack_bf16(acc[i][0] * k, acc[i][1] * k);
+        if (a.lse && lane == 0) a.lse[row] = ls;
     }
 }
 

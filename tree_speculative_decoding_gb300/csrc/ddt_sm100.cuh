@@ -328,6 +328,16 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// d += a b, one warp: a 16 x 16 and b 16 x 8 bf16, d 16 x 8 fp32.  Lane l has of a the rows l/4
+// and l/4 + 8 at columns 2 (l%4) and 8 + 2 (l%4), two each (row, row + 8, then the later columns);
+// of b the same rows of column l/4; of d the columns 2 (l%4), + 1 of rows l/4 and l/4 + 8.
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
