@@ -57,6 +57,28 @@ def test_attention_joins_parts_of_the_largest_values(ddt, H, T, ctas):
     assert ((out.double().cpu() / (1.5 * 2.0 ** 127) - 1).abs() <= 2.0 ** -8 * (1 + 2.0 ** -8) + 2.0 ** -8).all()
 
 
+@pytest.mark.parametrize("H,T", [(4, 4), (64, 3)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_whose_reference_moves_in_every_block_repeats_itself(ddt, H, T, D):
+    # each block's weights are taken twice, and the second ones have to be those that count
+    batch = ref.Batch([(3000, T)] * 20, 155, "tree")
+    q, k, v, kd, vd = base.attn_inputs(batch, H, 1, D, 156, q_scale=0.01)
+    at = torch.from_numpy(batch.slots.astype(np.int64))
+    for b in range(batch.B):     # 64 natural units up every 64 columns
+        n = int(batch.kv[b + 1] - batch.kv[b])
+        k[at[int(batch.kv[b]): int(batch.kv[b + 1])], 0, 0] = (torch.arange(n) // 64 * 2.0).to(torch.bfloat16)
+    q[:, :, 0] = 32.0
+    kd.copy_(k)
+    out, ls = base.run_attn(ddt, batch, q, kd, vd, 1.0)
+    clean(ddt)
+    o, l, bo, bl = attention_on_device(q, kd, vd, batch, 1.0)
+    assert ((out.double() - o).abs() <= bo).all() and ((ls.double() - l).abs() <= bl).all()
+    for ctas in (0, 0, 0, 0):
+        again, ls2 = base.run_attn(ddt, batch, q, kd, vd, 1.0, ctas)
+        assert torch.equal(again, out) and torch.equal(ls2, ls)
+    clean(ddt)
+
+
 # ---------------------------------------------------------------- infinities and NaN
 def attention_on_device(q, kd, vd, batch, scale):
     """ref.attention in float64 on the device, request by request and K/V head by K/V head, for long

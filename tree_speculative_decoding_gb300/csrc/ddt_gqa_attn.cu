@@ -1007,6 +1007,7 @@ gqa_attn_kernel(const __grid_constant__ GqaParams prm) {
                             mx *= sc;
                             const bool up = moves && mx > m_ref;
                             if (!__any_sync(0xffffffffu, up)) break;  // scores of -inf or NaN move nothing
+                            if (kKeep) tmem_wait_st();  // the next weights go to the same columns: stores have no order
                             const float alpha = up ? ex2(m_ref - mx) : 1.0f;
                             if (up) m_ref = mx;
                             l *= alpha;
