@@ -626,8 +626,8 @@ ddt_status ddt_selftest_wait_timeout(uint32_t poll_limit, void *stream);
  *          kv_len_b - q_len_b (the root sits right behind the prefix);
  *   q goes to q_out, k and v to rows kv_indices[kv_indptr[b] + prefix_len_b + i]
  *          of the pools.
- * Arithmetic is fp32 with one rounding to bf16 at the end (a row's mean square
- * has to be finite in fp32: values up to 2^63); v is copied.
+ * Arithmetic is fp32 with one rounding to bf16 at the end (a normed row's sum of
+ * squares has to be finite in fp32: values up to 2^60 in magnitude); v is copied.
  *
  *   q, k, v     (device) bf16 [total_q][heads][head_dim], token t at t * stride
  *               elements (q_stride, k_stride, v_stride: multiples of 8, at least

@@ -192,3 +192,24 @@ def test_attention_of_a_long_request_with_infinities_serves_the_others(ddt, H, G
     assert torch.equal(out[33:], first[33:]) and torch.equal(ls, first_lse)
     assert torch.equal(out[:, H // G:], first[:, H // G:])
     check_on_device(out, ls, q, kd, vd, batch, D ** -0.5)
+
+
+# ---------------------------------------------------------------- append
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_norms_values_up_to_its_bound(ddt, D, interleaved):
+    # every value of a row +-2^60, the largest that the documentation allows: D of their squares sum
+    # to 2^127 at most; rows of ordinary size next to them in a warp
+    H, G = 8, 2
+    batch = ref.Batch([(4, 9)], 181, "tree")
+    qkv, w, table = base.append_inputs(batch, H, G, D, 64, True, 182)
+    rows = qkv.view(9, H + 2 * G, D)
+    for t in range(9):
+        big = (torch.arange(H + 2 * G) + t) % 3 > 0
+        rows[t, big] = torch.where(rows[t, big] < 0, -1.0, 1.0).to(torch.bfloat16) * 2.0 ** 60
+    before = normal((batch.rows, G, D), 1), normal((batch.rows, G, D), 2)
+    pools = [t.to(DEV) for t in before]
+    q_out = base.run_append(ddt, batch, qkv, w, table, H, G, D, interleaved, True, pools)
+    clean(ddt)
+    assert torch.isfinite(q_out).all() and (q_out != 0).any(-1).all()
+    base.check_append(batch, qkv, w, table, H, G, D, interleaved, True, before, q_out, pools)
