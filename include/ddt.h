@@ -609,8 +609,9 @@ ddt_status ddt_selftest_wait_timeout(uint32_t poll_limit, void *stream);
  *
  * In these calls a request may have q_len_b = 0 (it is skipped), total_q may
  * exceed qo_indptr[batch] and qo_indptr[0] exceed 0: the rows behind the last
- * request and ahead of the first are left as they are.  total_kv and total_mask_words are the sizes of kv_indices
- * and mask; offsets beyond them latch DDT_DEVERR_KV_INDPTR / _MASK_INDPTR and
+ * request and ahead of the first are left as they are.  total_kv and
+ * total_mask_words are the sizes of kv_indices and mask (an empty one may be
+ * NULL); offsets beyond them latch DDT_DEVERR_KV_INDPTR / _MASK_INDPTR and
  * the request is skipped.  Every argument in device memory may be the output
  * of the kernel launched just before on the same stream.
  *

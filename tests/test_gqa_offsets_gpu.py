@@ -198,3 +198,41 @@ def test_commit_of_broken_offsets_leaves_the_request_and_serves_the_others(ddt, 
     torch.cuda.synchronize()
     assert ddt.ddt_get_error() == (5, 0x200)
     assert torch.equal(p.cpu(), want) and new_len.cpu().tolist() == new
+
+
+# ---------------------------------------------------------------- nothing to do
+@pytest.mark.parametrize("cached", [0, 300])
+@pytest.mark.parametrize("B", [1, 3, 40])
+def test_a_batch_without_new_tokens_is_left_alone(ddt, B, cached):
+    # padding: rows of q that belong to no request; the mask, and without cached rows the slots, are empty
+    batch = ref.Batch([(cached, 0)] * B, 144, "tree")
+    H, G, D = 8, 2, 64
+    q = normal((5, H, D), 145)
+    pool = normal((max(batch.rows, 1), G, D), 146).to(DEV)
+    before = pool.clone()
+    assert batch.words.size == 0 and (cached > 0 or batch.slots.size == 0)
+    for ctas, max_q in ((0, 0), (0, 4), (3, 4)):
+        batch.max_q, batch.max_kv = max_q, cached + 8
+        out, ls = base.run_attn(ddt, batch, q, pool, pool, 0.1, ctas)
+        clean(ddt)
+        assert (out == 7).all() and (ls == 7).all()
+    qkv, w, table = torch.ones(5, (H + 2 * G) * D, dtype=torch.bfloat16), [torch.ones(D, dtype=torch.bfloat16)] * 2, torch.ones(9, 64)
+    q_out = append_at(ddt, batch, qkv, w, table, H, G, D, None, [pool, pool.clone()])
+    clean(ddt)
+    assert (q_out == 7).all() and torch.equal(pool, before)
+    d = batch.device()
+    zero, new_len = torch.zeros(B, dtype=torch.int32, device=DEV), torch.full((B,), -5, dtype=torch.int32, device=DEV)
+    ddt.ddt_cache_commit(pool[None], d["kv_indices"], d["kv_indptr"], d["qo_indptr"], zero, zero[:, None].expand(-1, 8).contiguous(), 7, new_len)
+    clean(ddt)
+    assert torch.equal(pool, before) and (new_len == cached).all()
+
+
+def test_a_call_takes_an_empty_array_for_none(ddt):
+    # one request has new tokens, and the arrays say that it has no slots: refused on the device
+    batch = ref.Batch([(0, 2)], 147, "tree")
+    q, k, v, kd, vd = base.attn_inputs(batch, 4, 2, 64, 148)
+    batch.slots, batch.words = batch.slots[:0], batch.words[:0]
+    out, ls = base.run_attn(ddt, batch, q, kd, vd, 0.1)
+    torch.cuda.synchronize()
+    assert ddt.ddt_get_error() == (5, 0x2)
+    assert (out == 7).all() and (ls == 7).all()

@@ -75,8 +75,8 @@ ddt_status ddt_gqa_norm_rope_append(
     const int32_t *kv_indptr, int32_t batch, int32_t total_q, int32_t total_kv, int32_t num_heads,
     int32_t num_kv_heads, int32_t head_dim, uint16_t *q_out, uint16_t *k_pool, uint16_t *v_pool,
     int64_t pool_stride, int64_t pool_rows, void *stream) {
-    if (!q || !k || !v || !qo_indptr || !kv_indices || !kv_indptr || !q_out || !k_pool || !v_pool || batch < 0 ||
-        total_q < 0 || total_kv < 0 || pool_rows < 1 || !(eps >= 0.f) || !isfinite(eps) || rope_dim < 0 || max_pos < 0 ||
+    if (!q || !k || !v || !qo_indptr || (!kv_indices && total_kv != 0) || !kv_indptr || !q_out || !k_pool ||
+        !v_pool || batch < 0 || total_q < 0 || total_kv < 0 || pool_rows < 1 || !(eps >= 0.f) || !isfinite(eps) || rope_dim < 0 || max_pos < 0 ||
         (rope_dim > 0 && !cos_sin))
         return DDT_ERR_INVALID_ARG;
     const ddt_status heads = check_heads(num_heads, num_kv_heads, head_dim);
@@ -169,9 +169,9 @@ ddt_status ddt_gqa_verify_attn(
     int32_t total_mask_words, int32_t max_q_len, int32_t max_kv_len, float scale,
     int32_t num_ctas, uint16_t *out, float *lse, void *workspace, size_t workspace_bytes,
     void *stream) {
-    if (!q || !k_pool || !v_pool || !kv_indices || !kv_indptr || !qo_indptr || !mask || !mask_indptr || !out ||
-        batch < 0 || total_q < 0 || total_kv < 0 || total_mask_words < 0 || pool_rows < 1 || max_q_len < 0 ||
-        max_kv_len < max_q_len || !isfinite(scale) || !(scale > 0.f) || num_ctas < 0)
+    if (!q || !k_pool || !v_pool || (!kv_indices && total_kv != 0) || !kv_indptr || !qo_indptr ||
+        (!mask && total_mask_words != 0) || !mask_indptr || !out || batch < 0 || total_q < 0 || total_kv < 0 ||
+        total_mask_words < 0 || pool_rows < 1 || max_q_len < 0 || max_kv_len < max_q_len || !isfinite(scale) || !(scale > 0.f) || num_ctas < 0)
         return DDT_ERR_INVALID_ARG;
     const ddt_status heads = check_heads(num_heads, num_kv_heads, head_dim);
     if (heads != DDT_OK) return heads;
@@ -243,8 +243,8 @@ ddt_status ddt_cache_commit(void *slab, int64_t pool_bytes, int64_t pool_rows, i
                             const int32_t *qo_indptr, const int32_t *accept_len,
                             const int32_t *accepted_nodes, int32_t batch, int32_t total_kv,
                             int32_t max_depth, int32_t *new_len, void *stream) {
-    if (bad_slab(slab, pool_bytes, pool_rows, num_pools, row_bytes) || !kv_indices || !kv_indptr || !qo_indptr ||
-        !accept_len || !accepted_nodes || batch < 0 || total_kv < 0)
+    if (bad_slab(slab, pool_bytes, pool_rows, num_pools, row_bytes) || (!kv_indices && total_kv != 0) || !kv_indptr ||
+        !qo_indptr || !accept_len || !accepted_nodes || batch < 0 || total_kv < 0)
         return DDT_ERR_INVALID_ARG;
     if (max_depth < 1 || max_depth > DDT_MAX_DEPTH) return DDT_ERR_UNSUPPORTED;
     if (batch == 0) return DDT_OK;
