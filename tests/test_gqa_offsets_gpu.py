@@ -236,3 +236,28 @@ def test_a_call_takes_an_empty_array_for_none(ddt):
     torch.cuda.synchronize()
     assert ddt.ddt_get_error() == (5, 0x2)
     assert (out == 7).all() and (ls == 7).all()
+
+
+# ---------------------------------------------------------------- another stream
+def test_attention_reads_its_bounds_on_the_calls_stream(ddt):
+    # offsets that the call's stream writes late, without the host's bounds
+    batch = ref.Batch([(300, 4), (20, 9)], 149, "tree")
+    q, k, v, kd, vd = base.attn_inputs(batch, 8, 2, 64, 150)
+    d, qd = batch.device(), q.to(DEV)
+    late = {n: torch.zeros_like(d[n]) for n in ("qo_indptr", "kv_indptr")}
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device=DEV)
+    s = torch.cuda.Stream()
+    call = lambda **kw: ddt.ddt_gqa_verify_attn(  # noqa: E731
+        qd, kd, vd, d["kv_indices"], late["kv_indptr"], late["qo_indptr"], d["mask"], d["mask_indptr"], 0.1, out, **kw)
+    call()      # of requests without tokens; loads what the calls below run
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(1000)
+    torch.cuda.synchronize()
+    assert (out == 7).all()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(50_000_000)
+        for n, t in late.items():
+            t.copy_(d[n])
+    call(stream=s)
+    clean(ddt)
+    base.check_attn(out, None, q, k, v, batch, 0.1)

@@ -576,8 +576,9 @@ def ddt_gqa_verify_attn(q, k_pool, v_pool, kv_indices, kv_indptr, qo_indptr, mas
     if total_q == 0 or B == 0:
         return
     if max_q_len is None or max_kv_len is None:
-        max_q_len = int((qo_indptr[1:] - qo_indptr[:-1]).max())
-        max_kv_len = int((kv_indptr[1:] - kv_indptr[:-1]).max())
+        with torch.cuda.stream(stream):   # behind what writes them there
+            max_q_len = int((qo_indptr[1:] - qo_indptr[:-1]).max())
+            max_kv_len = int((kv_indptr[1:] - kv_indptr[:-1]).max())
     if workspace is None:
         ctas = num_ctas or lib.ddt_gqa_verify_attn_num_ctas(B, H, G, max_q_len, max_kv_len, 0)
         nbytes = lib.ddt_gqa_verify_attn_workspace_size(B, H, G, D, max_q_len, ctas)
