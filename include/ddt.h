@@ -638,7 +638,8 @@ ddt_status ddt_selftest_wait_timeout(uint32_t poll_limit, void *stream);
  *               rope_dim/2 sines; NULL when rope_dim is 0 (no rotation).
  *   depth       (device) int32 [total_q] or NULL.
  *   q_out       (device) bf16 [total_q][num_heads][head_dim]; may be q itself
- *               when q_stride = num_heads * head_dim.
+ *               when q_stride = num_heads * head_dim, else outside the memory from
+ *               the first to the last row of q, k and v.
  *   k_pool, v_pool (device) bf16, row r at r * pool_stride elements (a multiple
  *               of 8, at least num_kv_heads * head_dim).
  * All pointers 16-byte aligned (weights, cos_sin too).  Supported: head_dim 64
@@ -684,7 +685,7 @@ ddt_status ddt_gqa_norm_rope_append(
  *               deals to what the device holds at once, less where workspace_bytes
  *               is too small for that.
  *   out         (device) bf16 [total_q][num_heads][head_dim], 16-byte aligned:
- *               what the layer's output projection reads; not q itself.
+ *               what the layer's output projection reads; no part of q's memory.
  *   lse         (device) float [total_q][num_heads] or NULL.
  *   workspace   (device) 256-byte aligned; ddt_gqa_verify_attn_workspace_size
  *               bytes for num_ctas, or NULL when that is 0.  Calls that may overlap

@@ -26,6 +26,14 @@ bool bad_pool_stride(int64_t stride, int32_t num_kv_heads, int32_t head_dim) {
     return stride < (int64_t)num_kv_heads * head_dim || stride % 8;
 }
 
+// whether [a, a + na) and [b, b + nb) share a byte; sizes in elements of 2 bytes
+bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y ? (y - x) / 2 < (uint64_t)na : (x - y) / 2 < (uint64_t)nb;
+}
+// elements from the first row's start to the last row's end
+int64_t extent(int32_t rows, int64_t stride, int64_t width) { return (rows - 1) * stride + width; }
+
 // columns of a request that are counted in 32 bits, with a block behind them
 constexpr int32_t kMostColumns = INT32_MAX - 127;
 
@@ -92,6 +100,12 @@ ddt_status ddt_gqa_norm_rope_append(
     for (const void *p : aligned)
         if (misaligned(p, 16)) return DDT_ERR_INVALID_ARG;
     if (batch == 0 || total_q == 0) return DDT_OK;
+    // what a token reads may not be what another one writes
+    const int64_t q_out_size = extent(total_q, qw, qw);
+    if ((q_out != q && overlap(q_out, q_out_size, q, extent(total_q, q_stride, qw))) ||
+        overlap(q_out, q_out_size, k, extent(total_q, k_stride, kw)) ||
+        overlap(q_out, q_out_size, v, extent(total_q, v_stride, kw)))
+        return DDT_ERR_INVALID_ARG;
     unsigned int *err = ddt::device_error_word();
     if (!err) return DDT_ERR_CUDA;
     ddt::AppendArgs a;
@@ -182,7 +196,9 @@ ddt_status ddt_gqa_verify_attn(
         misaligned(workspace, 256) || bad_pool_stride(pool_stride, num_kv_heads, head_dim))
         return DDT_ERR_INVALID_ARG;
     if (batch == 0 || total_q == 0 || max_q_len == 0) return DDT_OK;
-    if (out == q) return DDT_ERR_INVALID_ARG;  // CTAs that share an item read its q, one maybe after another's output
+    // CTAs that share an item read its q, one maybe after another's output
+    const int64_t rows_size = (int64_t)total_q * num_heads * head_dim;
+    if (overlap(out, rows_size, q, rows_size)) return DDT_ERR_INVALID_ARG;
     unsigned int *err = ddt::device_error_word();
     if (!err) return DDT_ERR_CUDA;
 
