@@ -668,9 +668,13 @@ ddt_status ddt_gqa_norm_rope_append(
  *   out[t,h,:] = sum_j softmax(s)_j * v_pool[row_j][g,:],
  *   lse[t,h]   = log(sum_j exp(s_j))   (natural log).
  * Every mask bit is honoured: a column that a row does not see does not reach
- * it, whatever its K and V rows hold (infinities and NaN included).  A row with
- * no visible column gets out = 0 and lse = -inf.  Decode is q_len 1, a prefill
- * chunk the mask of ddt_build_chain_visibility.
+ * it, whatever its K and V rows hold (infinities and NaN included).  Such values
+ * in V rows cost time: 2 to 20 times the call's for a few, 80 where all are.  A
+ * row with no visible column, or with scores of -inf alone, gets out = 0 and lse
+ * = -inf.  Finite K, V and scores give finite results.  Arithmetic is fp32, with
+ * the softmax's weights rounded to bf16 for the product with V (2^-8 sum p|v| of
+ * a result at most) and one rounding to bf16 at the end.  Decode is q_len 1, a
+ * prefill chunk the mask of ddt_build_chain_visibility.
  *
  *   q           (device) bf16 [total_q][num_heads][head_dim], 16-byte aligned.
  *   k_pool, v_pool (device) bf16, row r at r * pool_stride elements (a multiple

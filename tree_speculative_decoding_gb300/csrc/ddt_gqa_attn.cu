@@ -30,12 +30,15 @@
 //
 // Measured with the combine kernel, D = 128: 64 requests of one token after
 // 1024..16384, 64 heads on 8: 345 us, 6.6 TB/s, bound by memory.  32 requests of
-// 17..33 tokens after 2048..8192, 32 heads on 4: 100 us, 3.7 TB/s and 730 TFLOP/s;
-// 65 tokens after 131072, 64 heads on 8: 271 us, 1030 TFLOP/s: a block of two tiles
-// takes ~2700 clk where its products take 2048, since a tile's next scores wait
-// for its softmax and its products (tensor memory is full; a third slot at D = 64,
-// where it fits, measured 6% slower).  Of the 100 us, 8 fill the first pipeline, 6
-// to 10 each go to a CTA's change of item, 9 to the combine.
+// 17..33 tokens after 2048..8192, 32 heads on 4: 99 us, 3.7 TB/s and 735 TFLOP/s;
+// 65 tokens after 131072, 64 heads on 8: 272 us, 1025 TFLOP/s, in short runs, 300 us
+// and 930 TFLOP/s held for seconds under the power limit: a block of two tiles takes
+// ~2700 clk where its products take 2048.  A tile's next scores wait for its softmax
+// and its products (tensor memory is full; a third slot at D = 64, where it fits,
+// measured 6% slower), and the gather takes issue slots from the softmax: with a
+// sixteenth of the copies (timing only) the long one took 227 us where it took 291,
+// the 32 requests 83 where they took 104.  Of the 99 us, 8 fill the first pipeline,
+// 6 to 10 each go to a CTA's change of item, 9 to the combine.
 //
 // Score slots: two buffers of one block's scores in tensor memory.  Work unit w
 // of a segment (block-major, tiles inside a block) uses slot w mod 2.  The MMA
@@ -53,10 +56,13 @@
 // The softmax does not look for a block's maximum: the weights of 64 columns are
 // taken against the row's reference, the maximum of the first columns it saw.
 // Only where their sum passes 2^40 (or the row had seen nothing) the maximum is
-// found, the reference moves, and the sums so far are scaled.  bf16 weights keep
-// their relative precision at any scale.  Sums against the reference overflow where
-// |v| is above ~2^67 (at a million columns): such a row is computed again with weights
-// that sum to 1, as below.
+// found, the reference moves, and the sums so far are scaled.  Statistics, sums and
+// partial results are fp32.  The weights are rounded to bf16 for the product with V,
+// since the tensor core takes both operands in V's type: 2^-8 of each at most, at any
+// scale, which adds up to 2^-8 sum p|v| to the result (0.0023 of the largest value
+// against 0.0017 for weights in fp32, both with the output's own rounding); their sum
+// is taken before that.  Sums against the reference overflow where |v| is above ~2^67
+// (at a million columns): such a row is computed again, as below.
 //
 // Columns that a row does not see get p = 0, but 0 * NaN is NaN: a V row that
 // holds NaN or infinities reaches the output rows that do not see it.  Rows whose
@@ -121,10 +127,10 @@ struct Cfg {
     static constexpr int kMmaWarp = kTiles == 2 ? kSoftWarps + kLoadWarps : kSoftWarps;
     static constexpr int kThreads = kTiles == 2 ? 640 : 256;
     // Registers of the two-tile kernel: a softmax thread's, another's; together no more than at
-    // launch.  65 tokens after 131072, and 32 requests of 17..33 after 2048..8192: 278 and 98.9 us
-    // with 128 / 72, 284 and 100.4 us with 120 / 72, 287 and 102.4 us with 112 / 80, 286 and
-    // 102.9 us with 136 / 64 (the last two spill).
-    static constexpr int kSoftRegs = 128, kOtherRegs = 72, kLaunchRegs = 96;
+    // launch.  65 tokens after 131072, and 8 requests of 33 after 1024..16384: 272 and 118 us with
+    // 120 / 72, 273 and 121 us with 128 / 72, 281 and 124 us with 136 / 64, 291 and 127 us with
+    // 112 / 80.
+    static constexpr int kSoftRegs = 120, kOtherRegs = 72, kLaunchRegs = 96;
     static_assert(32 * kSoftWarps * kSoftRegs + (640 - 32 * kSoftWarps) * kOtherRegs <= 640 * kLaunchRegs || kTiles == 1, "registers");
     static constexpr uint32_t kTmemCols = kTiles == 2 ? 512 : 256;
     static constexpr uint32_t kColS = 0, kColO = 2 * NB;
@@ -148,10 +154,11 @@ struct Cfg {
     // Cost of a block with all tiles and with one, in one unit; of an item besides its
     // blocks: a CTA that goes on to another one writes the last one's rows, loads q and
     // fills its pipeline anew, 6 to 10 us (two tiles) or 2 to 3 us; and the share that a CTA
-    // gets at least.  Measured with D = 128, 64 heads on 8: 8 requests of 33 tokens after
-    // 1024..16384 take 131 us with an item at 72, 149 us at 24, 135 us at 160; one request
-    // of 33 after 1024 20 us with shares of 48, 24 us of 80, 35 us of 200; one token after
-    // 600 12.2 us with an item at 48 and shares of 28, 14.0 us at 24 and 36, 15.2 us at 64 and 80.
+    // gets at least.  Measured with D = 128, 64 heads on 8.  An item at 80 / 48 (two tiles / one):
+    // 8 requests of 33 tokens after 1024..16384 take 119 us, one token after 4096 14.1 us; at 24 /
+    // 24 137 and 14.4 us, at 160 / 96 125 and 14.6 us.  Shares of 56 / 32: one request of 33 after
+    // 1024 14.5 us, one token after 600 11.9 us; of 28 / 16 16.2 and 10.8 us (and one token after
+    // 4096 16.0 us); of 120 / 80 18.7 and 15.6 us.
     static constexpr int kCostFull = kTiles == 2 ? 16 : 8, kCostOne = kTiles == 2 ? 11 : 8;
     static constexpr int kCostItem = kTiles == 2 ? 80 : 48, kMinShare = kTiles == 2 ? 56 : 32;
     static_assert(kTiles == 2 || (kKStages >= 2 && kKStages <= kVStages), "see the load warps");
@@ -211,14 +218,14 @@ __device__ __forceinline__ Request load_request(const GqaArgs &a, int group, int
     const int kv1 = a.kv_indptr[b + 1];
     r.m0 = a.mask_indptr[b];
     const int m1 = a.mask_indptr[b + 1];
-    // broken offsets, and the words of a long request, do not fit 32 bits
-    const int64_t T = (int64_t)qo1 - r.qo0, N = (int64_t)kv1 - r.kv0;
-    const bool bad_qo = T < 0 || T > a.max_q_len || r.qo0 < 0 || qo1 > a.total_q;
-    const bool bad_kv = N < T || N > a.max_kv_len || r.kv0 < 0 || kv1 > a.total_kv;
+    // Differences of broken offsets wrap, which is why their order counts; the words of a long
+    // request do not fit 32 bits.
+    r.T = (int)((uint32_t)qo1 - (uint32_t)r.qo0);
+    r.N = (int)((uint32_t)kv1 - (uint32_t)r.kv0);
+    const bool bad_qo = r.T < 0 || r.T > a.max_q_len || r.qo0 < 0 || qo1 > a.total_q || qo1 < r.qo0;
+    const bool bad_kv = r.N < r.T || r.N > a.max_kv_len || r.kv0 < 0 || kv1 > a.total_kv || kv1 < r.kv0;
     const bool bad_mask =
-        !bad_qo && !bad_kv && (r.m0 < 0 || (int64_t)m1 - r.m0 != T * ((N + 31) >> 5) || m1 > a.total_mask_words);
-    r.T = (int)T;
-    r.N = (int)N;
+        !bad_qo && !bad_kv && (r.m0 < 0 || (int64_t)m1 - r.m0 != (int64_t)r.T * ((r.N + 31) >> 5) || m1 > a.total_mask_words);
     if (bad_qo || bad_kv || bad_mask) {
         latch(err, (bad_qo ? DDT_DEVERR_QO_INDPTR : 0u) | (bad_kv ? DDT_DEVERR_KV_INDPTR : 0u) |
                        (bad_mask ? DDT_DEVERR_MASK_INDPTR : 0u));
@@ -349,11 +356,11 @@ struct Walk {
 // rows (r, r + 8): seen as +inf by either, as -inf by either (NaN: both).  The weights are
 // taken against the running maximum and 2^31 below it, so that the sums stay finite: a row
 // has no 2^31 columns.  Bound by the latency of a block's slots, rows and products (few
-// warps, little in flight): one request of 33 tokens after 4096, 64 heads on 8, takes 0.33 ms
-// with a NaN in a prefix row, 0.06 without; 32 such requests with one NaN 3.3 ms, 0.24 without
-// (72 ms with one row and column at a time).  Pieces of 32 values keep the registers below what
-// the softmax needs: with 64, a quarter faster, the kernels spill and lose 3 to 12% where
-// nothing is computed again.
+// warps, little in flight): one request of 33 tokens after 4096, 64 heads on 8, takes 0.39 ms
+// with a NaN in a prefix row, 0.06 without; 32 such requests with one NaN 4.2 ms, 0.24 without
+// (72 ms with one row and column at a time).  Pieces of 32 values, and a loop over the scores that
+// is not unrolled, keep the registers below what the softmax needs: with 64 values and the loop
+// unrolled this takes 2.4 ms, and the kernels lose 3 to 12% where nothing is computed again.
 constexpr int kKindWords = 32;
 
 template <int D>
@@ -429,7 +436,7 @@ __device__ __forceinline__ void rows_again_16(const GqaParams &prm, const Segmen
         // Scores.  A lane has 8 values in a row of each 32 of q and of K: any order will do, as
         // long as it is the same in both.
         float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
+#pragma unroll 1
         for (int d = 0; d < D; d += 32) {
             const uint4 q0 = *reinterpret_cast<const uint4 *>(q[0] + d), q1 = *reinterpret_cast<const uint4 *>(q[1] + d);
             const uint4 x0 = *reinterpret_cast<const uint4 *>(k0 + d), x1 = *reinterpret_cast<const uint4 *>(k1 + d);
@@ -1352,8 +1359,11 @@ int slots(int tiles, int num_sms) { return std::min(num_sms * (tiles == 2 ? 1 : 
 // two tiles halve the reads of K and V, one tile starts and ends faster.  The constants
 // are fitted to 224 shapes measured dealt and undealt, above 128 rows with one tile and
 // two (1 to 64 requests, 500 to 16000 columns even and ragged, 1 to 33 tokens, 4 to 16
-// K/V heads): each way within 10%.  The choice costs 1% over the best on average and 20%
-// at most, where one fixed way (two tiles above 128 rows, dealt) cost 17% and 100%.  64
+// K/V heads): each way within 10%.  The choice costs 1% over the best of these on average and
+// 20% at most (29% over some 100 other shapes, prompt chunks among them), where one fixed way
+// (two tiles above 128 rows, dealt) cost 17% and 100%.  The sizes are means over the call: one
+// long request among many short ones, and a kv_indices longer than its requests, are weighed
+// as an even batch of them.  64
 // requests of 33 tokens x 64 heads after 1000 take 230 us dealt with two tiles, 130 us
 // undealt with one; 4 of them after 16000 120 us dealt and 217 us undealt; 16 of 32
 // tokens after 8000 122 us undealt with two tiles, 140 us with one.
