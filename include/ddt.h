@@ -762,9 +762,9 @@ ddt_status ddt_cache_commit(void *slab, int64_t pool_bytes, int64_t pool_rows, i
  * rows stay where they are.  Rows n .. pool_rows - 1 are free afterwards; a
  * request is freed by leaving its slots out of kv_indices.
  *   kv_indices  (device) int32 [total].
- *   new_indices (device) int32 [total]: the slots after the move; may be
- *               kv_indices itself.
- *   live        (device) int32 [1]: n.
+ *   new_indices (device) int32 [total]: the slots after the move; kv_indices
+ *               itself or memory outside it.
+ *   live        (device) int32 [1]: n; outside both.
  *   workspace   (device) ddt_cache_compact_workspace_size(pool_rows) bytes,
  *               256-byte aligned; calls that may overlap need one each.
  * Supported: pool_rows <= DDT_CACHE_MAX_ROWS.  Device check: a slot outside the

@@ -4,7 +4,7 @@ import ctypes
 
 import pytest
 
-from tests.test_gqa_cpu import APPEND, ATTN, COMMIT, INVALID, call, lib  # noqa: F401  (lib: the fixture)
+from tests.test_gqa_cpu import APPEND, ATTN, COMMIT, COMPACT, INVALID, call, lib  # noqa: F401  (lib: the fixture)
 
 
 @pytest.mark.parametrize("name,good,array,size", [
@@ -36,3 +36,14 @@ def test_append_refuses_an_output_over_its_inputs(lib, name, where):  # noqa: F8
     far = {n: at((3 + i) << 16) for i, n in enumerate(("q", "k", "v"))}
     good = dict(APPEND, total_q=3, **far, q_out=at((far[name].value - (1 << 20)) + away))
     assert call(lib, "ddt_gqa_norm_rope_append", good) == INVALID
+
+
+def test_compact_refuses_results_over_its_slots(lib):  # noqa: F811
+    good = dict(COMPACT, total=5, idx=at(4096), new=at(8192), live=at(12288), ws=at(1 << 17),
+                wsb=lib.ddt_cache_compact_workspace_size(10))
+    f = lambda **c: call(lib, "ddt_cache_compact", good, **c)  # noqa: E731
+    for away in (4, 16, -4, -16):
+        assert f(new=at(4096 + away)) == INVALID
+    for place in ("idx", "new"):
+        for k in range(5):
+            assert f(live=ctypes.c_void_p(good[place].value + 4 * k)) == INVALID

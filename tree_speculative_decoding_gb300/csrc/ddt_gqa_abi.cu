@@ -26,10 +26,11 @@ bool bad_pool_stride(int64_t stride, int32_t num_kv_heads, int32_t head_dim) {
     return stride < (int64_t)num_kv_heads * head_dim || stride % 8;
 }
 
-// whether [a, a + na) and [b, b + nb) share a byte; sizes in elements of 2 bytes
-bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+// whether a[0 .. na) and b[0 .. nb) share a byte
+template <class T, class U>
+bool overlap(const T *a, int64_t na, const U *b, int64_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y ? (y - x) / 2 < (uint64_t)na : (x - y) / 2 < (uint64_t)nb;
+    return na > 0 && nb > 0 && (x < y ? (y - x) / sizeof(T) < (uint64_t)na : (x - y) / sizeof(U) < (uint64_t)nb);
 }
 // elements from the first row's start to the last row's end
 int64_t extent(int32_t rows, int64_t stride, int64_t width) { return (rows - 1) * stride + width; }
@@ -286,6 +287,10 @@ ddt_status ddt_cache_compact(void *slab, int64_t pool_bytes, int64_t pool_rows, 
     if (pool_rows > DDT_CACHE_MAX_ROWS) return DDT_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < ddt::cache_compact_workspace(pool_rows) || misaligned(workspace, 256))
         return DDT_ERR_WORKSPACE;
+    // slots that are still read may not be written: in place each is, by its own reader
+    if ((new_indices != kv_indices && overlap(new_indices, total, kv_indices, total)) ||
+        overlap(live, 1, kv_indices, total) || overlap(live, 1, new_indices, total))
+        return DDT_ERR_INVALID_ARG;
     unsigned int *err = ddt::device_error_word();
     if (!err) return DDT_ERR_CUDA;
     return launched(ddt::launch_cache_compact(slab, pool_bytes, pool_rows, num_pools, row_bytes, kv_indices, total,
