@@ -293,7 +293,8 @@ class GqaVerifyStep:
 
     def compact(self, stream=None):
         """The rows that kv_indices names to the front of every pool; kv_indices becomes their new
-        numbers, live their count."""
+        numbers, live their count.  After a commit it still names the step's rejected nodes: their
+        rows are free once the caller has written the next step's slots over them."""
         ddt.ddt_cache_compact(self.kv, self.kv_indices, self.kv_indices, self.live, self.workspace, stream)
 
     check_device_errors = VerifyStep.check_device_errors
