@@ -28,6 +28,8 @@
  * one V row per token in pools of their own:
  *   ddt_gqa_norm_rope_append  per-head norm and rotation of q and k, k and v into the cache
  *   ddt_gqa_verify_attn     tree-verify attention over grouped-query K/V rows
+ *   ddt_gqa_chunk_attn      attention of a chunk of any length: capped scores, distance
+ *                           bias, window, prefix mask
  *   ddt_cache_commit        ddt_commit_kv for every layer's pool of any row width
  *   ddt_cache_copy          rows copied to other rows in every layer's pool
  *   ddt_cache_compact       live rows moved to the front of every pool
@@ -88,7 +90,8 @@ extern "C" {
 #define DDT_MAX_SPLITS 128
 #define DDT_MAX_VOCAB 262144 /* ddt_accept_sampled */
 #define DDT_GQA_MAX_HEADS 128 /* query heads of the grouped-query calls */
-#define DDT_GQA_MAX_CTAS 512  /* ddt_gqa_verify_attn: CTAs that the work is dealt to */
+#define DDT_GQA_MAX_CTAS 512  /* grouped-query attention: CTAs that the work is dealt to */
+#define DDT_GQA_MAX_CHUNK (1 << 20) /* new tokens of a request in the chunk calls */
 #define DDT_CACHE_MAX_ROWS (1 << 24) /* ddt_cache_compact: rows of a pool */
 
 typedef enum {
@@ -722,6 +725,62 @@ ddt_status ddt_gqa_verify_attn(
     void *stream);
 
 /*
+ * Chunks.  The calls above take up to 128 new tokens under any mask.  A prompt,
+ * or a part of one, is longer, and its mask follows from positions: token i of
+ * request b is at position p = prefix_len_b + i (prefix_len_b = kv_len_b -
+ * q_len_b), column j at position j, and it sees the columns
+ *   j < full_len_b               (a prefix that every token sees: a prefix mask, or the
+ *                                first columns that stay visible behind a window), and
+ *   p - window < j <= p          (window 0: every j <= p).
+ * A score is, with z = scale * <q[t,h,:], k_pool[row_j][g,:]>,
+ *   z <- score_cap * tanh(z / score_cap)   where score_cap > 0, then
+ *   z <- z - slopes[h] * |p - j|           where slopes are given.
+ * Positions count columns: in a cache that rows have left (ddt_cache_evict) they
+ * are the places in what is left.
+ *
+ * ddt_gqa_chunk_attn -- out[t,h,:] = sum_j softmax(z)_j * v_pool[row_j][g,:] over
+ * the columns that token t sees, lse[t,h] = log(sum_j exp(z_j)) (natural log); the
+ * layouts and the meaning of q, the pools, kv_indices, the offsets, out, lse,
+ * num_ctas and workspace are those of ddt_gqa_verify_attn.  Chunks of any length
+ * up to DDT_GQA_MAX_CHUNK; a single token is a chunk of one.
+ * A column that a token does not see does not reach it, whatever its K and V rows
+ * hold (infinities and NaN included).  Scores of -inf alone give out = 0 and lse =
+ * -inf.  Finite scores and V give finite results.  Arithmetic is fp32, with the
+ * softmax's weights rounded to bf16 for the product with V (2^-8 sum p|v| of a
+ * result at most) and one rounding to bf16 at the end; values of V below 2^-73 lose
+ * precision.  A capped score is off by score_cap * 2^-21 at most.
+ *
+ *   score_cap   0 (none) up to 2^20.
+ *   slopes      (device) float [num_heads] or NULL.
+ *   window      0 (none) or the columns that a token sees, its own included.
+ *   full_len    (device) int32 [batch] or NULL (0); taken as 0 or kv_len_b where it
+ *               is below or above.
+ * Supported: as ddt_gqa_verify_attn, with max_q_len up to DDT_GQA_MAX_CHUNK;
+ * scale (or 2 scale / score_cap) within 2^-100 .. 2^100.
+ * Device checks (latched, the request's rows left unwritten): q_len outside
+ * [0, max_q_len] or offsets outside [0, total_q] (DDT_DEVERR_QO_INDPTR), kv_len
+ * outside [q_len, max_kv_len] or offsets outside [0, total_kv]
+ * (DDT_DEVERR_KV_INDPTR), a slot outside the pool (DDT_DEVERR_KV_INDEX: row 0 is
+ * read instead).
+ *
+ * ddt_gqa_chunk_attn_num_ctas() returns the count whose workspace is enough for
+ * every choice within these bounds, on num_sms SMs (<= 0: the current device's);
+ * 0: no workspace is used.
+ */
+int32_t ddt_gqa_chunk_attn_num_ctas(int32_t batch, int32_t num_heads, int32_t num_kv_heads,
+                                    int32_t max_q_len, int32_t max_kv_len, int32_t num_sms);
+size_t ddt_gqa_chunk_attn_workspace_size(int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                         int32_t max_q_len, int32_t num_ctas);
+ddt_status ddt_gqa_chunk_attn(
+    const uint16_t *q, const uint16_t *k_pool, const uint16_t *v_pool, int64_t pool_stride,
+    int64_t pool_rows, const int32_t *kv_indices, const int32_t *kv_indptr,
+    const int32_t *qo_indptr, int32_t batch, int32_t num_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t total_q, int32_t total_kv, int32_t max_q_len, int32_t max_kv_len,
+    float scale, float score_cap, const float *slopes, int32_t window, const int32_t *full_len,
+    int32_t num_ctas, uint16_t *out, float *lse, void *workspace, size_t workspace_bytes,
+    void *stream);
+
+/*
  * Cache rows of every layer at once.  The layers' pools are one slab: pool p
  * (p < num_pools: one per layer for a latent cache, one for K and one for V
  * per layer for a grouped-query one) starts at p * pool_bytes bytes and holds
@@ -777,7 +836,7 @@ ddt_status ddt_cache_compact(void *slab, int64_t pool_bytes, int64_t pool_rows, 
                              size_t workspace_bytes, void *stream);
 
 /*
- * ddt_call_words -- one of the five calls above with its arguments as 64-bit
+ * ddt_call_words -- one of the calls named below with its arguments as 64-bit
  * words, for bindings that pay for every argument (ctypes: 0.1 us each):
  * words[0] names the call, words[1] counts the arguments, which follow in the
  * order of the parameters: pointers and integers as they are, floats as the
@@ -789,7 +848,8 @@ enum {
     DDT_CALL_GQA_VERIFY_ATTN = 1,
     DDT_CALL_CACHE_COPY = 2,
     DDT_CALL_CACHE_COMMIT = 3,
-    DDT_CALL_CACHE_COMPACT = 4
+    DDT_CALL_CACHE_COMPACT = 4,
+    DDT_CALL_GQA_CHUNK_ATTN = 5
 };
 ddt_status ddt_call_words(const int64_t *words);
 

@@ -38,6 +38,50 @@ int64_t extent(int32_t rows, int64_t stride, int64_t width) { return (rows - 1) 
 // columns of a request that are counted in 32 bits, with a block behind them
 constexpr int32_t kMostColumns = INT32_MAX - 127;
 
+// what the chunk calls check alike; fills in a (but for what one of them alone has)
+ddt_status chunk_args(ddt::ChunkArgs &a, const uint16_t *q, const uint16_t *k_pool, int64_t pool_stride, int64_t pool_rows,
+                      const int32_t *kv_indices, const int32_t *kv_indptr, const int32_t *qo_indptr, int32_t batch,
+                      int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t total_q, int32_t total_kv,
+                      int32_t max_q_len, int32_t max_kv_len, float scale, float score_cap, const float *slopes, int32_t window,
+                      const int32_t *full_len, const void *workspace) {
+    if (!q || !k_pool || (!kv_indices && total_kv != 0) || !kv_indptr || !qo_indptr || batch < 0 || total_q < 0 ||
+        total_kv < 0 || pool_rows < 1 || max_q_len < 0 || max_kv_len < max_q_len || !isfinite(scale) || !(scale > 0.f) ||
+        !isfinite(score_cap) || !(score_cap >= 0.f) || window < 0)
+        return DDT_ERR_INVALID_ARG;
+    const ddt_status heads = check_heads(num_heads, num_kv_heads, head_dim);
+    if (heads != DDT_OK) return heads;
+    // the factors of a score in log2 units have to be normal numbers
+    const float lin = score_cap > 0.f ? 2.f * 1.4426950408889634f * scale / score_cap : scale * 1.4426950408889634f;
+    if (max_q_len > DDT_GQA_MAX_CHUNK || pool_rows > INT32_MAX || batch > 65535 || !(lin >= 0x1p-100f && lin <= 0x1p100f) ||
+        score_cap > 0x1p20f)
+        return DDT_ERR_UNSUPPORTED;
+    if (misaligned(q, 16) || misaligned(k_pool, 16) || misaligned(workspace, 256) ||
+        bad_pool_stride(pool_stride, num_kv_heads, head_dim))
+        return DDT_ERR_INVALID_ARG;
+    memset(&a, 0, sizeof a);
+    a.q = q;
+    a.k_pool = k_pool;
+    a.pool_stride = pool_stride;
+    a.pool_rows = pool_rows;
+    a.kv_indices = kv_indices;
+    a.kv_indptr = kv_indptr;
+    a.qo_indptr = qo_indptr;
+    a.batch = batch;
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.total_q = total_q;
+    a.total_kv = total_kv;
+    a.max_q_len = max_q_len;
+    a.max_kv_len = max_kv_len < kMostColumns ? max_kv_len : kMostColumns;
+    a.scale = scale;
+    a.score_cap = score_cap;
+    a.slopes = slopes;
+    a.window = window;
+    a.full_len = full_len;
+    return DDT_OK;
+}
+
 // layout of a slab of pools
 bool bad_slab(const void *slab, int64_t pool_bytes, int64_t pool_rows, int32_t num_pools, int64_t row_bytes) {
     if (!slab || misaligned(slab, 16) || pool_rows < 1 || num_pools < 1 || row_bytes < 16 || row_bytes % 16 ||
@@ -241,6 +285,68 @@ ddt_status ddt_gqa_verify_attn(
     return launched(ddt::launch_gqa_attn(a, num_sms, as_stream(stream)));
 }
 
+int32_t ddt_gqa_chunk_attn_num_ctas(int32_t batch, int32_t num_heads, int32_t num_kv_heads,
+                                    int32_t max_q_len, int32_t max_kv_len, int32_t num_sms) {
+    if (batch < 1 || num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads || max_q_len < 1 ||
+        max_kv_len < 1)
+        return 0;
+    if (num_sms <= 0) num_sms = ddt::device_sm_count();
+    return ddt::chunk_most_ctas(batch, num_heads, num_kv_heads, max_q_len, max_kv_len, num_sms);
+}
+
+size_t ddt_gqa_chunk_attn_workspace_size(int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                                         int32_t max_q_len, int32_t num_ctas) {
+    if (num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads || head_dim < 1 || max_q_len < 1 || num_ctas < 1)
+        return 0;
+    ddt::ChunkArgs a;
+    memset(&a, 0, sizeof a);
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.max_q_len = max_q_len;
+    a.tiles = ddt::chunk_tiles(max_q_len, num_heads / num_kv_heads);
+    a.num_ctas = num_ctas;
+    return ddt::chunk_layout(a, nullptr);
+}
+
+ddt_status ddt_gqa_chunk_attn(
+    const uint16_t *q, const uint16_t *k_pool, const uint16_t *v_pool, int64_t pool_stride,
+    int64_t pool_rows, const int32_t *kv_indices, const int32_t *kv_indptr,
+    const int32_t *qo_indptr, int32_t batch, int32_t num_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t total_q, int32_t total_kv, int32_t max_q_len, int32_t max_kv_len,
+    float scale, float score_cap, const float *slopes, int32_t window, const int32_t *full_len,
+    int32_t num_ctas, uint16_t *out, float *lse, void *workspace, size_t workspace_bytes,
+    void *stream) {
+    ddt::ChunkArgs a;
+    const ddt_status st = chunk_args(a, q, k_pool, pool_stride, pool_rows, kv_indices, kv_indptr, qo_indptr, batch, num_heads,
+                                     num_kv_heads, head_dim, total_q, total_kv, max_q_len, max_kv_len, scale, score_cap, slopes,
+                                     window, full_len, workspace);
+    if (st != DDT_OK) return st;
+    if (!v_pool || !out || num_ctas < 0 || misaligned(v_pool, 16) || misaligned(out, 16)) return DDT_ERR_INVALID_ARG;
+    if (num_ctas > DDT_GQA_MAX_CTAS || (num_ctas > 0 && batch > ddt::kChunkMaxDealtBatch)) return DDT_ERR_UNSUPPORTED;
+    if (batch == 0 || total_q == 0 || max_q_len == 0) return DDT_OK;
+    // CTAs that share an item read its q, one maybe after another's output
+    const int64_t rows_size = (int64_t)total_q * num_heads * head_dim, lse_size = lse ? (int64_t)total_q * num_heads : 0;
+    if (overlap(out, rows_size, q, rows_size) || overlap(lse, lse_size, q, rows_size) || overlap(lse, lse_size, out, rows_size))
+        return DDT_ERR_INVALID_ARG;
+    a.err = ddt::device_error_word();
+    if (!a.err) return DDT_ERR_CUDA;
+    a.v_pool = v_pool;
+    a.out = out;
+    a.lse = lse;
+    const int num_sms = ddt::device_sm_count();
+    if (num_ctas > 0) {
+        a.forced = 1;
+        a.tiles = ddt::chunk_tiles(max_q_len, num_heads / num_kv_heads);
+        a.num_ctas = num_ctas;
+        if (!workspace || workspace_bytes < ddt::chunk_layout(a, nullptr)) return DDT_ERR_WORKSPACE;
+    } else {
+        ddt::chunk_choose(a, workspace ? workspace_bytes : 0, num_sms);
+    }
+    if (a.num_ctas > 0) ddt::chunk_layout(a, workspace);
+    return launched(ddt::launch_chunk_attn(a, num_sms, as_stream(stream)));
+}
+
 ddt_status ddt_cache_copy(const void *src_slab, int64_t src_pool_bytes, int64_t src_pool_rows,
                           void *dst_slab, int64_t dst_pool_bytes, int64_t dst_pool_rows,
                           int32_t num_pools, int64_t row_bytes, const int32_t *src,
@@ -306,6 +412,7 @@ ddt_status ddt_call_words(const int64_t *words) {
         case DDT_CALL_CACHE_COPY: return call_words(ddt_cache_copy, words);
         case DDT_CALL_CACHE_COMMIT: return call_words(ddt_cache_commit, words);
         case DDT_CALL_CACHE_COMPACT: return call_words(ddt_cache_compact, words);
+        case DDT_CALL_GQA_CHUNK_ATTN: return call_words(ddt_gqa_chunk_attn, words);
     }
     return DDT_ERR_INVALID_ARG;
 }

@@ -1,0 +1,82 @@
+// ddt_gqa_chunk.cu -- chunk attention: sizes, the choice of how the work is split, launches.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "ddt_gqa_chunk_attn.cuh"
+
+namespace ddt {
+namespace chunk {
+extern template cudaError_t launch_attn_score<0>(AttnParams &, cudaStream_t);
+extern template cudaError_t launch_attn_score<kCap>(AttnParams &, cudaStream_t);
+extern template cudaError_t launch_attn_score<kBias>(AttnParams &, cudaStream_t);
+extern template cudaError_t launch_attn_score<kCap | kBias>(AttnParams &, cudaStream_t);
+extern template cudaError_t prepare_attn_score<0>();
+extern template cudaError_t prepare_attn_score<kCap>();
+extern template cudaError_t prepare_attn_score<kBias>();
+extern template cudaError_t prepare_attn_score<kCap | kBias>();
+
+namespace {
+int part_rows(int tiles, int max_q_len, int group) { return (int)std::min<int64_t>((int64_t)max_q_len * group, tiles * kRows); }
+int items_most(int tiles, int max_q_len, int group) {
+    return (int)(((int64_t)max_q_len * group + tiles * kRows - 1) / (tiles * kRows));
+}
+bool may_deal(int batch, int max_kv_len) { return batch <= kChunkMaxDealtBatch && max_kv_len > 256; }
+int slots(int tiles, int num_sms) { return std::min(num_sms * (tiles == 2 ? 1 : 2), DDT_GQA_MAX_CTAS); }
+}  // namespace
+}  // namespace chunk
+
+using namespace chunk;
+
+cudaError_t chunk_prepare_device() {
+    cudaError_t e = prepare_attn_score<0>();
+    if (e == cudaSuccess) e = prepare_attn_score<kCap>();
+    if (e == cudaSuccess) e = prepare_attn_score<kBias>();
+    if (e == cudaSuccess) e = prepare_attn_score<kCap | kBias>();
+    return e;
+}
+
+int chunk_tiles(int max_q_len, int group) { return (int64_t)max_q_len * group > kRows ? 2 : 1; }
+
+size_t chunk_layout(ChunkArgs &a, void *base) {
+    const int group = a.num_heads / a.num_kv_heads;
+    const size_t rows = (size_t)2 * a.num_ctas * part_rows(a.tiles, a.max_q_len, group);
+    auto align = [](size_t x) { return (x + 255) & ~size_t(255); };
+    const size_t notes = align((size_t)a.num_ctas * sizeof(int4)), o = align(rows * a.head_dim * sizeof(float));
+    if (base) {
+        char *p = static_cast<char *>(base);
+        a.notes = reinterpret_cast<int4 *>(p);
+        a.o_part = reinterpret_cast<float *>(p + notes);
+        a.lse_part = reinterpret_cast<float *>(p + notes + o);
+    }
+    return notes + o + align(rows * sizeof(float));
+}
+
+int chunk_most_ctas(int batch, int num_heads, int num_kv_heads, int max_q_len, int max_kv_len, int num_sms) {
+    return may_deal(batch, max_kv_len) ? slots(chunk_tiles(max_q_len, num_heads / num_kv_heads), num_sms) : 0;
+}
+
+void chunk_choose(ChunkArgs &a, size_t workspace_bytes, int num_sms) {
+    a.tiles = chunk_tiles(a.max_q_len, a.num_heads / a.num_kv_heads);
+    a.num_ctas = may_deal(a.batch, a.max_kv_len) ? slots(a.tiles, num_sms) : 0;
+    while (a.num_ctas > 0 && chunk_layout(a, nullptr) > workspace_bytes) --a.num_ctas;
+}
+
+cudaError_t launch_chunk_attn(const ChunkArgs &a, int num_sms, cudaStream_t s) {
+    AttnParams prm;
+    memset(&prm, 0, sizeof prm);
+    prm.a = a;
+    prm.group = a.num_heads / a.num_kv_heads;
+    prm.group_inv = 1.0f / (float)prm.group;
+    prm.part_rows = part_rows(a.tiles, a.max_q_len, prm.group);
+    prm.tgs_most = items_most(a.tiles, a.max_q_len, prm.group);
+    prm.score = score_scale(a.scale, a.score_cap);
+    switch ((a.score_cap > 0.f ? kCap : 0) | (a.slopes ? kBias : 0)) {
+        case kCap: return launch_attn_score<kCap>(prm, s);
+        case kBias: return launch_attn_score<kBias>(prm, s);
+        case kCap | kBias: return launch_attn_score<kCap | kBias>(prm, s);
+    }
+    return launch_attn_score<0>(prm, s);
+}
+
+}  // namespace ddt

@@ -1,0 +1,113 @@
+// ddt_gqa_chunk.cuh -- what the chunk kernels share: which columns a token sees,
+// how a score is made of a product, and the range of columns that a run of tokens reads.
+//
+// Token i of a request with P cached columns is at position p = P + i, column j at
+// position j.  It sees column j when j < full (a prefix that every token sees) or
+// p - window < j <= p (window 0: j <= p).  Its score is
+//   z = scale <q, k_j>;  z = cap tanh(z / cap) where cap > 0;  z -= slope |p - j|.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ddt_internal.cuh"
+#include "ddt_sm100.cuh"
+
+namespace ddt {
+namespace chunk {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kCap = 1, kBias = 2;  // bits of a kernel's kScore
+
+// A request's offsets, checked: T new tokens behind N - T cached columns.
+struct Request {
+    int qo0, T, kv0, N, full;
+};
+__device__ __forceinline__ Request load_request(const ChunkArgs &a, int b, unsigned int *err) {
+    Request r;
+    r.qo0 = a.qo_indptr[b];
+    const int qo1 = a.qo_indptr[b + 1];
+    r.kv0 = a.kv_indptr[b];
+    const int kv1 = a.kv_indptr[b + 1];
+    r.full = a.full_len ? a.full_len[b] : 0;
+    // differences of broken offsets wrap, which is why their order counts
+    r.T = (int)((uint32_t)qo1 - (uint32_t)r.qo0);
+    r.N = (int)((uint32_t)kv1 - (uint32_t)r.kv0);
+    const bool bad_qo = r.T < 0 || r.T > a.max_q_len || r.qo0 < 0 || qo1 > a.total_q || qo1 < r.qo0;
+    const bool bad_kv = r.N < r.T || r.N > a.max_kv_len || r.kv0 < 0 || kv1 > a.total_kv || kv1 < r.kv0;
+    if (bad_qo || bad_kv) {
+        latch(err, (bad_qo ? DDT_DEVERR_QO_INDPTR : 0u) | (bad_kv ? DDT_DEVERR_KV_INDPTR : 0u));
+        r.T = r.N = 0;
+    }
+    r.full = min(max(r.full, 0), r.N);
+    return r;
+}
+
+// n / group for 0 <= n < 128 * 128, 1 <= group <= 128 by the reciprocal: (n + 1/2) /
+// group is at least 1/256 from a whole number, and off by less than 16384.5 * 2^-22.
+__device__ __forceinline__ int quotient(int n, float group_inv) { return (int)(((float)n + 0.5f) * group_inv); }
+
+// Blocks of NB columns that tokens at positions [pa, pb] read: 0 .. a - 1 for the
+// prefix that all see, l .. r - 1 for the rest.
+struct Blocks {
+    int a, l, count;
+};
+template <int NB>
+__device__ __forceinline__ Blocks blocks_of(int pa, int pb, int window, int full) {
+    Blocks x;
+    const int lo = window > 0 ? max(0, pa - window + 1) : 0;
+    x.a = (full + NB - 1) / NB;
+    x.l = max(x.a, lo / NB);
+    x.count = x.a + max(x.l, pb / NB + 1) - x.l;
+    return x;
+}
+
+// whether tokens at positions [pa, pb] all see columns [c, c + n)
+__device__ __forceinline__ bool all_see(int c, int n, int pa, int pb, int window, int full) {
+    return c + n <= full || (c + n - 1 <= pa && (window <= 0 || c > pb - window));
+}
+// the low n bits (n may be negative or above 32)
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+// bit e: the token at position p sees column c + e (of N)
+__device__ __forceinline__ uint32_t seen_bits(int c, int p, int window, int full, int N) {
+    uint32_t w = low_bits(p + 1 - c);
+    if (window > 0) w &= ~low_bits(p - window + 1 - c);
+    return (w | low_bits(full - c)) & low_bits(N - c);
+}
+
+// A pair of scores in log2 units less a reference, from the products of q with columns j
+// and j + 1 (where kBias: at distances p - j = -d, -d - 1).  tanh(u) = 1 - 2 / (1 + e^2u):
+// off by 2^-22 at most, which is cap 2^-22 in a score; it stays right where e^2u is 0 or infinite.
+struct ScoreScale {
+    float lin;    // plain: scale log2(e); capped: 2 log2(e) scale / cap
+    float cap2;   // cap log2(e)
+    float slope;  // of the row's head, log2 units
+};
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <int kScore>
+__device__ __forceinline__ float2 score_pair(float s0, float s1, const ScoreScale &k, float add0, float add1) {
+    using namespace sm100;
+    if constexpr (kScore & kCap) {
+        const float2 t = f2fma(make_float2(s0, s1), make_float2(k.lin, k.lin), make_float2(0.f, 0.f));
+        const float2 w = f2add(make_float2(ex2(t.x), ex2(t.y)), make_float2(1.f, 1.f));
+        return f2fma(make_float2(rcp(w.x), rcp(w.y)), make_float2(-2.f * k.cap2, -2.f * k.cap2),
+                     f2add(make_float2(add0, add1), make_float2(k.cap2, k.cap2)));
+    } else {
+        return f2fma(make_float2(s0, s1), make_float2(k.lin, k.lin), make_float2(add0, add1));
+    }
+}
+__host__ __device__ inline ScoreScale score_scale(float scale, float cap) {
+    ScoreScale k;
+    k.lin = cap > 0.f ? 2.f * kLog2e * scale / cap : scale * kLog2e;
+    k.cap2 = cap * kLog2e;
+    k.slope = 0.f;
+    return k;
+}
+
+}  // namespace chunk
+}  // namespace ddt

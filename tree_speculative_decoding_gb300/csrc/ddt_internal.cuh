@@ -212,6 +212,50 @@ int gqa_tile_groups(int tiles, int max_q_len, int group);
 // bytes of the workspace for a.tiles and a.num_ctas; places its parts in a where base is given
 size_t gqa_layout(GqaArgs &a, void *base);
 
+// Arguments of one chunk call (attention or received weights) as seen by the kernels.
+struct ChunkArgs {
+    const uint16_t *q;
+    const uint16_t *k_pool, *v_pool;
+    int64_t pool_stride;  // elements per row
+    int64_t pool_rows;
+    const int32_t *kv_indices;
+    const int32_t *kv_indptr;
+    const int32_t *qo_indptr;
+    int batch;
+    int num_heads;
+    int num_kv_heads;
+    int head_dim;
+    int total_q;
+    int total_kv;
+    int max_q_len;
+    int max_kv_len;
+    float scale;
+    float score_cap;       // 0: none
+    const float *slopes;   // [num_heads] or null
+    int window;            // 0: none
+    const int32_t *full_len;  // [batch] or null
+    // attention
+    int num_ctas;     // CTAs that the blocks of columns are dealt to, or 0: one CTA per item
+    int forced;       // the caller gave the count: a CTA may get a single block
+    int tiles;        // tiles of 128 rows of an item: 1 or 2
+    uint16_t *out;    // [total_q, H, D] bf16
+    float *lse;       // [total_q, H]: out (or null) of the attention, input of the weights
+    int4 *notes;      // [num_ctas]: the cut item that ends in a CTA's share
+    float *o_part;    // [2 * num_ctas][part rows][D]
+    float *lse_part;  // [2 * num_ctas][part rows]
+    unsigned int *err;
+};
+constexpr int kChunkMaxDealtBatch = 256;  // a thread per request places it on the line
+cudaError_t chunk_prepare_device();
+cudaError_t launch_chunk_attn(const ChunkArgs &a, int num_sms, cudaStream_t s);
+// the most CTAs that the work may be dealt to for these bounds, or 0
+int chunk_most_ctas(int batch, int num_heads, int num_kv_heads, int max_q_len, int max_kv_len, int num_sms);
+int chunk_tiles(int max_q_len, int group);
+// a.tiles and a.num_ctas for the call's sizes, within the workspace
+void chunk_choose(ChunkArgs &a, size_t workspace_bytes, int num_sms);
+// bytes of the workspace for a.tiles and a.num_ctas; places its parts in a where base is given
+size_t chunk_layout(ChunkArgs &a, void *base);
+
 cudaError_t launch_cache_copy(const void *src_slab, int64_t src_pool_bytes, int64_t src_rows, void *dst_slab,
                               int64_t dst_pool_bytes, int64_t dst_rows, int num_pools, int64_t row_bytes,
                               const int32_t *src, const int32_t *dst, int n, unsigned int *err, cudaStream_t s);

@@ -34,7 +34,7 @@ class DDTError(RuntimeError):
 # arguments are packed into one buffer, which costs a fifth of what ctypes takes
 # for the 12 to 29 of them.
 _IN_WORDS = dict.fromkeys(("ddt_gqa_norm_rope_append", "ddt_gqa_verify_attn", "ddt_cache_copy", "ddt_cache_commit",
-                           "ddt_cache_compact"))
+                           "ddt_cache_compact", "ddt_gqa_chunk_attn"))
 
 
 def _call(name, *args):
@@ -82,6 +82,10 @@ def _load():
         "ddt_cache_commit": ([P, i64, i64, i32, i64, P, P, P, P, P, i32, i32, i32, P, P], i32),
         "ddt_cache_compact_workspace_size": ([i64], sz),
         "ddt_cache_compact": ([P, i64, i64, i32, i64, P, i32, P, P, P, sz, P], i32),
+        "ddt_gqa_chunk_attn_num_ctas": ([i32, i32, i32, i32, i32, i32], i32),
+        "ddt_gqa_chunk_attn_workspace_size": ([i32, i32, i32, i32, i32], sz),
+        "ddt_gqa_chunk_attn": ([P, P, P, i64, i64, P, P, P, i32, i32, i32, i32, i32, i32, i32, i32, f32,
+                                f32, P, i32, P, i32, P, P, P, sz, P], i32),
         "ddt_call_words": ([ctypes.c_char_p], i32),
         "ddt_get_error": ([P, P], i32),
         "ddt_selftest_wait_timeout": ([ctypes.c_uint32, P], i32),
@@ -684,6 +688,90 @@ def ddt_cache_compact(pool, kv_indices, new_indices, live, workspace=None, strea
         "ddt_cache_compact", pp, gap, rows, pools, row, _like(kv_indices, i32, dev, "kv_indices"), kv_indices.numel(),
         _like(new_indices, i32, dev, "new_indices"), _like(live, i32, dev, "live"), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
+
+
+# ---------------------------------------------------------------- chunks
+MAX_CHUNK = 1 << 20
+
+
+def _bounds(qo_indptr, kv_indptr, max_q_len, max_kv_len, stream):
+    """Host-side bounds; read on the call's stream (behind what writes the offsets) where not given."""
+    if max_q_len is None or max_kv_len is None:
+        with torch.cuda.stream(stream):
+            max_q_len = int((qo_indptr[1:] - qo_indptr[:-1]).max())
+            max_kv_len = int((kv_indptr[1:] - kv_indptr[:-1]).max())
+    return max_q_len, max_kv_len
+
+
+def _scores(slopes, full_len, H, B, dev):
+    """Pointers of what the chunk calls' scores and visibility take."""
+    if slopes is not None and slopes.numel() != H:
+        raise ValueError("slopes must hold a value per head")
+    if full_len is not None and full_len.numel() != B:
+        raise ValueError("full_len must hold a value per request")
+    return (0 if slopes is None else _like(slopes, torch.float32, dev, "slopes"),
+            0 if full_len is None else _like(full_len, _I32, dev, "full_len"))
+
+
+def _workspace(workspace, nbytes, dev, stream):
+    """Pointer and bytes of the caller's workspace, or of one allocated here (returned to be kept)."""
+    if workspace is None:
+        if not nbytes:
+            return None, 0, 0
+        workspace = _scratch(nbytes, dev, stream)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def ddt_gqa_chunk_attn_num_ctas(batch, num_heads, num_kv_heads, max_q_len, max_kv_len, num_sms=0):
+    return lib.ddt_gqa_chunk_attn_num_ctas(batch, num_heads, num_kv_heads, max_q_len, max_kv_len, num_sms)
+
+
+def ddt_gqa_chunk_attn_workspace_size(num_heads, num_kv_heads, head_dim, max_q_len, num_ctas):
+    return lib.ddt_gqa_chunk_attn_workspace_size(num_heads, num_kv_heads, head_dim, max_q_len, num_ctas)
+
+
+def ddt_gqa_chunk_attn(q, k_pool, v_pool, kv_indices, kv_indptr, qo_indptr, scale, out, lse=None,
+                       max_q_len=None, max_kv_len=None, score_cap=0.0, slopes=None, window=0, full_len=None,
+                       num_ctas=0, workspace=None, stream=None):
+    """Attention of a chunk of new tokens of any length over grouped-query rows.  q, out: [total_q, H, D]
+    bf16; k_pool, v_pool: [pool_rows, G, D] bf16; lse: float32 [total_q, H] or None.
+
+    Token i of a request is at position p = kv_len - q_len + i and sees the columns j < full_len[b]
+    (int32 [batch] or None) and p - window < j <= p (window 0: all up to p).  Scores are capped to
+    score_cap * tanh(z / score_cap) where score_cap > 0, then reduced by slopes[h] * |p - j| (float32 [H] or
+    None).  The other arguments are those of ddt_gqa_verify_attn."""
+    dev = _on_device(q, "q")
+    qp, qs, total_q, H, D = _heads(q, dev, "q")
+    kp, vp, stride, rows, G, Dp = _pools(k_pool, v_pool, dev)
+    if Dp != D:
+        raise ValueError("q and the pools must have the same head_dim")
+    if qs != H * D:
+        raise ValueError("q must be contiguous")
+    if out.shape != (total_q, H, D):
+        raise ValueError("out must have q's shape")
+    if lse is not None and lse.shape != (total_q, H):
+        raise ValueError("lse must be [total_q, H]")
+    B = qo_indptr.numel() - 1
+    if kv_indptr.numel() != B + 1:
+        raise ValueError("qo_indptr and kv_indptr must both hold batch + 1 entries")
+    slopes_p, full_p = _scores(slopes, full_len, H, B, dev)
+    if total_q == 0 or B == 0:
+        return
+    max_q_len, max_kv_len = _bounds(qo_indptr, kv_indptr, max_q_len, max_kv_len, stream)
+    nbytes = 0
+    if workspace is None:
+        ctas = num_ctas or lib.ddt_gqa_chunk_attn_num_ctas(B, H, G, max_q_len, max_kv_len, 0)
+        nbytes = lib.ddt_gqa_chunk_attn_workspace_size(H, G, D, max_q_len, ctas)
+    workspace, ws, ws_bytes = _workspace(workspace, nbytes, dev, stream)
+    i32 = _I32
+    _call(
+        "ddt_gqa_chunk_attn", qp, kp, vp, stride, rows, _like(kv_indices, i32, dev, "kv_indices"),
+        _like(kv_indptr, i32, dev, "kv_indptr"), _like(qo_indptr, i32, dev, "qo_indptr"), B, H, G, D, total_q,
+        kv_indices.numel(), max_q_len, max_kv_len, scale, score_cap, slopes_p, window, full_p, num_ctas,
+        _like(out, _BF16, dev, "out"), 0 if lse is None else _like(lse, torch.float32, dev, "lse"),
+        ws, ws_bytes, _raw_stream(stream, dev))
 
 
 def ddt_get_error(stream=None):
