@@ -30,9 +30,11 @@
  *   ddt_gqa_verify_attn     tree-verify attention over grouped-query K/V rows
  *   ddt_gqa_chunk_attn      attention of a chunk of any length: capped scores, distance
  *                           bias, window, prefix mask
+ *   ddt_gqa_chunk_weights   the attention that every column received from a chunk
  *   ddt_cache_commit        ddt_commit_kv for every layer's pool of any row width
  *   ddt_cache_copy          rows copied to other rows in every layer's pool
  *   ddt_cache_compact       live rows moved to the front of every pool
+ *   ddt_cache_evict         per request the columns that received most stay
  *
  * Conventions for every entry point:
  *   - Pointers marked (device) must be device memory of the current CUDA
@@ -781,6 +783,48 @@ ddt_status ddt_gqa_chunk_attn(
     void *stream);
 
 /*
+ * ddt_gqa_chunk_weights -- how much attention every column received from a chunk:
+ * for column j of request b
+ *   weights[kv_indptr[b] + j] = decay * prev_j + sum over heads h and counted
+ *                               tokens t that see j of exp(z_tj - lse[t,h]),
+ * with the scores z, the visibility and lse of ddt_gqa_chunk_attn (call it with
+ * the same q, k_pool, offsets, scale, score_cap, slopes, window and full_len; lse
+ * is its output).  A layer's call with prev = weights, decay 1 adds to what the
+ * layers before gave; a step's first call takes the sums that the columns had
+ * before the step.  Arithmetic is fp32; the result does not depend on timing.
+ *
+ *   lse         (device) float [total_q][num_heads].  A row with lse = -inf (nothing
+ *               seen) counts nothing.
+ *   last_rows   tokens of a request that count, from its last one on; 0: all.
+ *   prev        (device) float [total_prev] or NULL (0): earlier sums, those of
+ *               request b's first columns at prev_indptr[b] .. prev_indptr[b+1]; its
+ *               other columns have none.  A column in which prev is read but decay is
+ *               0 still takes part (0 * NaN is NaN): pass NULL to forget.
+ *   prev_indptr (device) int32 [batch+1], or NULL: kv_indptr (total_prev = total_kv).
+ *   decay       finite.
+ *   weights     (device) float [total_kv]; prev itself where prev_indptr is NULL, else
+ *               outside prev, lse and q.
+ *   num_ctas    1..DDT_GQA_MAX_CTAS (batch <= 256), or 0 = choose within the workspace.
+ *   workspace   (device) 256-byte aligned; ddt_gqa_chunk_weights_workspace_size bytes
+ *               for num_ctas (ddt_gqa_chunk_weights_num_ctas: what 0 chooses at most), or
+ *               NULL with num_ctas 0: slower.  Calls that may overlap need one each.
+ * A request without new tokens only decays.  Device checks: those of
+ * ddt_gqa_chunk_attn, and prev_indptr outside [0, total_prev] or with more columns
+ * than the request has (DDT_DEVERR_KV_INDPTR: its weights are left unwritten).
+ */
+int32_t ddt_gqa_chunk_weights_num_ctas(int32_t batch, int32_t num_sms);
+size_t ddt_gqa_chunk_weights_workspace_size(int32_t num_ctas);
+ddt_status ddt_gqa_chunk_weights(
+    const uint16_t *q, const uint16_t *k_pool, int64_t pool_stride, int64_t pool_rows,
+    const float *lse, const int32_t *kv_indices, const int32_t *kv_indptr,
+    const int32_t *qo_indptr, int32_t batch, int32_t num_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t total_q, int32_t total_kv, int32_t max_q_len, int32_t max_kv_len,
+    float scale, float score_cap, const float *slopes, int32_t window, const int32_t *full_len,
+    int32_t last_rows, const float *prev, const int32_t *prev_indptr, int32_t total_prev,
+    float decay, int32_t num_ctas, float *weights, void *workspace, size_t workspace_bytes,
+    void *stream);
+
+/*
  * Cache rows of every layer at once.  The layers' pools are one slab: pool p
  * (p < num_pools: one per layer for a latent cache, one for K and one for V
  * per layer for a grouped-query one) starts at p * pool_bytes bytes and holds
@@ -836,6 +880,38 @@ ddt_status ddt_cache_compact(void *slab, int64_t pool_bytes, int64_t pool_rows, 
                              size_t workspace_bytes, void *stream);
 
 /*
+ * ddt_cache_evict -- a cache cut down to the columns that received most attention:
+ * request b keeps min(kv_len_b, budget[b]) of its columns, those with the largest
+ * weights, where its first `sinks` and its last `recent` columns count as +inf and
+ * NaN as -inf, and ties go to the lower column.  What stays keeps its order:
+ *   new_indptr  (device) int32 [batch+1]: offsets of what is left, from 0 on;
+ *   new_indices (device) int32 [total_new]: its slots, by new_indptr;
+ *   new_weights (device) float [total_new] or NULL: their weights (with new_indptr
+ *               the next step's prev of ddt_gqa_chunk_weights);
+ *   evicted     (device) int32 [total_evicted] or NULL: the slots that leave, request
+ *               after request, in the order of their columns: request b's start at the
+ *               sum of kv_len - kept of the requests before it.
+ * No row moves: the rows of evicted slots are free (where no other request shares
+ * them), and ddt_cache_compact on new_indices brings the rest together.
+ *
+ *   weights     (device) float [total_kv], by kv_indptr, as ddt_gqa_chunk_weights
+ *               writes them.
+ *   kv_indices, kv_indptr (device) as in ddt_verify_attn; total_kv: the size of kv_indices.
+ *   budget      (device) int32 [batch]; below 0 is 0.
+ *   max_kv_len  host-side bound of kv_len_b.
+ *   outputs     no part of each other's or the inputs' memory; what is behind the last
+ *               entry is left as it is.
+ * Device checks: offsets outside [0, total_kv] or a kv_len above max_kv_len (the
+ * request counts as empty), more columns kept than total_new or left out than
+ * total_evicted (not written): DDT_DEVERR_KV_INDPTR.
+ */
+ddt_status ddt_cache_evict(const float *weights, const int32_t *kv_indices, const int32_t *kv_indptr,
+                           const int32_t *budget, int32_t batch, int32_t total_kv, int32_t max_kv_len,
+                           int32_t sinks, int32_t recent, int32_t *new_indices, int32_t total_new,
+                           int32_t *new_indptr, float *new_weights, int32_t *evicted,
+                           int32_t total_evicted, void *stream);
+
+/*
  * ddt_call_words -- one of the calls named below with its arguments as 64-bit
  * words, for bindings that pay for every argument (ctypes: 0.1 us each):
  * words[0] names the call, words[1] counts the arguments, which follow in the
@@ -849,7 +925,9 @@ enum {
     DDT_CALL_CACHE_COPY = 2,
     DDT_CALL_CACHE_COMMIT = 3,
     DDT_CALL_CACHE_COMPACT = 4,
-    DDT_CALL_GQA_CHUNK_ATTN = 5
+    DDT_CALL_GQA_CHUNK_ATTN = 5,
+    DDT_CALL_GQA_CHUNK_WEIGHTS = 6,
+    DDT_CALL_CACHE_EVICT = 7
 };
 ddt_status ddt_call_words(const int64_t *words);
 

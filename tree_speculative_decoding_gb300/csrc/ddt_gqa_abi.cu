@@ -1,5 +1,5 @@
 // ddt_gqa_abi.cu -- the extern "C" entry points of the grouped-query layer and
-// of the cache-row calls: host-side argument checks, sizing and launches.
+// of the chunk and cache-row calls: host-side argument checks, sizing and launches.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -347,6 +347,69 @@ ddt_status ddt_gqa_chunk_attn(
     return launched(ddt::launch_chunk_attn(a, num_sms, as_stream(stream)));
 }
 
+int32_t ddt_gqa_chunk_weights_num_ctas(int32_t batch, int32_t num_sms) {
+    if (batch < 1) return 0;
+    if (num_sms <= 0) num_sms = ddt::device_sm_count();
+    return ddt::chunk_weights_most_ctas(batch, num_sms);
+}
+
+size_t ddt_gqa_chunk_weights_workspace_size(int32_t num_ctas) {
+    if (num_ctas < 1) return 0;
+    ddt::ChunkArgs a;
+    memset(&a, 0, sizeof a);
+    a.num_ctas = num_ctas;
+    return ddt::chunk_weights_layout(a, nullptr);
+}
+
+ddt_status ddt_gqa_chunk_weights(
+    const uint16_t *q, const uint16_t *k_pool, int64_t pool_stride, int64_t pool_rows,
+    const float *lse, const int32_t *kv_indices, const int32_t *kv_indptr,
+    const int32_t *qo_indptr, int32_t batch, int32_t num_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t total_q, int32_t total_kv, int32_t max_q_len, int32_t max_kv_len,
+    float scale, float score_cap, const float *slopes, int32_t window, const int32_t *full_len,
+    int32_t last_rows, const float *prev, const int32_t *prev_indptr, int32_t total_prev,
+    float decay, int32_t num_ctas, float *weights, void *workspace, size_t workspace_bytes,
+    void *stream) {
+    ddt::ChunkArgs a;
+    // without tokens there are still columns whose sums decay
+    static const uint16_t none[8] __attribute__((aligned(16))) = {0};
+    const ddt_status st = chunk_args(a, total_q == 0 && !q ? none : q, k_pool, pool_stride, pool_rows, kv_indices, kv_indptr,
+                                     qo_indptr, batch, num_heads, num_kv_heads, head_dim, total_q, total_kv, max_q_len, max_kv_len,
+                                     scale, score_cap, slopes, window, full_len, workspace);
+    if (st != DDT_OK) return st;
+    if ((!lse && total_q != 0) || (!weights && total_kv != 0) || last_rows < 0 || num_ctas < 0 || total_prev < 0 ||
+        (prev && !isfinite(decay)))
+        return DDT_ERR_INVALID_ARG;
+    if (num_ctas > DDT_GQA_MAX_CTAS || (num_ctas > 0 && batch > ddt::kChunkMaxDealtBatch)) return DDT_ERR_UNSUPPORTED;
+    if (prev && !prev_indptr && total_prev != total_kv) return DDT_ERR_INVALID_ARG;
+    if (batch == 0 || total_kv == 0) return DDT_OK;
+    // what another CTA reads may not be what one writes: in place each sum is its own reader's
+    if ((prev && !(prev == weights && !prev_indptr) && overlap(weights, total_kv, prev, total_prev)) ||
+        overlap(weights, total_kv, lse, (int64_t)total_q * num_heads) ||
+        overlap(weights, total_kv, a.q, (int64_t)total_q * num_heads * head_dim))
+        return DDT_ERR_INVALID_ARG;
+    a.err = ddt::device_error_word();
+    if (!a.err) return DDT_ERR_CUDA;
+    a.lse = const_cast<float *>(lse);
+    ddt::WeightArgs w;
+    w.last_rows = last_rows;
+    w.prev = prev;
+    w.prev_indptr = prev_indptr;
+    w.total_prev = total_prev;
+    w.decay = decay;
+    w.weights = weights;
+    if (num_ctas > 0) {
+        a.forced = 1;
+        a.num_ctas = num_ctas;
+        if (!workspace || workspace_bytes < ddt::chunk_weights_layout(a, nullptr)) return DDT_ERR_WORKSPACE;
+    } else if (workspace) {
+        a.num_ctas = ddt::chunk_weights_most_ctas(batch, ddt::device_sm_count());
+        while (a.num_ctas > 0 && ddt::chunk_weights_layout(a, nullptr) > workspace_bytes) --a.num_ctas;
+    }
+    if (a.num_ctas > 0) ddt::chunk_weights_layout(a, workspace);
+    return launched(ddt::launch_chunk_weights(a, w, as_stream(stream)));
+}
+
 ddt_status ddt_cache_copy(const void *src_slab, int64_t src_pool_bytes, int64_t src_pool_rows,
                           void *dst_slab, int64_t dst_pool_bytes, int64_t dst_pool_rows,
                           int32_t num_pools, int64_t row_bytes, const int32_t *src,
@@ -404,6 +467,52 @@ ddt_status ddt_cache_compact(void *slab, int64_t pool_bytes, int64_t pool_rows, 
                                               as_stream(stream)));
 }
 
+ddt_status ddt_cache_evict(const float *weights, const int32_t *kv_indices, const int32_t *kv_indptr,
+                           const int32_t *budget, int32_t batch, int32_t total_kv, int32_t max_kv_len,
+                           int32_t sinks, int32_t recent, int32_t *new_indices, int32_t total_new,
+                           int32_t *new_indptr, float *new_weights, int32_t *evicted,
+                           int32_t total_evicted, void *stream) {
+    if (((!weights || !kv_indices) && total_kv != 0) || !kv_indptr || !budget || batch < 0 || total_kv < 0 || max_kv_len < 0 ||
+        sinks < 0 || recent < 0 || (!new_indices && total_new != 0) || total_new < 0 || !new_indptr || total_evicted < 0)
+        return DDT_ERR_INVALID_ARG;
+    if (batch > INT32_MAX / 16) return DDT_ERR_UNSUPPORTED;
+    if (batch == 0) return DDT_OK;
+    // every request reads the offsets and budgets of those before it, and its columns while others write theirs
+    struct Part {
+        const void *p;
+        int64_t n;
+    };
+    const Part in[] = {{weights, total_kv}, {kv_indices, total_kv}, {kv_indptr, (int64_t)batch + 1}, {budget, batch}};
+    const Part out[] = {{new_indices, total_new}, {new_indptr, (int64_t)batch + 1}, {new_weights, new_weights ? total_new : 0},
+                        {evicted, evicted ? total_evicted : 0}};
+    for (int i = 0; i < 4; ++i) {
+        const int32_t *o = static_cast<const int32_t *>(out[i].p);
+        for (const Part &x : in)
+            if (overlap(o, out[i].n, static_cast<const int32_t *>(x.p), x.n)) return DDT_ERR_INVALID_ARG;
+        for (int k = 0; k < i; ++k)
+            if (overlap(o, out[i].n, static_cast<const int32_t *>(out[k].p), out[k].n)) return DDT_ERR_INVALID_ARG;
+    }
+    ddt::EvictArgs a;
+    a.weights = weights;
+    a.kv_indices = kv_indices;
+    a.kv_indptr = kv_indptr;
+    a.budget = budget;
+    a.batch = batch;
+    a.total_kv = total_kv;
+    a.max_kv_len = max_kv_len;
+    a.sinks = sinks;
+    a.recent = recent;
+    a.new_indices = new_indices;
+    a.total_new = total_new;
+    a.new_indptr = new_indptr;
+    a.new_weights = new_weights;
+    a.evicted = evicted;
+    a.total_evicted = total_evicted;
+    a.err = ddt::device_error_word();
+    if (!a.err) return DDT_ERR_CUDA;
+    return launched(ddt::launch_cache_evict(a, as_stream(stream)));
+}
+
 ddt_status ddt_call_words(const int64_t *words) {
     if (!words) return DDT_ERR_INVALID_ARG;
     switch (words[0]) {
@@ -413,6 +522,8 @@ ddt_status ddt_call_words(const int64_t *words) {
         case DDT_CALL_CACHE_COMMIT: return call_words(ddt_cache_commit, words);
         case DDT_CALL_CACHE_COMPACT: return call_words(ddt_cache_compact, words);
         case DDT_CALL_GQA_CHUNK_ATTN: return call_words(ddt_gqa_chunk_attn, words);
+        case DDT_CALL_GQA_CHUNK_WEIGHTS: return call_words(ddt_gqa_chunk_weights, words);
+        case DDT_CALL_CACHE_EVICT: return call_words(ddt_cache_evict, words);
     }
     return DDT_ERR_INVALID_ARG;
 }

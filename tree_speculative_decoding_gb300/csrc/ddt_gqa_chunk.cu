@@ -1,9 +1,10 @@
-// ddt_gqa_chunk.cu -- chunk attention: sizes, the choice of how the work is split, launches.
+// ddt_gqa_chunk.cu -- chunk attention and received weights: sizes, the choice of how the work is split, launches.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
 
 #include "ddt_gqa_chunk_attn.cuh"
+#include "ddt_gqa_chunk_weights.cuh"
 
 namespace ddt {
 namespace chunk {
@@ -15,6 +16,16 @@ extern template cudaError_t prepare_attn_score<0>();
 extern template cudaError_t prepare_attn_score<kCap>();
 extern template cudaError_t prepare_attn_score<kBias>();
 extern template cudaError_t prepare_attn_score<kCap | kBias>();
+namespace received {
+extern template cudaError_t launch_weights_score<0>(Params &, int, cudaStream_t);
+extern template cudaError_t launch_weights_score<kCap>(Params &, int, cudaStream_t);
+extern template cudaError_t launch_weights_score<kBias>(Params &, int, cudaStream_t);
+extern template cudaError_t launch_weights_score<kCap | kBias>(Params &, int, cudaStream_t);
+extern template cudaError_t prepare_weights_score<0>();
+extern template cudaError_t prepare_weights_score<kCap>();
+extern template cudaError_t prepare_weights_score<kBias>();
+extern template cudaError_t prepare_weights_score<kCap | kBias>();
+}  // namespace received
 
 namespace {
 int part_rows(int tiles, int max_q_len, int group) { return (int)std::min<int64_t>((int64_t)max_q_len * group, tiles * kRows); }
@@ -33,6 +44,10 @@ cudaError_t chunk_prepare_device() {
     if (e == cudaSuccess) e = prepare_attn_score<kCap>();
     if (e == cudaSuccess) e = prepare_attn_score<kBias>();
     if (e == cudaSuccess) e = prepare_attn_score<kCap | kBias>();
+    if (e == cudaSuccess) e = received::prepare_weights_score<0>();
+    if (e == cudaSuccess) e = received::prepare_weights_score<kCap>();
+    if (e == cudaSuccess) e = received::prepare_weights_score<kBias>();
+    if (e == cudaSuccess) e = received::prepare_weights_score<kCap | kBias>();
     return e;
 }
 
@@ -77,6 +92,38 @@ cudaError_t launch_chunk_attn(const ChunkArgs &a, int num_sms, cudaStream_t s) {
         case kCap | kBias: return launch_attn_score<kCap | kBias>(prm, s);
     }
     return launch_attn_score<0>(prm, s);
+}
+
+int chunk_weights_most_ctas(int batch, int num_sms) {
+    return batch <= kChunkMaxDealtBatch ? std::min(num_sms, DDT_GQA_MAX_CTAS) : 0;
+}
+
+size_t chunk_weights_layout(ChunkArgs &a, void *base) {
+    const size_t notes = ((size_t)a.num_ctas * sizeof(int4) + 255) & ~size_t(255);
+    if (base) {
+        a.notes = static_cast<int4 *>(base);
+        a.o_part = reinterpret_cast<float *>(static_cast<char *>(base) + notes);
+    }
+    return notes + (size_t)2 * a.num_ctas * received::kCols * sizeof(float);
+}
+
+cudaError_t launch_chunk_weights(const ChunkArgs &a, const WeightArgs &w, cudaStream_t s) {
+    received::Params prm;
+    memset(&prm, 0, sizeof prm);
+    prm.a = a;
+    prm.w = w;
+    prm.group = a.num_heads / a.num_kv_heads;
+    prm.group_inv = 1.0f / (float)prm.group;
+    prm.items_most = (int)(((int64_t)a.max_kv_len + received::kCols - 1) / received::kCols);
+    prm.score = score_scale(a.scale, a.score_cap);
+    const int rows = w.last_rows > 0 ? std::min(w.last_rows, a.max_q_len) : a.max_q_len;
+    const int nq = (int64_t)rows * prm.group <= 16 ? 16 : 128;
+    switch ((a.score_cap > 0.f ? kCap : 0) | (a.slopes ? kBias : 0)) {
+        case kCap: return received::launch_weights_score<kCap>(prm, nq, s);
+        case kBias: return received::launch_weights_score<kBias>(prm, nq, s);
+        case kCap | kBias: return received::launch_weights_score<kCap | kBias>(prm, nq, s);
+    }
+    return received::launch_weights_score<0>(prm, nq, s);
 }
 
 }  // namespace ddt

@@ -20,6 +20,37 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kCap = 1, kBias = 2;  // bits of a kernel's kScore
 
+constexpr uint32_t kWaitLimit = 1u << 22;
+
+// The waits try the barrier first: the abort flag is read only where the phase is still open.
+__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *err) {
+    if (sm100::mbar_try_wait(bar, parity)) return true;
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        if (sm100::mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+    }
+    *abort = 1;
+    latch(err, DDT_DEVERR_TIMEOUT);
+    return false;
+}
+// The same for a whole warp: it succeeds for every lane or for none.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *err) {
+    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, err));
+}
+
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {  // a, b >= 0; nearly always small enough for 32 bits
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+// CTA c has the positions [lo, hi) of the line: [c q + min(c, rem), ...).
+struct Shares {
+    int64_t q, rem;
+    __device__ __forceinline__ int64_t lo(int64_t c) const { return c * q + (c < rem ? c : rem); }
+    __device__ __forceinline__ int owner(int64_t x) const {  // the CTA whose share holds position x
+        const int64_t cut = rem * (q + 1);
+        return (int)(x < cut ? divide(x, q + 1) : rem + divide(x - cut, q));
+    }
+};
+
 // A request's offsets, checked: T new tokens behind N - T cached columns.
 struct Request {
     int qo0, T, kv0, N, full;

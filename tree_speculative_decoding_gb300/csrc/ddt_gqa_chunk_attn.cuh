@@ -57,7 +57,6 @@ namespace chunk {
 using namespace sm100;
 
 constexpr int kRows = 128;  // rows per tile (TMEM lanes)
-constexpr uint32_t kWaitLimit = 1u << 22;
 // Weights against the reference: 2^-kShift where the reference was found.  64 of them may sum to
 // kSumLimit, and 2^31 columns to 2^25 kSumLimit = 1.  A value's weight loses bits below 2^-126,
 // which for the heaviest columns is |v| below 2^-73.
@@ -133,22 +132,6 @@ struct Cfg {
     static_assert(kSmemBytes <= (kTiles == 2 ? 232448 : 115712), "shared memory");
 };
 
-// The waits try the barrier first: the abort flag is read only where the phase is still open.
-__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *err) {
-    if (mbar_try_wait(bar, parity)) return true;
-    for (uint32_t i = 0; i < kWaitLimit; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (*abort) return false;
-    }
-    *abort = 1;
-    latch(err, DDT_DEVERR_TIMEOUT);
-    return false;
-}
-// The same for a whole warp: it succeeds for every lane or for none.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *err) {
-    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, err));
-}
-
 // ---------------------------------------------------------------- items
 // Item tg of a request's K/V head: rows [tg kPer, ...), its tokens' positions and its blocks.
 struct Item {
@@ -180,9 +163,6 @@ template <class C>
 __device__ __forceinline__ int64_t item_cost(const Item &i) {
     return C::kCostItem + (int64_t)i.x.count * unit_cost<C>(i);
 }
-__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {  // a, b >= 0; nearly always small enough for 32 bits
-    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
 // the item's blocks that start before position x (block k starts kCostItem + k unit behind the item)
 template <class C>
 __device__ __forceinline__ int blocks_before(int64_t item, int64_t x, int unit, int count) {
@@ -207,16 +187,6 @@ __device__ __forceinline__ int block_column(const Segment &s, int n) {
     const int at = s.x.count - 1 - s.k0 - n;  // latest first
     return (at < s.x.a ? at : s.x.l - s.x.a + at) * C::NB;
 }
-
-// CTA c has the positions [lo, hi) of the line: [c q + min(c, rem), ...).
-struct Shares {
-    int64_t q, rem;
-    __device__ __forceinline__ int64_t lo(int64_t c) const { return c * q + (c < rem ? c : rem); }
-    __device__ __forceinline__ int owner(int64_t x) const {  // the CTA whose share holds position x
-        const int64_t cut = rem * (q + 1);
-        return (int)(x < cut ? divide(x, q + 1) : rem + divide(x - cut, q));
-    }
-};
 
 // The walk over the CTA's segments.  It lives in shared memory: one thread steps it and
 // hands the segments to the warps through a ring of two.

@@ -245,6 +245,15 @@ struct ChunkArgs {
     float *lse_part;  // [2 * num_ctas][part rows]
     unsigned int *err;
 };
+// What a received-weights call has besides (in ChunkArgs: o_part [2 * num_ctas][256]).
+struct WeightArgs {
+    int last_rows;              // tokens of a request that count, from its end; 0: all
+    const float *prev;          // or null
+    const int32_t *prev_indptr; // or null: kv_indptr
+    int total_prev;
+    float decay;
+    float *weights;             // [total_kv]
+};
 constexpr int kChunkMaxDealtBatch = 256;  // a thread per request places it on the line
 cudaError_t chunk_prepare_device();
 cudaError_t launch_chunk_attn(const ChunkArgs &a, int num_sms, cudaStream_t s);
@@ -253,8 +262,32 @@ int chunk_most_ctas(int batch, int num_heads, int num_kv_heads, int max_q_len, i
 int chunk_tiles(int max_q_len, int group);
 // a.tiles and a.num_ctas for the call's sizes, within the workspace
 void chunk_choose(ChunkArgs &a, size_t workspace_bytes, int num_sms);
+cudaError_t launch_chunk_weights(const ChunkArgs &a, const WeightArgs &w, cudaStream_t s);
+int chunk_weights_most_ctas(int batch, int num_sms);
+size_t chunk_weights_layout(ChunkArgs &a, void *base);
 // bytes of the workspace for a.tiles and a.num_ctas; places its parts in a where base is given
 size_t chunk_layout(ChunkArgs &a, void *base);
+
+// Arguments of an eviction as seen by the kernel.
+struct EvictArgs {
+    const float *weights;        // [total_kv]
+    const int32_t *kv_indices;   // [total_kv]
+    const int32_t *kv_indptr;
+    const int32_t *budget;       // [batch]
+    int batch;
+    int total_kv;
+    int max_kv_len;
+    int sinks, recent;
+    int32_t *new_indices;        // [total_new]
+    int total_new;
+    int32_t *new_indptr;         // [batch + 1]
+    float *new_weights;          // [total_new] or null
+    int32_t *evicted;            // [total_evicted] or null
+    int total_evicted;
+    unsigned int *err;
+};
+cudaError_t evict_prepare_device();
+cudaError_t launch_cache_evict(const EvictArgs &a, cudaStream_t s);
 
 cudaError_t launch_cache_copy(const void *src_slab, int64_t src_pool_bytes, int64_t src_rows, void *dst_slab,
                               int64_t dst_pool_bytes, int64_t dst_rows, int num_pools, int64_t row_bytes,

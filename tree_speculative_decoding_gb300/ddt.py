@@ -34,7 +34,8 @@ class DDTError(RuntimeError):
 # arguments are packed into one buffer, which costs a fifth of what ctypes takes
 # for the 12 to 29 of them.
 _IN_WORDS = dict.fromkeys(("ddt_gqa_norm_rope_append", "ddt_gqa_verify_attn", "ddt_cache_copy", "ddt_cache_commit",
-                           "ddt_cache_compact", "ddt_gqa_chunk_attn"))
+                           "ddt_cache_compact", "ddt_gqa_chunk_attn", "ddt_gqa_chunk_weights",
+                           "ddt_cache_evict"))
 
 
 def _call(name, *args):
@@ -86,6 +87,11 @@ def _load():
         "ddt_gqa_chunk_attn_workspace_size": ([i32, i32, i32, i32, i32], sz),
         "ddt_gqa_chunk_attn": ([P, P, P, i64, i64, P, P, P, i32, i32, i32, i32, i32, i32, i32, i32, f32,
                                 f32, P, i32, P, i32, P, P, P, sz, P], i32),
+        "ddt_gqa_chunk_weights_num_ctas": ([i32, i32], i32),
+        "ddt_gqa_chunk_weights_workspace_size": ([i32], sz),
+        "ddt_gqa_chunk_weights": ([P, P, i64, i64, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, i32, f32,
+                                   f32, P, i32, P, i32, P, P, i32, f32, i32, P, P, sz, P], i32),
+        "ddt_cache_evict": ([P, P, P, P, i32, i32, i32, i32, i32, P, i32, P, P, P, i32, P], i32),
         "ddt_call_words": ([ctypes.c_char_p], i32),
         "ddt_get_error": ([P, P], i32),
         "ddt_selftest_wait_timeout": ([ctypes.c_uint32, P], i32),
@@ -772,6 +778,89 @@ def ddt_gqa_chunk_attn(q, k_pool, v_pool, kv_indices, kv_indptr, qo_indptr, scal
         kv_indices.numel(), max_q_len, max_kv_len, scale, score_cap, slopes_p, window, full_p, num_ctas,
         _like(out, _BF16, dev, "out"), 0 if lse is None else _like(lse, torch.float32, dev, "lse"),
         ws, ws_bytes, _raw_stream(stream, dev))
+
+
+def ddt_gqa_chunk_weights_num_ctas(batch, num_sms=0):
+    return lib.ddt_gqa_chunk_weights_num_ctas(batch, num_sms)
+
+
+def ddt_gqa_chunk_weights_workspace_size(num_ctas):
+    return lib.ddt_gqa_chunk_weights_workspace_size(num_ctas)
+
+
+def ddt_gqa_chunk_weights(q, k_pool, lse, kv_indices, kv_indptr, qo_indptr, scale, weights, prev=None,
+                          prev_indptr=None, decay=1.0, last_rows=0, max_q_len=None, max_kv_len=None, score_cap=0.0,
+                          slopes=None, window=0, full_len=None, num_ctas=0, workspace=None, stream=None):
+    """How much attention every column received from a chunk: weights (float32, an entry per entry of
+    kv_indices) = decay * prev + the sum over heads and tokens of the softmax's weights, given the chunk
+    attention's arguments and its lse (float32 [total_q, H]).
+
+    last_rows: only that many last tokens of a request count (0: all).  prev: float32 sums of earlier
+    steps, of each request's first columns by prev_indptr (int32 [batch + 1]; None: laid out as weights,
+    and then maybe weights itself: the layers of a step add up)."""
+    dev = _on_device(q, "q")
+    qp, qs, total_q, H, D = _heads(q, dev, "q")
+    kp, stride, rows, G, Dp = _heads(k_pool, dev, "k_pool")
+    if Dp != D:
+        raise ValueError("q and k_pool must have the same head_dim")
+    if qs != H * D:
+        raise ValueError("q must be contiguous")
+    if lse.shape != (total_q, H):
+        raise ValueError("lse must be [total_q, H]")
+    if weights.numel() != kv_indices.numel():
+        raise ValueError("weights must hold a value per entry of kv_indices")
+    B = qo_indptr.numel() - 1
+    if kv_indptr.numel() != B + 1 or (prev_indptr is not None and prev_indptr.numel() != B + 1):
+        raise ValueError("qo_indptr, kv_indptr and prev_indptr must all hold batch + 1 entries")
+    if prev is not None and prev_indptr is None and prev.numel() != weights.numel():
+        raise ValueError("prev must be laid out as weights, or come with prev_indptr")
+    slopes_p, full_p = _scores(slopes, full_len, H, B, dev)
+    if kv_indices.numel() == 0 or B == 0:
+        return
+    max_q_len, max_kv_len = _bounds(qo_indptr, kv_indptr, max_q_len, max_kv_len, stream)
+    nbytes = 0
+    if workspace is None:
+        nbytes = lib.ddt_gqa_chunk_weights_workspace_size(num_ctas or lib.ddt_gqa_chunk_weights_num_ctas(B, 0))
+    workspace, ws, ws_bytes = _workspace(workspace, nbytes, dev, stream)
+    i32, f32 = _I32, torch.float32
+    _call(
+        "ddt_gqa_chunk_weights", qp, kp, stride, rows, _like(lse, f32, dev, "lse"),
+        _like(kv_indices, i32, dev, "kv_indices"), _like(kv_indptr, i32, dev, "kv_indptr"),
+        _like(qo_indptr, i32, dev, "qo_indptr"), B, H, G, D, total_q, kv_indices.numel(), max_q_len, max_kv_len, scale,
+        score_cap, slopes_p, window, full_p, last_rows, 0 if prev is None else _like(prev, f32, dev, "prev"),
+        0 if prev is None or prev_indptr is None else _like(prev_indptr, i32, dev, "prev_indptr"),
+        0 if prev is None else prev.numel(), decay, num_ctas, _like(weights, f32, dev, "weights"), ws, ws_bytes,
+        _raw_stream(stream, dev))
+
+
+def ddt_cache_evict(weights, kv_indices, kv_indptr, budget, new_indices, new_indptr, new_weights=None,
+                    evicted=None, sinks=0, recent=0, max_kv_len=None, stream=None):
+    """Per request the budget[b] (int32 [batch]) columns with the largest weights stay, its first `sinks`
+    and last `recent` ones before all others, in their order: new_indices (int32), new_weights (float32,
+    as long, or None) and new_indptr (int32 [batch + 1], from 0 on); evicted (int32 or None) gets the slots
+    of the others.  new_indices and evicted hold what the budgets give, or more."""
+    dev = _on_device(weights, "weights")
+    B = kv_indptr.numel() - 1
+    if weights.numel() != kv_indices.numel():
+        raise ValueError("weights must hold a value per entry of kv_indices")
+    if budget.numel() != B or new_indptr.numel() != B + 1:
+        raise ValueError("budget must hold a value per request, new_indptr batch + 1 entries")
+    if new_weights is not None and new_weights.numel() != new_indices.numel():
+        raise ValueError("new_weights must be as long as new_indices")
+    if B <= 0:
+        return
+    if max_kv_len is None:
+        with torch.cuda.stream(stream):   # behind what writes them there
+            max_kv_len = int((kv_indptr[1:] - kv_indptr[:-1]).max())
+    i32, f32 = _I32, torch.float32
+    _call(
+        "ddt_cache_evict", _like(weights, f32, dev, "weights"), _like(kv_indices, i32, dev, "kv_indices"),
+        _like(kv_indptr, i32, dev, "kv_indptr"), _like(budget, i32, dev, "budget"), B, kv_indices.numel(), max_kv_len,
+        sinks, recent, _like(new_indices, i32, dev, "new_indices"), new_indices.numel(),
+        _like(new_indptr, i32, dev, "new_indptr"),
+        0 if new_weights is None else _like(new_weights, f32, dev, "new_weights"),
+        0 if evicted is None else _like(evicted, i32, dev, "evicted"), 0 if evicted is None else evicted.numel(),
+        _raw_stream(stream, dev))
 
 
 def ddt_get_error(stream=None):
