@@ -37,7 +37,7 @@
 // Infinities and NaN in V: a weight of 0 times NaN is NaN, so a V row that some row of the
 // item does not see may not reach the products with such a value.  Only blocks that not
 // all rows of the item see whole can hold one: there the load warps replace it by 0 and
-// keep the rows that do see it as bits (poison), which the epilogue adds to their results.
+// keep the rows that do see it as bits (poison), which are added to the results behind the epilogue.
 //
 // Every wait is bounded: on timeout the CTA latches DDT_DEVERR_TIMEOUT, waits for its own
 // copies and MMAs and leaves.
@@ -198,8 +198,8 @@ struct Walk {
     int b, tg, g, cta, tgs;
     int dealt, more;
 
-    // the next segment; one without blocks when the share is done
-    __device__ __forceinline__ Segment next(const AttnParams &prm) {
+    // the next segment into `to`; one without blocks when the share is done
+    __device__ __forceinline__ void next(const AttnParams &prm, Segment *to) {
         const ChunkArgs &a = prm.a;
         Segment s;
         s.blocks = 0;
@@ -245,7 +245,7 @@ struct Walk {
                 more = pos < end && b < a.batch;
             }
         }
-        return s;
+        *to = s;
     }
 };
 
@@ -288,22 +288,25 @@ __device__ __forceinline__ float weights_64(const uint32_t (&s)[2][32], uint32_t
     }
     return acc.x + acc.y;
 }
-// the largest of 8 seen scores from column c on, in log2 units
+// What a row's largest score is found with: of 8 seen columns from c on the largest product, or
+// (where heads have slopes, which change the order) the largest score; then the score of that.
 template <int kScore>
-__device__ __forceinline__ float largest_8(const uint32_t (&s)[8], uint32_t seen, int c, int p, const ScoreScale &sc) {
+__device__ __forceinline__ float reach_8(const uint32_t (&s)[8], uint32_t seen, int c, int p, const ScoreScale &sc) {
     float mx = -INFINITY;
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
-        float add0 = 0.f, add1 = 0.f;
-        if constexpr (kScore & kBias) {
-            add0 = -sc.slope * fabsf((float)(c + e - p));
-            add1 = -sc.slope * fabsf((float)(c + e + 1 - p));
-        }
-        const float2 x = score_pair<kScore>(__uint_as_float(s[e]), __uint_as_float(s[e + 1]), sc, add0, add1);
+        float2 x = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+        if constexpr (kScore & kBias)
+            x = score_pair<kScore>(x.x, x.y, sc, -sc.slope * fabsf((float)(c + e - p)), -sc.slope * fabsf((float)(c + e + 1 - p)));
         if ((seen >> e) & 1u) mx = fmaxf(mx, x.x);
         if ((seen >> (e + 1)) & 1u) mx = fmaxf(mx, x.y);
     }
     return mx;
+}
+template <int kScore>
+__device__ __forceinline__ float reached(float mx, const ScoreScale &sc) {
+    if (mx == -INFINITY || (kScore & kBias)) return mx;  // (capped, a product of -inf is a score of -cap)
+    return score_pair<kScore>(mx, mx, sc, 0.f, 0.f).x;
 }
 
 // halves of a word whose exponent is all ones: bits 15 and 31
@@ -504,6 +507,16 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
         if (lane == 0) mbar_arrive(bar(C::bSegEmpty + (n & 1)));
         return true;
     };
+    // by one warp: segment n for all of them
+    auto give_segment = [&](int n) -> bool {
+        if (n >= 2 && !warp_wait(bar(C::bSegEmpty + (n & 1)), ((n >> 1) - 1) & 1, abort_flag, a.err)) return false;
+        if (lane == 0) {
+            walk->next(prm, reinterpret_cast<Segment *>(smem + C::kOffWalk + C::kWalkBytes + (n & 1) * C::kSegBytes));
+            mbar_arrive(bar(C::bSegFull + (n & 1)));
+        }
+        __syncwarp();
+        return true;
+    };
     // rows r0, r0 + 32, ... below r1 of the segment's q, one warp, into the swizzled operand layout
     auto load_q = [&](const Segment &s, int r0, int r1, int step) {
         constexpr int kChunks = D / 8, kPer = 32 / kChunks;  // 16-byte pieces of a row; rows per instruction
@@ -548,25 +561,12 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
             const int64_t pitch = a.pool_stride * 2;
             int base = 0;  // blocks of the segments before
             bool ok = true;
-            auto give_segment = [&](int n) {  // by the first load warp
-                if (warp != kFirstLoad) return;
-                if (n >= 2) ok = warp_wait(bar(C::bSegEmpty + (n & 1)), ((n >> 1) - 1) & 1, abort_flag, a.err);
-                if (ok && lane == 0) {
-                    const Segment s = walk->next(prm);
-                    uint32_t w[kSegWords];
-                    memcpy(w, &s, sizeof s);
-#pragma unroll
-                    for (int i = 0; i < kSegWords; ++i) ring[(n & 1) * (C::kSegBytes / 4) + i] = w[i];
-                    mbar_arrive(bar(C::bSegFull + (n & 1)));
-                }
-                __syncwarp();
-            };
-            give_segment(0);
+            constexpr bool kWalks = kTiles == 1;  // the first load warp does, between its units
+            if (kWalks && warp == kFirstLoad) ok = give_segment(0);
             for (int seg = 0; ok; ++seg) {
                 ok = warp_segment(seg, sg);
                 if (!ok || sg.blocks == 0) break;
-                give_segment(seg + 1);
-                if (!ok) break;
+                bool gives = kWalks && warp == kFirstLoad;
                 const int64_t at = ((int64_t)sg.g * D + c * 8) * 2;
                 const char *kp = reinterpret_cast<const char *>(a.k_pool) + at, *vp = reinterpret_cast<const char *>(a.v_pool) + at;
                 const int32_t *slots = a.kv_indices + sg.kv0;
@@ -593,7 +593,13 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                 auto fetch = [&](int n) { return slots[min(column_of(n) + lane, sg.N - 1)]; };  // past the end: a valid row again
                 int n = v_warp ? lw - C::kUnits : lw;
                 int ahead = n < end ? fetch(n) : 0;
+                const int first_units = n + 2 * step;  // in flight before the walk goes on
                 for (; n < end; n += step) {
+                    if (kWalks && gives && n >= first_units) {
+                        ok = give_segment(seg + 1);
+                        if (!ok) break;
+                        gives = false;
+                    }
                     int slot = ahead;
                     if (slot < 0 || slot >= a.pool_rows) {
                         latch(a.err, DDT_DEVERR_KV_INDEX);
@@ -644,6 +650,7 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                     }
                     mbar_arrive(full);
                 }
+                if (ok && gives) ok = give_segment(seg + 1);
                 base += sg.blocks;
             }
             asm volatile("cp.async.wait_all;" ::: "memory");  // nothing may land after the CTA has left
@@ -748,9 +755,12 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
             }
             __syncwarp();
         } else if (kTiles == 2) {
-            // ================= q, a segment ahead =================
+            // ================= q, a segment ahead; the first warp walks =================
+            const bool walks = warp == kMmaWarp + 1;
+            if (walks) give_segment(0);
             for (int seg = 0;; ++seg) {
                 if (!warp_segment(seg, sg) || sg.blocks == 0) break;
+                if (walks && !give_segment(seg + 1)) break;
                 if (seg > 0 && !warp_wait(bar(C::bQEmpty), (seg - 1) & 1, abort_flag, a.err)) break;
                 load_q(sg, 32 * (warp - kMmaWarp - 1), kTiles * kRows, 32 * C::kQWarps);
             }
@@ -787,12 +797,12 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                 ok = warp_wait(bar(C::bSFull + slot), phase, abort_flag, a.err);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
+#pragma unroll 1  // (unrolled, the loop outgrows the instruction cache: 1142 us where this takes 981)
                 for (int h = 0; h < C::kHalves; ++h) {
                     // The one-tile kernel keeps the 64 scores until the weights are sure and stores these
-                    // as it goes; the two-tile kernel, short of registers, reads the scores again when
-                    // the reference moves and stores the weights at the end.
-                    constexpr bool kKeep = kTiles == 1;
+                    // as it goes; the two-tile kernel (and scores with cap and bias), short of registers,
+                    // reads the scores again when the reference moves and stores the weights at the end.
+                    constexpr bool kKeep = kTiles == 1 && kScore != (kCap | kBias);
                     const int c = c0 + 64 * h;
                     uint32_t seen0 = 0xffffffffu, seen1 = 0xffffffffu;
                     if (!fast) {
@@ -805,13 +815,31 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                         tmem_ld32(col + 64 * h + 32, s[1]);
                         tmem_wait_ld();
                     };
-                    if (kKeep) take();
+                    if (kKeep) take();  // (nothing is stored before)
                     uint32_t pw[2][16];  // the weights as bf16 pairs
                     float sum;
                     auto store = [&](int k) {
                         if (kKeep) tmem_st16(col + 32 * h + 16 * k, pw[k]);  // over scores that have been read
                     };
+                    auto reach = [&]() {  // the row's largest score of these 64
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            mx = fmaxf(mx, reach_8<kScore>(reinterpret_cast<const uint32_t(&)[8]>(s[q >> 2][8 * (q & 3)]),
+                                                           (q < 4 ? seen0 : seen1) >> (8 * (q & 3)), c + 8 * q, p, sc));
+                        return reached<kScore>(mx, sc);
+                    };
                     while (true) {
+                        if (!fast && !__any_sync(0xffffffffu, (seen0 | seen1) != 0)) {  // no row of the warp sees any
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) pw[k][e] = 0;
+                                store(k);
+                            }
+                            sum = 0.f;
+                            break;
+                        }
                         if (!kKeep) take();
                         const float m = m_ref == -INFINITY ? 0.f : m_ref;  // nothing seen yet: the weights are taken again below
                         sum = fast ? weights_64<kScore, true>(s, pw, seen0, seen1, c, p, m, sc, store)
@@ -822,18 +850,16 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                         // against the old one shrinks; then the weights are taken again.
                         float mx = -INFINITY;
                         if (kKeep) {
-#pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                mx = fmaxf(mx, largest_8<kScore>(reinterpret_cast<const uint32_t(&)[8]>(s[q >> 2][8 * (q & 3)]),
-                                                                 (q < 4 ? seen0 : seen1) >> (8 * (q & 3)), c + 8 * q, p, sc));
+                            mx = reach();
                         } else {
 #pragma unroll 1
                             for (int q = 0; q < 8; ++q) {
                                 uint32_t o8[8];
                                 tmem_ld8(col + 64 * h + 8 * q, o8);
                                 tmem_wait_ld();
-                                mx = fmaxf(mx, largest_8<kScore>(o8, (q < 4 ? seen0 : seen1) >> (8 * (q & 3)), c + 8 * q, p, sc));
+                                mx = fmaxf(mx, reach_8<kScore>(o8, (q < 4 ? seen0 : seen1) >> (8 * (q & 3)), c + 8 * q, p, sc));
                             }
+                            mx = reached<kScore>(mx, sc);
                         }
                         mx += kShift;
                         const bool up = moves && mx > m_ref;
@@ -930,14 +956,6 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                     float o[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : __uint_as_float(t32[e]) * inv;
-                    if (poisoned_now) {
-                        const uint32_t *w = poison + 64 * q * (C::kPer / 32) + first / 32;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            if ((w[2 * e * (C::kPer / 32)] >> lane) & 1u) o[e] += INFINITY;
-                            if ((w[(2 * e + 1) * (C::kPer / 32)] >> lane) & 1u) o[e] -= INFINITY;
-                        }
-                    }
                     if (part) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -964,9 +982,25 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                     else if (a.lse) a.lse[row] = lse;
                 }
                 tc_fence_before();  // the output has been read before the next segment's first product
+                if (poisoned_now) {  // rows that have left get what their columns of V held
+                    __syncwarp();
+#pragma unroll 1
+                    for (int e = 0; e < D; ++e) {
+                        uint32_t *w = poison + 2 * e * (C::kPer / 32) + first / 32;
+                        const bool plus = (w[0] >> lane) & 1u, minus = (w[C::kPer / 32] >> lane) & 1u;
+                        __syncwarp();
+                        if (lane == 0) w[0] = w[C::kPer / 32] = 0;
+                        if (!plus && !minus) continue;
+                        const float x = plus ? minus ? NAN : INFINITY : -INFINITY;
+                        if (part) {
+                            a.o_part[(prow + lane) * D + e] += x;
+                        } else {
+                            __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(a.out) + row * D + e;
+                            *o = __float2bfloat16_rn(__bfloat162float(*o) + x);
+                        }
+                    }
+                }
             }
-            if (poisoned_now && warp_on)  // this warp's rows are words of their own
-                for (int i = lane; i < 2 * D; i += 32) poison[i * (C::kPer / 32) + first / 32] = 0;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::bSegDone));
         }

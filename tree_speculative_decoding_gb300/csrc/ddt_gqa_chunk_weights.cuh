@@ -54,8 +54,9 @@ struct Cfg {
     static constexpr int kQStages = NQ == 128 ? (D == 128 ? 2 : 4) : 4;
     static constexpr int kSoftWarps = 8, kLoadWarps = 8, kFirstLoad = 8, kMmaWarp = 16, kThreads = 544;
     static constexpr int kOffK = 0, kOffQ = kOffK + kKStages * kKBytes;
-    static constexpr int kOffRow = kOffQ + kQStages * kQBytes;  // per stage: NQ x (-lse, slope, position - the first's), first position
-    static constexpr int kRowBytes = NQ * 12 + 16;
+    // per stage NQ each of: -lse, slope, position less the first row's (as a number of either kind); the first position
+    static constexpr int kOffRow = kOffQ + kQStages * kQBytes;
+    static constexpr int kRowBytes = NQ * 16 + 16;
     static constexpr int kOffBar = kOffRow + kQStages * kRowBytes;
     static constexpr int bKFull = 0, bKEmpty = bKFull + kKStages, bQFull = bKEmpty + kKStages, bQEmpty = bQFull + kQStages,
                          bRFull = bQEmpty + kQStages, bSFull = bRFull + kQStages, bSEmpty = bSFull + 4, bDrain = bSEmpty + 4,
@@ -197,37 +198,32 @@ struct Walk {
 };
 
 // ---------------------------------------------------------------- the sums of one step
-// e^(z - lse) of 16 rows for the thread's column, summed.  row: -lse (log2 units), slopes and
-// positions less the first row's of these rows; away: the first row's position less the column.
-template <int kScore, bool kFast>
-__device__ __forceinline__ float sum_16(const uint32_t (&s)[16], const float *nlse, const float *slope, const float *rel, int away,
-                                        int window, bool full, int valid, const ScoreScale &sc) {
+// e^(z - lse) of 16 rows for the thread's column, summed.  list: -lse (log2 units), slopes and
+// positions less the first row's, from the first of these rows on; away: the first row's position
+// less the column.  A row sees the column where the distance, unsigned, is at most `most`.
+template <int kScore, bool kFast, int NQ>
+__device__ __forceinline__ float sum_16(const uint32_t (&s)[16], const float *list, int away, uint32_t most, const ScoreScale &sc) {
     float2 acc = make_float2(0.f, 0.f);
     const float base = (float)away;
 #pragma unroll
     for (int e = 0; e < 16; e += 4) {
-        const float4 l = *reinterpret_cast<const float4 *>(nlse + e);
-        float4 d = make_float4(0.f, 0.f, 0.f, 0.f), k = d;
-        if (!kFast || (kScore & kBias)) d = *reinterpret_cast<const float4 *>(rel + e);
-        if (kScore & kBias) k = *reinterpret_cast<const float4 *>(slope + e);
-        const float ls[4] = {l.x, l.y, l.z, l.w}, ds[4] = {d.x, d.y, d.z, d.w}, ks[4] = {k.x, k.y, k.z, k.w};
+        const float4 l = *reinterpret_cast<const float4 *>(list + e);
+        float add[4] = {l.x, l.y, l.z, l.w};
+        if constexpr (kScore & kBias) {
+            const float4 k = *reinterpret_cast<const float4 *>(list + NQ + e), d = *reinterpret_cast<const float4 *>(list + 2 * NQ + e);
+            const float ks[4] = {k.x, k.y, k.z, k.w}, ds[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) add[u] = fmaf(-ks[u], kFast ? base + ds[u] : fabsf(base + ds[u]), add[u]);
+        }
+        int4 r = make_int4(0, 0, 0, 0);
+        if (!kFast) r = *reinterpret_cast<const int4 *>(list + 3 * NQ + e);
+        const int rs[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
         for (int u = 0; u < 4; u += 2) {
-            float add[2] = {ls[u], ls[u + 1]};
-            if (kScore & kBias) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float far = kFast ? base + ds[u + i] : fabsf(base + ds[u + i]);
-                    add[i] = fmaf(-ks[u + i], far, add[i]);
-                }
-            }
-            float2 x = score_pair<kScore>(__uint_as_float(s[e + u]), __uint_as_float(s[e + u + 1]), sc, add[0], add[1]);
+            float2 x = score_pair<kScore>(__uint_as_float(s[e + u]), __uint_as_float(s[e + u + 1]), sc, add[u], add[u + 1]);
             if (!kFast) {
-                const int a0 = away + (int)ds[u], a1 = away + (int)ds[u + 1];
-                const bool in0 = e + u < valid && (full || (a0 >= 0 && (window <= 0 || a0 < window)));
-                const bool in1 = e + u + 1 < valid && (full || (a1 >= 0 && (window <= 0 || a1 < window)));
-                x.x = in0 ? x.x : -INFINITY;
-                x.y = in1 ? x.y : -INFINITY;
+                x.x = (uint32_t)(away + rs[u]) <= most ? x.x : -INFINITY;
+                x.y = (uint32_t)(away + rs[u + 1]) <= most ? x.y : -INFINITY;
             }
             acc = f2add(acc, make_float2(ex2(x.x), ex2(x.y)));
         }
@@ -442,9 +438,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) chunk_weights_kernel(
                 const int64_t row0 = (int64_t)(sg.qo0 + sg.token) * a.num_heads + g * prm.group;
                 // this lane's row of the list beside the q tile
                 const bool lists = 32 * lw < NQ && 32 * lw + lane < NQ;
-                const int n = first + 32 * lw + lane, token = n / prm.group, head = n - token * prm.group;
+                // (behind the last row: that one again, with a sum of infinity, which counts nothing)
+                const int own = first + 32 * lw + lane, n = min(own, last), token = n / prm.group, head = n - token * prm.group;
                 float lse = INFINITY, slope = 0.f;
-                if (lists && n <= last) {
+                if (lists && own <= last) {
                     lse = a.lse[row0 + (int64_t)token * a.num_heads + head];
                     if (kScore & kBias) slope = a.slopes[g * prm.group + head] * kLog2e;
                 }
@@ -468,8 +465,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) chunk_weights_kernel(
                         list[32 * lw + lane] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;  // a row that saw nothing counts nothing
                         list[NQ + 32 * lw + lane] = slope;
                         list[2 * NQ + 32 * lw + lane] = (float)(token - t0);
+                        reinterpret_cast<int *>(list)[3 * NQ + 32 * lw + lane] = token - t0;
                     }
-                    if (lw == 0 && lane == 0) *reinterpret_cast<int *>(list + 3 * NQ) = sg.P + sg.token + t0;
+                    if (lw == 0 && lane == 0) reinterpret_cast<int *>(list)[4 * NQ] = sg.P + sg.token + t0;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(C::bRFull + s));
                 }
@@ -556,12 +554,13 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) chunk_weights_kernel(
                 if (!ok) break;
                 if (tile_on) {
                     const int buf = 2 * t + (tn & 1);
-                    const int valid = sg.rows - tile * NQ;
-                    const int away = *reinterpret_cast<const int *>(list + 3 * NQ) - j;  // the first row's position less the column
-                    const int spread = (int)list[3 * NQ - 1];                           // the last one's less the first one's
+                    const int *ints = reinterpret_cast<const int *>(list);
+                    const int away = ints[4 * NQ] - j;                       // the first row's position less the column
+                    const int spread = (sg.rows - tile * NQ < NQ) ? -1 : ints[4 * NQ - 1];  // the last one's less the first one's
                     const bool lane_fast = (full || (away >= 0 && (a.window <= 0 || away + spread < a.window))) &&
                                            (!(kScore & kBias) || away >= 0);
-                    const bool fast = valid >= NQ && __all_sync(0xffffffffu, lane_fast);
+                    const bool fast = spread >= 0 && __all_sync(0xffffffffu, lane_fast);
+                    const uint32_t most = full ? 0xffffffffu : a.window > 0 ? (uint32_t)a.window - 1u : 0x7fffffffu;
                     ok = warp_wait(bar(C::bSFull + buf), (tn >> 1) & 1, abort_flag, a.err);
                     if (!ok) break;
                     tc_fence_after();
@@ -576,10 +575,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) chunk_weights_kernel(
 #pragma unroll
                         for (int h = 0; h < (NQ > 16 ? 2 : 1); ++h) {
                             const int m = n + 16 * h;
-                            sum += fast ? sum_16<kScore, true>(s[h], list + m, list + NQ + m, list + 2 * NQ + m, away, a.window, full,
-                                                               valid - m, sc)
-                                        : sum_16<kScore, false>(s[h], list + m, list + NQ + m, list + 2 * NQ + m, away, a.window, full,
-                                                                valid - m, sc);
+                            sum += fast ? sum_16<kScore, true, NQ>(s[h], list + m, away, most, sc)
+                                        : sum_16<kScore, false, NQ>(s[h], list + m, away, most, sc);
                         }
                     }
                     total += sum;
