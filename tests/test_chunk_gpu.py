@@ -187,6 +187,22 @@ def test_scores_of_minus_infinity_alone_give_an_empty_row(ddt):
         assert not out.any() and bool((ls == -torch.inf).all())
 
 
+def test_capped_scores_of_infinite_products(ddt):
+    # a product of -inf is a score of -cap, one of +inf a score of cap; the first request has nothing but those
+    c = ref.Chunk([(150, 2), (90, 3)], 9)
+    q, k, v = inputs(c, 2, 2, 64, 12)
+    q = q.abs() + 1
+    rows = c.slots.astype(np.int64)
+    k[rows[: c.N[0]]] = -torch.inf
+    k[rows[c.N[0] + 5]] = torch.inf
+    k[rows[c.N[0] + 60:]] = -torch.inf
+    out, ls = run(ddt, c, q, k, v, 0.1, cap=6.0)
+    clean(ddt)
+    kk = k.clone()
+    kk[torch.isinf(k)] = torch.sign(k[torch.isinf(k)]) * 1e4
+    check(out, ls, ref.attention(q, kk, v, c, 0.1, cap=6.0))
+
+
 def test_strided_pools_rows_left_alone_and_no_lse(ddt):
     c = ref.Chunk([(150, 40), (0, 0), (33, 1)], 4)
     H, G, D, extra = 16, 4, 128, 5

@@ -1,4 +1,6 @@
 // ddt_gqa_chunk.cu -- chunk attention and received weights: sizes, the choice of how the work is split, launches.
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -77,10 +79,37 @@ void chunk_choose(ChunkArgs &a, size_t workspace_bytes, int num_sms) {
     while (a.num_ctas > 0 && chunk_layout(a, nullptr) > workspace_bytes) --a.num_ctas;
 }
 
+namespace {
+// cuTensorMapEncodeTiled from the driver, looked up once through the runtime
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+// a pool with boxes of 32 rows x 64 values
+bool encode_pool(CUtensorMap *map, const uint16_t *pool, const ChunkArgs &a) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)a.num_kv_heads * a.head_dim, (cuuint64_t)a.pool_rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)a.pool_stride * 2};
+    const cuuint32_t box[2] = {64, 32}, elem[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(pool), dims, strides, box, elem,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace
+
 cudaError_t launch_chunk_attn(const ChunkArgs &a, int num_sms, cudaStream_t s) {
     AttnParams prm;
     memset(&prm, 0, sizeof prm);
     prm.a = a;
+    if (!encode_pool(&prm.k_map, a.k_pool, a) || !encode_pool(&prm.v_map, a.v_pool, a)) return cudaErrorInvalidValue;
     prm.group = a.num_heads / a.num_kv_heads;
     prm.group_inv = 1.0f / (float)prm.group;
     prm.part_rows = part_rows(a.tiles, a.max_q_len, prm.group);

@@ -14,7 +14,8 @@
 //     shared memory, so two CTAs share an SM (decode, small chunks: the loads bound it).
 //   * kTiles = 2: blocks of 128 columns, all of tensor memory; the tensor core works on
 //     one tile while the softmax of the other runs.  Where an item's last rows fill one
-//     tile only, its blocks alternate between the two score slots instead.
+//     tile only, its blocks alternate between the two tiles' warps and outputs, each with a
+//     reference and sum of its own, and the two are joined at the end.
 // A CTA takes one item; or the blocks of all items, weighted by what they cost, form one
 // line (request, K/V head, rows, columns) that is dealt to the resident CTAs in equal
 // shares: a CTA takes the end of one item, whole items, and the start of another.  Every
@@ -26,11 +27,11 @@
 // P (bf16) overwrites the scores in place and is the A operand of PV from tensor memory;
 // V is read as an MN-major operand from its rows.
 //
-// The softmax does not look for a block's maximum: the weights of 64 columns are taken
-// against the row's reference, the maximum of the first columns it saw plus kShift.  Only
-// where their sum passes kSumLimit (or the row had seen nothing) the maximum is found, the
-// reference moves, and the sums so far are scaled.  kShift keeps every sum finite: a row's
-// weights sum to 1 at most, so its result is at most the largest |v|.
+// The softmax takes weights against the row's reference, the maximum of the first columns it saw
+// plus kShift.  The tensor-memory load brings the largest product of every 32 columns with it: only
+// where a score could pass the reference by 2^22 the reference moves, and the sums so far are scaled.
+// kShift keeps every sum finite: a row's weights sum to 1 at most, so its result is at most the
+// largest |v|.
 // Statistics, sums and partial results are fp32; the weights are rounded to bf16 for the
 // product with V, since the tensor core takes both operands in V's type (2^-8 of each at most).
 //
@@ -43,6 +44,7 @@
 // copies and MMAs and leaves.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -57,13 +59,13 @@ namespace chunk {
 using namespace sm100;
 
 constexpr int kRows = 128;  // rows per tile (TMEM lanes)
-// Weights against the reference: 2^-kShift where the reference was found.  64 of them may sum to
-// kSumLimit, and 2^31 columns to 2^25 kSumLimit = 1.  A value's weight loses bits below 2^-126,
-// which for the heaviest columns is |v| below 2^-73.
-constexpr float kShift = 53.f;
-constexpr float kSumLimit = 1.f / 33554432.f;  // 2^-25: 2^28 times the weight at the reference
+// Weights against the reference: 2^-kShift where the reference was found, 2^-kMost at most, so that
+// 2^31 columns sum to 1 at most.  A value's weight loses bits below 2^-126, which for the heaviest
+// columns is |v| below 2^-73.
+constexpr float kShift = 53.f, kMost = 31.f;
 
 struct AttnParams {
+    CUtensorMap k_map, v_map;  // the pools as [pool_rows][K/V heads * D], boxes of 32 rows x 64 values
     ChunkArgs a;
     int group;        // query heads per K/V head
     float group_inv;  // 1 / group
@@ -110,14 +112,15 @@ struct Cfg {
     // barriers
     static constexpr int bKFull = 0, bKEmpty = bKFull + kKStages, bVFull = bKEmpty + kKStages,
                          bVEmpty = bVFull + kVStages, bSFull = bVEmpty + kVStages, bPFull = bSFull + 2,
-                         bQFull = bPFull + 2 * kHalves, bQEmpty = bQFull + 1, bHalf = bQEmpty + 1, bODone = bHalf + 2,
-                         bOFin = bODone + 1, bDrain = bOFin + 1, bSegDone = bDrain + 1, bSegFull = bSegDone + 1,
+                         bQFull = bPFull + 2 * kHalves, bQEmpty = bQFull + 1, bHalf = bQEmpty + 1, bODone = bHalf + 2, bJoin = bODone + 1,
+                         bOFin = bJoin + 1, bDrain = bOFin + 1, bSegDone = bDrain + 1, bSegFull = bSegDone + 1,
                          bSegEmpty = bSegFull + 2, bCount = bSegEmpty + 2;
     static constexpr int kOffHolder = kOffBar + 8 * bCount;  // tensor memory, abort, poison in use, -
     static constexpr int kOffWalk = kOffHolder + 16;
     static constexpr int kWalkBytes = 128, kSegBytes = 96;
     static constexpr int kOffPlan = kOffWalk + kWalkBytes + 2 * kSegBytes;  // a sum per warp; the share's request
-    static constexpr int kSmemUsed = kOffPlan + 8 * (kThreads / 32) + 32;
+    static constexpr int kOffJoin = kOffPlan + 8 * (kThreads / 32) + 32;  // the second tile's references and sums
+    static constexpr int kSmemUsed = kOffJoin + (kTiles == 2 ? kRows * 8 : 0);
     static constexpr int kSmemBytes = kSmemUsed + 1024;  // slack for the 1024-byte alignment of swizzle atoms
     static constexpr int kOffCosts = kOffK;  // while the work is dealt: a cost per request
     static constexpr uint32_t kIdescS = idesc_bf16(kRows, NB, 0, 0);
@@ -250,18 +253,37 @@ struct Walk {
 };
 
 // ---------------------------------------------------------------- weights of 64 columns
-// pw: the weights of the raw scores s (columns c .. c + 63 of a row at position p) against the
-// reference m, as bf16 pairs; store(k) is called when pw[k] is complete.  Returns their sum.
+// 32 consecutive 32-bit columns of this thread's lane, and the largest of them (kAbs: the largest
+// magnitude) as floats; NaN counts only where all are.
+template <bool kAbs>
+__device__ __forceinline__ void tmem_ld32_max(uint32_t taddr, uint32_t (&r)[32], float &most) {
+#define DDT_LD32_MAX(abs)                                                                                                      \
+    asm volatile("tcgen05.ld.red.sync.aligned.32x32b.x32.max" abs ".f32 "                                                      \
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"                                                     \
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"                               \
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), \
+                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),      \
+                   "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),     \
+                   "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(most)       \
+                 : "r"(taddr))
+    if constexpr (kAbs) DDT_LD32_MAX(".abs");
+    else DDT_LD32_MAX("");
+#undef DDT_LD32_MAX
+}
+
+// The weights of the products s (columns c .. c + 63 of a row at position p) against the reference
+// m as bf16 pairs, handed to store(k, pairs) 32 columns at a time.  Returns their sum.
 // kFast: all 64 are seen, at columns up to p where heads have slopes.
 template <int kScore, bool kFast, class Store>
-__device__ __forceinline__ float weights_64(const uint32_t (&s)[2][32], uint32_t (&pw)[2][16], uint32_t seen0, uint32_t seen1, int c,
-                                            int p, float m, const ScoreScale &sc, Store store) {
-    float2 acc = make_float2(0.f, 0.f);
+__device__ __forceinline__ float weights_64(const uint32_t (&s)[2][32], uint32_t seen0, uint32_t seen1, int c, int p, float m,
+                                            const ScoreScale &sc, Store store) {
+    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     const float away = (float)(c - p);  // column less position
     const float base = (kScore & kBias) && kFast ? fmaf(sc.slope, away, -m) : -m;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const uint32_t seen = k ? seen1 : seen0;
+        uint32_t pw[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
             float add0 = base, add1 = base;
@@ -281,31 +303,32 @@ __device__ __forceinline__ float weights_64(const uint32_t (&s)[2][32], uint32_t
                 x.y = (seen >> (e + 1)) & 1u ? x.y : -INFINITY;
             }
             const float p0 = ex2(x.x), p1 = ex2(x.y);
-            acc = f2add(acc, make_float2(p0, p1));
-            pw[k][e / 2] = pack_bf16(p0, p1);
+            acc[(e >> 1) & 1] = f2add(acc[(e >> 1) & 1], make_float2(p0, p1));
+            pw[e / 2] = pack_bf16(p0, p1);
         }
-        store(k);
+        store(k, pw);
     }
-    return acc.x + acc.y;
+    return (acc[0].x + acc[1].x) + (acc[0].y + acc[1].y);
 }
-// What a row's largest score is found with: of 8 seen columns from c on the largest product, or
-// (where heads have slopes, which change the order) the largest score; then the score of that.
+// What a row's largest score is found with: of 64 columns from c on the largest seen product, or
+// (where heads have slopes, which change the order) the largest seen score; then the score of that.
 template <int kScore>
-__device__ __forceinline__ float reach_8(const uint32_t (&s)[8], uint32_t seen, int c, int p, const ScoreScale &sc) {
+__device__ __forceinline__ float reach_64(const uint32_t (&s)[2][32], uint32_t seen0, uint32_t seen1, int c, int p, const ScoreScale &sc) {
     float mx = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-        float2 x = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+    for (int e = 0; e < 64; e += 2) {
+        float2 x = make_float2(__uint_as_float(s[e >> 5][e & 31]), __uint_as_float(s[e >> 5][(e & 31) + 1]));
         if constexpr (kScore & kBias)
             x = score_pair<kScore>(x.x, x.y, sc, -sc.slope * fabsf((float)(c + e - p)), -sc.slope * fabsf((float)(c + e + 1 - p)));
-        if ((seen >> e) & 1u) mx = fmaxf(mx, x.x);
-        if ((seen >> (e + 1)) & 1u) mx = fmaxf(mx, x.y);
+        const uint32_t seen = (e < 32 ? seen0 : seen1) >> (e & 31);
+        if (seen & 1u) mx = fmaxf(mx, x.x);
+        if (seen & 2u) mx = fmaxf(mx, x.y);
     }
     return mx;
 }
 template <int kScore>
-__device__ __forceinline__ float reached(float mx, const ScoreScale &sc) {
-    if (mx == -INFINITY || (kScore & kBias)) return mx;  // (capped, a product of -inf is a score of -cap)
+__device__ __forceinline__ float reached(float mx, bool some, const ScoreScale &sc) {
+    if (!some || (kScore & kBias)) return mx;
     return score_pair<kScore>(mx, mx, sc, 0.f, 0.f).x;
 }
 
@@ -373,6 +396,7 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
             mbar_init(bar(i), i < C::bKEmpty || (i >= C::bVFull && i < C::bVEmpty) ? 32 * C::kUnits  // load lanes
                       : i >= C::bPFull && i < C::bQFull                            ? 4               // row quarters
                       : i == C::bQFull                                             ? C::kQWarps
+                      : i == C::bJoin                                              ? 4
                       : i == C::bSegDone                                           ? C::kSoftWarps
                       : i >= C::bSegEmpty ? C::kSoftWarps + C::kLoadWarps + 1 + (kTiles == 2 ? C::kQWarps : 0)
                                           : 1);
@@ -572,9 +596,9 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                 const int32_t *slots = a.kv_indices + sg.kv0;
                 constexpr bool kApart = kTiles == 2;
                 const int lw = warp - kFirstLoad;
-                const bool v_warp = kApart && lw >= C::kUnits;
+                const bool v_warp = kApart && lw >= C::kLoadWarps / 2;
                 const int last = 2 * sg.blocks - 1, end = (kApart ? 1 : 2) * sg.blocks * C::kUnits;
-                const int step = kApart ? C::kUnits : C::kLoadWarps;
+                const int step = kApart ? C::kLoadWarps / 2 : C::kLoadWarps;
                 // block of unit n, and whether it is its V
                 auto block_of = [&](int n, bool &is_v) {
                     const int q = n / C::kUnits;
@@ -591,7 +615,7 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                     return block_column<C>(sg, j) + 32 * (n % C::kUnits);
                 };
                 auto fetch = [&](int n) { return slots[min(column_of(n) + lane, sg.N - 1)]; };  // past the end: a valid row again
-                int n = v_warp ? lw - C::kUnits : lw;
+                int n = v_warp ? lw - C::kLoadWarps / 2 : lw;
                 int ahead = n < end ? fetch(n) : 0;
                 const int first_units = n + 2 * step;  // in flight before the walk goes on
                 for (; n < end; n += step) {
@@ -615,13 +639,30 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                                         (n % C::kUnits) * 32 * 128;
                     const uint32_t full = bar((is_v ? C::bVFull : C::bKFull) + s);
                     const char *pool = is_v ? vp : kp;
+                    const int col = column_of(n);
+                    const bool whole = !is_v || all_see(col / NB * NB, NB, sg.pa, sg.pb, a.window, sg.full);
+                    // Slots in a row (a page, or rows taken in order) are one tile copy for each 64 values, which
+                    // takes no issue slots; others, and V that has to be looked at, 16 bytes a lane.
+                    const int slot0 = __shfl_sync(0xffffffffu, slot, 0);
+                    if (whole && __all_sync(0xffffffffu, slot == slot0 + lane)) {
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(full, 32 * D * 2);
+                            const uint32_t at = sbase + (is_v ? C::kOffV : C::kOffK) + s * C::kBlockBytes + (n % C::kUnits) * 32 * 128;
+#pragma unroll
+                            for (int x = 0; x < C::kBoxes; ++x)
+                                tma_load_2d(at + x * C::kBoxBytes, is_v ? &prm.v_map : &prm.k_map, sg.g * D + 64 * x, slot0, full);
+                        } else {
+                            mbar_arrive(full);
+                        }
+                        __syncwarp();
+                        continue;
+                    }
 #pragma unroll
                     for (int i = 0; i < 32 / kPer; ++i) {
                         const int k = i * kPer + sub;
                         cp_async_16(sbase + to + k * 128 + (((c & 7) ^ (k & 7)) << 4), pool + __shfl_sync(0xffffffffu, slot, k) * pitch);
                     }
-                    const int col = column_of(n);
-                    if (!is_v || all_see(col / NB * NB, NB, sg.pa, sg.pb, a.window, sg.full)) {
+                    if (whole) {
                         cp_async_arrive(full);
                         continue;
                     }
@@ -654,6 +695,8 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                 base += sg.blocks;
             }
             asm volatile("cp.async.wait_all;" ::: "memory");  // nothing may land after the CTA has left
+            // (tile copies that the MMA warp has not waited for: it gave up, and this wait runs out long after they landed)
+            if (!ok) mbar_wait(bar(C::bDrain), 1, 1u << 12);
         } else if (warp == kMmaWarp) {
             // ================= MMA =================
             if (elect_one()) {
@@ -665,7 +708,8 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                 // The tensor pipe is idle while this thread waits or computes: the loop is
                 // unrolled over tiles and slots and keeps its stages and phases in counters.
                 auto run = [&](auto tile_count, int items) {
-                    constexpr int A = decltype(tile_count)::value;  // tiles of the segment: outputs that work units alternate between
+                    constexpr int A = decltype(tile_count)::value;  // tiles of the segment
+                    constexpr int kOuts = kTiles;                   // outputs that work units alternate between
                     int w = 0;
                     auto issue_s = [&](int slot, int n) {
                         const int t = A == 2 ? slot : 0;
@@ -699,8 +743,8 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                             fence_proxy_async_smem();
                         }
                         const uint64_t vd = v0 + (uint32_t)vs * (C::kBlockBytes >> 4);
-                        const uint32_t p = tmem + C::kColS + NB * slot, d = tmem + C::kColO + D * t;
-                        const uint32_t later = w >= A;  // an output's first product overwrites
+                        const uint32_t p = tmem + C::kColS + NB * slot, d = tmem + C::kColO + D * (kOuts == 2 ? slot : 0);
+                        const uint32_t later = w >= kOuts;  // an output's first product overwrites
 #pragma unroll
                         for (int h = 0; h < C::kHalves; ++h) {
                             ok = wait_or_abort(bar(C::bPFull + C::kHalves * slot + h), pph[slot], abort_flag, a.err);
@@ -712,7 +756,7 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                             if (h + 1 < C::kHalves) mma_commit(bar(C::bHalf + slot));
                         }
                         pph[slot] ^= 1;
-                        if (A == 1) mma_commit(bar(C::bODone));
+                        if (kOuts == 1) mma_commit(bar(C::bODone));
                         if (t == A - 1) {
                             mma_commit(bar(C::bVEmpty + vs));
                             if (++vs == C::kVStages) {
@@ -734,6 +778,7 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                         }
                     }
                 };
+                bool was_lone = false;
                 for (int seg = 0; ok; ++seg) {
                     ok = wait_or_abort(bar(C::bSegFull + (seg & 1)), (seg >> 1) & 1, abort_flag, a.err);
                     if (!ok) break;
@@ -743,6 +788,11 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                     ok = wait_or_abort(bar(C::bQFull), seg & 1, abort_flag, a.err);
                     if (!ok) break;
                     if constexpr (kTiles == 2) {
+                        // A lone tile's second output is read by the first tile's warps, which the second
+                        // tile's do not wait for.
+                        if (was_lone) ok = wait_or_abort(bar(C::bSegDone), (seg - 1) & 1, abort_flag, a.err);
+                        if (!ok) break;
+                        was_lone = sg.tiles == 1;
                         if (sg.tiles == 2) run(std::integral_constant<int, 2>{}, 2 * sg.blocks);
                         else run(std::integral_constant<int, 1>{}, sg.blocks);
                     } else {
@@ -772,13 +822,14 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
         const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
         ScoreScale sc = prm.score;
         uint32_t uses0 = 0, uses1 = 0;  // of the slots, in the segments before
-        uint32_t done = 0;          // products of segments with one tile
+        uint32_t done = 0, joins = 0;           // blocks, and joins, so far
         bool ok = true;
         for (int seg = 0; ok; ++seg) {
             ok = warp_segment(seg, sg);
             if (!ok || sg.blocks == 0) break;
-            const bool single = kTiles == 1 || sg.tiles == 1;  // one tile, alternating between the slots
-            const int first = t * kRows + 32 * wq;             // the warp's first row in the item
+            const bool lone = kTiles == 2 && sg.tiles == 1;          // one tile, served by both tiles' warps
+            const int first = (lone ? 0 : t * kRows) + 32 * wq;      // the warp's first row in the item
+            const int j0 = lone ? t : 0, step = lone ? 2 : 1;        // its blocks
             if constexpr (kTiles == 1) load_q(sg, first, first + 32, 32);
             const bool warp_on = first < sg.rows;  // the warp has rows
             const bool row_on = first + lane < sg.rows;
@@ -787,9 +838,9 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
             const int p = sg.pa + node;
             if constexpr (kScore & kBias) sc.slope = a.slopes[sg.g * prm.group + rn - node * prm.group] * kLog2e;
             float m_ref = -INFINITY, l = 0.f;  // the reference in log2 units, the sum against it
-            for (int j = 0; warp_on && j < sg.blocks; ++j) {
-                const int slot = single ? j & 1 : t;
-                const uint32_t phase = ((slot ? uses1 : uses0) + (single ? j >> 1 : j)) & 1;
+            for (int j = j0; warp_on && j < sg.blocks; j += step) {
+                const int slot = kTiles == 2 ? t : j & 1;
+                const uint32_t phase = ((slot ? uses1 : uses0) + (lone || kTiles == 1 ? j >> 1 : j)) & 1;
                 const uint32_t col = tmem + lane_off + C::kColS + NB * slot;
                 const int c0 = block_column<C>(sg, j);
                 const bool lane_fast = all_see(c0, NB, p, p, a.window, sg.full) && (!(kScore & kBias) || c0 + NB - 1 <= p);
@@ -799,101 +850,70 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                 tc_fence_after();
 #pragma unroll 1  // (unrolled, the loop outgrows the instruction cache: 1142 us where this takes 981)
                 for (int h = 0; h < C::kHalves; ++h) {
-                    // The one-tile kernel keeps the 64 scores until the weights are sure and stores these
-                    // as it goes; the two-tile kernel (and scores with cap and bias), short of registers,
-                    // reads the scores again when the reference moves and stores the weights at the end.
-                    constexpr bool kKeep = kTiles == 1 && kScore != (kCap | kBias);
                     const int c = c0 + 64 * h;
+                    uint32_t s[2][32];  // the products
+                    float r[2];         // and the largest of each 32
+                    tmem_ld32_max<(kScore & kCap) != 0>(col + 64 * h, s[0], r[0]);
+                    tmem_ld32_max<(kScore & kCap) != 0>(col + 64 * h + 32, s[1], r[1]);
                     uint32_t seen0 = 0xffffffffu, seen1 = 0xffffffffu;
                     if (!fast) {
                         seen0 = seen_bits(c, p, a.window, sg.full, sg.N);
                         seen1 = seen_bits(c + 32, p, a.window, sg.full, sg.N);
                     }
-                    uint32_t s[2][32];  // the scores
-                    auto take = [&]() {
-                        tmem_ld32(col + 64 * h, s[0]);
-                        tmem_ld32(col + 64 * h + 32, s[1]);
-                        tmem_wait_ld();
-                    };
-                    if (kKeep) take();  // (nothing is stored before)
-                    uint32_t pw[2][16];  // the weights as bf16 pairs
-                    float sum;
-                    auto store = [&](int k) {
-                        if (kKeep) tmem_st16(col + 32 * h + 16 * k, pw[k]);  // over scores that have been read
-                    };
-                    auto reach = [&]() {  // the row's largest score of these 64
-                        float mx = -INFINITY;
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            mx = fmaxf(mx, reach_8<kScore>(reinterpret_cast<const uint32_t(&)[8]>(s[q >> 2][8 * (q & 3)]),
-                                                           (q < 4 ? seen0 : seen1) >> (8 * (q & 3)), c + 8 * q, p, sc));
-                        return reached<kScore>(mx, sc);
-                    };
-                    while (true) {
-                        if (!fast && !__any_sync(0xffffffffu, (seen0 | seen1) != 0)) {  // no row of the warp sees any
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) pw[k][e] = 0;
-                                store(k);
-                            }
-                            sum = 0.f;
-                            break;
-                        }
-                        if (!kKeep) take();
-                        const float m = m_ref == -INFINITY ? 0.f : m_ref;  // nothing seen yet: the weights are taken again below
-                        sum = fast ? weights_64<kScore, true>(s, pw, seen0, seen1, c, p, m, sc, store)
-                                   : weights_64<kScore, false>(s, pw, seen0, seen1, c, p, m, sc, store);
-                        const bool moves = row_on && (sum > kSumLimit || (m_ref == -INFINITY && (seen0 | seen1)));
-                        if (!__any_sync(0xffffffffu, moves)) break;
-                        // The reference moves to the largest of these scores, and what was summed
-                        // against the old one shrinks; then the weights are taken again.
-                        float mx = -INFINITY;
-                        if (kKeep) {
-                            mx = reach();
-                        } else {
+                    tmem_wait_ld();
+                    // How far the scores reach: at most (seen whole), or exactly.
+                    float top;
+                    if (fast) {
+                        top = reached<kScore & kCap>(fmaxf(r[0], r[1]), true, sc);
+                        if constexpr (kScore & kBias) top += fmaxf(sc.slope * (float)(c + 63 - p), sc.slope * (float)(c - p));
+                    } else {
+                        top = reached<kScore>(reach_64<kScore>(s, seen0, seen1, c, p, sc), (seen0 | seen1) != 0, sc);
+                    }
+                    if (__any_sync(0xffffffffu, row_on && top > m_ref - kMost)) {
+                        // The reference moves to the largest of these scores, and what was summed against
+                        // the old one shrinks.
+                        if ((kScore != 0) && fast) top = reached<kScore>(reach_64<kScore>(s, seen0, seen1, c, p, sc), (seen0 | seen1) != 0, sc);
+                        const bool up = row_on && top > m_ref - kMost;
+                        if (__any_sync(0xffffffffu, up)) {
+                            const float alpha = up ? ex2(m_ref - (top + kShift)) : 1.0f;
+                            if (up) m_ref = top + kShift;
+                            l *= alpha;
+                            // The products so far have to be done before the output is scaled: of this
+                            // block's first half; or of the output's last block (with two outputs S(w) was
+                            // issued behind it, so it is done).
+                            if (h > 0) ok = warp_wait(bar(C::bHalf + slot), phase, abort_flag, a.err);
+                            else if (kTiles == 1 && j > 0) ok = warp_wait(bar(C::bODone), (done + j - 1) & 1, abort_flag, a.err);
+                            if (!ok) break;
+                            if (h > 0 || j > j0) {
+                                tc_fence_after();
+                                const uint32_t oc = tmem + lane_off + C::kColO + D * t;
 #pragma unroll 1
-                            for (int q = 0; q < 8; ++q) {
-                                uint32_t o8[8];
-                                tmem_ld8(col + 64 * h + 8 * q, o8);
-                                tmem_wait_ld();
-                                mx = fmaxf(mx, reach_8<kScore>(o8, (q < 4 ? seen0 : seen1) >> (8 * (q & 3)), c + 8 * q, p, sc));
-                            }
-                            mx = reached<kScore>(mx, sc);
-                        }
-                        mx += kShift;
-                        const bool up = moves && mx > m_ref;
-                        if (!__any_sync(0xffffffffu, up)) break;  // scores of -inf or NaN move nothing
-                        if (kKeep) tmem_wait_st();  // the next weights go to the same columns: stores have no order
-                        const float alpha = up ? ex2(m_ref - mx) : 1.0f;
-                        if (up) m_ref = mx;
-                        l *= alpha;
-                        // The products so far have to be done before the output is scaled: of this
-                        // block's first half; or of the output's last block (with two tiles S(w) was
-                        // issued behind it, so it is done).
-                        if (h > 0) ok = warp_wait(bar(C::bHalf + slot), phase, abort_flag, a.err);
-                        else if (single && j > 0) ok = warp_wait(bar(C::bODone), (done + j - 1) & 1, abort_flag, a.err);
-                        if (!ok) break;
-                        if (h > 0 || j > 0) {
-                            tc_fence_after();
-                            const uint32_t oc = tmem + lane_off + C::kColO + D * t;
-#pragma unroll 1
-                            for (int q = 0; q < D / 8; ++q) {
-                                uint32_t o8[8];
-                                tmem_ld8(oc + 8 * q, o8);
-                                tmem_wait_ld();
+                                for (int q = 0; q < D / 8; ++q) {
+                                    uint32_t o8[8];
+                                    tmem_ld8(oc + 8 * q, o8);
+                                    tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) o8[e] = __float_as_uint(__uint_as_float(o8[e]) * alpha);
-                                tmem_st8(oc + 8 * q, o8);
+                                    for (int e = 0; e < 8; ++e) o8[e] = __float_as_uint(__uint_as_float(o8[e]) * alpha);
+                                    tmem_st8(oc + 8 * q, o8);
+                                }
                             }
                         }
                     }
-                    if (!ok) break;
+                    const float m = m_ref == -INFINITY ? 0.f : m_ref;  // nothing seen yet: the weights are 0
+                    auto store = [&](int k, const uint32_t (&pw)[16]) {  // over products that have been read
+                        tmem_st16(col + 32 * h + 16 * k, pw);
+                    };
+                    float sum = 0.f;
+                    if (fast) {
+                        sum = weights_64<kScore, true>(s, seen0, seen1, c, p, m, sc, store);
+                    } else if (__any_sync(0xffffffffu, (seen0 | seen1) != 0)) {
+                        sum = weights_64<kScore, false>(s, seen0, seen1, c, p, m, sc, store);
+                    } else {  // no row of the warp sees any
+                        const uint32_t none[16] = {};
+                        store(0, none);
+                        store(1, none);
+                    }
                     l += sum;
-                    if (!kKeep) {
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) tmem_st16(col + 32 * h + 16 * k, pw[k]);
-                    }
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -902,24 +922,56 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                 if (!ok) break;
             }
             // a tile's warps without rows hand their part of the weights on as it is: its rows go nowhere
-            const bool tile_on = t * kRows < sg.rows;
-            for (int j = 0; ok && !warp_on && tile_on && j < sg.blocks; ++j) {
-                const int slot = single ? j & 1 : t;
-                ok = warp_wait(bar(C::bSFull + slot), ((slot ? uses1 : uses0) + (single ? j >> 1 : j)) & 1, abort_flag, a.err);
+            for (int j = j0; ok && !warp_on && j < sg.blocks; j += step) {
+                const int slot = kTiles == 2 ? t : j & 1;
+                ok = warp_wait(bar(C::bSFull + slot), ((slot ? uses1 : uses0) + (lone || kTiles == 1 ? j >> 1 : j)) & 1, abort_flag, a.err);
                 if (!ok) break;
 #pragma unroll
                 for (int h = 0; h < C::kHalves; ++h)
                     if (lane == 0) mbar_arrive(bar(C::bPFull + C::kHalves * slot + h));
             }
             if (!ok) break;
-            uses0 += single ? (sg.blocks + 1) >> 1 : sg.blocks;
-            uses1 += single ? sg.blocks >> 1 : sg.blocks;
-            if (single) done += sg.blocks;
+            uses0 += lone || kTiles == 1 ? (sg.blocks + 1) >> 1 : sg.blocks;
+            uses1 += lone || kTiles == 1 ? sg.blocks >> 1 : sg.blocks;
+            done += sg.blocks;
             // ---- epilogue ----
             ok = warp_wait(bar(C::bOFin), seg & 1, abort_flag, a.err);
             if (!ok) break;
             const bool poisoned_now = *poisoned != 0;
-            if (warp_on) {
+            if (lone) {
+                // (the wait above: the first tile's warps have left the segment before, so these places are free)
+                volatile float *place = reinterpret_cast<volatile float *>(smem + C::kOffJoin) + 2 * (32 * wq + lane);
+                if (t == 1) {
+                    place[0] = m_ref;
+                    place[1] = l;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::bJoin));
+                } else {
+                    ok = warp_wait(bar(C::bJoin), joins & 1, abort_flag, a.err);
+                    if (!ok) break;
+                    const float m1 = place[0], l1 = place[1], m = fmaxf(m_ref, m1);
+                    // what the two outputs count (without a reference the sum is 0, or NaN)
+                    const float keep0 = m_ref == -INFINITY ? l : ex2(m_ref - m), keep1 = m1 == -INFINITY ? l1 : ex2(m1 - m);
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int q = 0; q < D / 8; ++q) {
+                        uint32_t o0[8], o1[8];
+                        tmem_ld8(tmem + lane_off + C::kColO + 8 * q, o0);
+                        tmem_ld8(tmem + lane_off + C::kColO + D + 8 * q, o1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            o0[e] = __float_as_uint((keep0 != 0.f ? __uint_as_float(o0[e]) * keep0 : 0.f) +
+                                                    (keep1 != 0.f ? __uint_as_float(o1[e]) * keep1 : 0.f));
+                        tmem_st8(tmem + lane_off + C::kColO + 8 * q, o0);
+                    }
+                    tmem_wait_st();
+                    l = (keep0 != 0.f ? l * keep0 : 0.f) + (keep1 != 0.f ? l1 * keep1 : 0.f);
+                    m_ref = m;
+                }
+                ++joins;
+            }
+            if (warp_on && !(lone && t == 1)) {
                 tc_fence_after();
                 const int64_t row = (int64_t)(sg.qo0 + sg.node0 + node) * a.num_heads + sg.g * prm.group + rn - node * prm.group;
                 const bool part = sg.part >= 0;
@@ -955,7 +1007,8 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                     tmem_wait_ld();
                     float o[32];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : __uint_as_float(t32[e]) * inv;
+                    for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(t32[e]);
+                    for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
                     if (part) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
