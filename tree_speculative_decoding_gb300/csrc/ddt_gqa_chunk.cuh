@@ -20,13 +20,25 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kCap = 1, kBias = 2;  // bits of a kernel's kScore
 
-constexpr uint32_t kWaitLimit = 1u << 22;
+constexpr uint32_t kWaitLimit = 1u << 17;  // of 20 us
 
-// The waits try the barrier first: the abort flag is read only where the phase is still open.
+// Waits that give up.  A wait sleeps in the barrier for up to 20 us at a time: the short default makes
+// the waiting warps poll, and their instructions took a tenth of the attention's time (a prompt of 8192
+// 1068 us, with longer sleeps 914).  The abort flag is read only where the phase is still open.
+__device__ __forceinline__ bool mbar_sleep_wait(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000; "
+        "selp.u32 %0, 1, 0, p; }"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *err) {
-    if (sm100::mbar_try_wait(bar, parity)) return true;
+    if (mbar_sleep_wait(bar, parity)) return true;
     for (uint32_t i = 0; i < kWaitLimit; ++i) {
-        if (sm100::mbar_try_wait(bar, parity)) return true;
+        if (mbar_sleep_wait(bar, parity)) return true;
         if (*abort) return false;
     }
     *abort = 1;

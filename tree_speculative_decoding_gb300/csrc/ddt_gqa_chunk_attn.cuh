@@ -36,8 +36,8 @@
 // product with V, since the tensor core takes both operands in V's type (2^-8 of each at most).
 //
 // Infinities and NaN in V: a weight of 0 times NaN is NaN, so a V row that some row of the
-// item does not see may not reach the products with such a value.  Only blocks that not
-// all rows of the item see whole can hold one: there the load warps replace it by 0 and
+// item does not see may not reach the products with such a value.  V rows that no row of the
+// item sees are zeros; in those that some see and others do not the load warps replace it by 0 and
 // keep the rows that do see it as bits (poison), which are added to the results behind the epilogue.
 //
 // Every wait is bounded: on timeout the CTA latches DDT_DEVERR_TIMEOUT, waits for its own
@@ -63,6 +63,11 @@ constexpr int kRows = 128;  // rows per tile (TMEM lanes)
 // 2^31 columns sum to 1 at most.  A value's weight loses bits below 2^-126, which for the heaviest
 // columns is |v| below 2^-73.
 constexpr float kShift = 53.f, kMost = 31.f;
+
+// 16 bytes from global to shared memory, or zeros
+__device__ __forceinline__ void cp_async_16_or_0(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
 
 struct AttnParams {
     CUtensorMap k_map, v_map;  // the pools as [pool_rows][K/V heads * D], boxes of 32 rows x 64 values
@@ -128,7 +133,7 @@ struct Cfg {
     // Cost of a block with all tiles and with one, in one unit; of an item besides its blocks; the
     // share that a CTA gets at least.
     static constexpr int kCostFull = kTiles == 2 ? 16 : 8, kCostOne = kTiles == 2 ? 11 : 8;
-    static constexpr int kCostItem = kTiles == 2 ? 40 : 48, kMinShare = kTiles == 2 ? 56 : 32;
+    static constexpr int kCostItem = kTiles == 2 ? 80 : 48, kMinShare = kTiles == 2 ? 56 : 32;
     static_assert(kTiles == 2 || kKStages >= 2, "see the load warps");
     static_assert(kOffPlan % 8 == 0 && kOffWalk % 8 == 0 && kOffBar % 8 == 0, "alignment");
     static_assert(kColO + kTiles * D <= kTmemCols, "tensor memory");
@@ -639,12 +644,16 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                                         (n % C::kUnits) * 32 * 128;
                     const uint32_t full = bar((is_v ? C::bVFull : C::bKFull) + s);
                     const char *pool = is_v ? vp : kp;
-                    const int col = column_of(n);
-                    const bool whole = !is_v || all_see(col / NB * NB, NB, sg.pa, sg.pb, a.window, sg.full);
+                    // Columns that no row of the item sees (behind the last one, or outside its window) are zeros:
+                    // the products of their weights, which are 0, then are too.
+                    const int col = column_of(n), mine = col + lane;
+                    const bool in_full = mine < sg.full;
+                    const uint32_t some = __ballot_sync(0xffffffffu, in_full || (mine <= sg.pb && (a.window <= 0 || mine > sg.pa - a.window)));
+                    const uint32_t every = __ballot_sync(0xffffffffu, in_full || (mine <= sg.pa && (a.window <= 0 || mine > sg.pb - a.window)));
                     // Slots in a row (a page, or rows taken in order) are one tile copy for each 64 values, which
-                    // takes no issue slots; others, and V that has to be looked at, 16 bytes a lane.
+                    // takes no issue slots; others 16 bytes a lane.
                     const int slot0 = __shfl_sync(0xffffffffu, slot, 0);
-                    if (whole && __all_sync(0xffffffffu, slot == slot0 + lane)) {
+                    if (every == 0xffffffffu && __all_sync(0xffffffffu, slot == slot0 + lane)) {
                         if (lane == 0) {
                             mbar_arrive_expect_tx(full, 32 * D * 2);
                             const uint32_t at = sbase + (is_v ? C::kOffV : C::kOffK) + s * C::kBlockBytes + (n % C::kUnits) * 32 * 128;
@@ -660,13 +669,14 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
 #pragma unroll
                     for (int i = 0; i < 32 / kPer; ++i) {
                         const int k = i * kPer + sub;
-                        cp_async_16(sbase + to + k * 128 + (((c & 7) ^ (k & 7)) << 4), pool + __shfl_sync(0xffffffffu, slot, k) * pitch);
+                        cp_async_16_or_0(sbase + to + k * 128 + (((c & 7) ^ (k & 7)) << 4), pool + __shfl_sync(0xffffffffu, slot, k) * pitch,
+                                         (some >> k) & 1u);
                     }
-                    if (whole) {
+                    if (!is_v || some == every) {
                         cp_async_arrive(full);
                         continue;
                     }
-                    // a block of V that some row does not see whole
+                    // rows of V that some row sees and another does not
                     asm volatile("cp.async.wait_all;" ::: "memory");
                     uint32_t bad = 0;
 #pragma unroll
