@@ -115,6 +115,7 @@ cudaError_t launch_chunk_attn(const ChunkArgs &a, int num_sms, cudaStream_t s) {
     prm.part_rows = part_rows(a.tiles, a.max_q_len, prm.group);
     prm.tgs_most = items_most(a.tiles, a.max_q_len, prm.group);
     prm.score = score_scale(a.scale, a.score_cap);
+    prm.cap_most = a.score_cap / a.scale;
     switch ((a.score_cap > 0.f ? kCap : 0) | (a.slopes ? kBias : 0)) {
         case kCap: return launch_attn_score<kCap>(prm, s);
         case kBias: return launch_attn_score<kBias>(prm, s);

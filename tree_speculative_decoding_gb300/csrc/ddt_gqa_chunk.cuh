@@ -144,6 +144,37 @@ __device__ __forceinline__ float2 score_pair(float s0, float s1, const ScoreScal
         return f2fma(make_float2(s0, s1), make_float2(k.lin, k.lin), make_float2(add0, add1));
     }
 }
+// The same where every |z / cap| of the pair is below 1: cap tanh(u) = cap u P(u^2), P the interpolation
+// of tanh(sqrt t) / sqrt t at seven Chebyshev nodes of [0, 1] (1.4e-7 of the value in fp32, measured over
+// the range).  Ten multiply-adds in place of two special functions, of which a reciprocal takes 8 cycles of
+// a warp's share of the unit and 2^x 4.  The factors are pairs in registers: a packed multiply-add takes
+// no immediate, and read from constant memory they took longer than the special functions.
+struct CapPoly {
+    uint64_t u, cap2, c[7];
+    __device__ __forceinline__ static uint64_t both(float x) {
+        uint64_t r;
+        asm volatile("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));  // (volatile: made once, not at every use)
+        return r;
+    }
+    __device__ __forceinline__ void set(const ScoreScale &k) {
+        constexpr float kP[7] = {0.99999994039f, -0.33332827688f, 0.13325075805f, -0.053451646119f, 0.020279707387f, -0.0061943246983f, 0.0010380251333f};
+        u = both(k.lin * (0.5f / kLog2e));
+        cap2 = both(k.cap2);
+#pragma unroll
+        for (int i = 0; i < 7; ++i) c[i] = both(kP[i]);
+    }
+};
+__device__ __forceinline__ float2 score_pair_poly(float s0, float s1, const CapPoly &k, float add0, float add1) {
+    float2 x;
+    asm("{ .reg .b64 u, t, y, z; mov.b64 u, {%2, %3}; mul.rn.f32x2 u, u, %6; mul.rn.f32x2 t, u, u; "
+        "fma.rn.f32x2 y, %14, t, %13; fma.rn.f32x2 y, y, t, %12; fma.rn.f32x2 y, y, t, %11; fma.rn.f32x2 y, y, t, %10; "
+        "fma.rn.f32x2 y, y, t, %9; fma.rn.f32x2 y, y, t, %8; mul.rn.f32x2 u, u, %7; mov.b64 z, {%4, %5}; "
+        "fma.rn.f32x2 z, u, y, z; mov.b64 {%0, %1}, z; }"
+        : "=f"(x.x), "=f"(x.y)
+        : "f"(s0), "f"(s1), "f"(add0), "f"(add1), "l"(k.u), "l"(k.cap2), "l"(k.c[0]), "l"(k.c[1]), "l"(k.c[2]), "l"(k.c[3]),
+          "l"(k.c[4]), "l"(k.c[5]), "l"(k.c[6]));
+    return x;
+}
 __host__ __device__ inline ScoreScale score_scale(float scale, float cap) {
     ScoreScale k;
     k.lin = cap > 0.f ? 2.f * kLog2e * scale / cap : scale * kLog2e;

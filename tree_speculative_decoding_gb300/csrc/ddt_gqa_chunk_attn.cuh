@@ -77,6 +77,7 @@ struct AttnParams {
     int part_rows;    // rows of a partial result
     int tgs_most;     // items per K/V head of the longest request
     ScoreScale score;
+    float cap_most;   // products below this may use it
 };
 
 template <int D, int kTiles>
@@ -278,10 +279,12 @@ __device__ __forceinline__ void tmem_ld32_max(uint32_t taddr, uint32_t (&r)[32],
 
 // The weights of the products s (columns c .. c + 63 of a row at position p) against the reference
 // m as bf16 pairs, handed to store(k, pairs) 32 columns at a time.  Returns their sum.
-// kFast: all 64 are seen, at columns up to p where heads have slopes.
+// kFast: all 64 are seen, at columns up to p where heads have slopes, and products that are capped
+// are small enough for CapPoly (but for kSpecial pairs of 16, which balance the units).
+constexpr int kSpecial = 4;
 template <int kScore, bool kFast, class Store>
 __device__ __forceinline__ float weights_64(const uint32_t (&s)[2][32], uint32_t seen0, uint32_t seen1, int c, int p, float m,
-                                            const ScoreScale &sc, Store store) {
+                                            const ScoreScale &sc, const CapPoly &poly, Store store) {
     float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     const float away = (float)(c - p);  // column less position
     const float base = (kScore & kBias) && kFast ? fmaf(sc.slope, away, -m) : -m;
@@ -302,7 +305,10 @@ __device__ __forceinline__ float weights_64(const uint32_t (&s)[2][32], uint32_t
                     add1 = fmaf(-sc.slope, fabsf(away + (float)(n + 1)), base);
                 }
             }
-            float2 x = score_pair<kScore>(__uint_as_float(s[k][e]), __uint_as_float(s[k][e + 1]), sc, add0, add1);
+            constexpr bool kPoly = (kScore & kCap) && kFast;
+            const float s0 = __uint_as_float(s[k][e]), s1 = __uint_as_float(s[k][e + 1]);
+            float2 x = kPoly && (e >> 1) % 16 * kSpecial % 16 >= kSpecial ? score_pair_poly(s0, s1, poly, add0, add1)
+                                                                        : score_pair<kScore>(s0, s1, sc, add0, add1);
             if (!kFast) {
                 x.x = (seen >> e) & 1u ? x.x : -INFINITY;
                 x.y = (seen >> (e + 1)) & 1u ? x.y : -INFINITY;
@@ -831,6 +837,8 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
         const int t = warp >> 2, wq = warp & 3;
         const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
         ScoreScale sc = prm.score;
+        CapPoly poly;
+        if constexpr (kScore & kCap) poly.set(sc);
         uint32_t uses0 = 0, uses1 = 0;  // of the slots, in the segments before
         uint32_t done = 0, joins = 0;           // blocks, and joins, so far
         bool ok = true;
@@ -873,6 +881,8 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                     tmem_wait_ld();
                     // How far the scores reach: at most (seen whole), or exactly.
                     float top;
+                    bool quick = fast;
+                    if constexpr (kScore & kCap) quick = fast && __all_sync(0xffffffffu, fmaxf(r[0], r[1]) < prm.cap_most);
                     if (fast) {
                         top = reached<kScore & kCap>(fmaxf(r[0], r[1]), true, sc);
                         if constexpr (kScore & kBias) top += fmaxf(sc.slope * (float)(c + 63 - p), sc.slope * (float)(c - p));
@@ -914,10 +924,10 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                         tmem_st16(col + 32 * h + 16 * k, pw);
                     };
                     float sum = 0.f;
-                    if (fast) {
-                        sum = weights_64<kScore, true>(s, seen0, seen1, c, p, m, sc, store);
-                    } else if (__any_sync(0xffffffffu, (seen0 | seen1) != 0)) {
-                        sum = weights_64<kScore, false>(s, seen0, seen1, c, p, m, sc, store);
+                    if (quick) {
+                        sum = weights_64<kScore, true>(s, seen0, seen1, c, p, m, sc, poly, store);
+                    } else if (fast || __any_sync(0xffffffffu, (seen0 | seen1) != 0)) {
+                        sum = weights_64<kScore, false>(s, seen0, seen1, c, p, m, sc, poly, store);
                     } else {  // no row of the warp sees any
                         const uint32_t none[16] = {};
                         store(0, none);
