@@ -41,6 +41,7 @@ struct Params {
     float group_inv;  // 1 / group
     int items_most;   // items of the longest request
     ScoreScale score;
+    float cap_most;   // products below this may use CapPoly
 };
 
 template <int D, int NQ>
@@ -52,14 +53,15 @@ struct Cfg {
     static constexpr int kQBytes = kBoxes * kQBoxBytes;
     static constexpr int kKStages = NQ == 128 ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 6);
     static constexpr int kQStages = NQ == 128 ? (D == 128 ? 2 : 4) : 4;
+    static constexpr int kRStages = 4;  // of the lists beside the q tiles, which the sums read longer than the products do
     static constexpr int kSoftWarps = 8, kLoadWarps = 8, kFirstLoad = 8, kMmaWarp = 16, kThreads = 544;
     static constexpr int kOffK = 0, kOffQ = kOffK + kKStages * kKBytes;
     // per stage NQ each of: -lse, slope, position less the first row's (as a number of either kind); the first position
     static constexpr int kOffRow = kOffQ + kQStages * kQBytes;
     static constexpr int kRowBytes = NQ * 16 + 16;
-    static constexpr int kOffBar = kOffRow + kQStages * kRowBytes;
+    static constexpr int kOffBar = kOffRow + kRStages * kRowBytes;
     static constexpr int bKFull = 0, bKEmpty = bKFull + kKStages, bQFull = bKEmpty + kKStages, bQEmpty = bQFull + kQStages,
-                         bRFull = bQEmpty + kQStages, bSFull = bRFull + kQStages, bSEmpty = bSFull + 4, bDrain = bSEmpty + 4,
+                         bRFull = bQEmpty + kQStages, bREmpty = bRFull + kRStages, bSFull = bREmpty + kRStages, bSEmpty = bSFull + 4, bDrain = bSEmpty + 4,
                          bSegFull = bDrain + 1, bSegEmpty = bSegFull + 2, bCount = bSegEmpty + 2;
     static constexpr int kOffHolder = kOffBar + 8 * bCount;
     static constexpr int kOffWalk = kOffHolder + 8;
@@ -201,8 +203,11 @@ struct Walk {
 // e^(z - lse) of 16 rows for the thread's column, summed.  list: -lse (log2 units), slopes and
 // positions less the first row's, from the first of these rows on; away: the first row's position
 // less the column.  A row sees the column where the distance, unsigned, is at most `most`.
+// kFast: the column is seen by all, from no later position where heads have slopes, and capped products are small
+// (CapPoly takes three pairs of four).
 template <int kScore, bool kFast, int NQ>
-__device__ __forceinline__ float sum_16(const uint32_t (&s)[16], const float *list, int away, uint32_t most, const ScoreScale &sc) {
+__device__ __forceinline__ float sum_16(const uint32_t *s, const float *list, int away, uint32_t most, const ScoreScale &sc,
+                                        const CapPoly &poly) {
     float2 acc = make_float2(0.f, 0.f);
     const float base = (float)away;
 #pragma unroll
@@ -220,7 +225,9 @@ __device__ __forceinline__ float sum_16(const uint32_t (&s)[16], const float *li
         const int rs[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
         for (int u = 0; u < 4; u += 2) {
-            float2 x = score_pair<kScore>(__uint_as_float(s[e + u]), __uint_as_float(s[e + u + 1]), sc, add[u], add[u + 1]);
+            const float s0 = __uint_as_float(s[e + u]), s1 = __uint_as_float(s[e + u + 1]);
+            float2 x = (kScore & kCap) && kFast && (e + u) % 8 != 0 ? score_pair_poly(s0, s1, poly, add[u], add[u + 1])
+                                                                   : score_pair<kScore>(s0, s1, sc, add[u], add[u + 1]);
             if (!kFast) {
                 x.x = (uint32_t)(away + rs[u]) <= most ? x.x : -INFINITY;
                 x.y = (uint32_t)(away + rs[u + 1]) <= most ? x.y : -INFINITY;
@@ -257,8 +264,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) chunk_weights_kernel(
         for (int i = 0; i < C::bCount; ++i)
             mbar_init(bar(i), i < C::bKEmpty                          ? 32 * C::kLoadWarps  // load lanes
                               : i >= C::bQFull && i < C::bQEmpty      ? 32 * C::kLoadWarps
-                              : i >= C::bQEmpty && i < C::bRFull      ? 1 + C::kSoftWarps
-                              : i >= C::bRFull && i < C::bSFull       ? (NQ + 31) / 32
+                              : i >= C::bRFull && i < C::bREmpty      ? (NQ + 31) / 32
+                              : i >= C::bREmpty && i < C::bSFull      ? C::kSoftWarps
                               : i >= C::bSEmpty && i < C::bDrain      ? 4
                               : i >= C::bSegEmpty                     ? C::kSoftWarps + C::kLoadWarps + 1
                                                                       : 1);
@@ -434,12 +441,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) chunk_weights_kernel(
                     ++kn;
                 }
                 const int s = qn % C::kQStages, u = qn / C::kQStages;
+                const int rs = qn % C::kRStages, ru = qn / C::kRStages;
                 const int first = tile * NQ, last = sg.rows - 1;
+                const int t0 = first / prm.group, rem = first - t0 * prm.group;  // the first row's token, and head
                 const int64_t row0 = (int64_t)(sg.qo0 + sg.token) * a.num_heads + g * prm.group;
                 // this lane's row of the list beside the q tile
                 const bool lists = 32 * lw < NQ && 32 * lw + lane < NQ;
                 // (behind the last row: that one again, with a sum of infinity, which counts nothing)
-                const int own = first + 32 * lw + lane, n = min(own, last), token = n / prm.group, head = n - token * prm.group;
+                const int own = first + 32 * lw + lane, n = rem + min(own, last) - first;
+                const int step = quotient(n, prm.group_inv), token = t0 + step, head = n - step * prm.group;
                 float lse = INFINITY, slope = 0.f;
                 if (lists && own <= last) {
                     lse = a.lse[row0 + (int64_t)token * a.num_heads + head];
@@ -453,14 +463,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) chunk_weights_kernel(
                 for (int i = 0; i < (kMine + kPer - 1) / kPer; ++i) {
                     const int r = lw * kMine + i * kPer + sub;
                     if (kMine % kPer != 0 && i * kPer + sub >= kMine) continue;
-                    const int m = min(first + r, last), t = m / prm.group;  // past the end: the last row again
+                    const int m = rem + min(first + r, last) - first, t = quotient(m, prm.group_inv);  // past the end: the last row again
                     cp_async_16(to + (r >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4),
-                                a.q + (row0 + (int64_t)t * a.num_heads + m - t * prm.group) * D + c * 8);
+                                a.q + (row0 + (int64_t)(t0 + t) * a.num_heads + m - t * prm.group) * D + c * 8);
                 }
                 cp_async_arrive(bar(C::bQFull + s));
                 if (32 * lw < NQ) {
-                    float *list = reinterpret_cast<float *>(smem + C::kOffRow + s * C::kRowBytes);
-                    const int t0 = first / prm.group;  // the first row's token
+                    if (ru > 0) ok = warp_wait(bar(C::bREmpty + rs), (ru - 1) & 1, abort_flag, a.err);
+                    if (!ok) break;
+                    float *list = reinterpret_cast<float *>(smem + C::kOffRow + rs * C::kRowBytes);
                     if (lists) {
                         list[32 * lw + lane] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;  // a row that saw nothing counts nothing
                         list[NQ + 32 * lw + lane] = slope;
@@ -469,7 +480,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) chunk_weights_kernel(
                     }
                     if (lw == 0 && lane == 0) reinterpret_cast<int *>(list)[4 * NQ] = sg.P + sg.token + t0;
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(C::bRFull + s));
+                    if (lane == 0) mbar_arrive(bar(C::bRFull + rs));
                 }
                 ++qn;
                 if (++tile == sg.tiles) {
@@ -537,6 +548,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) chunk_weights_kernel(
         const int t = warp >> 2, wq = warp & 3;
         const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
         const ScoreScale sc = prm.score;
+        CapPoly poly;
+        if constexpr (kScore & kCap) poly.set(sc);
         int qn = 0;
         uint32_t tn = 0;
         bool ok = true;
@@ -548,9 +561,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) chunk_weights_kernel(
             float total = 0.f;
             int tile = sg.k0 % sg.tiles;
             for (int k = 0; k < sg.steps; ++k) {
-                const int qs = qn % C::kQStages;
+                const int qs = qn % C::kRStages;
                 const float *list = reinterpret_cast<const float *>(smem + C::kOffRow + qs * C::kRowBytes);
-                ok = warp_wait(bar(C::bRFull + qs), (qn / C::kQStages) & 1, abort_flag, a.err);
+                ok = warp_wait(bar(C::bRFull + qs), (qn / C::kRStages) & 1, abort_flag, a.err);
                 if (!ok) break;
                 if (tile_on) {
                     const int buf = 2 * t + (tn & 1);
@@ -568,15 +581,23 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) chunk_weights_kernel(
                     float sum = 0.f;
 #pragma unroll 1
                     for (int n = 0; n < NQ; n += 32) {
-                        uint32_t s[2][16];
-                        tmem_ld16(col + n, s[0]);
-                        if (NQ > 16) tmem_ld16(col + n + 16, s[1]);
-                        tmem_wait_ld();
+                        uint32_t s[32];
+                        bool quick = fast;
+                        if constexpr (NQ > 16) {
+                            float most_of;
+                            tmem_ld32_max<(kScore & kCap) != 0>(col + n, s, most_of);
+                            tmem_wait_ld();
+                            if constexpr (kScore & kCap) quick = fast && __all_sync(0xffffffffu, most_of < prm.cap_most);
+                        } else {
+                            tmem_ld16(col + n, reinterpret_cast<uint32_t(&)[16]>(s));
+                            tmem_wait_ld();
+                            if constexpr (kScore & kCap) quick = false;
+                        }
 #pragma unroll
                         for (int h = 0; h < (NQ > 16 ? 2 : 1); ++h) {
                             const int m = n + 16 * h;
-                            sum += fast ? sum_16<kScore, true, NQ>(s[h], list + m, away, most, sc)
-                                        : sum_16<kScore, false, NQ>(s[h], list + m, away, most, sc);
+                            sum += quick ? sum_16<kScore, true, NQ>(s + 16 * h, list + m, away, most, sc, poly)
+                                         : sum_16<kScore, false, NQ>(s + 16 * h, list + m, away, most, sc, poly);
                         }
                     }
                     total += sum;
@@ -586,7 +607,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) chunk_weights_kernel(
                     ++tn;
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::bQEmpty + qs));
+                if (lane == 0) mbar_arrive(bar(C::bREmpty + qs));
                 ++qn;
                 if (++tile == sg.tiles) tile = 0;
             }
