@@ -14,7 +14,7 @@
 // items that were cut leave partial sums (at most two per CTA), which a second kernel adds up
 // in the order of the steps.  Everything is fp32 but the products' bf16 inputs.
 //
-// Warps: four softmax warps per K tile, eight load warps (32 K rows and NQ / 8 q rows each),
+// Warps: four softmax warps per K tile (eight with NQ = 128: a thread has half of the rows), eight load warps (32 K rows and NQ / 8 q rows each),
 // one that issues MMAs.  Scores are double-buffered in tensor memory (2 x 2 x 128 columns).
 // Every wait is bounded: on timeout the CTA latches DDT_DEVERR_TIMEOUT, waits for its own
 // copies and MMAs and leaves.
@@ -54,20 +54,25 @@ struct Cfg {
     static constexpr int kKStages = NQ == 128 ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 6);
     static constexpr int kQStages = NQ == 128 ? (D == 128 ? 2 : 4) : 4;
     static constexpr int kRStages = 4;  // of the lists beside the q tiles, which the sums read longer than the products do
-    static constexpr int kSoftWarps = 8, kLoadWarps = 8, kFirstLoad = 8, kMmaWarp = 16, kThreads = 544;
+    // Warps that share a column.  With 128 rows in a step the sums are what takes the time, and two warps of a
+    // scheduler do not fill it: two capped chunks of 2048 take 652 us with one warp, 589 with two.
+    static constexpr int kSplit = NQ == 128 ? 2 : 1;
+    static constexpr int kSoftWarps = 8 * kSplit, kLoadWarps = 8, kFirstLoad = kSoftWarps, kMmaWarp = kSoftWarps + kLoadWarps,
+                         kThreads = 32 * (kMmaWarp + 1);
     static constexpr int kOffK = 0, kOffQ = kOffK + kKStages * kKBytes;
     // per stage NQ each of: -lse, slope, position less the first row's (as a number of either kind); the first position
     static constexpr int kOffRow = kOffQ + kQStages * kQBytes;
     static constexpr int kRowBytes = NQ * 16 + 16;
     static constexpr int kOffBar = kOffRow + kRStages * kRowBytes;
     static constexpr int bKFull = 0, bKEmpty = bKFull + kKStages, bQFull = bKEmpty + kKStages, bQEmpty = bQFull + kQStages,
-                         bRFull = bQEmpty + kQStages, bREmpty = bRFull + kRStages, bSFull = bREmpty + kRStages, bSEmpty = bSFull + 4, bDrain = bSEmpty + 4,
-                         bSegFull = bDrain + 1, bSegEmpty = bSegFull + 2, bCount = bSegEmpty + 2;
+                         bRFull = bQEmpty + kQStages, bREmpty = bRFull + kRStages, bSFull = bREmpty + kRStages, bSEmpty = bSFull + 4, bDrain = bSEmpty + 4, bPair = bDrain + 1, bPairEmpty = bPair + 1,
+                         bSegFull = bPairEmpty + 1, bSegEmpty = bSegFull + 2, bCount = bSegEmpty + 2;
     static constexpr int kOffHolder = kOffBar + 8 * bCount;
     static constexpr int kOffWalk = kOffHolder + 8;
     static constexpr int kWalkBytes = 128, kSegBytes = 96;
     static constexpr int kOffPlan = kOffWalk + kWalkBytes + 2 * kSegBytes;
-    static constexpr int kSmemBytes = kOffPlan + 8 * (kThreads / 32) + 1024;
+    static constexpr int kOffPair = kOffPlan + 8 * (kThreads / 32);  // the second warps' sums
+    static constexpr int kSmemBytes = kOffPair + (kSplit == 2 ? 4 * kCols : 0) + 1024;
     static constexpr int kOffCosts = kOffK;
     static constexpr uint32_t kIdesc = idesc_bf16(128, NQ, 0, 0);
     // Cost of a step and of an item besides; the share that a CTA gets at least.
@@ -200,18 +205,18 @@ struct Walk {
 };
 
 // ---------------------------------------------------------------- the sums of one step
-// e^(z - lse) of 16 rows for the thread's column, summed.  list: -lse (log2 units), slopes and
+// e^(z - lse) of kN rows for the thread's column, summed.  list: -lse (log2 units), slopes and
 // positions less the first row's, from the first of these rows on; away: the first row's position
 // less the column.  A row sees the column where the distance, unsigned, is at most `most`.
 // kFast: the column is seen by all, from no later position where heads have slopes, and capped products are small
 // (CapPoly takes three pairs of four).
-template <int kScore, bool kFast, int NQ>
-__device__ __forceinline__ float sum_16(const uint32_t *s, const float *list, int away, uint32_t most, const ScoreScale &sc,
+template <int kScore, bool kFast, int NQ, int kN>
+__device__ __forceinline__ float sum_rows(const uint32_t (&s)[kN], const float *list, int away, uint32_t most, const ScoreScale &sc,
                                         const CapPoly &poly) {
-    float2 acc = make_float2(0.f, 0.f);
+    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     const float base = (float)away;
 #pragma unroll
-    for (int e = 0; e < 16; e += 4) {
+    for (int e = 0; e < kN; e += 4) {
         const float4 l = *reinterpret_cast<const float4 *>(list + e);
         float add[4] = {l.x, l.y, l.z, l.w};
         if constexpr (kScore & kBias) {
@@ -232,18 +237,23 @@ __device__ __forceinline__ float sum_16(const uint32_t *s, const float *list, in
                 x.x = (uint32_t)(away + rs[u]) <= most ? x.x : -INFINITY;
                 x.y = (uint32_t)(away + rs[u + 1]) <= most ? x.y : -INFINITY;
             }
-            acc = f2add(acc, make_float2(ex2(x.x), ex2(x.y)));
+            acc[u >> 1] = f2add(acc[u >> 1], make_float2(ex2(x.x), ex2(x.y)));
         }
     }
-    return acc.x + acc.y;
+    return (acc[0].x + acc[1].x) + (acc[0].y + acc[1].y);
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
+// 16 consecutive 32-bit columns of this thread's lane, and the largest of them (kAbs: the largest magnitude)
+template <bool kAbs>
+__device__ __forceinline__ void tmem_ld16_max(uint32_t taddr, uint32_t (&r)[16], float &most) {
+#define DDT_LD16_MAX(abs)                                                                                                      \
+    asm volatile("tcgen05.ld.red.sync.aligned.32x32b.x16.max" abs ".f32 "                                                      \
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, %16, [%17];"                                        \
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), \
+                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=f"(most)        \
+                 : "r"(taddr))
+    if constexpr (kAbs) DDT_LD16_MAX(".abs");
+    else DDT_LD16_MAX("");
+#undef DDT_LD16_MAX
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -266,7 +276,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) chunk_weights_kernel(
                               : i >= C::bQFull && i < C::bQEmpty      ? 32 * C::kLoadWarps
                               : i >= C::bRFull && i < C::bREmpty      ? (NQ + 31) / 32
                               : i >= C::bREmpty && i < C::bSFull      ? C::kSoftWarps
-                              : i >= C::bSEmpty && i < C::bDrain      ? 4
+                              : i >= C::bSEmpty && i < C::bDrain      ? 4 * C::kSplit
+                              : i == C::bPair || i == C::bPairEmpty   ? 8
                               : i >= C::bSegEmpty                     ? C::kSoftWarps + C::kLoadWarps + 1
                                                                       : 1);
         *abort_flag = 0;
@@ -545,7 +556,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) chunk_weights_kernel(
         __syncwarp();
     } else if (warp < C::kSoftWarps) {
         // ================= sums (thread = column = TMEM lane of its tile) =================
-        const int t = warp >> 2, wq = warp & 3;
+        const int wq = warp & 3, t = (warp >> 2) & 1, half = warp >> 3;  // half: which rows of a step
         const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
         const ScoreScale sc = prm.score;
         CapPoly poly;
@@ -579,26 +590,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) chunk_weights_kernel(
                     tc_fence_after();
                     const uint32_t col = tmem + lane_off + 128 * buf;
                     float sum = 0.f;
+                    // (16 rows at a time, in a loop that is not unrolled: 32 or 64 in a go, or the next products
+                    // loaded ahead, outgrow the instruction cache and take up to half as long again)
 #pragma unroll 1
-                    for (int n = 0; n < NQ; n += 32) {
-                        uint32_t s[32];
+                    for (int n = NQ / C::kSplit * half; n < NQ / C::kSplit * (half + 1); n += 16) {
+                        uint32_t s[16];
+                        float r;
+                        tmem_ld16_max<(kScore & kCap) != 0>(col + n, s, r);
+                        tmem_wait_ld();
                         bool quick = fast;
-                        if constexpr (NQ > 16) {
-                            float most_of;
-                            tmem_ld32_max<(kScore & kCap) != 0>(col + n, s, most_of);
-                            tmem_wait_ld();
-                            if constexpr (kScore & kCap) quick = fast && __all_sync(0xffffffffu, most_of < prm.cap_most);
-                        } else {
-                            tmem_ld16(col + n, reinterpret_cast<uint32_t(&)[16]>(s));
-                            tmem_wait_ld();
-                            if constexpr (kScore & kCap) quick = false;
-                        }
-#pragma unroll
-                        for (int h = 0; h < (NQ > 16 ? 2 : 1); ++h) {
-                            const int m = n + 16 * h;
-                            sum += quick ? sum_16<kScore, true, NQ>(s + 16 * h, list + m, away, most, sc, poly)
-                                         : sum_16<kScore, false, NQ>(s + 16 * h, list + m, away, most, sc, poly);
-                        }
+                        if constexpr (kScore & kCap) quick = fast && __all_sync(0xffffffffu, r < prm.cap_most);
+                        sum += quick ? sum_rows<kScore, true, NQ, 16>(s, list + n, away, most, sc, poly)
+                                     : sum_rows<kScore, false, NQ, 16>(s, list + n, away, most, sc, poly);
                     }
                     total += sum;
                     tc_fence_before();
@@ -612,6 +615,22 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, 1) chunk_weights_kernel(
                 if (++tile == sg.tiles) tile = 0;
             }
             if (!ok) break;
+            if constexpr (C::kSplit == 2) {
+                float *place = reinterpret_cast<float *>(smem + C::kOffPair) + 128 * t + 32 * wq + lane;
+                if (half == 1) {
+                    if (seg > 0) ok = warp_wait(bar(C::bPairEmpty), (seg - 1) & 1, abort_flag, a.err);
+                    if (!ok) break;
+                    *place = total;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::bPair));
+                    continue;
+                }
+                ok = warp_wait(bar(C::bPair), seg & 1, abort_flag, a.err);
+                if (!ok) break;
+                total += *place;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::bPairEmpty));
+            }
             if (sg.part >= 0) {
                 a.o_part[(int64_t)sg.part * kCols + 128 * t + 32 * wq + lane] = total;
             } else if (j < sg.N) {
