@@ -66,7 +66,7 @@ def test_many_requests(ddt):  # noqa: F811
     run(ddt, weights_of("ties", sum(lens), 4), lens, [int(n) for n in rng.integers(0, 30, 1500)], 2, 3)
 
 
-@pytest.mark.parametrize("n", [131072, 16 * 45056 + 777])
+@pytest.mark.parametrize("n", [131072, 8 * 45056 + 777])
 def test_long_requests(ddt, n):  # noqa: F811
     # the second has more columns than a cluster's shared memory
     run(ddt, weights_of("spread", n + 9, 6), [n, 9], [n // 8, 4], 4, 1000)

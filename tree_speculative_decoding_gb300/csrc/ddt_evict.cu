@@ -28,9 +28,11 @@ namespace {
 using namespace sm100;
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kCopies = 4;           // of a histogram, against conflicts
+constexpr int kAhead = 4;            // loads in flight of a thread
 constexpr int kMostKeys = 45056;     // of a CTA in shared memory; further ones are read again
-constexpr int kColumnsOfCta = 8192;  // a cluster grows up to 16 CTAs to keep a CTA's columns below
+// A cluster grows up to 8 CTAs to keep a CTA's columns below.  (Of 16 the SMs that share a cluster hold one at a
+// time: 8 requests of 131072 take 37 us, with 8 CTAs 25.)
+constexpr int kColumnsOfCta = 8192;
 constexpr uint32_t kTop = 0xff800000u;  // key of +inf
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -60,39 +62,24 @@ __device__ __forceinline__ int columns_of(const EvictArgs &a, int b) {
 __global__ void __launch_bounds__(kThreads, 1) evict_kernel(const __grid_constant__ EvictParams prm) {
     const EvictArgs &a = prm.a;
     extern __shared__ uint32_t keys[];
-    __shared__ uint32_t copies[256 * kCopies], counts[4][256], sums[256];
-    __shared__ uint32_t above[kWarps], equal[kWarps], totals[2], found[2];
-    __shared__ int64_t kept_before[kWarps], gone_before[kWarps];
+    __shared__ uint4 copies[256];  // a histogram, four counts for each byte
+    __shared__ uint32_t counts[4][256], sums[256];
+    __shared__ uint32_t above[kWarps], equal[kWarps], totals[2], found[3], before[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cluster = prm.cluster, b = blockIdx.x / cluster, rank = blockIdx.x - b * cluster;
     auto sync_all = [&]() {  // and what the cluster's CTAs wrote is seen
         if (cluster > 1) cluster_sync();
         else __syncthreads();
     };
+    if (tid < 256) copies[tid] = make_uint4(0, 0, 0, 0);
+    if (tid < 2) before[tid] = 0;
     pdl_wait();
     pdl_trigger();
 
-    // ---- the request, and what the ones before it keep ----
+    // ---- the request, and its columns' keys ----
     const int checked = columns_of(a, b), N = max(checked, 0);
     if (checked < 0 && rank == 0 && tid == 0) latch(a.err, DDT_DEVERR_KV_INDPTR);
     const int kept = min(N, max(a.budget[b], 0)), kv0 = a.kv_indptr[b];
-    int64_t stay = 0, go = 0;
-    for (int i = tid; i < b; i += kThreads) {
-        const int n = max(columns_of(a, i), 0), k = min(n, max(a.budget[i], 0));
-        stay += k;
-        go += n - k;
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        stay += __shfl_xor_sync(kAll, stay, o);
-        go += __shfl_xor_sync(kAll, go, o);
-    }
-    if (lane == 0) {
-        kept_before[warp] = stay;
-        gone_before[warp] = go;
-    }
-
-    // ---- keys ----
     const int per = (int)((((int64_t)N + cluster - 1) / cluster + 31) & ~31);
     const int c0 = (int)min((int64_t)N, (int64_t)rank * per), n = min(per, N - c0);  // the CTA's columns
     const float *w = a.weights + kv0 + c0;
@@ -102,9 +89,31 @@ __global__ void __launch_bounds__(kThreads, 1) evict_kernel(const __grid_constan
         return j < a.sinks || j >= recent_from ? kTop : key_of(w[i]);
     };
     auto key = [&](int i) { return i < prm.keys ? keys[i] : make_key(i); };
-    for (int i = tid; i < min(n, prm.keys); i += kThreads) keys[i] = make_key(i);
-    for (int i = tid; i < 256 * kCopies; i += kThreads) copies[i] = 0;
+    const int here = min(n, prm.keys);
+    for (int i0 = tid; i0 < here; i0 += kAhead * kThreads) {
+        uint32_t k[kAhead];
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) k[e] = i0 + e * kThreads < here ? make_key(i0 + e * kThreads) : 0u;
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e)
+            if (i0 + e * kThreads < here) keys[i0 + e * kThreads] = k[e];
+    }
     __syncthreads();
+    // what the requests before this one keep, and leave (sums of broken offsets may wrap: every place is checked)
+    uint32_t stay = 0, go = 0;
+    for (int i = tid; i < b; i += kThreads) {
+        const int m = max(columns_of(a, i), 0), k = min(m, max(a.budget[i], 0));
+        stay += k;
+        go += m - k;
+    }
+    if (b > 32 * warp) {
+        stay = __reduce_add_sync(kAll, stay);
+        go = __reduce_add_sync(kAll, go);
+        if (lane == 0) {
+            atomicAdd(&before[0], stay);
+            atomicAdd(&before[1], go);
+        }
+    }
 
     // ---- the smallest key that stays, and how many columns that have it do ----
     uint32_t prefix = 0, mask = 0, left = kept;
@@ -117,59 +126,64 @@ __global__ void __launch_bounds__(kThreads, 1) evict_kernel(const __grid_constan
             const int shift = 24 - 8 * pass;
             for (int i = tid; i < n; i += kThreads) {
                 const uint32_t k = key(i);
-                if ((k & mask) == prefix) atomicAdd(&copies[((k >> shift) & 255u) * kCopies + (lane & (kCopies - 1))], 1u);
+                if ((k & mask) == prefix) atomicAdd(&reinterpret_cast<uint32_t *>(copies)[((k >> shift) & 255u) * 4 + (lane & 3)], 1u);
             }
             __syncthreads();
-            if (tid < 256) {
-                uint32_t s = 0;
+            if (cluster > 1) {
+                if (tid < 256) {
+                    const uint4 v = copies[tid];
+                    counts[pass][tid] = (v.x + v.y) + (v.z + v.w);
+                }
+                cluster_sync();
+                uint32_t v[2];  // thread (byte, q) adds those of CTAs q and q + 4
 #pragma unroll
-                for (int c = 0; c < kCopies; ++c) {
-                    s += copies[tid * kCopies + c];
-                    copies[tid * kCopies + c] = 0;
+                for (int r = 0; r < 2; ++r) {
+                    const int from = (tid >> 8) + 4 * r;
+                    v[r] = from < cluster ? remote_u32(smem_u32(&counts[pass][tid & 255]), from) : 0u;
                 }
-                counts[pass][tid] = s;
+                reinterpret_cast<uint32_t *>(copies)[(tid & 255) * 4 + (tid >> 8)] = v[0] + v[1];
+                __syncthreads();
             }
-            sync_all();
-            if (tid < 256) {
-                uint32_t s = counts[pass][tid];
-                if (cluster > 1) {
-                    s = 0;
-                    for (int r = 0; r < cluster; ++r) s += remote_u32(smem_u32(&counts[pass][tid]), r);
-                }
-                sums[tid] = s;
+            if (warp < 8) {
+                const uint4 v = copies[tid];
+                sums[255 - tid] = (v.x + v.y) + (v.z + v.w);  // the highest byte first
+                copies[tid] = make_uint4(0, 0, 0, 0);
             }
             __syncthreads();
             if (warp == 0) {  // lane l has the bytes 255 - 8 l and the 7 below
-                uint32_t v[8], mine = 0;
+                const uint4 lo = reinterpret_cast<const uint4 *>(sums)[2 * lane], hi = reinterpret_cast<const uint4 *>(sums)[2 * lane + 1];
+                const uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                uint32_t mine = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    v[i] = sums[255 - 8 * lane - i];
-                    mine += v[i];
-                }
+                for (int i = 0; i < 8; ++i) mine += v[i];
                 uint32_t upto = mine;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const uint32_t x = __shfl_up_sync(kAll, upto, o);
                     if (lane >= o) upto += x;
                 }
-                const int at = __ffs(__ballot_sync(kAll, upto >= left)) - 1;
-                if (lane == at) {
-                    uint32_t before = upto - mine;
-                    int i = 0;
+                if (upto >= left && upto - mine < left) {
+                    uint32_t sum = upto - mine;
 #pragma unroll
-                    for (int e = 0; e < 7; ++e)
-                        if (i == e && before + v[e] < left) {
-                            before += v[e];
-                            i = e + 1;
+                    for (int e = 0; e < 8; ++e) {
+                        if (sum < left && sum + v[e] >= left) {
+                            found[0] = 255 - 8 * lane - e;
+                            found[1] = left - sum;
+                            found[2] = v[e] == left - sum;
                         }
-                    found[0] = 255 - 8 * lane - i;
-                    found[1] = left - before;
+                        sum += v[e];
+                    }
                 }
             }
             __syncthreads();
             prefix |= found[0] << shift;
             mask |= 255u << shift;
             left = found[1];
+            if (found[2]) {  // all that agree so far stay: nothing is left to find
+                prefix -= 1;
+                left = 0;
+                break;
+            }
         }
     }
 
@@ -177,92 +191,74 @@ __global__ void __launch_bounds__(kThreads, 1) evict_kernel(const __grid_constan
     // a warp has a run of the CTA's columns, which it goes through in order
     const int run = ((n + kWarps - 1) / kWarps + 31) & ~31, r0 = min(n, warp * run), r1 = min(n, r0 + run);
     uint32_t up = 0, same = 0;
-    for (int i0 = r0; i0 < r1; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t k = i < r1 ? key(i) : 0u;
-        up += __popc(__ballot_sync(kAll, i < r1 && k > prefix));
-        same += __popc(__ballot_sync(kAll, i < r1 && k == prefix));
+    for (int i = r0 + lane; i < r1; i += 32) {
+        const uint32_t k = key(i);
+        up += k > prefix;
+        same += k == prefix;
     }
+    up = __reduce_add_sync(kAll, up);
+    same = __reduce_add_sync(kAll, same);
     if (lane == 0) {
         above[warp] = up;
         equal[warp] = same;
     }
     __syncthreads();
-    if (warp == 0) {
-        uint32_t u = above[lane], s = equal[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t x = __shfl_up_sync(kAll, u, o), y = __shfl_up_sync(kAll, s, o);
-            if (lane >= o) {
-                u += x;
-                s += y;
-            }
-        }
-        if (lane == 31) {
-            totals[0] = u;
-            totals[1] = s;
-        }
-        above[lane] = u - above[lane];
-        equal[lane] = s - equal[lane];
-    }
-    sync_all();
-    uint32_t up_before = above[warp], same_before = equal[warp];
+    uint32_t up_before = __reduce_add_sync(kAll, lane < warp ? above[lane] : 0u);
+    uint32_t same_before = __reduce_add_sync(kAll, lane < warp ? equal[lane] : 0u);
     if (cluster > 1) {
+        if (tid == kThreads - 32) {  // the last warp knows the sums
+            totals[0] = up_before + up;
+            totals[1] = same_before + same;
+        }
+        cluster_sync();
         const uint32_t u = lane < rank ? remote_u32(smem_u32(&totals[0]), lane) : 0u;
         const uint32_t s = lane < rank ? remote_u32(smem_u32(&totals[1]), lane) : 0u;
         up_before += __reduce_add_sync(kAll, u);
         same_before += __reduce_add_sync(kAll, s);
-        cluster_sync();  // no CTA leaves while another one reads its counts
     }
-    int64_t base = 0, gone = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        base += kept_before[i];
-        gone += gone_before[i];
-    }
+    const uint32_t base = before[0], gone = before[1];
     if (rank == 0 && tid == 0) {
         if (b == 0) a.new_indptr[0] = 0;
         a.new_indptr[b + 1] = (int)(base + kept);
-        if (base + kept > a.total_new || (a.evicted && gone + N - kept > a.total_evicted)) latch(a.err, DDT_DEVERR_KV_INDPTR);
+        if (base + kept > (uint32_t)a.total_new || (a.evicted && gone + (N - kept) > (uint32_t)a.total_evicted)) latch(a.err, DDT_DEVERR_KV_INDPTR);
     }
+    const uint32_t lanes = (1u << lane) - 1u;
+#pragma unroll 2
     for (int i0 = r0; i0 < r1; i0 += 32) {
         const int i = i0 + lane;
         const bool in = i < r1;
-        const uint32_t k = in ? key(i) : 0u, lanes = (1u << lane) - 1u;
+        const int slot = in ? a.kv_indices[kv0 + c0 + i] : 0;
+        const float x = in ? w[i] : 0.f;
+        const uint32_t k = in ? key(i) : 0u;
         const uint32_t ups = __ballot_sync(kAll, in && k > prefix), sames = __ballot_sync(kAll, in && k == prefix);
         const uint32_t u = up_before + __popc(ups & lanes), s = same_before + __popc(sames & lanes);
-        if (in) {
-            const bool stays = k > prefix || (k == prefix && s < left);
-            const uint32_t stayed = u + min(s, left);  // of the request's columns before this one
-            const int slot = a.kv_indices[kv0 + c0 + i];
-            if (stays) {
-                const int64_t to = base + stayed;
-                if (to < a.total_new) {
-                    a.new_indices[to] = slot;
-                    if (a.new_weights) a.new_weights[to] = w[i];
-                }
-            } else if (a.evicted) {
-                const int64_t to = gone + c0 + i - stayed;
-                if (to < a.total_evicted) a.evicted[to] = slot;
+        const uint32_t stayed = u + min(s, left);  // of the request's columns before this one
+        if (in && (k > prefix || (k == prefix && s < left))) {
+            const uint32_t to = base + stayed;
+            if (to < (uint32_t)a.total_new) {
+                a.new_indices[to] = slot;
+                if (a.new_weights) a.new_weights[to] = x;
             }
+        } else if (in && a.evicted) {
+            const uint32_t to = gone + c0 + i - stayed;
+            if (to < (uint32_t)a.total_evicted) a.evicted[to] = slot;
         }
         up_before += __popc(ups);
         same_before += __popc(sames);
     }
+    if (cluster > 1) cluster_sync();  // no CTA leaves while another one reads its counts
 }
 
 int cluster_of(int max_kv_len) {
     int c = 1;
-    while (c < 16 && (int64_t)c * kColumnsOfCta < max_kv_len) c *= 2;
+    while (c < 8 && (int64_t)c * kColumnsOfCta < max_kv_len) c *= 2;
     return c;
 }
 
 }  // namespace
 
 cudaError_t evict_prepare_device() {
-    cudaError_t e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostKeys * 4);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    return e;
+    return cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostKeys * 4);
 }
 
 cudaError_t launch_cache_evict(const EvictArgs &a, cudaStream_t s) {
