@@ -298,3 +298,90 @@ class GqaVerifyStep:
         ddt.ddt_cache_compact(self.kv, self.kv_indices, self.kv_indices, self.live, self.workspace, stream)
 
     check_device_errors = VerifyStep.check_device_errors
+
+
+class GqaChunkStep:
+    """One chunk of new tokens per request (a prompt, a part of one, or a single token) through a stack
+    of grouped-query layers, on a cache that may be a GqaVerifyStep's, and what keeps that cache within
+    a budget.
+
+    ``kv`` is the cache, [2 * num_layers, rows, num_kv_heads, head_dim] (layer l's K pool at 2 l, its V
+    pool at 2 l + 1); ``kv_indices`` (int32, on the device) has per request the slots of its prefix_len
+    cached tokens, then those of its q_len new ones (host arrays).  Per layer ``layer`` takes the
+    projections' q, k and v and returns what the output projection reads; score_cap, slopes, window and
+    full_len are the layer's (``ddt.ddt_gqa_chunk_attn``), given here for all of them or to ``layer``.
+
+    With ``observe`` the step also sums what every column receives, over all layers, from all of the
+    chunk's tokens or from the last ``last_rows`` of them, on top of decay * prev (``received``, of the
+    step before: its new_weights and new_indptr).  ``evict`` then cuts every request down to its budget.
+    Positions count columns: where rows have left the cache, ``position`` (int32 per new token, on the
+    device: its place behind the cached columns, so i + what has left) keeps the rotation's."""
+
+    def __init__(self, kv, kv_indices, prefix_len, q_len, num_heads, cos_sin=None, eps=1e-6, interleaved=False,
+                 scale=None, score_cap=0.0, slopes=None, window=0, full_len=None, position=None, observe=False,
+                 last_rows=0, prev=None, prev_indptr=None, decay=1.0):
+        self.kv, self.kv_indices, self.device = kv, kv_indices, kv.device
+        dev, G, D = kv.device, kv.shape[2], kv.shape[3]
+        self.prefix_len, self.q_len = np.asarray(prefix_len, np.int64), np.asarray(q_len, np.int64)
+        self.kv_len = self.prefix_len + self.q_len
+        self.B, self.num_layers = len(self.q_len), kv.shape[0] // 2
+        offsets = lambda n: np.concatenate([[0], np.cumsum(n)])  # noqa: E731
+        self.qo_indptr, self.kv_indptr = _i32(offsets(self.q_len), dev), _i32(offsets(self.kv_len), dev)
+        self.total_q, self.total_kv = int(self.q_len.sum()), int(self.kv_len.sum())
+        if kv_indices.numel() != self.total_kv:
+            raise ValueError("kv_indices must hold prefix_len + q_len slots per request")
+        self.max_q_len, self.max_kv_len = int(self.q_len.max(initial=0)), int(self.kv_len.max(initial=0))
+        self.cos_sin, self.eps, self.interleaved, self.position = cos_sin, float(eps), interleaved, position
+        self.scale = D ** -0.5 if scale is None else float(scale)
+        self.scores = dict(score_cap=score_cap, slopes=slopes, window=window, full_len=full_len)
+        self.observe, self.last_rows = observe, last_rows
+        self.prev, self.prev_indptr, self.decay = prev, prev_indptr, decay
+        empty = lambda *shape, dtype: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+        self.q = empty(self.total_q, num_heads, D, dtype=torch.bfloat16)  # normed and rotated
+        self.out = torch.empty_like(self.q)
+        self.lse = empty(self.total_q, num_heads, dtype=torch.float32)
+        self.weights = empty(self.total_kv, dtype=torch.float32)
+        self.live = empty(1, dtype=torch.int32)
+        ctas = ddt.ddt_gqa_chunk_attn_num_ctas(self.B, num_heads, G, self.max_q_len, self.max_kv_len)
+        # the layers' calls and the compaction use it one after another
+        self.workspace = empty(max(ddt.ddt_gqa_chunk_attn_workspace_size(num_heads, G, D, max(1, self.max_q_len), ctas),
+                                   ddt.ddt_gqa_chunk_weights_workspace_size(ddt.ddt_gqa_chunk_weights_num_ctas(self.B)),
+                                   ddt.ddt_cache_compact_workspace_size(kv.shape[1]), 256), dtype=torch.uint8)
+
+    def layer(self, index, q, k, v, q_weight=None, k_weight=None, stream=None, **scores):
+        """Layer `index` between its projections: q [total_q, heads, head_dim], k and v [total_q,
+        K/V heads, head_dim] bf16; returns the attention's output, good until the next layer.  Layers
+        run in order; the first one takes the earlier sums along."""
+        k_pool, v_pool = self.kv[2 * index], self.kv[2 * index + 1]
+        how = dict(self.scores, max_q_len=self.max_q_len, max_kv_len=self.max_kv_len, workspace=self.workspace, stream=stream, **scores)
+        ddt.ddt_gqa_norm_rope_append(q, k, v, q_weight, k_weight, self.eps, self.cos_sin, self.position,
+                                     self.qo_indptr, self.kv_indices, self.kv_indptr, self.q, k_pool, v_pool,
+                                     interleaved=self.interleaved, stream=stream)
+        ddt.ddt_gqa_chunk_attn(self.q, k_pool, v_pool, self.kv_indices, self.kv_indptr, self.qo_indptr, self.scale,
+                               self.out, self.lse if self.observe else None, **how)
+        if self.observe:
+            before = (self.weights, None, 1.0) if index else (self.prev, self.prev_indptr, self.decay)
+            ddt.ddt_gqa_chunk_weights(self.q, k_pool, self.lse, self.kv_indices, self.kv_indptr, self.qo_indptr, self.scale,
+                                      self.weights, prev=before[0], prev_indptr=before[1], decay=before[2],
+                                      last_rows=self.last_rows, **how)
+        return self.out
+
+    def evict(self, budget, sinks=0, recent=0, stream=None):
+        """Every request down to budget (host array) columns: its first `sinks` and last `recent` ones and
+        those that received most.  Returns (kv_indices, kv_indptr, weights, evicted) of what is left: slots,
+        offsets and sums, on the device, and the slots that left; new_len has the lengths on the host."""
+        budget = np.asarray(budget, np.int64)
+        self.new_len = np.minimum(self.kv_len, np.maximum(budget, 0))
+        kept = int(self.new_len.sum())
+        new = lambda n, dtype=torch.int32: torch.empty(n, dtype=dtype, device=self.device)  # noqa: E731
+        left = new(kept), new(self.B + 1), new(kept, torch.float32), new(self.total_kv - kept)
+        ddt.ddt_cache_evict(self.weights, self.kv_indices, self.kv_indptr, _i32(budget, self.device), left[0], left[1], left[2],
+                            left[3], sinks=sinks, recent=recent, max_kv_len=self.max_kv_len, stream=stream)
+        return left
+
+    def compact(self, kv_indices, stream=None):
+        """The rows that kv_indices names to the front of every pool, their new numbers into kv_indices, their
+        count into live."""
+        ddt.ddt_cache_compact(self.kv, kv_indices, kv_indices, self.live, self.workspace, stream)
+
+    check_device_errors = VerifyStep.check_device_errors
