@@ -143,6 +143,7 @@ __device__ __forceinline__ void tmem_ld32_max(uint32_t taddr, uint32_t (&r)[32],
 struct ScoreScale {
     float lin;    // plain: scale log2(e); capped: 2 log2(e) scale / cap
     float cap2;   // cap log2(e)
+    float u;      // scale / cap
     float slope;  // of the row's head, log2 units
 };
 __device__ __forceinline__ float rcp(float x) {
@@ -176,7 +177,7 @@ struct CapPoly {
     }
     __device__ __forceinline__ void set(const ScoreScale &k) {
         constexpr float kP[7] = {0.99999994039f, -0.33332827688f, 0.13325075805f, -0.053451646119f, 0.020279707387f, -0.0061943246983f, 0.0010380251333f};
-        u = both(k.lin * (0.5f / kLog2e));
+        u = both(k.u);
         cap2 = both(k.cap2);
 #pragma unroll
         for (int i = 0; i < 7; ++i) c[i] = both(kP[i]);
@@ -193,10 +194,13 @@ __device__ __forceinline__ float2 score_pair_poly(float s0, float s1, const CapP
           "l"(k.c[4]), "l"(k.c[5]), "l"(k.c[6]));
     return x;
 }
-__host__ __device__ inline ScoreScale score_scale(float scale, float cap) {
+// (in 64 bits, with one rounding each: an error here is one of every score, and does not average out)
+inline ScoreScale score_scale(double scale, double cap) {
+    constexpr double log2e = 1.4426950408889634;
     ScoreScale k;
-    k.lin = cap > 0.f ? 2.f * kLog2e * scale / cap : scale * kLog2e;
-    k.cap2 = cap * kLog2e;
+    k.lin = (float)(cap > 0 ? 2 * log2e * scale / cap : scale * log2e);
+    k.cap2 = (float)(cap * log2e);
+    k.u = (float)(cap > 0 ? scale / cap : 0);
     k.slope = 0.f;
     return k;
 }
