@@ -92,13 +92,13 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     }();
     return fn;
 }
-// a pool with boxes of 32 rows x 64 values
+// a pool with boxes of 16 rows x 64 values
 bool encode_pool(CUtensorMap *map, const uint16_t *pool, const ChunkArgs &a) {
     const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)a.num_kv_heads * a.head_dim, (cuuint64_t)a.pool_rows};
     const cuuint64_t strides[1] = {(cuuint64_t)a.pool_stride * 2};
-    const cuuint32_t box[2] = {64, 32}, elem[2] = {1, 1};
+    const cuuint32_t box[2] = {64, 16}, elem[2] = {1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(pool), dims, strides, box, elem,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

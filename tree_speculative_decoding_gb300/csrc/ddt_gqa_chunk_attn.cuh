@@ -70,7 +70,7 @@ __device__ __forceinline__ void cp_async_16_or_0(uint32_t dst, const void *src, 
 }
 
 struct AttnParams {
-    CUtensorMap k_map, v_map;  // the pools as [pool_rows][K/V heads * D], boxes of 32 rows x 64 values
+    CUtensorMap k_map, v_map;  // the pools as [pool_rows][K/V heads * D], boxes of 16 rows x 64 values
     ChunkArgs a;
     int group;        // query heads per K/V head
     float group_inv;  // 1 / group
@@ -634,22 +634,24 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                     const char *pool = is_v ? vp : kp;
                     // Columns that no row of the item sees (behind the last one, or outside its window) are zeros:
                     // the products of their weights, which are 0, then are too.
-                    const int col = column_of(n), mine = col + lane;
-                    const bool in_full = mine < sg.full;
-                    const uint32_t some = __ballot_sync(0xffffffffu, in_full || (mine <= sg.pb && (a.window <= 0 || mine > sg.pa - a.window)));
-                    const uint32_t every = __ballot_sync(0xffffffffu, in_full || (mine <= sg.pa && (a.window <= 0 || mine > sg.pb - a.window)));
-                    // Slots in a row (a page, or rows taken in order) are one tile copy for each 64 values, which
-                    // takes no issue slots; others 16 bytes a lane.
-                    const int slot0 = __shfl_sync(0xffffffffu, slot, 0);
-                    if (every == 0xffffffffu && __all_sync(0xffffffffu, slot == slot0 + lane)) {
-                        if (lane == 0) {
-                            mbar_arrive_expect_tx(full, 32 * D * 2);
-                            const uint32_t at = sbase + (is_v ? C::kOffV : C::kOffK) + s * C::kBlockBytes + (n % C::kUnits) * 32 * 128;
+                    const int col = column_of(n);
+                    uint32_t some = 0xffffffffu, every = 0xffffffffu;
+                    if (!all_see(col, 32, sg.pa, sg.pb, a.window, sg.full)) {
+                        const int mine = col + lane;
+                        const bool in_full = mine < sg.full;
+                        some = __ballot_sync(0xffffffffu, in_full || (mine <= sg.pb && (a.window <= 0 || mine > sg.pa - a.window)));
+                        every = __ballot_sync(0xffffffffu, in_full || (mine <= sg.pa && (a.window <= 0 || mine > sg.pb - a.window)));
+                    }
+                    // 16 slots in a row (a page, or rows taken in order) are one tile copy for each 64 values,
+                    // which takes few issue slots; others 16 bytes a lane.
+                    if (every == 0xffffffffu && __all_sync(0xffffffffu, slot == __shfl_sync(0xffffffffu, slot, lane & 16) + (lane & 15))) {
+                        if (lane == 0) mbar_arrive_expect_tx(full, 32 * D * 2);
+                        else mbar_arrive(full);
+                        if ((lane & 15) == 0) {
+                            const uint32_t at = sbase + (is_v ? C::kOffV : C::kOffK) + s * C::kBlockBytes + ((n % C::kUnits) * 32 + lane) * 128;
 #pragma unroll
                             for (int x = 0; x < C::kBoxes; ++x)
-                                tma_load_2d(at + x * C::kBoxBytes, is_v ? &prm.v_map : &prm.k_map, sg.g * D + 64 * x, slot0, full);
-                        } else {
-                            mbar_arrive(full);
+                                tma_load_2d(at + x * C::kBoxBytes, is_v ? &prm.v_map : &prm.k_map, sg.g * D + 64 * x, slot, full);
                         }
                         __syncwarp();
                         continue;
