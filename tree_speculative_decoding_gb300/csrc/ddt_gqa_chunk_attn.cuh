@@ -319,6 +319,14 @@ __device__ __forceinline__ float reach_64(const uint32_t (&s)[2][32], uint32_t s
     }
     return mx;
 }
+// The largest score where slope (j - p) is taken off (and products of unseen columns are -inf).
+__device__ __forceinline__ float reach_linear(const uint32_t (&s)[2][32], int c, int p, const ScoreScale &sc) {
+    float mx = -INFINITY;
+    const float base = sc.slope * (float)(c - p);
+#pragma unroll
+    for (int e = 0; e < 64; ++e) mx = fmaxf(mx, fmaf(__uint_as_float(s[e >> 5][e & 31]), sc.lin, fmaf(sc.slope, (float)e, base)));
+    return mx;
+}
 template <int kScore>
 __device__ __forceinline__ float reached(float mx, bool some, const ScoreScale &sc) {
     if (!some || (kScore & kBias)) return mx;
@@ -863,20 +871,41 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                         seen1 = seen_bits(c + 32, p, a.window, sg.full, sg.N);
                     }
                     tmem_wait_ld();
-                    // How far the scores reach: at most (seen whole), or exactly.
+                    // How far the scores reach: at most (seen whole, or no cap), or exactly.
                     float top;
-                    bool quick = fast;
-                    if constexpr (kScore & kCap) quick = fast && __all_sync(0xffffffffu, fmaxf(r[0], r[1]) < prm.cap_most);
-                    if (fast) {
-                        top = reached<kScore & kCap>(fmaxf(r[0], r[1]), true, sc);
-                        if constexpr (kScore & kBias) top += fmaxf(sc.slope * (float)(c + 63 - p), sc.slope * (float)(c - p));
+                    bool quick = fast;  // the weights do not look at what is seen
+                    if constexpr (kScore & kCap) {
+                        quick = fast && __all_sync(0xffffffffu, fmaxf(r[0], r[1]) < prm.cap_most);
+                        if (fast) top = reached<kCap>(fmaxf(r[0], r[1]), true, sc);
+                        else top = reached<kScore>(reach_64<kScore>(s, seen0, seen1, c, p, sc), (seen0 | seen1) != 0, sc);
                     } else {
-                        top = reached<kScore>(reach_64<kScore>(s, seen0, seen1, c, p, sc), (seen0 | seen1) != 0, sc);
+                        if (!fast) {  // products of columns that the row does not see: their weights are 0 whatever is added
+                            r[0] = r[1] = -INFINITY;
+                            // The weights take slope (j - p) off as slope |p - j|: columns behind the row's own position
+                            // (of a prefix that all see) get twice that back, as a product.
+                            const float back = (kScore & kBias) ? -2.f * sc.slope / sc.lin : 0.f;
+#pragma unroll
+                            for (int e = 0; e < 64; ++e) {
+                                if constexpr (kScore & kBias)
+                                    s[e >> 5][e & 31] = __float_as_uint(fmaf(back, fmaxf((float)(c - p) + (float)e, 0.f), __uint_as_float(s[e >> 5][e & 31])));
+                                s[e >> 5][e & 31] = ((e < 32 ? seen0 : seen1) >> (e & 31)) & 1u ? s[e >> 5][e & 31] : 0xff800000u;
+                                r[e & 1] = fmaxf(r[e & 1], __uint_as_float(s[e >> 5][e & 31]));
+                            }
+                            quick = true;
+                        }
+                        top = reached<0>(fmaxf(r[0], r[1]), true, sc);
+                    }
+                    if constexpr (kScore & kBias) {
+                        if (fast || !(kScore & kCap)) {  // less the nearest column's distance (or, of a slope below 0, the farthest's)
+                            const float d0 = fabsf((float)(c - p)), d1 = fabsf((float)(c + 63 - p));
+                            top -= sc.slope * (sc.slope < 0.f ? fmaxf(d0, d1) : d0 + d1 <= 63.f ? 0.f : fminf(d0, d1));
+                        }
                     }
                     if (__any_sync(0xffffffffu, row_on && top > m_ref - kMost)) {
                         // The reference moves to the largest of these scores, and what was summed against
                         // the old one shrinks.
-                        if ((kScore != 0) && fast) top = reached<kScore>(reach_64<kScore>(s, seen0, seen1, c, p, sc), (seen0 | seen1) != 0, sc);
+                        if constexpr (kScore == kBias) top = reach_linear(s, c, p, sc);
+                        else if ((kScore & kCap) && fast) top = reached<kScore>(reach_64<kScore>(s, seen0, seen1, c, p, sc), (seen0 | seen1) != 0, sc);
                         const bool up = row_on && top > m_ref - kMost;
                         if (__any_sync(0xffffffffu, up)) {
                             const float alpha = up ? ex2(m_ref - (top + kShift)) : 1.0f;
@@ -910,7 +939,7 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                     float sum = 0.f;
                     if (quick) {
                         sum = weights_64<kScore, true>(s, seen0, seen1, c, p, m, sc, poly, store);
-                    } else if (fast || __any_sync(0xffffffffu, (seen0 | seen1) != 0)) {
+                    } else if ((kScore & kCap) && (fast || __any_sync(0xffffffffu, (seen0 | seen1) != 0))) {
                         sum = weights_64<kScore, false>(s, seen0, seen1, c, p, m, sc, poly, store);
                     } else {  // no row of the warp sees any
                         const uint32_t none[16] = {};
