@@ -153,14 +153,14 @@ __device__ __forceinline__ int items_of(const Request &r, int group) {
     return (int)(((int64_t)r.T * group + C::kPer - 1) / C::kPer);
 }
 template <class C>
-__device__ __forceinline__ Item item_of(const Request &r, int tg, int group, int window) {
+__device__ __forceinline__ Item item_of(const Request &r, int tg, int group, float group_inv, int window) {
     Item i;
     const int row0 = tg * C::kPer;
     i.rows = min(C::kPer, r.T * group - row0);
-    i.node0 = (int)((uint32_t)row0 / (uint32_t)group);
+    i.node0 = tg == 0 ? 0 : (int)((uint32_t)row0 / (uint32_t)group);
     i.rem0 = row0 - i.node0 * group;
     i.pa = r.N - r.T + i.node0;
-    i.pb = i.pa + (i.rem0 + i.rows - 1) / group;
+    i.pb = i.pa + quotient(i.rem0 + i.rows - 1, group_inv);
     i.x = blocks_of<C::NB>(i.pa, i.pb, window, r.full);
     return i;
 }
@@ -177,8 +177,10 @@ template <class C>
 __device__ __forceinline__ int blocks_before(int64_t item, int64_t x, int unit, int count) {
     const int64_t d = x - (item + C::kCostItem);
     if (d <= 0) return 0;
-    const int64_t k = divide(d + unit - 1, unit);
-    return k < count ? (int)k : count;
+    // (by constants: a division by a variable takes longer than the rest of the walk's step)
+    const uint64_t k = C::kCostOne == C::kCostFull || unit == C::kCostFull ? (uint64_t)(d + C::kCostFull - 1) / C::kCostFull
+                                                                           : (uint64_t)(d + C::kCostOne - 1) / C::kCostOne;
+    return k < (uint64_t)count ? (int)k : count;
 }
 
 // What a CTA does in one go: blocks k0 .. k0 + blocks - 1 of an item.
@@ -213,7 +215,7 @@ struct Walk {
         Segment s;
         s.blocks = 0;
         while (more && s.blocks == 0) {
-            const Item i = item_of<C>(r, tg, prm.group, a.window);
+            const Item i = item_of<C>(r, tg, prm.group, prm.group_inv, a.window);
             const int unit = unit_cost<C>(i);
             const int64_t lo = dealt ? shares.lo(cta) : 0;
             const int b0 = dealt ? blocks_before<C>(pos, lo, unit, i.x.count) : 0;
@@ -420,7 +422,7 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
             const Request r = load_request(a, b, blockIdx.x == 0 && lane == 0 ? a.err : nullptr);
             const int tgs = items_of<C>(r, prm.group);
             int64_t sum = 0;
-            for (int tg = lane; tg < tgs; tg += 32) sum += item_cost<C>(item_of<C>(r, tg, prm.group, a.window));
+            for (int tg = lane; tg < tgs; tg += 32) sum += item_cost<C>(item_of<C>(r, tg, prm.group, prm.group_inv, a.window));
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             if (lane == 0) costs[b] = sum;
@@ -466,7 +468,7 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
             int64_t pos = walk->pos;
             int tg = 0;
             for (int t0 = 0; t0 < tgs; t0 += 32) {
-                const int64_t own = t0 + lane < tgs ? item_cost<C>(item_of<C>(r, t0 + lane, prm.group, a.window)) : 0;
+                const int64_t own = t0 + lane < tgs ? item_cost<C>(item_of<C>(r, t0 + lane, prm.group, prm.group_inv, a.window)) : 0;
                 int64_t ends = own;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -1118,7 +1120,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) chunk_combine_kernel(const
     const int4 note = a.notes[cta];
     if (note.x < 0) return;
     const Request r = load_request(a, note.x, nullptr);
-    const Item it = item_of<C>(r, note.z, prm.group, a.window);
+    const Item it = item_of<C>(r, note.z, prm.group, prm.group_inv, a.window);
     if (first_row >= it.rows) return;
     const int c0 = note.w >> 1, parts = cta - c0 + 1;
     auto place = [&](int s) { return (int64_t)(s == 0 ? note.w : 2 * (c0 + s)) * prm.part_rows + first_row; };
