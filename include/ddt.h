@@ -750,7 +750,7 @@ ddt_status ddt_gqa_verify_attn(
  * -inf.  Finite scores and V give finite results.  Arithmetic is fp32, with the
  * softmax's weights rounded to bf16 for the product with V (2^-8 sum p|v| of a
  * result at most) and one rounding to bf16 at the end; values of V below 2^-73 lose
- * precision.  A capped score is off by score_cap * 2^-21 at most.
+ * precision.  A capped score is off by score_cap * 2^-20 at most.
  *
  *   score_cap   0 (none) up to 2^20.
  *   slopes      (device) float [num_heads] or NULL.
@@ -758,7 +758,8 @@ ddt_status ddt_gqa_verify_attn(
  *   full_len    (device) int32 [batch] or NULL (0); taken as 0 or kv_len_b where it
  *               is below or above.
  * Supported: as ddt_gqa_verify_attn, with max_q_len up to DDT_GQA_MAX_CHUNK;
- * scale (or 2 scale / score_cap) within 2^-100 .. 2^100.
+ * pool_stride below 2^39; scale log2(e) (capped: 2 log2(e) scale / score_cap) within
+ * 2^-100 .. 2^100.
  * Device checks (latched, the request's rows left unwritten): q_len outside
  * [0, max_q_len] or offsets outside [0, total_q] (DDT_DEVERR_QO_INDPTR), kv_len
  * outside [q_len, max_kv_len] or offsets outside [0, total_kv]

@@ -35,7 +35,7 @@ def test_chunk_host_checks(lib, name, good):  # noqa: F811
                 dict(stride=1016), dict(stride=1028), dict(max_q=-1)):
         assert f(**bad) == INVALID, bad
     for bad in (dict(D=96), dict(D=256, stride=2048), dict(H=136), dict(max_q=2 ** 20 + 1, max_kv=2 ** 21), dict(ctas=513),
-                dict(ctas=2, batch=257), dict(rows=2 ** 31), dict(batch=65536), dict(cap=2.0 ** 21), dict(scale=1e-35),
+                dict(ctas=2, batch=257), dict(rows=2 ** 31), dict(stride=2 ** 39), dict(batch=65536), dict(cap=2.0 ** 21), dict(scale=1e-35),
                 dict(scale=1e35), dict(scale=1e-25, cap=2.0 ** 20), dict(scale=1e30, cap=1e-6)):
         assert f(**bad) == UNSUPPORTED, bad
     assert f(max_q=2 ** 20, max_kv=2 ** 31 - 1) == 0

@@ -324,3 +324,56 @@ def test_slots_past_two_billion_bytes(ddt):
     ddt.ddt_gqa_chunk_attn(q.to(DEV), pool[:, 0], pool[:, 1], far.to(torch.int32).to(DEV), d["kv_indptr"], d["qo_indptr"], 0.1, out)
     clean(ddt)
     check(out, None, ref.attention(q, k, v, c, 0.1))
+
+
+def test_any_workspace_and_one_that_is_too_small(ddt):
+    # without a count the work is dealt to what the workspace holds, down to none; with one it is refused
+    c = ref.Chunk([(900, 40), (10, 70)], 6)
+    q, k, v = inputs(c, 16, 2, 64, 8)
+    want = ref.attention(q, k, v, c, 0.1)
+    for ctas in (0, 1, 2, 7, 100):
+        nbytes = max(256, ddt.ddt_gqa_chunk_attn_workspace_size(16, 2, 64, c.max_q, ctas))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=DEV)
+        out, ls = run(ddt, c, q, k, v, 0.1, workspace=ws)
+        clean(ddt)
+        check(out, ls, want)
+        with pytest.raises(ddt.DDTError, match="DDT_ERR_WORKSPACE"):
+            run(ddt, c, q, k, v, 0.1, workspace=ws, num_ctas=ctas + 1)
+    clean(ddt)
+
+
+def test_windows_and_prefixes_at_their_limits(ddt):
+    c = ref.Chunk([(200, 30), (0, 9)], 6)
+    q, k, v = inputs(c, 4, 4, 64, 8)
+    for window, full in ((2 ** 31 - 1, None), (230, [-5, 2 ** 31 - 1]), (229, [-2 ** 31, 3]), (1, [0, 0]), (2 ** 30, [230, 9])):
+        out, ls = run(ddt, c, q, k, v, 0.1, window=window, full=full)
+        clean(ddt)
+        check(out, ls, ref.attention(q, k, v, c, 0.1, window=window, full=full))
+
+
+def test_nothing_to_do(ddt):
+    c = ref.Chunk([(20, 0), (0, 0)], 6)
+    q, k, v = inputs(c, 4, 4, 64, 8)
+    run(ddt, c, q, k, v, 0.1)
+    c = ref.Chunk([(20, 0), (0, 3), (5, 0)], 6)
+    q, k, v = inputs(c, 4, 4, 64, 8)
+    out, ls = run(ddt, c, q, k, v, 0.1)
+    clean(ddt)
+    check(out, ls, ref.attention(q, k, v, c, 0.1))
+
+
+@pytest.mark.parametrize("H,G", [(8, 1), (128, 1), (6, 6)])
+def test_a_long_chunk(ddt, H, G):
+    # more items than CTAs, and items whose columns differ a lot; checked on some of the rows
+    T = 20000 // H
+    c = ref.Chunk([(300, T), (1, 5)], 3, 16)
+    q, k, v = inputs(c, H, G, 128, 8)
+    out, ls = run(ddt, c, q, k, v, 0.09, window=700, full=[40, 2])
+    clean(ddt)
+    few = ref.Chunk([(300, T), (1, 5)], 3, 16)
+    rng = np.random.default_rng(1)
+    for i in sorted({0, 1, T - 1, *rng.integers(0, T, 12).tolist()}):   # one row: a chunk of one behind all before it
+        one = ref.Chunk([(300 + i, 1)], 3)
+        one.slots = few.slots[: 300 + i + 1]
+        want = ref.attention(q[i: i + 1], k, v, one, 0.09, window=700, full=[40])
+        check(out[i: i + 1], ls[i: i + 1], want)

@@ -154,3 +154,41 @@ def test_graph_and_more_requests_than_can_be_dealt(ddt):  # noqa: F811
     g.replay()
     clean(ddt)
     check(w, want)
+
+
+def test_requests_without_new_tokens_decay(ddt):  # noqa: F811
+    c = ref.Chunk([(300, 0), (0, 0), (40, 0)], 2)
+    prev = torch.rand(340, generator=torch.Generator().manual_seed(3))
+    empty = torch.zeros(0, 4, 64, dtype=torch.bfloat16)
+    k = normal((c.rows, 2, 64), 1)
+    w = run(ddt, c, empty, k, torch.zeros(0, 4), 0.1, prev=prev, prev_lens=[300, 0, 40], decay=0.5)
+    clean(ddt)
+    assert torch.equal(w.cpu(), prev * 0.5)
+    w = run(ddt, c, empty, k, torch.zeros(0, 4), 0.1)
+    clean(ddt)
+    assert not w.any()
+
+
+def test_without_a_workspace_and_with_less(ddt):  # noqa: F811
+    c = ref.Chunk([(700, 40), (10, 70)], 6)
+    q, k = inputs(c, 16, 2, 64, 8)
+    lse = row_sums(q, k, c, 0.1)
+    want = ref.received(q, k, lse, c, 0.1)
+    for nbytes in (256, 4096, 100000):
+        w = run(ddt, c, q, k, lse, 0.1, workspace=torch.empty(nbytes, dtype=torch.uint8, device=DEV))
+        clean(ddt)
+        check(w, want)
+    with pytest.raises(ddt.DDTError, match="DDT_ERR_WORKSPACE"):
+        run(ddt, c, q, k, lse, 0.1, workspace=torch.empty(256, dtype=torch.uint8, device=DEV), num_ctas=2)
+
+
+def test_a_row_that_is_not_a_number_stays_in_its_columns(ddt):  # noqa: F811
+    # the last rows of a tile are the last token's again where there are no more
+    c = ref.Chunk([(100, 5)], 6)
+    q, k = inputs(c, 4, 2, 64, 8)
+    lse = row_sums(q, k, c, 0.1, window=30)
+    q[4] = torch.nan
+    w = run(ddt, c, q, k, lse, 0.1, window=30).cpu()
+    clean(ddt)
+    seen = ref.visible(c, 0, 30, None)[4]
+    assert torch.equal(torch.isnan(w), seen)

@@ -52,7 +52,7 @@ ddt_status chunk_args(ddt::ChunkArgs &a, const uint16_t *q, const uint16_t *k_po
     if (heads != DDT_OK) return heads;
     // the factors of a score in log2 units have to be normal numbers
     const float lin = score_cap > 0.f ? 2.f * 1.4426950408889634f * scale / score_cap : scale * 1.4426950408889634f;
-    if (max_q_len > DDT_GQA_MAX_CHUNK || pool_rows > INT32_MAX || batch > 65535 || !(lin >= 0x1p-100f && lin <= 0x1p100f) ||
+    if (max_q_len > DDT_GQA_MAX_CHUNK || pool_rows > INT32_MAX || pool_stride >= (int64_t)1 << 39 || batch > 65535 || !(lin >= 0x1p-100f && lin <= 0x1p100f) ||
         score_cap > 0x1p20f)
         return DDT_ERR_UNSUPPORTED;
     if (misaligned(q, 16) || misaligned(k_pool, 16) || misaligned(workspace, 256) ||

@@ -705,8 +705,9 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                 base += sg.blocks;
             }
             asm volatile("cp.async.wait_all;" ::: "memory");  // nothing may land after the CTA has left
-            // (tile copies that the MMA warp has not waited for: it gave up, and this wait runs out long after they landed)
-            if (!ok) mbar_wait(bar(C::bDrain), 1, 1u << 12);
+            // (nor a tile copy, which only the MMA warp waits for: where it gave up, they have this long)
+            if (!ok)
+                for (int i = 0; i < 1000; ++i) __nanosleep(1000);
         } else if (warp == kMmaWarp) {
             // ================= MMA =================
             if (elect_one()) {
