@@ -60,8 +60,11 @@ def test_sizing(lib):  # noqa: F811
     size = lib.ddt_gqa_chunk_attn_workspace_size
     assert size(64, 8, 128, 33, 0) == 0 and size(64, 7, 128, 33, 4) == 0 and size(64, 8, 128, 0, 4) == 0
     for h, g, d, t, c in ((64, 8, 128, 1, 304), (64, 8, 128, 16, 9), (64, 8, 64, 17, 5), (128, 1, 128, 8192, 512)):
-        rows = min(t * (h // g), 128 if t * (h // g) <= 128 else 256)
-        assert size(h, g, d, t, c) == up(16 * c) + up(2 * c * rows * d * 4) + up(2 * c * rows * 4)
+        # two parts per CTA of as many rows as an item has, at most 128 or (two tiles) 256; with two tiles also
+        # enough for one and twice as many CTAs
+        need = lambda rows, c: up(16 * c) + up(2 * c * rows * d * 4) + up(2 * c * rows * 4)  # noqa: B023,E731
+        rows = t * (h // g)
+        assert size(h, g, d, t, c) == (need(rows, c) if rows <= 128 else max(need(min(rows, 256), c), need(128, 2 * c)))
     ctas = lib.ddt_gqa_chunk_attn_num_ctas
     assert ctas(1, 64, 8, 8192, 8192, 152) == 152 and ctas(64, 64, 8, 1, 16384, 152) == 304 and ctas(257, 64, 8, 1, 16384, 152) == 0
     assert ctas(1, 64, 8, 9, 30, 152) == 0 and ctas(0, 64, 8, 9, 4000, 152) == 0 and ctas(1, 64, 7, 9, 4000, 152) == 0

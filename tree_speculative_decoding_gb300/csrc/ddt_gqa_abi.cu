@@ -306,7 +306,14 @@ size_t ddt_gqa_chunk_attn_workspace_size(int32_t num_heads, int32_t num_kv_heads
     a.max_q_len = max_q_len;
     a.tiles = ddt::chunk_tiles(max_q_len, num_heads / num_kv_heads);
     a.num_ctas = num_ctas;
-    return ddt::chunk_layout(a, nullptr);
+    size_t bytes = ddt::chunk_layout(a, nullptr);
+    if (a.tiles == 2) {  // num_ctas = 0 may take one tile and twice as many CTAs instead
+        a.tiles = 1;
+        a.num_ctas = 2 * num_ctas;
+        const size_t other = ddt::chunk_layout(a, nullptr);
+        if (other > bytes) bytes = other;
+    }
+    return bytes;
 }
 
 ddt_status ddt_gqa_chunk_attn(
