@@ -12,6 +12,7 @@
 // ones as are left.  A count of both per warp, scanned over the CTA and the cluster, then gives
 // every column its place.  Nothing depends on the order of atomics (they count).
 //
+// Measured back to back: 4097 columns 8.4 us, 64 requests of 1024..16384 15 us, 8 of 131072 24 us.
 // Bound by latency: a launch, one pass over 8 bytes a column, four histograms with a cluster
 // barrier each, one pass that writes.
 #include <cuda_runtime.h>

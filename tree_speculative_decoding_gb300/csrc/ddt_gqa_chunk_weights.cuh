@@ -14,6 +14,12 @@
 // items that were cut leave partial sums (at most two per CTA), which a second kernel adds up
 // in the order of the steps.  Everything is fp32 but the products' bf16 inputs.
 //
+// Measured, D = 128: 32 tokens of 32 requests after 2048..8192, 64 heads on 8, 68 us, 4.9 TB/s (memory, one CTA
+// per SM); 32 observers of 32768 columns 41 us; two chunks of 2048 after 4096..8192, 32 heads on 4, 365 us, 755
+// TFLOP/s of what is seen, with a cap 602 us.  A step of 128 rows takes ~3100 clk for 1024 of products (whose
+// operands both come from shared memory, at its whole rate) and 1024 of exponentials: the sums of 16 rows at a
+// time wait for tensor memory and for each other.
+//
 // Warps: four softmax warps per K tile (eight with NQ = 128: a thread has half of the rows), eight load warps (32 K rows and NQ / 8 q rows each),
 // one that issues MMAs.  Scores are double-buffered in tensor memory (2 x 2 x 128 columns).
 // Every wait is bounded: on timeout the CTA latches DDT_DEVERR_TIMEOUT, waits for its own
