@@ -117,3 +117,45 @@ def test_chunk_step_as_a_graph(ddt):  # noqa: F811
     g.replay()
     clean(ddt)
     assert all(torch.equal(a, b) for a, b in zip(first, outs)) and torch.equal(step.weights, sums)
+
+
+def test_evict_on_another_stream(ddt):  # noqa: F811
+    # the budgets' copy is read when the stream gets there: the current stream may not have its memory before
+    from tree_speculative_decoding_gb300.pipeline import GqaChunkStep
+    c = ref.Chunk([(700, 4), (90, 1), (30, 0)], 7)
+    kv = torch.zeros(2, c.rows, 2, 64, dtype=torch.bfloat16, device=DEV)
+    step = GqaChunkStep(kv, torch.from_numpy(c.slots).to(DEV), c.P, c.T, 4)
+    step.weights.copy_(normal((c.total_kv,), 5).float())
+    side = torch.cuda.Stream()
+    for sleep in (1000, 50_000_000):  # (the first time for what is loaded with the first call)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(sleep)
+        out = step.evict([300, 1 << 40, 11], 2, 3, stream=side)
+        others = [torch.zeros(n, dtype=torch.int32, device=DEV) for n in (3, 4, 402) for _ in range(40)]
+        pending = not side.query()
+    torch.cuda.synchronize()
+    assert pending  # else nothing is tested
+    left, indptr, weights, gone = out
+    clean(ddt)
+    stay, want_indptr, want_w, want_gone = ref.evict(step.weights.cpu(), c.slots, c.N, [300, 1 << 20, 11], 2, 3)
+    assert indptr.tolist() == want_indptr and left.tolist() == stay and gone.tolist() == want_gone
+    assert weights.cpu().tolist() == want_w and all(int(x.sum()) == 0 for x in others)
+
+
+@pytest.mark.parametrize("lens", [[(40, 0), (300, 0)], []])
+def test_step_without_new_tokens(ddt, lens):  # noqa: F811
+    # the earlier sums decay; there is nothing else to do
+    from tree_speculative_decoding_gb300.pipeline import GqaChunkStep
+    c = ref.Chunk(lens, 7)
+    kv = torch.zeros(4, c.rows, 2, 64, dtype=torch.bfloat16, device=DEV)
+    prev = normal((c.total_kv,), 5).float().to(DEV)
+    step = GqaChunkStep(kv, torch.from_numpy(c.slots).to(DEV), c.P, c.T, 4, observe=True, prev=prev, decay=0.5)
+    none = lambda heads: torch.empty(0, heads, 64, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    for n in range(2):
+        assert step.layer(n, none(4), none(2), none(2)).shape == (0, 4, 64)
+    clean(ddt)
+    assert torch.equal(step.weights, 0.5 * prev)
+    left, indptr, weights, gone = step.evict([20] * len(lens))
+    clean(ddt)
+    assert weights.numel() == 20 * len(lens) and indptr[1:].tolist() == [20 * (b + 1) for b in range(len(lens))]

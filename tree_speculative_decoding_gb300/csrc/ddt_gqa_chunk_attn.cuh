@@ -68,8 +68,8 @@ namespace chunk {
 using namespace sm100;
 
 constexpr int kRows = 128;  // rows per tile (TMEM lanes)
-// Cost of an item besides its blocks (Cfg::kCostItem): with 40 instead of 80 the CTAs of a prompt of 8192 end
-// 12% apart, with 120 it takes 893 us where it takes 872.
+// Cost of an item besides its blocks (Cfg::kCostItem): with 40 instead of 80 the CTAs of a prompt of 8192, dealt,
+// end 12% apart, with 120 it takes 893 us where it takes 872.
 //
 // Weights against the reference: 2^-kShift where the reference was found, 2^-kMost at most, so that
 // 2^31 columns sum to 1 at most.  A value's weight loses bits below 2^-126, which for the heaviest

@@ -369,14 +369,17 @@ class GqaChunkStep:
     def evict(self, budget, sinks=0, recent=0, stream=None):
         """Every request down to budget (host array) columns: its first `sinks` and last `recent` ones and
         those that received most.  Returns (kv_indices, kv_indptr, weights, evicted) of what is left: slots,
-        offsets and sums, on the device, and the slots that left; new_len has the lengths on the host."""
-        budget = np.asarray(budget, np.int64)
-        self.new_len = np.minimum(self.kv_len, np.maximum(budget, 0))
+        offsets and sums, on the device (of the call's stream), and the slots that left; new_len has the
+        lengths on the host."""
+        self.new_len = np.minimum(self.kv_len, np.maximum(np.asarray(budget, np.int64), 0))
         kept = int(self.new_len.sum())
         new = lambda n, dtype=torch.int32: torch.empty(n, dtype=dtype, device=self.device)  # noqa: E731
-        left = new(kept), new(self.B + 1), new(kept, torch.float32), new(self.total_kv - kept)
-        ddt.ddt_cache_evict(self.weights, self.kv_indices, self.kv_indptr, _i32(budget, self.device), left[0], left[1], left[2],
-                            left[3], sinks=sinks, recent=recent, max_kv_len=self.max_kv_len, stream=stream)
+        # on the call's stream: it may still need the budgets' memory when this returns
+        with torch.cuda.stream(stream):
+            left = new(kept), new(self.B + 1), new(kept, torch.float32), new(self.total_kv - kept)
+            budgets = torch.from_numpy(self.new_len.astype(np.int32)).pin_memory().to(self.device, non_blocking=True)
+            ddt.ddt_cache_evict(self.weights, self.kv_indices, self.kv_indptr, budgets, left[0], left[1], left[2], left[3],
+                                sinks=sinks, recent=recent, max_kv_len=self.max_kv_len)
         return left
 
     def compact(self, kv_indices, stream=None):
