@@ -193,6 +193,9 @@ cudaError_t launch_chunk_weights(const ChunkArgs &a, const WeightArgs &w, cudaSt
     prm.items_most = (int)(((int64_t)a.max_kv_len + received::kCols - 1) / received::kCols);
     prm.score = score_scale(a.scale, a.score_cap);
     prm.cap_most = a.score_cap / a.scale;
+    const double log2e = a.score_cap > 0.f ? (double)prm.score.cap2 / a.score_cap : (double)prm.score.lin / a.scale;
+    prm.log2e = (float)log2e;
+    prm.log2e_rest = (float)(log2e - prm.log2e);
     const int rows = w.last_rows > 0 ? std::min(w.last_rows, a.max_q_len) : a.max_q_len;
     const int nq = (int64_t)rows * prm.group <= 16 ? 16 : 128;
     switch ((a.score_cap > 0.f ? kCap : 0) | (a.slopes ? kBias : 0)) {

@@ -163,9 +163,9 @@ __device__ __forceinline__ float2 score_pair(float s0, float s1, const ScoreScal
         return f2fma(make_float2(s0, s1), make_float2(k.lin, k.lin), make_float2(add0, add1));
     }
 }
-// The same where every |z / cap| of the pair is below 1: cap tanh(u) = cap u P(u^2), P the interpolation
-// of tanh(sqrt t) / sqrt t at seven Chebyshev nodes of [0, 1] (1.4e-7 of the value in fp32, measured over
-// the range).  Ten multiply-adds in place of two special functions, of which a reciprocal takes 8 cycles of
+// The same where every |z / cap| of the pair is below 1: cap tanh(u) = cap u P(u^2), P of degree 6 with the
+// least largest error of u P(u^2) over [0, 1] (Lawson's weighted least squares, coefficients rounded one after
+// another and the rest fitted again: 2.0e-8; in fp32 6.4e-8 at most, measured over the range).  Ten multiply-adds in place of two special functions, of which a reciprocal takes 8 cycles of
 // a warp's share of the unit and 2^x 4.  The factors are pairs in registers: a packed multiply-add takes
 // no immediate, and read from constant memory they took longer than the special functions.
 struct CapPoly {
@@ -176,7 +176,7 @@ struct CapPoly {
         return r;
     }
     __device__ __forceinline__ void set(const ScoreScale &k) {
-        constexpr float kP[7] = {0.99999994039f, -0.33332827688f, 0.13325075805f, -0.053451646119f, 0.020279707387f, -0.0061943246983f, 0.0010380251333f};
+        constexpr float kP[7] = {0.99999970198f, -0.33332145214f, 0.13319680095f, -0.053268551826f, 0.01997718215f, -0.0059540499933f, 0.00096454482991f};
         u = both(k.u);
         cap2 = both(k.cap2);
 #pragma unroll
