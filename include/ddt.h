@@ -747,7 +747,7 @@ ddt_status ddt_gqa_verify_attn(
  * up to DDT_GQA_MAX_CHUNK; a single token is a chunk of one.
  * A column that a token does not see does not reach it, whatever its K and V rows
  * hold (infinities and NaN included).  Scores of -inf alone give out = 0 and lse =
- * -inf.  Finite scores and V give finite results.  Arithmetic is fp32, with the
+ * -inf.  Finite scores (with |slope| kv_len up to 2^26) and V give finite results.  Arithmetic is fp32, with the
  * softmax's weights rounded to bf16 for the product with V (2^-8 sum p|v| of a
  * result at most) and one rounding to bf16 at the end; values of V below 2^-73 lose
  * precision.  A capped score is off by score_cap * 2^-20 at most.

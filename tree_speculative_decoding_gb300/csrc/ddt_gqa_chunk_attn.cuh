@@ -275,15 +275,15 @@ struct Walk {
 // ---------------------------------------------------------------- weights of 64 columns
 // The weights of the products s (columns c .. c + 63 of a row at position p) against the reference
 // m as bf16 pairs, handed to store(k, pairs) 32 columns at a time.  Returns their sum.
-// kFast: all 64 are seen, at columns up to p where heads have slopes, and products that are capped
+// kFast: all 64 are seen, at columns up to p where `slope` is not 0, and products that are capped
 // are small enough for CapPoly (but for kSpecial pairs of 16, which balance the units).
 constexpr int kSpecial = 4;
 template <int kScore, bool kFast, class Store>
-__device__ __forceinline__ float weights_64(const uint32_t (&s)[2][32], uint32_t seen0, uint32_t seen1, int c, int p, float m,
+__device__ __forceinline__ float weights_64(const uint32_t (&s)[2][32], uint32_t seen0, uint32_t seen1, int c, int p, float m, float slope,
                                             const ScoreScale &sc, const CapPoly &poly, Store store) {
     float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     const float away = (float)(c - p);  // column less position
-    const float base = (kScore & kBias) && kFast ? fmaf(sc.slope, away, -m) : -m;
+    const float base = (kScore & kBias) && kFast ? fmaf(slope, away, -m) : -m;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const uint32_t seen = k ? seen1 : seen0;
@@ -294,11 +294,11 @@ __device__ __forceinline__ float weights_64(const uint32_t (&s)[2][32], uint32_t
             if constexpr (kScore & kBias) {
                 const int n = 32 * k + e;
                 if (kFast) {
-                    add0 = fmaf(sc.slope, (float)n, base);
-                    add1 = fmaf(sc.slope, (float)(n + 1), base);
+                    add0 = fmaf(slope, (float)n, base);
+                    add1 = fmaf(slope, (float)(n + 1), base);
                 } else {
-                    add0 = fmaf(-sc.slope, fabsf(away + (float)n), base);
-                    add1 = fmaf(-sc.slope, fabsf(away + (float)(n + 1)), base);
+                    add0 = fmaf(-slope, fabsf(away + (float)n), base);
+                    add1 = fmaf(-slope, fabsf(away + (float)(n + 1)), base);
                 }
             }
             constexpr bool kPoly = (kScore & kCap) && kFast;
@@ -333,7 +333,7 @@ __device__ __forceinline__ float reach_64(const uint32_t (&s)[2][32], uint32_t s
     }
     return mx;
 }
-// The largest score where slope (j - p) is taken off (and products of unseen columns are -inf).
+// The largest score of columns up to p that are all seen.
 __device__ __forceinline__ float reach_linear(const uint32_t (&s)[2][32], int c, int p, const ScoreScale &sc) {
     float mx = -INFINITY;
     const float base = sc.slope * (float)(c - p);
@@ -896,13 +896,13 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                     } else {
                         if (!fast) {  // products of columns that the row does not see: their weights are 0 whatever is added
                             r[0] = r[1] = -INFINITY;
-                            // The weights take slope (j - p) off as slope |p - j|: columns behind the row's own position
-                            // (of a prefix that all see) get twice that back, as a product.
-                            const float back = (kScore & kBias) ? -2.f * sc.slope / sc.lin : 0.f;
+                            // The distance, too, goes off the products: the weights' slope (j - p) is slope |p - j| up to
+                            // the row's own position alone, and columns behind it (of a prefix that all see) are here.
+                            const float less = (kScore & kBias) ? -sc.slope / sc.lin : 0.f;
 #pragma unroll
                             for (int e = 0; e < 64; ++e) {
                                 if constexpr (kScore & kBias)
-                                    s[e >> 5][e & 31] = __float_as_uint(fmaf(back, fmaxf((float)(c - p) + (float)e, 0.f), __uint_as_float(s[e >> 5][e & 31])));
+                                    s[e >> 5][e & 31] = __float_as_uint(fmaf(less, fabsf((float)(c - p) + (float)e), __uint_as_float(s[e >> 5][e & 31])));
                                 s[e >> 5][e & 31] = ((e < 32 ? seen0 : seen1) >> (e & 31)) & 1u ? s[e >> 5][e & 31] : 0xff800000u;
                                 r[e & 1] = fmaxf(r[e & 1], __uint_as_float(s[e >> 5][e & 31]));
                             }
@@ -910,16 +910,12 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                         }
                         top = reached<0>(fmaxf(r[0], r[1]), true, sc);
                     }
-                    if constexpr (kScore & kBias) {
-                        if (fast || !(kScore & kCap)) {  // less the nearest column's distance (or, of a slope below 0, the farthest's)
-                            const float d0 = fabsf((float)(c - p)), d1 = fabsf((float)(c + 63 - p));
-                            top -= sc.slope * (sc.slope < 0.f ? fmaxf(d0, d1) : d0 + d1 <= 63.f ? 0.f : fminf(d0, d1));
-                        }
-                    }
+                    // less the nearest column's distance (or, of a slope below 0, the farthest's)
+                    if ((kScore & kBias) && fast) top += fmaxf(sc.slope * (float)(c - p), sc.slope * (float)(c + 63 - p));
                     if (__any_sync(0xffffffffu, row_on && top > m_ref - kMost)) {
                         // The reference moves to the largest of these scores, and what was summed against
                         // the old one shrinks.
-                        if constexpr (kScore == kBias) top = reach_linear(s, c, p, sc);
+                        if (kScore == kBias && fast) top = reach_linear(s, c, p, sc);
                         else if ((kScore & kCap) && fast) top = reached<kScore>(reach_64<kScore>(s, seen0, seen1, c, p, sc), (seen0 | seen1) != 0, sc);
                         const bool up = row_on && top > m_ref - kMost;
                         if (__any_sync(0xffffffffu, up)) {
@@ -953,9 +949,9 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                     };
                     float sum = 0.f;
                     if (quick) {
-                        sum = weights_64<kScore, true>(s, seen0, seen1, c, p, m, sc, poly, store);
+                        sum = weights_64<kScore, true>(s, seen0, seen1, c, p, m, fast ? sc.slope : 0.f, sc, poly, store);
                     } else if ((kScore & kCap) && (fast || __any_sync(0xffffffffu, (seen0 | seen1) != 0))) {
-                        sum = weights_64<kScore, false>(s, seen0, seen1, c, p, m, sc, poly, store);
+                        sum = weights_64<kScore, false>(s, seen0, seen1, c, p, m, sc.slope, sc, poly, store);
                     } else {  // no row of the warp sees any
                         const uint32_t none[16] = {};
                         store(0, none);
