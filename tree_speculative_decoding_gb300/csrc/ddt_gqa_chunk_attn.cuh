@@ -131,7 +131,7 @@ struct Cfg {
     static constexpr int bKFull = 0, bKEmpty = bKFull + kKStages, bVFull = bKEmpty + kKStages,
                          bVEmpty = bVFull + kVStages, bSFull = bVEmpty + kVStages, bPFull = bSFull + 2,
                          bQFull = bPFull + 2 * kHalves, bQEmpty = bQFull + 1, bHalf = bQEmpty + 1, bODone = bHalf + 2, bJoin = bODone + 1,
-                         bOFin = bJoin + 1, bDrain = bOFin + 1, bSegDone = bDrain + 1, bSegFull = bSegDone + 1,
+                         bOFin = bJoin + 1, bDrain = bOFin + 1, bSegDone = bDrain + 1, bSegFull = bSegDone + 2,
                          bSegEmpty = bSegFull + 2, bCount = bSegEmpty + 2;
     static constexpr int kOffHolder = kOffBar + 8 * bCount;  // tensor memory, abort, poison in use, -
     static constexpr int kOffWalk = kOffHolder + 16;
@@ -412,7 +412,7 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                       : i >= C::bPFull && i < C::bQFull                            ? 4               // row quarters
                       : i == C::bQFull                                             ? C::kQWarps
                       : i == C::bJoin                                              ? 4
-                      : i == C::bSegDone                                           ? C::kSoftWarps
+                      : i >= C::bSegDone && i < C::bSegFull                        ? C::kSoftWarps
                       : i >= C::bSegEmpty ? C::kSoftWarps + C::kLoadWarps + 1 + (kTiles == 2 ? C::kQWarps : 0)
                                           : 1);
         *abort_flag = 0;
@@ -579,6 +579,12 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::bQFull));
     };
+    // What a wait until the softmax warps have left segment n waits for, and its parity.  Two barriers in turn: the
+    // ring hands segment n + 1 out once all have left n - 2, so of n's barrier the phase before n's is
+    // over, and the one behind it cannot end without who waits.  (With one barrier a wait in segment n + 1 would also
+    // pass while n - 1 is still being left.)
+    auto seg_done = [&](int n) { return bar(C::bSegDone + (n & 1)); };
+    auto seg_parity = [](int n) { return (uint32_t)(n >> 1) & 1u; };
     Segment sg;
 
     if (warp >= C::kSoftWarps) {
@@ -699,7 +705,7 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                     }
                     if (__any_sync(0xffffffffu, bad)) {
                         // the poison is the segment's own: the one before has to be through with it
-                        if (seg > 0) ok = warp_wait(bar(C::bSegDone), (seg - 1) & 1, abort_flag, a.err);
+                        if (seg > 0) ok = warp_wait(seg_done(seg - 1), seg_parity(seg - 1), abort_flag, a.err);
                         if (!ok) break;
                         for (; bad; bad &= bad - 1) {
                             const int k = (__ffs(bad) - 1) * kPer + sub;
@@ -813,7 +819,7 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                     if constexpr (kTiles == 2) {
                         // A lone tile's second output is read by the first tile's warps, which the second
                         // tile's do not wait for.
-                        if (was_lone) ok = wait_or_abort(bar(C::bSegDone), (seg - 1) & 1, abort_flag, a.err);
+                        if (was_lone) ok = wait_or_abort(seg_done(seg - 1), seg_parity(seg - 1), abort_flag, a.err);
                         if (!ok) break;
                         was_lone = sg.tiles == 1;
                         if (sg.tiles == 2) run(std::integral_constant<int, 2>{}, 2 * sg.blocks);
@@ -1099,7 +1105,7 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::bSegDone));
+            if (lane == 0) mbar_arrive(seg_done(seg));
         }
     }
 
