@@ -38,3 +38,15 @@ def test_values_that_are_not_finite_stay_in_their_requests(ddt, H, G, D, ctas): 
     assert torch.equal(torch.nan_to_num(got[special], 5.5), torch.nan_to_num(want[special], 5.5))
     zero = torch.zeros_like(got)
     check(torch.where(special, zero, got), ls, (torch.where(special, zero, plain[0]), *plain[1:]))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ctas", [1, 2, 3, 7])
+def test_single_blocks_of_one_tile_between_two_tiles(ddt, D, ctas):  # noqa: F811
+    rng = np.random.default_rng(D)
+    lens = [(int(rng.integers(0, 90)), int(rng.integers(17, 33) if b % 3 == 0 else rng.integers(1, 17))) for b in range(120)]
+    c = ref.Chunk(lens, 9)
+    q, k, v = inputs(c, 16, 2, D, 5)
+    out, ls = run(ddt, c, q, k, v, D ** -0.5, num_ctas=ctas)
+    clean(ddt)
+    check(out, ls, ref.attention(q, k, v, c, D ** -0.5))

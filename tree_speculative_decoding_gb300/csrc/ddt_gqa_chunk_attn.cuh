@@ -824,6 +824,11 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                         was_lone = sg.tiles == 1;
                         if (sg.tiles == 2) run(std::integral_constant<int, 2>{}, 2 * sg.blocks);
                         else run(std::integral_constant<int, 1>{}, sg.blocks);
+                        // Of a lone tile's single block the second tile's warps have no part: they may not have read
+                        // bOFin's phase of the segment before yet, which this one's would hide from them.
+                        if (ok && seg > 0 && sg.tiles == 1 && sg.blocks == 1)
+                            ok = wait_or_abort(seg_done(seg - 1), seg_parity(seg - 1), abort_flag, a.err);
+                        if (!ok) break;
                     } else {
                         run(std::integral_constant<int, 1>{}, sg.blocks);
                     }
@@ -1084,7 +1089,6 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                     if (part) a.lse_part[prow + lane] = lse;
                     else if (a.lse) a.lse[row] = lse;
                 }
-                tc_fence_before();  // the output has been read before the next segment's first product
                 if (poisoned_now) {  // rows that have left get what their columns of V held
                     __syncwarp();
 #pragma unroll 1
@@ -1104,6 +1108,7 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                     }
                 }
             }
+            tc_fence_before();  // the outputs have been read before the next segment's first products
             __syncwarp();
             if (lane == 0) mbar_arrive(seg_done(seg));
         }
