@@ -24,6 +24,18 @@ def test_prefix_ahead_of_the_tokens(ddt, H, G, D, lens, full, ctas):  # noqa: F8
     check(out, ls, ref.attention(q, k, v, c, D ** -0.5, **kw))
 
 
+@pytest.mark.parametrize("slopes", [[0.25, 1.0], [-0.5, 30.0], [1000.0, -0.01], [8192.0, 1e-4]])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_long_prefix_and_slopes_of_any_size(ddt, slopes, cap):  # noqa: F811
+    c = ref.Chunk([(0, 2048)], 22)
+    q, k, v = inputs(c, 2, 1, 64, 5, 6.0 if cap else 1.5)
+    kw = dict(cap=cap, slopes=torch.tensor(slopes), full=[2048])
+    out, ls = run(ddt, c, q, k, v, 0.125, **kw)
+    clean(ddt)
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(ls).all())
+    check(out, ls, ref.attention(q, k, v, c, 0.125, **kw))
+
+
 def test_products_that_outweigh_the_distance(ddt):  # noqa: F811
     # columns behind the row's position whose products exceed the others' by more than the slope takes
     c = ref.Chunk([(10, 300)], 23)

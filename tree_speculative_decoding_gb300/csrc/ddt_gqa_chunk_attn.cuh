@@ -283,7 +283,9 @@ __device__ __forceinline__ float weights_64(const uint32_t (&s)[2][32], uint32_t
                                             const ScoreScale &sc, const CapPoly &poly, Store store) {
     float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     const float away = (float)(c - p);  // column less position
-    const float base = (kScore & kBias) && kFast ? fmaf(slope, away, -m) : -m;
+    // (from the last column, the nearest, on: what is added to it is rounded by the columns' own distances, from the
+    // first one on it would be by 63 slope next to the token)
+    const float base = (kScore & kBias) && kFast ? fmaf(slope, (float)(c + 63 - p), -m) : -m;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const uint32_t seen = k ? seen1 : seen0;
@@ -294,8 +296,8 @@ __device__ __forceinline__ float weights_64(const uint32_t (&s)[2][32], uint32_t
             if constexpr (kScore & kBias) {
                 const int n = 32 * k + e;
                 if (kFast) {
-                    add0 = fmaf(slope, (float)n, base);
-                    add1 = fmaf(slope, (float)(n + 1), base);
+                    add0 = fmaf(slope, (float)(n - 63), base);
+                    add1 = fmaf(slope, (float)(n - 62), base);
                 } else {
                     add0 = fmaf(-slope, fabsf(away + (float)n), base);
                     add1 = fmaf(-slope, fabsf(away + (float)(n + 1)), base);
