@@ -74,7 +74,7 @@ constexpr int kRows = 128;  // rows per tile (TMEM lanes)
 // Weights against the reference: 2^-kShift where the reference was found, 2^-kMost at most, so that
 // 2^31 columns sum to 1 at most.  A value's weight loses bits below 2^-126, which for the heaviest
 // columns is |v| below 2^-73.
-constexpr float kShift = 53.f, kMost = 31.f;
+constexpr float kShift = 53.f, kMost = 31.f, kUnshift = 0x1p53f;
 
 // 16 bytes from global to shared memory, or zeros
 __device__ __forceinline__ void cp_async_16_or_0(uint32_t dst, const void *src, bool there) {
@@ -1087,7 +1087,8 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
                     }
                 }
                 if (row_on) {
-                    const float lse = none ? -INFINITY : (m_ref + log2f(l)) * kLn2;
+                    // (the shift goes before the logarithm, as a power of two: -53 + log2 would be rounded by 53's size)
+                    const float lse = none ? -INFINITY : ((m_ref - kShift) + log2f(l * kUnshift)) * kLn2;
                     if (part) a.lse_part[prow + lane] = lse;
                     else if (a.lse) a.lse[row] = lse;
                 }
@@ -1147,7 +1148,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) chunk_combine_kernel(const
     const int c0 = note.w >> 1, parts = cta - c0 + 1;
     auto place = [&](int s) { return (int64_t)(s == 0 ? note.w : 2 * (c0 + s)) * prm.part_rows + first_row; };
     // weights of 2^-9 at most: those of DDT_GQA_MAX_CTAS parts sum to 1, and finite parts to a finite value
-    constexpr float kLess = 9.f;
+    constexpr float kLess = 9.f, kMore = 512.f;
     static_assert(DDT_GQA_MAX_CTAS <= 512, "parts of a row");
     float m = -INFINITY, den = 0.f;
     float acc[E];
@@ -1191,7 +1192,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) chunk_combine_kernel(const
             }
         }
     }
-    const float inv = den == 0.f ? 0.f : 1.f / den, lse = den == 0.f ? -INFINITY : m + (log2f(den) + kLess) * kLn2;
+    const float inv = den == 0.f ? 0.f : 1.f / den, lse = den == 0.f ? -INFINITY : m + log2f(den * kMore) * kLn2;
     const int n = it.rem0 + first_row, node = quotient(n, prm.group_inv);
     const int64_t row = (int64_t)(r.qo0 + it.node0 + node) * a.num_heads + note.y * prm.group + n - node * prm.group;
     uint16_t *dst = a.out + row * D + lane * E;
