@@ -312,8 +312,8 @@ class GqaChunkStep:
     full_len are the layer's (``ddt.ddt_gqa_chunk_attn``), given here for all of them or to ``layer``.
 
     With ``observe`` the step also sums what every column receives, over all layers, from all of the
-    chunk's tokens or from the last ``last_rows`` of them, on top of decay * prev (``received``, of the
-    step before: its new_weights and new_indptr).  ``evict`` then cuts every request down to its budget.
+    chunk's tokens or from the last ``last_rows`` of them, on top of decay * prev (the step before's: the
+    weights and offsets that its ``evict`` returned).  ``evict`` then cuts every request down to its budget.
     Positions count columns: where rows have left the cache, ``position`` (int32 per new token, on the
     device: its place behind the cached columns, so i + what has left) keeps the rotation's."""
 
@@ -340,13 +340,25 @@ class GqaChunkStep:
         self.q = empty(self.total_q, num_heads, D, dtype=torch.bfloat16)  # normed and rotated
         self.out = torch.empty_like(self.q)
         self.lse = empty(self.total_q, num_heads, dtype=torch.float32)
-        self.weights = empty(self.total_kv, dtype=torch.float32)
+        self._weights = empty(self.total_kv, dtype=torch.float32)
+        self._observed = None   # the layer that was added to the weights last
+        self._given = False     # the weights were handed out before any was
         self.live = empty(1, dtype=torch.int32)
         ctas = ddt.ddt_gqa_chunk_attn_num_ctas(self.B, num_heads, G, self.max_q_len, self.max_kv_len)
         # the layers' calls and the compaction use it one after another
         self.workspace = empty(max(ddt.ddt_gqa_chunk_attn_workspace_size(num_heads, G, D, max(1, self.max_q_len), ctas),
                                    ddt.ddt_gqa_chunk_weights_workspace_size(ddt.ddt_gqa_chunk_weights_num_ctas(self.B)),
                                    ddt.ddt_cache_compact_workspace_size(kv.shape[1]), 256), dtype=torch.uint8)
+
+    @property
+    def weights(self):
+        """The sums, float32 by kv_indptr.  A step that observes nothing evicts by what is put here."""
+        self._given = True
+        return self._weights
+
+    @weights.setter
+    def weights(self, sums):
+        self._weights, self._given = sums, True
 
     def layer(self, index, q, k, v, q_weight=None, k_weight=None, stream=None, **scores):
         """Layer `index` between its projections: q [total_q, heads, head_dim], k and v [total_q,
@@ -360,10 +372,11 @@ class GqaChunkStep:
         ddt.ddt_gqa_chunk_attn(self.q, k_pool, v_pool, self.kv_indices, self.kv_indptr, self.qo_indptr, self.scale,
                                self.out, self.lse if self.observe else None, **how)
         if self.observe:
-            before = (self.weights, None, 1.0) if index else (self.prev, self.prev_indptr, self.decay)
+            before = (self._weights, None, 1.0) if index else (self.prev, self.prev_indptr, self.decay)
             ddt.ddt_gqa_chunk_weights(self.q, k_pool, self.lse, self.kv_indices, self.kv_indptr, self.qo_indptr, self.scale,
-                                      self.weights, prev=before[0], prev_indptr=before[1], decay=before[2],
+                                      self._weights, prev=before[0], prev_indptr=before[1], decay=before[2],
                                       last_rows=self.last_rows, **how)
+            self._observed = index
         return self.out
 
     def evict(self, budget, sinks=0, recent=0, stream=None):
@@ -371,6 +384,8 @@ class GqaChunkStep:
         those that received most.  Returns (kv_indices, kv_indptr, weights, evicted) of what is left: slots,
         offsets and sums, on the device (of the call's stream), and the slots that left; new_len has the
         lengths on the host."""
+        if self._observed is None and not self._given:
+            raise ValueError("nothing to evict by: no layer was observed, nor were weights given")
         self.new_len = np.minimum(self.kv_len, np.maximum(np.asarray(budget, np.int64), 0))
         kept = int(self.new_len.sum())
         new = lambda n, dtype=torch.int32: torch.empty(n, dtype=dtype, device=self.device)  # noqa: E731
@@ -378,7 +393,7 @@ class GqaChunkStep:
         with torch.cuda.stream(stream):
             left = new(kept), new(self.B + 1), new(kept, torch.float32), new(self.total_kv - kept)
             budgets = torch.from_numpy(self.new_len.astype(np.int32)).pin_memory().to(self.device, non_blocking=True)
-            ddt.ddt_cache_evict(self.weights, self.kv_indices, self.kv_indptr, budgets, left[0], left[1], left[2], left[3],
+            ddt.ddt_cache_evict(self._weights, self.kv_indices, self.kv_indptr, budgets, left[0], left[1], left[2], left[3],
                                 sinks=sinks, recent=recent, max_kv_len=self.max_kv_len)
         return left
 
