@@ -311,9 +311,10 @@ class GqaChunkStep:
     projections' q, k and v and returns what the output projection reads; score_cap, slopes, window and
     full_len are the layer's (``ddt.ddt_gqa_chunk_attn``), given here for all of them or to ``layer``.
 
-    With ``observe`` the step also sums what every column receives, over all layers, from all of the
-    chunk's tokens or from the last ``last_rows`` of them, on top of decay * prev (the step before's: the
-    weights and offsets that its ``evict`` returned).  ``evict`` then cuts every request down to its budget.
+    With ``observe`` (given here for all layers or to ``layer``) the step also sums what every column
+    receives, over the layers that are observed, from all of the chunk's tokens or from the last
+    ``last_rows`` of them, on top of decay * prev (the step before's: the weights and offsets that its
+    ``evict`` returned).  ``evict`` then cuts every request down to its budget.
     Positions count columns: where rows have left the cache, ``position`` (int32 per new token, on the
     device: its place behind the cached columns, so i + what has left) keeps the rotation's."""
 
@@ -360,19 +361,21 @@ class GqaChunkStep:
     def weights(self, sums):
         self._weights, self._given = sums, True
 
-    def layer(self, index, q, k, v, q_weight=None, k_weight=None, stream=None, **scores):
+    def layer(self, index, q, k, v, q_weight=None, k_weight=None, stream=None, observe=None, **scores):
         """Layer `index` between its projections: q [total_q, heads, head_dim], k and v [total_q,
         K/V heads, head_dim] bf16; returns the attention's output, good until the next layer.  Layers
-        run in order; the first one takes the earlier sums along."""
+        run in order; the first one that is observed takes the earlier sums along."""
+        observe = self.observe if observe is None else observe
         k_pool, v_pool = self.kv[2 * index], self.kv[2 * index + 1]
         how = dict(self.scores, max_q_len=self.max_q_len, max_kv_len=self.max_kv_len, workspace=self.workspace, stream=stream, **scores)
         ddt.ddt_gqa_norm_rope_append(q, k, v, q_weight, k_weight, self.eps, self.cos_sin, self.position,
                                      self.qo_indptr, self.kv_indices, self.kv_indptr, self.q, k_pool, v_pool,
                                      interleaved=self.interleaved, stream=stream)
         ddt.ddt_gqa_chunk_attn(self.q, k_pool, v_pool, self.kv_indices, self.kv_indptr, self.qo_indptr, self.scale,
-                               self.out, self.lse if self.observe else None, **how)
-        if self.observe:
-            before = (self._weights, None, 1.0) if index else (self.prev, self.prev_indptr, self.decay)
+                               self.out, self.lse if observe else None, **how)
+        if observe:
+            first = self._observed is None or index <= self._observed
+            before = (self.prev, self.prev_indptr, self.decay) if first else (self._weights, None, 1.0)
             ddt.ddt_gqa_chunk_weights(self.q, k_pool, self.lse, self.kv_indices, self.kv_indptr, self.qo_indptr, self.scale,
                                       self._weights, prev=before[0], prev_indptr=before[1], decay=before[2],
                                       last_rows=self.last_rows, **how)
