@@ -50,3 +50,22 @@ def test_evict_by_weights_of_the_caller(ddt):  # noqa: F811
         clean(ddt)
         stay, want_indptr, want_w, want_gone = ref.evict(given, c.slots, c.N, [30, 4], 2, 3)
         assert left.tolist() == stay and indptr.tolist() == want_indptr and gone.tolist() == want_gone and weights.tolist() == want_w
+
+
+def test_evict_refuses_a_capture(ddt):  # noqa: F811
+    # its budgets are the host's: a replay would copy from memory that is long somebody else's
+    from tree_speculative_decoding_gb300.pipeline import GqaChunkStep
+    c = ref.Chunk([(70, 4)], 7)
+    kv = torch.zeros(2, c.rows, 2, 64, dtype=torch.bfloat16, device=DEV)
+    step = GqaChunkStep(kv, torch.from_numpy(c.slots).to(DEV), c.P, c.T, 4)
+    step.weights.zero_()
+    step.evict([30])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        with pytest.raises(RuntimeError, match="captured"):
+            step.evict([20])
+    assert step.new_len.tolist() == [30]
+    left, indptr, _, _ = step.evict([20])
+    clean(ddt)
+    assert left.numel() == 20 and indptr.tolist() == [0, 20]

@@ -386,9 +386,12 @@ class GqaChunkStep:
         """Every request down to budget (host array) columns: its first `sinks` and last `recent` ones and
         those that received most.  Returns (kv_indices, kv_indptr, weights, evicted) of what is left: slots,
         offsets and sums, on the device (of the call's stream), and the slots that left; new_len has the
-        lengths on the host."""
+        lengths on the host.  The budgets come from the host: a graph takes ``ddt.ddt_cache_evict``."""
         if self._observed is None and not self._given:
             raise ValueError("nothing to evict by: no layer was observed, nor were weights given")
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("evict cannot be captured: it copies its budgets from the host")
         self.new_len = np.minimum(self.kv_len, np.maximum(np.asarray(budget, np.int64), 0))
         kept = int(self.new_len.sum())
         new = lambda n, dtype=torch.int32: torch.empty(n, dtype=dtype, device=self.device)  # noqa: E731
