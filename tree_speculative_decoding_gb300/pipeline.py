@@ -225,15 +225,19 @@ class GqaVerifyStep:
     attention: its result is what the output projection reads), then ``accept`` on the target's
     tokens and ``commit``, which moves the accepted rows of every layer at once.  ``kv`` is the
     cache: [2 * num_layers, rows, num_kv_heads, head_dim], layer l's K pool at 2 l, its V pool at
-    2 l + 1.  ``compact`` moves the rows in use to the front of all of them."""
+    2 l + 1.  ``compact`` moves the rows in use to the front of all of them.
+
+    A token is rotated by its request's cached tokens and its depth.  Where rows have left the cache (a
+    GqaChunkStep's ``evict``) that is too little: ``position`` (int32 per new token, on the device: its
+    depth and what has left its request) then takes the depth's place in the rotation."""
 
     def __init__(self, wl, num_layers, num_heads, num_kv_heads, head_dim, cos_sin=None, eps=1e-6,
-                 interleaved=False, scale=None, device="cuda"):
+                 interleaved=False, scale=None, device="cuda", position=None):
         self.wl, self.num_layers = wl, num_layers
         self.device = dev = torch.device(device)
         self.B, self.total_q = wl.B, wl.total_q
         self.max_q_len, self.max_kv_len = int(wl.q_len.max()), int(wl.kv_len.max())
-        self.cos_sin, self.eps, self.interleaved = cos_sin, float(eps), interleaved
+        self.cos_sin, self.eps, self.interleaved, self.position = cos_sin, float(eps), interleaved, position
         self.scale = head_dim ** -0.5 if scale is None else float(scale)
         mip = ddt.ddt_mask_indptr(torch.from_numpy(wl.qo_indptr.astype(np.int32)),
                                   torch.from_numpy(wl.prefix_len.astype(np.int32)))
@@ -269,7 +273,8 @@ class GqaVerifyStep:
         """Layer `index` between its projections: q [total_q, heads, head_dim], k and v [total_q,
         K/V heads, head_dim] bf16; returns the attention's output, good until the next layer."""
         k_pool, v_pool = self.kv[2 * index], self.kv[2 * index + 1]
-        ddt.ddt_gqa_norm_rope_append(q, k, v, q_weight, k_weight, self.eps, self.cos_sin, self.depth,
+        place = self.depth if self.position is None else self.position
+        ddt.ddt_gqa_norm_rope_append(q, k, v, q_weight, k_weight, self.eps, self.cos_sin, place,
                                      self.qo_indptr, self.kv_indices, self.kv_indptr, self.q, k_pool, v_pool,
                                      interleaved=self.interleaved, stream=stream)
         ddt.ddt_gqa_verify_attn(self.q, k_pool, v_pool, self.kv_indices, self.kv_indptr, self.qo_indptr, self.mask,
