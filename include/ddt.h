@@ -885,7 +885,8 @@ ddt_status ddt_cache_compact(void *slab, int64_t pool_bytes, int64_t pool_rows, 
  * request b keeps min(kv_len_b, budget[b]) of its columns, those with the largest
  * weights, where its first `sinks` and its last `recent` columns count as +inf and
  * NaN as -inf, and ties go to the lower column.  What stays keeps its order:
- *   new_indptr  (device) int32 [batch+1]: offsets of what is left, from 0 on;
+ *   new_indptr  (device) int32 [batch+1]: offsets of what is left, from 0 on (with
+ *               batch 0 nothing is written: the one 0 is the caller's);
  *   new_indices (device) int32 [total_new]: its slots, by new_indptr;
  *   new_weights (device) float [total_new] or NULL: their weights (with new_indptr
  *               the next step's prev of ddt_gqa_chunk_weights);

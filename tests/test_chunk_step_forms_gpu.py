@@ -131,3 +131,21 @@ def test_evict_refuses_a_capture(ddt):  # noqa: F811
     left, indptr, _, _ = step.evict([20])
     clean(ddt)
     assert left.numel() == 20 and indptr.tolist() == [0, 20]
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_evict_without_requests(ddt, side):  # noqa: F811
+    from tree_speculative_decoding_gb300.pipeline import GqaChunkStep
+    i32 = lambda n, x: torch.full((n,), x, dtype=torch.int32, device=DEV)  # noqa: E731
+    indptr = i32(1, -7)
+    stream = torch.cuda.Stream() if side else None
+    torch.cuda.synchronize()
+    ddt.ddt_cache_evict(torch.zeros(0, device=DEV), i32(0, 0), i32(1, 0), i32(0, 0), i32(0, 0), indptr, stream=stream)
+    clean(ddt)
+    assert indptr.tolist() == [0]
+    kv = torch.zeros(2, 10, 2, 64, dtype=torch.bfloat16, device=DEV)
+    step = GqaChunkStep(kv, i32(0, 0), [], [], 4)
+    step.weights.zero_()
+    left, indptr, weights, gone = step.evict([])
+    clean(ddt)
+    assert indptr.tolist() == [0] and left.numel() == weights.numel() == gone.numel() == 0

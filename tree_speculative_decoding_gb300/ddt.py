@@ -848,6 +848,8 @@ def ddt_cache_evict(weights, kv_indices, kv_indptr, budget, new_indices, new_ind
     if new_weights is not None and new_weights.numel() != new_indices.numel():
         raise ValueError("new_weights must be as long as new_indices")
     if B <= 0:
+        with torch.cuda.stream(stream):
+            new_indptr.zero_()   # the call itself writes nothing then
         return
     if max_kv_len is None:
         with torch.cuda.stream(stream):   # behind what writes them there
