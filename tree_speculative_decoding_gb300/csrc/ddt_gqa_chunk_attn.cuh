@@ -451,6 +451,7 @@ chunk_attn_kernel(const __grid_constant__ AttnParams prm) {
             if (lane >= o) sum += x;
         }
         if (lane == 31) plan[warp] = sum;
+        fence_proxy_async_smem();  // the costs' place is K's, which tile copies write
         __syncthreads();
         int64_t total = 0, at = sum - cost;
 #pragma unroll
