@@ -747,10 +747,10 @@ ddt_status ddt_gqa_verify_attn(
  * up to DDT_GQA_MAX_CHUNK; a single token is a chunk of one.
  * A column that a token does not see does not reach it, whatever its K and V rows
  * hold (infinities and NaN included).  Scores of -inf alone give out = 0 and lse =
- * -inf.  Finite scores (with |slope| kv_len up to 2^26) and V give finite results.  Arithmetic is fp32, with the
- * softmax's weights rounded to bf16 for the product with V (2^-8 sum p|v| of a
- * result at most) and one rounding to bf16 at the end; values of V below 2^-73 lose
- * precision.  A capped score is off by score_cap * 2^-20 at most.
+ * -inf.  Finite scores (with |slope| kv_len up to 2^26) and V give finite results.
+ * Arithmetic is fp32 (the tensor core truncates its sums of products), with the softmax's
+ * weights rounded to bf16 for the product with V (2^-8 sum p|v| of a result at most) and one
+ * rounding to bf16 at the end; values of V below 2^-73 lose precision.  A capped score is off by score_cap * 2^-20 at most.
  *
  *   score_cap   0 (none) up to 2^20.
  *   slopes      (device) float [num_heads] or NULL.
@@ -792,7 +792,8 @@ ddt_status ddt_gqa_chunk_attn(
  * the same q, k_pool, offsets, scale, score_cap, slopes, window and full_len; lse
  * is its output).  A layer's call with prev = weights, decay 1 adds to what the
  * layers before gave; a step's first call takes the sums that the columns had
- * before the step.  Arithmetic is fp32; the result does not depend on timing.
+ * before the step.  Arithmetic is fp32 (the tensor core truncates its sums of products);
+ * the result does not depend on timing.
  *
  *   lse         (device) float [total_q][num_heads].  A row with lse = -inf (nothing
  *               seen) counts nothing.

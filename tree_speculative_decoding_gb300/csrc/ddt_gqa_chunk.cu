@@ -77,12 +77,12 @@ namespace {
 // Microseconds that a call takes, roughly: with its blocks dealt to `ctas` CTAs, or (ctas = 0) with a CTA
 // per item, which the hardware hands out as others end.  Dealing costs the plan, cut items and the join, and
 // evens out long or few items; two tiles halve the reads of K and V, one tile starts and ends faster.  The
-// constants are fitted to 104 shapes measured all four ways (plain scores; D = 128 with 64 heads on 8 and D =
+// constants are fitted to 104 shapes measured all four ways (plain scores alone; D = 128 with 64 heads on 8 and D =
 // 64 with 16 heads, 17 to 1024 tokens, after 300 to 16000, 1 to 16 requests): each way within 24%, 5% on
 // average.  The choice costs 1% over the best of the four on average and 20% at most; two tiles, dealt, cost
 // 35% and 115%.  One chunk of 32 after 300 takes 27 us dealt with two tiles, 13 us with a CTA per item and one;
 // 16 of 64 after 16000 433 us and 542 us; 16 of 32 after 4000 93 us dealt with two tiles, 73 us with a CTA per
-// item.  The sizes are means over the call, and a prefix that all tokens see is not known here.
+// item.  The sizes are means over the call, and caps, slopes and a prefix that all tokens see are not known here.
 double estimate(const ChunkArgs &a, int tiles, int ctas, int num_sms) {
     const double group = (double)a.num_heads / a.num_kv_heads, q = std::min((double)a.total_q / a.batch, (double)a.max_q_len);
     const double rows = q * group, items = (double)a.batch * a.num_kv_heads * std::ceil(rows / (tiles * kRows));

@@ -25,9 +25,9 @@
 // estimate() weighs the four ways.
 //
 // Measured, D = 128, 64 heads on 8 but where stated: a prompt of 8192 880 us, 1250 TFLOP/s of what is
-// seen; 2048 tokens after 30720, 32 heads on 4, 798 us, 1340 TFLOP/s (products alone would take 537,
-// with loads 575, with the softmax 750), with a cap 1301 us; 64 tokens of 64 requests in windows of 4096
-// 169 us, 6.0 TB/s.  Two tiles are bound by a tile's chain (scores, softmax, products): ~3300 clk a
+// seen; 2048 tokens after 30720, 32 heads on 4, 798 to 830 us by the GPU's clocks (products alone would take 537,
+// with loads 575, with the softmax 750), with a cap 1294 us; 64 tokens of 64 requests in windows of 4096
+// 171 us, 5.9 TB/s.  Two tiles are bound by a tile's chain (scores, softmax, products): ~3300 clk a
 // block where its products take 2048, with the exponentials at 27% and issue at 45% of their rates;
 // one tile with few rows by memory.
 //
@@ -276,7 +276,8 @@ struct Walk {
 // The weights of the products s (columns c .. c + 63 of a row at position p) against the reference
 // m as bf16 pairs, handed to store(k, pairs) 32 columns at a time.  Returns their sum.
 // kFast: all 64 are seen, at columns up to p where `slope` is not 0, and products that are capped
-// are small enough for CapPoly (but for kSpecial pairs of 16, which balance the units).
+// are small enough for CapPoly (but for kSpecial pairs of 16, which balance the units: 2048 tokens after 30720 take
+// 1342, 1312, 1294, 1309 us with 1, 2, 4, 8).
 constexpr int kSpecial = 4;
 template <int kScore, bool kFast, class Store>
 __device__ __forceinline__ float weights_64(const uint32_t (&s)[2][32], uint32_t seen0, uint32_t seen1, int c, int p, float m, float slope,

@@ -12,10 +12,12 @@
 // bound it), else 128.
 // The steps of all items form one line that is dealt to the resident CTAs in equal shares;
 // items that were cut leave partial sums (at most two per CTA), which a second kernel adds up
-// in the order of the steps.  Everything is fp32 but the products' bf16 inputs.
+// in the order of the steps.  Everything is fp32 but the products' bf16 inputs; the tensor core truncates
+// their sums, which leaves heavy scores low: about half of what the weights are off by (5e-7 with 32 observers;
+// the other half is the rounding of the score's factor, which does not average out either).
 //
-// Measured, D = 128: 32 tokens of 32 requests after 2048..8192, 64 heads on 8, 68 us, 4.9 TB/s (memory, one CTA
-// per SM); 32 observers of 32768 columns 41 us; two chunks of 2048 after 4096..8192, 32 heads on 4, 365 us, 755
+// Measured, D = 128: 32 tokens of 32 requests after 2048..8192, 64 heads on 8, 70 us, 4.7 TB/s (memory, one CTA
+// per SM); 32 observers of 32768 columns 41 us; two chunks of 2048 after 4096..8192, 32 heads on 4, 378 us, 730
 // TFLOP/s of what is seen, with a cap 602 us.  A step of 128 rows takes ~3100 clk for 1024 of products (whose
 // operands both come from shared memory, at its whole rate) and 1024 of exponentials: the sums of 16 rows at a
 // time wait for tensor memory and for each other.
