@@ -38,6 +38,30 @@ def test_some_layers_are_observed(ddt, observed, with_prev):  # noqa: F811
         check_weights(step._weights, (want, bound))
 
 
+def test_layers_captured_one_by_one(ddt):  # noqa: F811
+    # every layer runs once before its capture: a layer's graph adds to the sums unless it is the lowest
+    from tree_speculative_decoding_gb300.pipeline import GqaChunkStep
+    H, G, D, layers = 4, 2, 64, 3
+    c = ref.Chunk([(120, 30), (0, 9)], 3)
+    kv = torch.zeros(2 * layers, c.rows, G, D, dtype=torch.bfloat16, device=DEV)
+    x = [[normal((c.total_q, h, D), 10 * n + i).to(DEV) for i, h in enumerate((H, G, G))] for n in range(layers)]
+    make = lambda: GqaChunkStep(kv, torch.from_numpy(c.slots).to(DEV), c.P, c.T, H, observe=True)  # noqa: E731
+    plain, step, graphs = make(), make(), []
+    outs = [plain.layer(n, *x[n]).clone() for n in range(layers)]
+    for n in range(layers):
+        step.layer(n, *x[n])
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            step.layer(n, *x[n])
+    for _ in range(2):
+        for n in range(layers):
+            graphs[n].replay()
+            assert torch.equal(step.out, outs[n])
+    clean(ddt)
+    assert torch.equal(step.weights, plain.weights)
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_norm_and_rotation_behind_an_eviction(ddt, interleaved):  # noqa: F811
     # what has left moves the columns but not the rotation: tokens behind an eviction are rotated by their place in

@@ -347,7 +347,7 @@ class GqaChunkStep:
         self.out = torch.empty_like(self.q)
         self.lse = empty(self.total_q, num_heads, dtype=torch.float32)
         self._weights = empty(self.total_kv, dtype=torch.float32)
-        self._observed = None   # the layer that was added to the weights last
+        self._observed = None   # the lowest layer that was observed: it starts the sums
         self._given = False     # the weights were handed out before any was
         self.live = empty(1, dtype=torch.int32)
         ctas = ddt.ddt_gqa_chunk_attn_num_ctas(self.B, num_heads, G, self.max_q_len, self.max_kv_len)
@@ -369,7 +369,7 @@ class GqaChunkStep:
     def layer(self, index, q, k, v, q_weight=None, k_weight=None, stream=None, observe=None, **scores):
         """Layer `index` between its projections: q [total_q, heads, head_dim], k and v [total_q,
         K/V heads, head_dim] bf16; returns the attention's output, good until the next layer.  Layers
-        run in order; the first one that is observed takes the earlier sums along."""
+        run in order; the lowest one that is observed starts the sums, with the earlier ones."""
         observe = self.observe if observe is None else observe
         k_pool, v_pool = self.kv[2 * index], self.kv[2 * index + 1]
         how = dict(self.scores, max_q_len=self.max_q_len, max_kv_len=self.max_kv_len, workspace=self.workspace, stream=stream, **scores)
@@ -379,12 +379,13 @@ class GqaChunkStep:
         ddt.ddt_gqa_chunk_attn(self.q, k_pool, v_pool, self.kv_indices, self.kv_indptr, self.qo_indptr, self.scale,
                                self.out, self.lse if observe else None, **how)
         if observe:
-            first = self._observed is None or index <= self._observed
-            before = (self.prev, self.prev_indptr, self.decay) if first else (self._weights, None, 1.0)
+            starts = self._observed is None or index <= self._observed
+            before = (self.prev, self.prev_indptr, self.decay) if starts else (self._weights, None, 1.0)
             ddt.ddt_gqa_chunk_weights(self.q, k_pool, self.lse, self.kv_indices, self.kv_indptr, self.qo_indptr, self.scale,
                                       self._weights, prev=before[0], prev_indptr=before[1], decay=before[2],
                                       last_rows=self.last_rows, **how)
-            self._observed = index
+            if starts:
+                self._observed = index
         return self.out
 
     def evict(self, budget, sinks=0, recent=0, stream=None):
