@@ -750,7 +750,8 @@ ddt_status ddt_gqa_verify_attn(
  * -inf.  Finite scores (with |slope| kv_len up to 2^26) and V give finite results.
  * Arithmetic is fp32 (the tensor core truncates its sums of products), with the softmax's
  * weights rounded to bf16 for the product with V (2^-8 sum p|v| of a result at most) and one
- * rounding to bf16 at the end; values of V below 2^-73 lose precision.  A capped score is off by score_cap * 2^-20 at most.
+ * rounding to bf16 at the end; values of V below 2^-73 lose precision.  A capped score is
+ * off by score_cap * 2^-20 at most.
  *
  *   score_cap   0 (none) up to 2^20.
  *   slopes      (device) float [num_heads] or NULL.
